@@ -1,6 +1,6 @@
 """Measured cases of the router-load and 4-bit dense operators.
 
-Four operators: the 4-bit group-scaled matrix-vector product (moe_q4_linear),
+Four operators: the 4-bit group-scaled matrix-vector product (moe_quant_linear),
 the per-expert counts of a selection (moe_expert_counts), the balance loss with
 its gradient (moe_balance_fwd / moe_balance_bwd) and the gradient of the
 renormalised routing weights (moe_route_bwd).  `own` chooses between their
@@ -111,8 +111,8 @@ def prepare(case, seed):
         state["y"] = torch.zeros((C, N + case["pad"]), dtype=t, device=dev)[:, :N]
         if own:
             import routed_expert_fp4_amd as rf
-            state["m"] = rf.Q4Matrix(state["codes"], state["scales"], K, G, state["zeros"])
-            state["ws"] = rf.Q4Workspace(state["m"], C, t)
+            state["m"] = rf.QuantMatrix(state["codes"], state["scales"], K, G, state["zeros"])
+            state["ws"] = rf.QuantWorkspace(state["m"], C, t)
         return state
 
     C, E, k, S = case["C"], case["E"], case["k"], case["S"]
@@ -156,7 +156,7 @@ def run(state):
     if own:
         import routed_expert_fp4_amd as rf
         if op == "q4":
-            rf.moe_q4_linear(state["m"], state["x"], case["C"], state["y"], state["ws"])
+            rf.moe_quant_linear(state["m"], state["x"], case["C"], state["y"], state["ws"])
             return state["y"]
         C, E, k, S = case["C"], case["E"], case["k"], case["S"]
         if op == "counts":
