@@ -265,6 +265,136 @@ moe_status moe_layer_fwd_noalloc(const moe_bank *bank, const float *w_router, co
                                  int32_t C, int32_t k, float *out, int32_t *topk_idx_out,
                                  float *topk_w_out, int32_t *error_out, void *stream);
 
+/* Dense matrices in 4-bit codes with group scales, for the dense steps around
+ * the routed experts (the latent layer's routed_down and routed_up, a head)
+ * where a checkpoint holds them as uniform 4-bit integers:
+ *   W[n][k] = scale[n][g] * (q[n][k] - zero[n][g]),   g = k / group,
+ * q the unsigned code 0 .. 15.  Codes are packed as the banks pack theirs:
+ * row-major, K contiguous, element 2j in bits 3..0 of byte j and element
+ * 2j+1 in bits 7..4.  The last group of a row may be partial; what is behind
+ * column cols - 1 in a row's bytes is ignored.
+ * Requirements (checked): 1 <= rows <= MOE_MAX_QUANT_ROWS, 1 <= cols <=
+ * MOE_MAX_QUANT_COLS; group 32, 64 or a multiple of 128; codes and code_pitch
+ * multiples of 16, code_pitch >= cols / 2 rounded up; scale_pitch and (where
+ * zeros are given) zero_pitch >= the number of groups; scales aligned to
+ * their type.  A row's bytes are read in units of 16, so rows * code_pitch
+ * bytes, or up to the end of the last row's last unit, must be readable. */
+typedef enum { MOE_DT_F32 = 1, MOE_DT_BF16 = 2, MOE_DT_F16 = 3 } moe_dtype;
+
+#define MOE_MAX_QUANT_ROWS (1 << 22)
+#define MOE_MAX_QUANT_COLS (1 << 17)
+
+typedef struct {
+  int32_t rows;          /* N: outputs                                        */
+  int32_t cols;          /* K: inputs                                         */
+  int32_t group;         /* codes of a row that share a scale                 */
+  int32_t scale_dtype;   /* moe_dtype of the scales                           */
+  const void *codes;     /* [rows][code_pitch] bytes                          */
+  int64_t code_pitch;    /* bytes between rows                                */
+  const void *scales;    /* [rows][scale_pitch]                               */
+  int64_t scale_pitch;   /* elements between rows                             */
+  const uint8_t *zeros;  /* [rows][zero_pitch] zero points, or NULL: 8        */
+  int64_t zero_pitch;    /* bytes between rows                                */
+} moe_quant_matrix;
+
+/* Workspace bytes of moe_quant_linear for C tokens of the type `dtype` (at
+ * least 256; 0 outside the supported range).  It needs no initialisation. */
+size_t moe_quant_workspace_size(const moe_quant_matrix *m, int32_t dtype, int32_t C);
+
+/* y[c][n] = sum_k x[c][k] W[n][k], or y += where `accumulate` is not 0, for
+ * 1 <= C <= MOE_MAX_TOKENS tokens.
+ *  x [C][x_pitch], y [C][y_pitch]: both of `dtype` (moe_dtype), pitches in
+ *  elements (x_pitch >= cols, y_pitch >= rows), aligned to their type, any
+ *  row alignment; y may not alias x.  Elements behind a row are neither read
+ *  nor written.  Products are exact and sums are fp32; y (with accumulate,
+ *  the sum with the old y) is rounded once to its type.  fp32 and bf16
+ *  activations enter as fp16 terms under a power-of-two scale per token and
+ *  slab of columns (two terms for fp32: an element keeps 22 bits, and at
+ *  least 2^-39 of its slab's largest).  The result does not depend on what
+ *  ran before: the same call gives the same bits. */
+moe_status moe_quant_linear(const moe_quant_matrix *m, int32_t dtype, const void *x,
+                            int64_t x_pitch, int32_t C, void *y, int64_t y_pitch,
+                            int32_t accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/* Load statistics of a selection, the balance loss over it and the gradients
+ * a router is trained with: what calibrating the router of a pruned bank for
+ * its top-k needs next to moe_route (page "Kimi-K3 on 2x A40": 896 experts cut
+ * to 448 "with the router calibrated for 16 active").
+ *
+ * Common arguments:
+ *  C tokens, 1 <= C <= MOE_MAX_BATCH_TOKENS (the logits of several moe_route
+ *  calls together), E experts 1 .. MOE_MAX_EXPERTS, 1 <= k <= min(E,
+ *  MOE_MAX_TOPK).
+ *  logits     [C][E] fp32; topk_idx [C][k] int32, as moe_route writes them.
+ *             An index outside [0, E) is skipped.
+ *  seq_off    NULL: all tokens are one sequence (S must be 1).  Otherwise a
+ *             device array of S + 1 int32, non-decreasing, in [0, C]: sequence
+ *             s is the tokens seq_off[s] .. seq_off[s+1] - 1, and may be
+ *             empty.  Tokens outside every sequence take no part: their rows
+ *             of logits are not read and their rows of dlogits are left as
+ *             they were.  1 <= S <= MOE_MAX_SEQUENCES.
+ *  token_mask NULL, or [C] bytes: a token whose byte is 0 is padding.  Its
+ *             logits and selection are not read, it counts nowhere, and its
+ *             row of dlogits is written as zeros (left alone where the call
+ *             accumulates).
+ *  score      how a token's logits become its shares p over the experts:
+ *             MOE_SCORE_SIGMOID  p_e = sigmoid(l_e) / sum_j sigmoid(l_j)
+ *             MOE_SCORE_SOFTMAX  p_e = exp(l_e) / sum_j exp(l_j)
+ *             both formed so that they hold where every sigmoid underflows.
+ *             A logit of -inf has share 0; a token whose logits are all -inf
+ *             has shares 0 and a zero gradient, and still counts as a token.
+ * Sums are fp32 in a fixed order, so a call repeated gives the same bits. */
+#define MOE_MAX_BATCH_TOKENS (1 << 20)
+#define MOE_MAX_SEQUENCES 65535
+typedef enum { MOE_SCORE_SIGMOID = 1, MOE_SCORE_SOFTMAX = 2 } moe_score;
+
+/* counts[s][e] = how many (token, slot) of sequence s chose expert e, and
+ * tokens[s] = the sequence's tokens that are not padding (NULL to skip).
+ * With accumulate both are added to what is there (running totals of a
+ * serving loop; int32). */
+moe_status moe_expert_counts(const int32_t *topk_idx, int32_t C, int32_t k, int32_t E,
+                             const int32_t *seq_off, int32_t S, const uint8_t *token_mask,
+                             int32_t *counts, int32_t *tokens, int32_t accumulate, void *stream);
+
+/* Workspace of moe_balance_fwd (0 outside the supported range); it must be
+ * initialised once with moe_workspace_init. */
+size_t moe_balance_workspace_size(int32_t C, int32_t E, int32_t S);
+
+/* The balance loss of a selection:
+ *   P[s][e] = mean over the tokens of s of p_e,   f[s][e] = E counts[s][e] / (k tokens[s]),
+ *   loss    = alpha / S * sum_s sum_e f[s][e] P[s][e]        (1 * alpha when balanced).
+ * A sequence without tokens has P = 0 and adds nothing.
+ *  counts [S][E] int32, tokens [S] int32, probs [S][E] fp32 (P), loss [1]
+ *  fp32: all written. */
+moe_status moe_balance_fwd(const float *logits, const int32_t *topk_idx, int32_t C, int32_t k,
+                           int32_t E, const int32_t *seq_off, int32_t S,
+                           const uint8_t *token_mask, int32_t score, float alpha,
+                           int32_t *counts, int32_t *tokens, float *probs, float *loss,
+                           void *ws, size_t ws_bytes, void *stream);
+
+/* Its gradient, the counts held constant:
+ *   g_e = grad_loss * alpha / (S tokens[s]) * f[s][e],
+ *   dlogits_e = p_e (g_e - sum_j p_j g_j) * (sigmoid(-l_e) for MOE_SCORE_SIGMOID, else 1).
+ *  counts and tokens as moe_balance_fwd wrote them; grad_loss: a device fp32.
+ *  dlogits [C][E] fp32 is written, or added to where accumulate is not 0. */
+moe_status moe_balance_bwd(const float *logits, const int32_t *counts, const int32_t *tokens,
+                           int32_t C, int32_t k, int32_t E, const int32_t *seq_off, int32_t S,
+                           const uint8_t *token_mask, int32_t score, float alpha,
+                           const float *grad_loss, float *dlogits, int32_t accumulate,
+                           void *stream);
+
+/* Gradient of moe_route's weights w_s = sigmoid(l_s) / sum_r sigmoid(l_r) over
+ * a token's k chosen experts, l_s = logits[topk_idx[s]]:
+ *   dl_s = w_s sigmoid(-l_s) (topk_dw_s - sum_r w_r topk_dw_r).
+ *  topk_dw [C][k] fp32: the gradient of the weights.  dlogits [C][E] fp32 is
+ *  written (zeros where nothing was chosen), or added to at the chosen
+ *  experts where accumulate is not 0.  Slots that name one expert add up; an
+ *  index outside [0, E) is skipped.  A token whose chosen logits are all -inf
+ *  has a zero gradient.  The selection itself is held constant. */
+moe_status moe_route_bwd(const float *logits, const int32_t *topk_idx, const float *topk_dw,
+                         int32_t C, int32_t k, int32_t E, const uint8_t *token_mask,
+                         float *dlogits, int32_t accumulate, void *stream);
+
 /* Test export: dequantise one matrix of one expert to fp32.
  *  matrix 0 = gate [I][H], 1 = up [I][H], 2 = down [H][I].
  *  MXFP4: w = e2m1 * 2^(b-127), exact (IEEE denormals kept).

@@ -27,7 +27,14 @@ BLOCK = {MOE_FMT_MXFP4: 32, MOE_FMT_NVFP4: 16}
 EXPORTS = ("moe_version", "moe_status_string", "moe_bank_layout", "moe_workspace_size",
            "moe_workspace_init", "moe_route", "moe_expert_fwd", "moe_layer_fwd", "moe_dequant",
            "moe_latent_workspace_size", "moe_latent_layer_fwd", "moe_mx_mma_workspace_size",
-           "moe_expert_fwd_mx_mma", "moe_layer_fwd_noalloc")
+           "moe_expert_fwd_mx_mma", "moe_layer_fwd_noalloc", "moe_quant_workspace_size",
+           "moe_quant_linear", "moe_expert_counts", "moe_balance_workspace_size",
+           "moe_balance_fwd", "moe_balance_bwd", "moe_route_bwd")
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 1, 2, 3
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 1, 2
+MOE_MAX_QUANT_ROWS, MOE_MAX_QUANT_COLS = 1 << 22, 1 << 17
+MOE_MAX_BATCH_TOKENS, MOE_MAX_SEQUENCES = 1 << 20, 65535
+SCORES = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 
 
 class MoeError(RuntimeError):
@@ -50,6 +57,14 @@ class moe_latent_layer(ctypes.Structure):
                 ("routed", moe_bank), ("shared", moe_bank)]
 
 
+class moe_quant_matrix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("code_pitch", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_pitch", ctypes.c_int64), ("zeros", ctypes.c_void_p),
+                ("zero_pitch", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -62,6 +77,7 @@ def lib() -> ctypes.CDLL:
                                "(or routed_expert_fp4_amd.build.build_library()) first")
         L = ctypes.CDLL(LIB_PATH)
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        f32 = ctypes.c_float
         sig = {
             "moe_version": ([], i32),
             "moe_status_string": ([i32], ctypes.c_char_p),
@@ -77,6 +93,13 @@ def lib() -> ctypes.CDLL:
             "moe_mx_mma_workspace_size": ([P, i32, i32, i32], sz),
             "moe_expert_fwd_mx_mma": ([P, P, i32, i32, P, P, P, i32, P, sz, P], i32),
             "moe_layer_fwd_noalloc": ([P, P, P, i32, i32, P, P, P, P, P], i32),
+            "moe_quant_workspace_size": ([P, i32, i32], sz),
+            "moe_quant_linear": ([P, i32, P, i64, i32, P, i64, i32, P, sz, P], i32),
+            "moe_expert_counts": ([P, i32, i32, i32, P, i32, P, P, P, i32, P], i32),
+            "moe_balance_workspace_size": ([i32, i32, i32], sz),
+            "moe_balance_fwd": ([P, P, i32, i32, i32, P, i32, P, i32, f32, P, P, P, P, P, sz, P], i32),
+            "moe_balance_bwd": ([P, P, P, i32, i32, i32, P, i32, P, i32, f32, P, P, i32, P], i32),
+            "moe_route_bwd": ([P, P, P, i32, i32, i32, P, P, i32, P], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -319,3 +342,213 @@ def moe_expert_fwd_mx_mma(bank: Bank, x, C, k, topk_idx, topk_w, out, terms: int
         _bank(bank), _ptr(x, torch.float32, (C, H), "x"), C, k,
         _ptr(topk_idx, torch.int32, (C, k), "topk_idx"), _ptr(topk_w, torch.float32, (C, k), "topk_w"),
         _ptr(out, torch.float32, (C, H), "out"), terms, ws.ptr, ws.nbytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Dense matrices in 4-bit codes with group scales
+# ---------------------------------------------------------------------------
+class _Scratch:
+    """A device workspace of `nbytes`, zero-initialised where `init`."""
+
+    def __init__(self, fn: str, nbytes: int, device, init: bool, stream=None):
+        import torch
+        if nbytes == 0:
+            raise MoeError(fn, MOE_ERR_UNSUPPORTED)
+        self.tensor = torch.empty((nbytes + 255) // 256 * 64, dtype=torch.int32, device=device)
+        self.nbytes = self.tensor.numel() * 4
+        if init:
+            with torch.cuda.device(self.tensor.device):
+                moe_workspace_init(self.tensor, stream)
+
+
+class _Call:
+    """Checks the tensors of one call and launches it on their device: they
+    must all lie on one GPU, and the stream (by default that GPU's current
+    one) must be of that GPU too."""
+
+    __slots__ = ("device",)
+
+    def __init__(self, tensor, name):
+        if not tensor.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        self.device = tensor.device
+
+    def ptr(self, t, dtype, shape, name):
+        """Device pointer of a contiguous tensor of this type and shape (None -> NULL)."""
+        if t is None:
+            return None
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def rows(self, t, dtype, shape, name):
+        """(pointer, pitch in elements) of a matrix whose rows are dense."""
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        pitch, step = t.stride()
+        if (step != 1 and shape[1] > 1) or (pitch < shape[1] and shape[0] > 1):
+            raise ValueError(f"{name} must have dense rows, got strides {(pitch, step)}")
+        return t.data_ptr(), pitch if shape[0] > 1 else shape[1]
+
+    def __call__(self, fn, *args, stream=None):
+        import torch
+        dev = self.device
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"the stream must be of {dev}, got {stream.device}")
+        f = getattr(lib(), fn)
+        if torch.cuda.current_device() == dev.index:
+            status = f(*args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(dev):
+                status = f(*args, stream.cuda_stream)
+        if status != MOE_OK:
+            raise MoeError(fn, status)
+
+
+def _moe_dtype(dtype):
+    import torch
+    d = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}.get(dtype)
+    if d is None:
+        raise ValueError(f"type must be float32, bfloat16 or float16, got {dtype}")
+    return d
+
+
+class QuantMatrix:
+    """The device tensors of one dense 4-bit matrix [N][K] and its
+    moe_quant_matrix struct: W[n][k] = scales[n][k // group] *
+    (code[n][k] - zeros[n][k // group]), zeros 8 where none are given.
+    codes [N][>= K / 2] uint8 (element 2j in the low half of byte j), rows
+    16-byte aligned; scales [N][>= K / group] fp32, bf16 or fp16; zeros uint8."""
+
+    def __init__(self, codes, scales, K: int, group: int, zeros=None):
+        import torch
+        if codes.dim() != 2 or K < 1 or group < 1:
+            raise ValueError(f"codes must be a matrix and K, group >= 1, got {tuple(codes.shape)}, {K}, {group}")
+        call = _Call(codes, "codes")
+        N, ng = codes.shape[0], -(-K // group)
+        units = -(-K // 32)
+        _, pitch = call.rows(codes, torch.uint8, codes.shape, "codes")
+        if N == 1:
+            pitch = 16 * units                       # no second row to be a pitch away
+        if codes.shape[1] < -(-K // 2):
+            raise ValueError(f"codes must have {-(-K // 2)} bytes a row, got {codes.shape[1]}")
+        # the last row's last 16-byte unit is read whole
+        have = codes.untyped_storage().nbytes() - codes.storage_offset()
+        if have < (N - 1) * pitch + 16 * units:
+            raise ValueError("codes: the last row must be readable up to a multiple of 16 bytes")
+        self.tables = []
+        for t, name, dtype in ((scales, "scales", scales.dtype), (zeros, "zeros", torch.uint8)):
+            if t is None:
+                self.tables += [None, 0]
+                continue
+            if t.dim() != 2 or t.shape[0] != N or t.shape[1] < ng:
+                raise ValueError(f"{name} must have shape {(N, ng)}, got {tuple(t.shape)}")
+            self.tables += call.rows(t, dtype, t.shape, name)
+        self.N, self.K, self.group, self.device = N, K, group, codes.device
+        self.keep = (codes, scales, zeros)
+        self.struct = moe_quant_matrix(N, K, group, _moe_dtype(scales.dtype), codes.data_ptr(), pitch,
+                                       *self.tables)
+        self.ref = ctypes.byref(self.struct)
+
+
+class QuantWorkspace(_Scratch):
+    def __init__(self, matrix: QuantMatrix, C: int, dtype):
+        n = lib().moe_quant_workspace_size(matrix.ref, _moe_dtype(dtype), C)
+        super().__init__("moe_quant_workspace_size", n, matrix.device, False)
+
+
+def moe_quant_linear(matrix: QuantMatrix, x, C, y, ws: QuantWorkspace, accumulate=False, stream=None):
+    """y [C][N] = x [C][K] W^T (or y += with accumulate); x and y of one type,
+    rows dense, any pitch."""
+    call = _Call(x, "x")
+    if matrix.device != call.device or ws.tensor.device != call.device:
+        raise ValueError(f"matrix and workspace must be on {call.device}")
+    xp, xs = call.rows(x, x.dtype, (C, matrix.K), "x")
+    yp, ys = call.rows(y, x.dtype, (C, matrix.N), "y")
+    call("moe_quant_linear", matrix.ref, _moe_dtype(x.dtype), xp, xs, C, yp, ys, int(accumulate),
+         ws.tensor.data_ptr(), ws.nbytes, stream=stream)
+
+
+# ---------------------------------------------------------------------------
+# Router load: counts, the balance loss, and the gradients of a router
+# ---------------------------------------------------------------------------
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def moe_expert_counts(topk_idx, C, E, k, counts, tokens=None, seq_offsets=None, S=1, token_mask=None,
+                      accumulate=False, stream=None):
+    """counts [S][E] (and tokens [S]) int32 of a selection topk_idx [C][k]."""
+    import torch
+    call = _Call(topk_idx, "topk_idx")
+    call("moe_expert_counts", call.ptr(topk_idx, torch.int32, (C, k), "topk_idx"), C, k, E,
+         call.ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S,
+         call.ptr(token_mask, torch.uint8, (C,), "token_mask"),
+         call.ptr(counts, torch.int32, (S, E), "counts"),
+         call.ptr(tokens, torch.int32, (S,), "tokens"), int(accumulate), stream=stream)
+
+
+class BalanceWorkspace(_Scratch):
+    def __init__(self, C: int, E: int, S: int = 1, device="cuda", stream=None):
+        super().__init__("moe_balance_workspace_size", lib().moe_balance_workspace_size(C, E, S),
+                         device, True, stream)
+
+
+def moe_balance_fwd(logits, topk_idx, C, E, k, alpha, counts, tokens, probs, loss,
+                    ws: BalanceWorkspace, score="sigmoid", seq_offsets=None, S=1, token_mask=None,
+                    stream=None):
+    """The balance loss of a selection, with its counts [S][E], tokens [S] and
+    mean shares probs [S][E]."""
+    import torch
+    call = _Call(logits, "logits")
+    if ws.tensor.device != call.device:
+        raise ValueError(f"workspace must be on {call.device}")
+    call("moe_balance_fwd", call.ptr(logits, torch.float32, (C, E), "logits"),
+         call.ptr(topk_idx, torch.int32, (C, k), "topk_idx"), C, k, E,
+         call.ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S,
+         call.ptr(token_mask, torch.uint8, (C,), "token_mask"), _score(score), alpha,
+         call.ptr(counts, torch.int32, (S, E), "counts"),
+         call.ptr(tokens, torch.int32, (S,), "tokens"),
+         call.ptr(probs, torch.float32, (S, E), "probs"), call.ptr(loss, torch.float32, (1,), "loss"),
+         ws.tensor.data_ptr(), ws.nbytes, stream=stream)
+
+
+def moe_balance_bwd(logits, counts, tokens, C, E, k, alpha, grad_loss, dlogits, score="sigmoid",
+                    seq_offsets=None, S=1, token_mask=None, accumulate=False, stream=None):
+    """dlogits [C][E] of the balance loss, from what moe_balance_fwd wrote and
+    grad_loss [1]."""
+    import torch
+    call = _Call(logits, "logits")
+    call("moe_balance_bwd", call.ptr(logits, torch.float32, (C, E), "logits"),
+         call.ptr(counts, torch.int32, (S, E), "counts"),
+         call.ptr(tokens, torch.int32, (S,), "tokens"), C, k, E,
+         call.ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S,
+         call.ptr(token_mask, torch.uint8, (C,), "token_mask"), _score(score), alpha,
+         call.ptr(grad_loss, torch.float32, (1,), "grad_loss"),
+         call.ptr(dlogits, torch.float32, (C, E), "dlogits"), int(accumulate), stream=stream)
+
+
+def moe_route_bwd(logits, topk_idx, topk_dw, C, E, k, dlogits, token_mask=None, accumulate=False,
+                  stream=None):
+    """dlogits [C][E] from topk_dw [C][k], the gradient of moe_route's weights."""
+    import torch
+    call = _Call(logits, "logits")
+    call("moe_route_bwd", call.ptr(logits, torch.float32, (C, E), "logits"),
+         call.ptr(topk_idx, torch.int32, (C, k), "topk_idx"),
+         call.ptr(topk_dw, torch.float32, (C, k), "topk_dw"), C, k, E,
+         call.ptr(token_mask, torch.uint8, (C,), "token_mask"),
+         call.ptr(dlogits, torch.float32, (C, E), "dlogits"), int(accumulate), stream=stream)

@@ -1,0 +1,569 @@
+// libroutedfp4, router load: per-expert counts of a selection, the balance
+// loss over it with its gradient, and the gradient of the renormalised
+// routing weights.
+//
+//   p_t    = a token's logits as shares over the experts (normalised sigmoid,
+//            or softmax)
+//   P[s]   = mean of p_t over the T_s tokens of sequence s
+//   f[s]   = E counts[s] / (k T_s)
+//   loss   = alpha / S * sum_s f[s] . P[s]
+//   dl_e   = p_e (g_e - p . g) (* sigmoid(-l_e)),  g = dloss alpha / (S T_s) f[s]
+//
+// Both passes over the logits are bound by reading them (the backward pass by
+// reading and writing C*E floats); a row of up to 1024 logits lies in one
+// wave's registers (16 a lane), so each pass reads it once.
+//
+// Kernels:
+//   k_bal_part    a slot of up to TB tokens of one sequence: the slot's sums
+//                 of shares, its counts and its number of tokens
+//   k_bal_final   per sequence and 64 experts: the slots added in order, the
+//                 loss from the last workgroup to arrive
+//   k_bal_bwd     one wave per token
+//   k_count_fill / k_count   counts without logits
+//   k_route_bwd   one wave per token
+#include "common.h"
+
+namespace rf4 {
+namespace {
+
+constexpr int kBalWG = 256;           // four waves
+constexpr int kBalWaves = kBalWG / 64;
+
+// Sequence bounds from the device offsets, clipped to the batch so that no
+// content of seq_off makes a kernel leave its tensors.
+__device__ __forceinline__ int seq_at(const int32_t* off, int i, int S, int C) {
+  const int v = off ? off[i] : (i < S ? 0 : C);
+  return v < 0 ? 0 : v > C ? C : v;
+}
+
+// The sequence that token t lies in (the last one that starts at or before
+// t, so empty ones are passed over), or -1.
+__device__ __forceinline__ int seq_of(const int32_t* off, int t, int S, int C) {
+  if (!off) return 0;
+  int lo = 0, hi = S;                 // largest i in [0, S] with off[i] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seq_at(off, mid, S, C) <= t) lo = mid; else hi = mid - 1;
+  }
+  return (lo < S && seq_at(off, lo, S, C) <= t) ? lo : -1;
+}
+
+// Tokens per slot: about 256 slots for a prefill chunk and 1024 for a large
+// batch, whose partial sums (one row of E per slot) stay a small share of the
+// logits read.  A power of two, so that a sequence's first slot is a shift.
+__host__ __device__ inline int slot_shift(int C) {
+  int s = 3;
+  while (s < 10 && (C >> s) > 1024) ++s;
+  return s;
+}
+// Slots of sequence s: from (off[s] >> shift) + s, one per TB tokens.  The
+// next sequence's first slot is at least that many further on, so slots need
+// no prefix sum over the sequences.
+__host__ __device__ inline int num_slots(int C, int S) { return (C >> slot_shift(C)) + S; }
+
+struct BalWs {
+  size_t ctrl, psum, pcnt, ptok, dots, total;
+};
+inline int expert_blocks(int E) { return (E + 63) / 64; }
+inline BalWs bal_ws(int C, int E, int S) {
+  BalWs W;
+  size_t o = 0;
+  const size_t n = (size_t)num_slots(C, S);
+  W.ctrl = o; o = align256(o + 64 * sizeof(uint32_t));
+  W.psum = o; o = align256(o + n * E * sizeof(float));
+  W.pcnt = o; o = align256(o + n * E * sizeof(uint16_t));
+  W.ptok = o; o = align256(o + n * sizeof(int32_t));
+  W.dots = o; o = align256(o + (size_t)S * expert_blocks(E) * sizeof(float));
+  W.total = o;
+  return W;
+}
+
+struct BalArgs {
+  const float* logits;
+  const int32_t* idx;
+  const int32_t* off;
+  const uint8_t* mask;
+  int C, k, E, S;
+  int32_t* counts;
+  int32_t* tokens;
+  float* probs;
+  float* loss;
+  float alpha;
+  // workspace
+  uint32_t* ticket;
+  float* psum;
+  uint16_t* pcnt;
+  int32_t* ptok;
+  float* dots;
+  // backward
+  const float* grad;
+  float* dlogits;
+  int accumulate;
+  bool vec;            // rows of logits (and dlogits) are 16-byte aligned
+};
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
+  return v;
+}
+
+// A row of E logits over a wave: lane l holds experts 4 (l + 64 j) + c in
+// v[4 j + c]; past E: fill.  vec: every row is 16-byte aligned (E % 4 == 0 and
+// an aligned base); a slice of logits may start anywhere.
+template <int NJ>
+__device__ __forceinline__ void load_row(const float* row, int E, bool vec, float fill, float (&v)[4 * NJ]) {
+  const int lane = threadIdx.x & 63;
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int e = 4 * (lane + 64 * j);
+      float4 q = make_float4(fill, fill, fill, fill);
+      if (e < E) q = *reinterpret_cast<const float4*>(row + e);
+      v[4 * j] = q.x; v[4 * j + 1] = q.y; v[4 * j + 2] = q.z; v[4 * j + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int e = 4 * (lane + 64 * j) + c;
+        v[4 * j + c] = e < E ? row[e] : fill;
+      }
+  }
+}
+
+// The shares of one row, in place of its logits, and for the sigmoid score
+// sigmoid(-l).  Sigmoid scores underflow where the whole row lies far below
+// zero; the shares are then formed from sigmoid(l) e^-m, m the largest logit,
+// which is e^(l - m) / (1 + e^l).  A row of -inf (m = -inf) has shares 0.
+template <int NJ, bool SIG>
+__device__ __forceinline__ void shares(float (&v)[4 * NJ], float (&neg)[4 * NJ]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < 4 * NJ; ++i) m = fmaxf(m, v[i]);
+  m = wave_max(m);
+  float z = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4 * NJ; ++i) {
+    const float l = v[i];
+    if (SIG) {
+      const float u = expf(-fabsf(l));
+      const float r = 1.0f / (1.0f + u);
+      neg[i] = l >= 0.0f ? u * r : r;
+      v[i] = l >= 0.0f ? r : u * r;
+      if (m < -60.0f) v[i] = m == -INFINITY ? l - l : expf(l - m) * r;
+      if (m == -INFINITY && l == -INFINITY) v[i] = 0.0f;
+      // l != l: NaN in every term above
+    } else {
+      v[i] = m == -INFINITY && l == -INFINITY ? 0.0f : expf(l - m);
+    }
+    z += v[i];
+  }
+  z = wave_sum(z);
+  const float iz = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+  for (int i = 0; i < 4 * NJ; ++i) v[i] *= iz;
+}
+
+template <int NJ, bool SIG>
+__global__ __launch_bounds__(kBalWG) void k_bal_part(BalArgs a) {
+  __shared__ float s_sum[MOE_MAX_EXPERTS];
+  __shared__ uint32_t s_cnt[MOE_MAX_EXPERTS];
+  __shared__ int s_tok;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int E = a.E, slot = blockIdx.x;
+  const int sh = slot_shift(a.C);
+  // the sequence whose slots this one is among: largest s with
+  // (off[s] >> sh) + s <= slot
+  int lo = 0, hi = a.S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((seq_at(a.off, mid, a.S, a.C) >> sh) + mid <= slot) lo = mid; else hi = mid - 1;
+  }
+  const int b = seq_at(a.off, lo, a.S, a.C), end = seq_at(a.off, lo + 1, a.S, a.C);
+  const int first = slot - ((b >> sh) + lo);
+  if (first < 0) return;
+  const int64_t t0 = b + ((int64_t)first << sh);
+  if (t0 >= end) return;
+  const int n = (int)(end - t0 < (1 << sh) ? end - t0 : (1 << sh));
+
+  for (int e = tid; e < E; e += kBalWG) { s_sum[e] = 0.0f; s_cnt[e] = 0u; }
+  if (tid == 0) s_tok = 0;
+  __syncthreads();
+  // counts (integers: any order gives the same)
+  for (int i = tid; i < n * a.k; i += kBalWG) {
+    const int t = i / a.k;
+    if (a.mask && !a.mask[t0 + t]) continue;
+    const int e = a.idx[t0 * a.k + i];
+    if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1u);
+  }
+  // sums of shares: each wave its tokens in order, then the waves in order
+  float acc[4 * NJ];
+#pragma unroll
+  for (int i = 0; i < 4 * NJ; ++i) acc[i] = 0.0f;
+  int live = 0;
+  for (int t = wave; t < n; t += kBalWaves) {
+    if (a.mask && !a.mask[t0 + t]) continue;
+    ++live;
+    float v[4 * NJ], neg[4 * NJ];
+    load_row<NJ>(a.logits + (t0 + t) * E, E, a.vec, -INFINITY, v);
+    shares<NJ, SIG>(v, neg);
+#pragma unroll
+    for (int i = 0; i < 4 * NJ; ++i) acc[i] += v[i];
+  }
+  if (lane == 0 && live) atomicAdd(&s_tok, live);
+  for (int w = 0; w < kBalWaves; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) {
+        const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
+        if (e < E) s_sum[e] += acc[i];
+      }
+    }
+    __syncthreads();
+  }
+  for (int e = tid; e < E; e += kBalWG) {
+    a.psum[(size_t)slot * E + e] = s_sum[e];
+    a.pcnt[(size_t)slot * E + e] = (uint16_t)s_cnt[e];   // at most 1024 tokens * 32 slots
+  }
+  if (tid == 0) a.ptok[slot] = s_tok;
+}
+
+// Experts 64 x .. 64 x + 63 of sequence y: 16 threads per expert add every
+// 16th slot, then their sums in order.
+constexpr int kFinWG = 1024;
+__global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
+  __shared__ float s_p[kFinWG];
+  __shared__ int s_c[kFinWG];
+  __shared__ int s_t[kFinWG];
+  __shared__ int s_flag;
+  const int tid = threadIdx.x, le = tid & 63, row = tid >> 6;
+  const int s = blockIdx.y, e = blockIdx.x * 64 + le, E = a.E;
+  const int sh = slot_shift(a.C), total = num_slots(a.C, a.S);
+  const int b = seq_at(a.off, s, a.S, a.C), end = seq_at(a.off, s + 1, a.S, a.C);
+  const int len = end > b ? end - b : 0;
+  const int j0 = (b >> sh) + s;
+  int n = (len + (1 << sh) - 1) >> sh;
+  if (n > total - j0) n = total - j0;
+  float p = 0.0f;
+  int c = 0, t = 0;
+  for (int j = row; j < n; j += kFinWG / 64) {
+    if (e < E) {
+      p += a.psum[(size_t)(j0 + j) * E + e];
+      c += a.pcnt[(size_t)(j0 + j) * E + e];
+    }
+    t += a.ptok[j0 + j];
+  }
+  s_p[tid] = p; s_c[tid] = c; s_t[tid] = t;
+  __syncthreads();
+  if (row == 0) {
+    for (int r = 1; r < kFinWG / 64; ++r) {
+      p += s_p[64 * r + le];
+      c += s_c[64 * r + le];
+      t += s_t[64 * r + le];
+    }
+    const float it = t > 0 ? 1.0f / (float)t : 0.0f;
+    const float P = p * it;
+    const float f = (float)c * it * ((float)E / (float)a.k);
+    if (e < E) {
+      a.probs[(size_t)s * E + e] = P;
+      a.counts[(size_t)s * E + e] = c;
+    }
+    const float d = wave_sum(e < E ? f * P : 0.0f);
+    if (le == 0) {
+      if (blockIdx.x == 0) a.tokens[s] = t;
+      store_coherent(a.dots + (size_t)s * gridDim.x + blockIdx.x, d);
+    }
+  }
+  const uint32_t nb = gridDim.x * gridDim.y;
+  if (!last_to_arrive(a.ticket, nb, &s_flag)) return;
+  if (tid == 0) reset_ticket(a.ticket);
+  const __amdgpu_buffer_rsrc_t v = coherent_view(a.dots, nb * 4u);
+  float d = 0.0f;
+  for (uint32_t i = tid; i < nb; i += kFinWG) d += coherent_ld(v, 4u * i);
+  s_p[tid] = d;
+  __syncthreads();
+  for (int w = kFinWG / 2; w >= 1; w >>= 1) {
+    if (tid < w) s_p[tid] += s_p[tid + w];
+    __syncthreads();
+  }
+  if (tid == 0) a.loss[0] = a.alpha / (float)a.S * s_p[0];
+}
+
+template <int NJ, bool SIG>
+__global__ __launch_bounds__(kBalWG) void k_bal_bwd(BalArgs a) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int E = a.E;
+  const int64_t t = (int64_t)blockIdx.x * kBalWaves + wave;
+  if (t >= a.C) return;
+  const int s = seq_of(a.off, (int)t, a.S, a.C);
+  if (s < 0 || t >= seq_at(a.off, s + 1, a.S, a.C)) return;
+  float* out = a.dlogits + t * E;
+  float d[4 * NJ];
+  if (a.mask && !a.mask[t]) {
+    if (a.accumulate) return;
+#pragma unroll
+    for (int i = 0; i < 4 * NJ; ++i) d[i] = 0.0f;
+  } else {
+    float v[4 * NJ], neg[4 * NJ], g[4 * NJ];
+    load_row<NJ>(a.logits + t * E, E, a.vec, -INFINITY, v);
+    shares<NJ, SIG>(v, neg);
+    const int n = a.tokens[s];
+    const float it = n > 0 ? 1.0f / (float)n : 0.0f;
+    const float w = a.grad[0] * (a.alpha / (float)a.S) * it * it * ((float)E / (float)a.k);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4 * NJ; ++i) {
+      const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
+      g[i] = e < E ? w * (float)a.counts[(size_t)s * E + e] : 0.0f;
+      dot += v[i] * g[i];
+    }
+    dot = wave_sum(dot);
+#pragma unroll
+    for (int i = 0; i < 4 * NJ; ++i) {
+      d[i] = v[i] * (g[i] - dot);
+      if (SIG) d[i] *= neg[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * NJ; ++i) {
+    const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
+    if (e < E) out[e] = a.accumulate ? out[e] + d[i] : d[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Counts without logits
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void k_count_fill(int32_t* counts, int32_t* tokens, int64_t n, int S) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) counts[i] = 0;
+  if (tokens && i < S) tokens[i] = 0;
+}
+
+// Workgroup (s, j): the j-th of gridDim.x parts of sequence s.  One part:
+// the row is written (or added to) as a whole; more: the parts' integer
+// counts are added to the row by atomics, whose order does not matter.
+__global__ __launch_bounds__(256) void k_count(const int32_t* idx, const int32_t* off, const uint8_t* mask,
+                                               int C, int k, int E, int S, int32_t* counts,
+                                               int32_t* tokens, int accumulate) {
+  __shared__ int32_t s_cnt[MOE_MAX_EXPERTS];
+  __shared__ int32_t s_tok;
+  const int tid = threadIdx.x, s = blockIdx.y, parts = gridDim.x;
+  for (int e = tid; e < E; e += 256) s_cnt[e] = 0;
+  if (tid == 0) s_tok = 0;
+  __syncthreads();
+  const int b = seq_at(off, s, S, C), end = seq_at(off, s + 1, S, C);
+  const int len = end > b ? end - b : 0;
+  const int per = (len + parts - 1) / parts;
+  const int t0 = b + (int)((int64_t)per * blockIdx.x < len ? per * blockIdx.x : len);
+  const int t1 = t0 + per < end ? t0 + per : end;
+  for (int64_t i = (int64_t)t0 * k + tid; i < (int64_t)t1 * k; i += 256) {
+    if (mask && !mask[i / k]) continue;
+    const int e = idx[i];
+    if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+  }
+  if (tokens) {
+    int live = 0;
+    for (int t = t0 + tid; t < t1; t += 256) live += mask ? mask[t] != 0 : 1;
+    if (live) atomicAdd(&s_tok, live);
+  }
+  __syncthreads();
+  int32_t* row = counts + (size_t)s * E;
+  for (int e = tid; e < E; e += 256) {
+    if (parts > 1) { if (s_cnt[e]) atomicAdd(&row[e], s_cnt[e]); }
+    else row[e] = accumulate ? row[e] + s_cnt[e] : s_cnt[e];
+  }
+  if (tokens && tid == 0) {
+    if (parts > 1) atomicAdd(&tokens[s], s_tok);
+    else tokens[s] = accumulate ? tokens[s] + s_tok : s_tok;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the routing weights
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kBalWG) void k_route_bwd(const float* logits, const int32_t* idx,
+                                                      const float* dw, int C, int k, int E,
+                                                      const uint8_t* mask, float* dlogits, int accumulate) {
+  __shared__ float s_row[kBalWaves][MOE_MAX_EXPERTS];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * kBalWaves + wave;
+  if (t >= C) return;                       // whole waves: no barrier below
+  const bool live = !mask || mask[t] != 0;
+  if (!live && accumulate) return;
+  float* srow = s_row[wave];
+  if (!accumulate) {
+    for (int e = lane; e < E; e += 64) srow[e] = 0.0f;
+    wave_lds_fence();
+  }
+  int e = -1;
+  float l = -INFINITY, d = 0.0f;
+  if (live && lane < k) {
+    e = idx[t * k + lane];
+    if (e < 0 || e >= E) e = -1;
+    if (e >= 0) {
+      l = logits[t * E + e];
+      d = dw[t * k + lane];
+    }
+  }
+  const float m = wave_max(l);
+  const float u = expf(-fabsf(l)), r = 1.0f / (1.0f + u);
+  const float neg = l >= 0.0f ? u * r : r;
+  float sg = l >= 0.0f ? r : u * r;
+  if (m < -60.0f) sg = m == -INFINITY ? 0.0f : expf(l - m) * r;   // every sigmoid underflows
+  if (e < 0) sg = 0.0f;
+  if (l != l) sg = l;
+  const float z = wave_sum(sg);
+  const float w = z == 0.0f ? 0.0f : sg / z;
+  const float dot = wave_sum(e >= 0 ? w * d : 0.0f);
+  const float dl = e >= 0 ? w * neg * (d - dot) : 0.0f;
+  // slots that name one expert: the first adds them up, in slot order
+  float mine = 0.0f;
+  bool firsts = e >= 0;
+  for (int s = 0; s < k; ++s) {
+    const int es = __builtin_amdgcn_readlane(e, s);
+    const float ds = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(dl), s));
+    if (es == e) {
+      if (s < lane) firsts = false;
+      mine += ds;
+    }
+  }
+  if (accumulate) {
+    if (firsts && lane < k) dlogits[t * E + e] += mine;
+    return;
+  }
+  if (firsts && lane < k) srow[e] = mine;
+  wave_lds_fence();
+  for (int i = lane; i < E; i += 64) dlogits[t * E + i] = srow[i];
+}
+
+bool batch_ok(int C, int k, int E) {
+  return C >= 1 && C <= MOE_MAX_BATCH_TOKENS && E >= 1 && E <= MOE_MAX_EXPERTS && k >= 1 &&
+         k <= MOE_MAX_TOPK && k <= E;
+}
+bool seq_ok(const int32_t* off, int S) { return S >= 1 && S <= MOE_MAX_SEQUENCES && (off || S == 1); }
+bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
+
+moe_status launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE; }
+
+#define RF4_BY_ROW(KERNEL, E, SIG, GRID, WG, ST, ...)                                              \
+  do {                                                                                             \
+    const int nj_ = ((E) + 255) / 256;                                                             \
+    if (SIG) {                                                                                     \
+      if (nj_ == 1) hipLaunchKernelGGL((KERNEL<1, true>), GRID, dim3(WG), 0, ST, __VA_ARGS__);     \
+      else if (nj_ == 2) hipLaunchKernelGGL((KERNEL<2, true>), GRID, dim3(WG), 0, ST, __VA_ARGS__);\
+      else if (nj_ == 3) hipLaunchKernelGGL((KERNEL<3, true>), GRID, dim3(WG), 0, ST, __VA_ARGS__);\
+      else hipLaunchKernelGGL((KERNEL<4, true>), GRID, dim3(WG), 0, ST, __VA_ARGS__);              \
+    } else {                                                                                       \
+      if (nj_ == 1) hipLaunchKernelGGL((KERNEL<1, false>), GRID, dim3(WG), 0, ST, __VA_ARGS__);    \
+      else if (nj_ == 2) hipLaunchKernelGGL((KERNEL<2, false>), GRID, dim3(WG), 0, ST, __VA_ARGS__);\
+      else if (nj_ == 3) hipLaunchKernelGGL((KERNEL<3, false>), GRID, dim3(WG), 0, ST, __VA_ARGS__);\
+      else hipLaunchKernelGGL((KERNEL<4, false>), GRID, dim3(WG), 0, ST, __VA_ARGS__);             \
+    }                                                                                              \
+  } while (0)
+
+}  // namespace
+}  // namespace rf4
+
+using namespace rf4;
+
+extern "C" {
+
+moe_status moe_expert_counts(const int32_t* topk_idx, int32_t C, int32_t k, int32_t E,
+                             const int32_t* seq_off, int32_t S, const uint8_t* token_mask,
+                             int32_t* counts, int32_t* tokens, int32_t accumulate, void* stream) {
+  if (!topk_idx || !counts) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(topk_idx) || !aligned4(counts) || !aligned4(tokens) || !aligned4(seq_off))
+    return MOE_ERR_INVALID_ARG;
+  if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
+  if (!seq_ok(seq_off, S)) return MOE_ERR_INVALID_ARG;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  // parts of about 4096 choices of an average sequence
+  int64_t parts = ((int64_t)C * k / S + 4095) / 4096;
+  if (parts < 1) parts = 1;
+  if (parts > 256) parts = 256;
+  if (parts > 1 && !accumulate) {
+    const int64_t n = (int64_t)S * E;
+    hipLaunchKernelGGL(k_count_fill, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, counts, tokens, n, S);
+  }
+  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3(256), 0, st, topk_idx, seq_off, token_mask,
+                     C, k, E, S, counts, tokens, accumulate);
+  return launched();
+}
+
+size_t moe_balance_workspace_size(int32_t C, int32_t E, int32_t S) {
+  if (!batch_ok(C, 1, E) || S < 1 || S > MOE_MAX_SEQUENCES) return 0;
+  return bal_ws(C, E, S).total;
+}
+
+moe_status moe_balance_fwd(const float* logits, const int32_t* topk_idx, int32_t C, int32_t k,
+                           int32_t E, const int32_t* seq_off, int32_t S,
+                           const uint8_t* token_mask, int32_t score, float alpha,
+                           int32_t* counts, int32_t* tokens, float* probs, float* loss,
+                           void* ws, size_t ws_bytes, void* stream) {
+  if (!logits || !topk_idx || !counts || !tokens || !probs || !loss) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(topk_idx) || !aligned4(counts) || !aligned4(tokens) ||
+      !aligned4(probs) || !aligned4(loss) || !aligned4(seq_off))
+    return MOE_ERR_INVALID_ARG;
+  if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
+  if (!seq_ok(seq_off, S) || (score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SOFTMAX))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws) return MOE_ERR_WORKSPACE;
+  const BalWs W = bal_ws(C, E, S);
+  if (ws_bytes < W.total || (uintptr_t)ws % 256) return MOE_ERR_WORKSPACE;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  BalArgs a = {};
+  a.logits = logits; a.idx = topk_idx; a.off = seq_off; a.mask = token_mask;
+  a.C = C; a.k = k; a.E = E; a.S = S;
+  a.vec = E % 4 == 0 && (uintptr_t)logits % 16 == 0;
+  a.counts = counts; a.tokens = tokens; a.probs = probs; a.loss = loss; a.alpha = alpha;
+  a.ticket = reinterpret_cast<uint32_t*>(w8 + W.ctrl);
+  a.psum = reinterpret_cast<float*>(w8 + W.psum);
+  a.pcnt = reinterpret_cast<uint16_t*>(w8 + W.pcnt);
+  a.ptok = reinterpret_cast<int32_t*>(w8 + W.ptok);
+  a.dots = reinterpret_cast<float*>(w8 + W.dots);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  RF4_BY_ROW(k_bal_part, E, score == MOE_SCORE_SIGMOID, dim3(num_slots(C, S)), kBalWG, st, a);
+  hipLaunchKernelGGL(k_bal_final, dim3(expert_blocks(E), S), dim3(kFinWG), 0, st, a);
+  return launched();
+}
+
+moe_status moe_balance_bwd(const float* logits, const int32_t* counts, const int32_t* tokens,
+                           int32_t C, int32_t k, int32_t E, const int32_t* seq_off, int32_t S,
+                           const uint8_t* token_mask, int32_t score, float alpha,
+                           const float* grad_loss, float* dlogits, int32_t accumulate,
+                           void* stream) {
+  if (!logits || !counts || !tokens || !grad_loss || !dlogits || logits == dlogits) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(dlogits) || !aligned4(counts) || !aligned4(tokens) ||
+      !aligned4(grad_loss) || !aligned4(seq_off))
+    return MOE_ERR_INVALID_ARG;
+  if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
+  if (!seq_ok(seq_off, S) || (score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SOFTMAX))
+    return MOE_ERR_INVALID_ARG;
+  BalArgs a = {};
+  a.logits = logits; a.off = seq_off; a.mask = token_mask;
+  a.C = C; a.k = k; a.E = E; a.S = S; a.alpha = alpha;
+  a.vec = E % 4 == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)dlogits % 16 == 0;
+  a.counts = const_cast<int32_t*>(counts); a.tokens = const_cast<int32_t*>(tokens);
+  a.grad = grad_loss; a.dlogits = dlogits; a.accumulate = accumulate;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  RF4_BY_ROW(k_bal_bwd, E, score == MOE_SCORE_SIGMOID, dim3((C + kBalWaves - 1) / kBalWaves), kBalWG, st, a);
+  return launched();
+}
+
+moe_status moe_route_bwd(const float* logits, const int32_t* topk_idx, const float* topk_dw,
+                         int32_t C, int32_t k, int32_t E, const uint8_t* token_mask,
+                         float* dlogits, int32_t accumulate, void* stream) {
+  if (!logits || !topk_idx || !topk_dw || !dlogits || logits == dlogits) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(topk_idx) || !aligned4(topk_dw) || !aligned4(dlogits))
+    return MOE_ERR_INVALID_ARG;
+  if (!batch_ok(C, k, E)) return MOE_ERR_UNSUPPORTED;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL(k_route_bwd, dim3((C + kBalWaves - 1) / kBalWaves), dim3(kBalWG), 0, st, logits,
+                     topk_idx, topk_dw, C, k, E, token_mask, dlogits, accumulate);
+  return launched();
+}
+
+}  // extern "C"
