@@ -1,9 +1,40 @@
 // libroutedfp4, dense matrices in 4-bit codes with group scales:
 //
 //   y[c][n] = sum_k x[c][k] W[n][k],   W[n][k] = s[n][g] (q[n][k] - z[n][g]),  g = k / G
+//           = sum_g s[n][g] * ( sum_{k in g} x[c][k] (q[n][k] - z[n][g]) )
 //
-// One wave per output row: its lanes take 16-byte units of the row's codes
-// (32 columns, inside one group), the tokens' products are summed in fp32.
+// The inner sums run on the fp16 matrix cores (16x16x32): q - z is an integer
+// of at most 8 bits, exact in fp16, and x enters as fp16 terms, so every
+// product is exact and only fp32 sums round; the group's scale multiplies its
+// fp32 sum.  fp16 x is taken as it is.  bf16 x (8 bits) is one fp16 term under
+// a power of two per token that puts the token's largest value below 2^15:
+// exact down to 2^-29 of that value, and off by at most 2^-39 of it below.
+// fp32 x is two such terms (22 bits).
+//
+// Codes become fp16 without conversions: a nibble OR-ed into the fp16 1024 is
+// 1024 + q, one in the next four bits of the fp16 64 is 64 + q, and one packed
+// subtraction each takes 1024 + z or 64 + z away exactly: 9 instructions for 8
+// codes.  That leaves x's columns in the order 0 4 1 5 2 6 3 7, in which its
+// terms are laid out too.
+//
+// Lane l of a wave holds, of a 16-row tile, row l % 16 and one 16-byte unit
+// (32 columns) of each 128-column chunk, unit l / 16.  Groups of 128 or more
+// columns (G % 128 == 0) then need no exchange: product j of a chunk takes
+// dword j of every unit.  For G 32 and 64 a 4x4 transpose over the lane
+// quarters (four permlane swaps) first gives product j the whole of unit j,
+// so that its sum lies inside one group.
+//
+// Kernels:
+//   k_qone     one token: bound by reading the codes; its terms are made in LDS
+//              by every workgroup, whose waves split the rows, the columns of
+//              a row tile, or both
+//   k_qfew     2 .. 16 tokens: workgroups take rows x column slices, make the
+//              slice's terms in LDS and stream its codes; k_qreduce adds the
+//              ranges of slices
+//   k_qterms   x to fp16 terms in the workspace, in the operand order
+//   k_qgemm    17 and more tokens: workgroup tiles of tokens x rows, x's terms
+//              through LDS (loaded there directly, two buffers), the codes
+//              from memory to registers; k_qreduce adds split column ranges
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 
@@ -12,76 +43,763 @@
 namespace rf4 {
 namespace {
 
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+
+constexpr int kQChunk = 128;          // columns per chunk: 64 bytes of a row's codes
+constexpr int kQWG = 512;             // threads of the stream and matrix kernels
+constexpr int kQWaves = kQWG / 64;
+constexpr int kQTermBytes = 4096;     // terms of 16 tokens x 128 columns
+constexpr int kQStageBytes = 49152;   // LDS for one token's terms
+
 struct QArgs {
   const uint8_t* codes;
   int64_t code_pitch;
-  const void* scales;
-  int64_t scale_pitch;
+  const uint8_t* scales;
+  int64_t scale_pitch;                // bytes
   const uint8_t* zeros;
   int64_t zero_pitch;
-  int N, K, G;
+  int zero_step;                      // 0 where one byte (8) serves every group
+  int scale_bf16;                     // 16-bit scales: bf16, else fp16
+  int N, K;
+  int units;                          // 16-byte units of a row
+  int nch;                            // chunks of a row
+  int ng;                             // groups of a row
+  int gshift;                         // G 32, 64: log2 G
+  uint32_t gmul;                      // G >= 128: group of chunk c = (c * gmul) >> 20
   const void* x;
   int64_t x_pitch;
+  int x_dt, x_vec;                    // x_vec: rows are 16-byte aligned
   int C;
   void* y;
   int64_t y_pitch;
   int accumulate;
+  float* inv;                         // [C]: takes the terms' power of two out again
+  uint8_t* terms;                     // [P][C / 16][nch][16 blocks][16 tokens][16 bytes]
+  float* part;                        // [splits][C][N]
+  int wk;                             // stream: waves of a workgroup that split the columns
+  int splits, per_split;              // matrix kernel: column ranges, chunks in each
+  int row_groups;
 };
 
-template <int DT>
-__device__ __forceinline__ float ld(const void* p, int64_t i) {
-  if (DT == MOE_DT_F32) return static_cast<const float*>(p)[i];
-  if (DT == MOE_DT_BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-template <int DT>
-__device__ __forceinline__ void st(void* p, int64_t i, float v) {
-  if (DT == MOE_DT_F32) static_cast<float*>(p)[i] = v;
-  else if (DT == MOE_DT_BF16) static_cast<__hip_bfloat16*>(p)[i] = __float2bfloat16(v);
-  else static_cast<__half*>(p)[i] = __float2half(v);
+__device__ const uint8_t kEight[16] = {8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8};
+
+// Token t of a 16-token tile is row 4 (t % 4) + t / 4 of the first operand, so
+// that up to 4 tokens need one result register (row 4 (l / 16) + r is register
+// r of lane l), up to 8 two.
+__device__ __forceinline__ int token_row(int t) { return 4 * (t & 3) + (t >> 2); }
+__device__ __forceinline__ int row_token(int r) { return (r >> 2) + 4 * (r & 3); }
+
+// ---------------------------------------------------------------------------
+// Codes
+// ---------------------------------------------------------------------------
+struct Unit {
+  uint4v q;         // 32 codes
+  uint32_t s, z;    // their group's scale (as stored) and zero point
+};
+
+// A wave's view of the codes, scales and zero points of the rows from n0 on:
+// buffer loads whose row and unit are a per-lane offset, and whose tile and
+// chunk are a scalar one.  Offsets past the last row's last unit read zeros.
+struct View {
+  __amdgpu_buffer_rsrc_t codes, scales, zeros;
+  uint32_t vc, vs, vz;      // per-lane offsets: row (and, for codes, unit)
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t qview(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
-constexpr int kQTok = 8;
+template <int SS>
+__device__ __forceinline__ View view_rows(const QArgs& a, int n0, int rows, int row, int quarter) {
+  View v;
+  int left = a.N - n0 < rows ? a.N - n0 : rows;
+  if (left < 1) { left = 1; n0 = a.N - 1; }
+  v.codes = qview(a.codes + (int64_t)n0 * a.code_pitch, (int64_t)(left - 1) * a.code_pitch + 16 * a.units);
+  v.scales = qview(a.scales + (int64_t)n0 * a.scale_pitch, (int64_t)(left - 1) * a.scale_pitch + SS * a.ng);
+  v.zeros = a.zeros ? qview(a.zeros + (int64_t)n0 * a.zero_pitch, (int64_t)(left - 1) * a.zero_pitch + a.ng)
+                    : qview(kEight, sizeof(kEight));
+  v.vc = (uint32_t)(row * a.code_pitch) + 16u * quarter;
+  v.vs = (uint32_t)(row * a.scale_pitch);
+  v.vz = (uint32_t)(row * a.zero_pitch);
+  return v;
+}
 
-template <int DT, int SDT>
-__global__ __launch_bounds__(256) void k_quant_row(QArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int n = blockIdx.x * 4 + wave;
-  const int c0 = blockIdx.y * kQTok;
-  if (n >= a.N) return;
-  const uint8_t* row = a.codes + (int64_t)n * a.code_pitch;
-  float acc[kQTok];
+// Tile i (16 rows each) of the view, chunk c.  Units past the last column read
+// what lies there (a code is finite, and x is zero); their scale is the last
+// group's, since what lies behind a row of scales may be no number.  `live`
+// false: nothing is read.  The loads are always issued, so that the count of
+// loads in flight is the same on every path and a wait for one step's codes
+// leaves the next step's in flight.
+constexpr uint32_t kOutside = 0x80000000u;
+template <bool TR, int SS>
+__device__ __forceinline__ void load_unit(const QArgs& a, const View& v, int i, int c, int quarter, bool live,
+                                          Unit& u) {
+  const uint32_t out = live ? 0u : kOutside;
+  u.q = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
+      v.codes, (int)(v.vc | out), 64 * c + 16 * i * (int)a.code_pitch, kCachePolicyNt));
+  uint32_t os = v.vs | out, oz = v.vz | out;
+  int g;
+  if (TR) {
+    const int gl = (4 * c + quarter) >> (a.gshift - 5);
+    g = 0;
+    os += SS * (gl < a.ng ? gl : a.ng - 1);
+    oz += a.zero_step * (gl < a.ng ? gl : a.ng - 1);
+  } else {
+    g = (int)(((uint32_t)c * a.gmul) >> 20);
+  }
+  const int ss = SS * g + 16 * i * (int)a.scale_pitch, sz = a.zero_step * g + 16 * i * (int)a.zero_pitch;
+  if (SS == 4) u.s = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)os, ss, 0);
+  else u.s = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)os, ss, 0);
+  u.z = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)oz, sz, 0);
+}
+
+template <int SS>
+__device__ __forceinline__ float scale_of(const QArgs& a, uint32_t s) {
+  if (SS == 4) return __uint_as_float(s);
+  // both readings and a mask: a branch would cost more
+  const uint32_t h = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)s));
+  const uint32_t b = a.scale_bf16 ? 0xFFFFFFFFu : 0u;
+  return __uint_as_float(((s << 16) & b) | (h & ~b));
+}
+
+__device__ __forceinline__ half2v as_half2(uint32_t v) { return __builtin_bit_cast(half2v, v); }
+
+// zero points as the fp16 pair (1024 + z, 64 + z)
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
+  const _Float16 h = (_Float16)(float)(64u + z);
+  return (0x6400u | z) | ((uint32_t)__builtin_bit_cast(uint16_t, h) << 16);
+}
+
+// The unpacking constants, one pair in scalar and one in vector registers: an
+// AND-OR takes at most one scalar and no literal, and the compiler, left to
+// itself, uses literals and two instructions.
+struct Magic {
+  uint32_t m0, m1, k1024, k64;
+};
+__device__ __forceinline__ Magic magic() {
+  Magic k;
+  asm("s_mov_b32 %0, 0x000f000f" : "=s"(k.m0));
+  asm("s_mov_b32 %0, 0x00f000f0" : "=s"(k.m1));
+  asm("v_mov_b32 %0, 0x64006400" : "=v"(k.k1024));
+  asm("v_mov_b32 %0, 0x54005400" : "=v"(k.k64));
+  return k;
+}
+
+// eight codes as q - z in the column order 0 4 1 5 2 6 3 7
+__device__ __forceinline__ half8 unpack8(const Magic& k, uint32_t d, uint32_t zp) {
+  const half2v z = as_half2(zp);
+  const half2v z0 = {z[0], z[0]}, z1 = {z[1], z[1]};
+  const uint32_t e = d >> 8;
+  const half2v t0 = as_half2((d & k.m0) | k.k1024) - z0;
+  const half2v t1 = as_half2((d & k.m1) | k.k64) - z1;
+  const half2v t2 = as_half2((e & k.m0) | k.k1024) - z0;
+  const half2v t3 = as_half2((e & k.m1) | k.k64) - z1;
+  return half8{t0[0], t0[1], t1[0], t1[1], t2[0], t2[1], t3[0], t3[1]};
+}
+
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0]; b = r[1];
+}
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0]; b = r[1];
+}
+// d[j] of lane quarter q <- d[q] of lane quarter j
+__device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
+  swap16(d[0], d[1]);
+  swap16(d[2], d[3]);
+  swap32(d[0], d[2]);
+  swap32(d[1], d[3]);
+}
+// v of quarter j, in every quarter, as o[j]
+__device__ __forceinline__ void spread4(uint32_t v, uint32_t (&o)[4]) {
+  o[0] = v; o[2] = v;
+  swap32(o[0], o[2]);
+  o[1] = o[0]; o[3] = o[2];
+  swap16(o[0], o[1]);
+  swap16(o[2], o[3]);
+}
+
+// A unit ready for its four products: dword j, scale and zero pair of product j.
+template <bool TR>
+struct Ready {
+  uint32_t d[4], z[4];
+  float s[4];
+};
+template <bool TR, int SS>
+__device__ __forceinline__ void ready(const QArgs& a, const Unit& u, Ready<TR>& r) {
 #pragma unroll
-  for (int t = 0; t < kQTok; ++t) acc[t] = 0.0f;
-  for (int k0 = 32 * lane; k0 < a.K; k0 += 32 * 64) {
-    const uint4 q = *reinterpret_cast<const uint4*>(row + k0 / 2);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    const int g = k0 / a.G;
-    const float s = ld<SDT>(a.scales, (int64_t)n * a.scale_pitch + g);
-    const float z = a.zeros ? (float)a.zeros[(int64_t)n * a.zero_pitch + g] : 8.0f;
-    float p[kQTok];
+  for (int j = 0; j < 4; ++j) r.d[j] = u.q[j];
+  const float s = scale_of<SS>(a, u.s);
+  const uint32_t z = zero_pair(u.z);
+  if (TR) {
+    transpose4(r.d);
+    uint32_t t[4];
+    spread4(__float_as_uint(s), t);
 #pragma unroll
-    for (int t = 0; t < kQTok; ++t) p[t] = 0.0f;
-    for (int i = 0; i < 32 && k0 + i < a.K; ++i) {
-      const float v = (float)((w[i >> 3] >> (4 * (i & 7))) & 15u) - z;
+    for (int j = 0; j < 4; ++j) r.s[j] = __uint_as_float(t[j]);
+    spread4(z, r.z);
+  } else {
 #pragma unroll
-      for (int t = 0; t < kQTok; ++t)
-        if (c0 + t < a.C) p[t] += v * ld<DT>(a.x, (int64_t)(c0 + t) * a.x_pitch + k0 + i);
+    for (int j = 0; j < 4; ++j) { r.s[j] = s; r.z[j] = z; }
+  }
+}
+
+__device__ __forceinline__ float4v mma(half8 x, half8 w, float4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w, c, 0, 0, 0);
+}
+
+// The block (of 8 columns, 16 in a chunk) that product j takes in quarter q.
+template <bool TR>
+__device__ __forceinline__ int block_of(int j, int q) { return TR ? 4 * j + q : 4 * q + j; }
+
+// ---------------------------------------------------------------------------
+// Activations as fp16 terms
+// ---------------------------------------------------------------------------
+// The power of two that takes a token's largest |x| (fp32 bits) below 2^15,
+// within fp32's normal range, and its inverse.  Infinity or NaN: 1.
+__device__ __forceinline__ void term_scale(uint32_t maxbits, float& m, float& inv) {
+  int e = 14 - ((int)(maxbits >> 23) - 127);
+  if (maxbits >= 0x7F800000u) e = 0;
+  e = e > 126 ? 126 : e;
+  m = __uint_as_float((uint32_t)(127 + e) << 23);
+  inv = __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// v (scaled) as hi + lo.  A token with an infinity or NaN is not scaled: its
+// finite values are held within fp16's range (its results are infinite or NaN
+// whatever they are), and the infinity itself has no second term.
+__device__ __forceinline__ void split_term(float v, bool finite, _Float16& hi, _Float16& lo) {
+  if (!finite && fabsf(v) < INFINITY) v = fminf(fmaxf(v, -65504.0f), 65504.0f);
+  hi = (_Float16)v;
+  lo = (_Float16)(v - (float)hi);
+  if (!finite && !(fabsf(v) < INFINITY)) lo = (_Float16)0.0f;
+}
+
+// Eight columns of a row of x as stored (0 past the last column), through a
+// buffer view of x whose loads outside it give zeros.  vec: every row starts
+// 16-byte aligned and has a multiple of 8 columns; else element by element.
+template <int DT>
+struct Raw { uint4v v[DT == MOE_DT_F32 ? 2 : 1]; };
+
+template <int DT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t x_view(const QArgs& a, int t, int rows) {
+  constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
+  return qview(static_cast<const uint8_t*>(a.x) + (int64_t)t * a.x_pitch * B, ((rows - 1) * a.x_pitch + a.K) * B);
+}
+template <int DT>
+__device__ __forceinline__ void load8(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
+                                      Raw<DT>& r) {
+  constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
+  if (a.x_vec) {
+    const uint32_t o = live && k < a.K ? row + (uint32_t)(k * B) : kOutside;
+#pragma unroll
+    for (int i = 0; i < B / 2; ++i)
+      r.v[i] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + 16 * i), 0, 0));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t o = live && k + i < a.K ? row + (uint32_t)((k + i) * B) : kOutside;
+      if (DT == MOE_DT_F32) {
+        r.v[i >> 2][i & 3] = __builtin_amdgcn_raw_buffer_load_b32(x, (int)o, 0, 0);
+      } else {
+        const uint32_t h = __builtin_amdgcn_raw_buffer_load_b16(x, (int)o, 0, 0);
+        r.v[0][i >> 1] = (i & 1) ? r.v[0][i >> 1] | (h << 16) : h;
+      }
     }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ float raw_f32(const Raw<DT>& r, int i) {
+  if (DT == MOE_DT_F32) return __uint_as_float(r.v[i >> 2][i & 3]);
+  const uint32_t w = r.v[0][i >> 1];
+  return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);        // bf16
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t raw_max(const Raw<DT>& r, uint32_t m) {
 #pragma unroll
-    for (int t = 0; t < kQTok; ++t) acc[t] += s * p[t];
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(raw_f32<DT>(r, i)) & 0x7FFFFFFFu;
+    m = b > m ? b : m;
+  }
+  return m;
+}
+
+// The block's terms in the operand order.
+template <int DT>
+__device__ __forceinline__ void make_terms(const Raw<DT>& r, float m, bool finite, half8& hi, half8& lo) {
+  constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = order[i];
+    if (DT == MOE_DT_F16) {
+      const uint32_t w = r.v[0][k >> 1];
+      hi[i] = __builtin_bit_cast(_Float16, (uint16_t)((k & 1) ? w >> 16 : w));
+    } else {
+      _Float16 h, l;
+      split_term(raw_f32<DT>(r, k) * m, finite, h, l);
+      hi[i] = h;
+      if (DT == MOE_DT_F32) lo[i] = l;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, m, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// Token blockIdx.x: its largest value, then its terms.
+constexpr int kTermWG = 256;
+template <int DT>
+__global__ __launch_bounds__(kTermWG) void k_qterms(QArgs a) {
+  __shared__ uint32_t s_max[kTermWG / 64];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const int nblk = a.nch * (kQChunk / 8);
+  const __amdgpu_buffer_rsrc_t x = x_view<DT>(a, t, 1);
+  float m = 1.0f, inv = 1.0f;
+  bool finite = true;
+  if (DT != MOE_DT_F16) {
+    uint32_t mx = 0;
+    for (int b = tid; b < nblk; b += kTermWG) {
+      Raw<DT> r;
+      load8<DT>(a, x, 0, 8 * b, true, r);
+      mx = raw_max<DT>(r, mx);
+    }
+    mx = wave_umax(mx);
+    if ((tid & 63) == 0) s_max[tid >> 6] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTermWG / 64; ++w) mx = s_max[w] > mx ? s_max[w] : mx;
+    term_scale(mx, m, inv);
+    finite = mx < 0x7F800000u;
+  }
+  if (tid == 0) a.inv[t] = inv;
+  const int ct = (a.C + 15) / 16;
+  const int64_t plane = (int64_t)ct * a.nch * kQTermBytes;
+  uint8_t* out = a.terms + (int64_t)(t >> 4) * a.nch * kQTermBytes + token_row(t & 15) * 16;
+  for (int b = tid; b < nblk; b += kTermWG) {
+    Raw<DT> r;
+    load8<DT>(a, x, 0, 8 * b, true, r);
+    half8 hi, lo;
+    make_terms<DT>(r, m, finite, hi, lo);
+    *reinterpret_cast<half8*>(out + (int64_t)b * 256) = hi;
+    if (DT == MOE_DT_F32) *reinterpret_cast<half8*>(out + plane + (int64_t)b * 256) = lo;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Results
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void put(const QArgs& a, int t, int n, float v) {
+  const int64_t i = (int64_t)t * a.y_pitch + n;
+  if (a.x_dt == MOE_DT_F32) {
+    float* y = static_cast<float*>(a.y) + i;
+    *y = a.accumulate ? *y + v : v;
+  } else if (a.x_dt == MOE_DT_BF16) {
+    __hip_bfloat16* y = static_cast<__hip_bfloat16*>(a.y) + i;
+    *y = __float2bfloat16(a.accumulate ? __bfloat162float(*y) + v : v);
+  } else {
+    __half* y = static_cast<__half*>(a.y) + i;
+    *y = __float2half(a.accumulate ? __half2float(*y) + v : v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One unit's four products
+// ---------------------------------------------------------------------------
+// acc[r] += the chunk's scaled sums; frag(p, j) gives x's term p of product j.
+template <int P, int NR, bool TR, int SS, class F>
+__device__ __forceinline__ void multiply(const QArgs& a, const Magic& mg, const Unit& u, F frag, float (&acc)[NR]) {
+  Ready<TR> w;
+  ready<TR, SS>(a, u, w);
+  float4v d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const half8 b = unpack8(mg, w.d[j], w.z[j]);
+    if (TR) d = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int p = 0; p < P; ++p) d = mma(frag(p, j), b, d);
+    if (TR || j == 3) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) acc[r] += w.s[j] * d[r];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One token
+// ---------------------------------------------------------------------------
+constexpr int kQAhead = 4;            // chunks a wave loads together, twice in flight
+
+// The workgroup makes the token's terms in LDS ([P][blocks] of 16 bytes) while
+// the first codes are on their way (x's loads are issued before theirs: loads
+// complete in order).  It takes kQWaves / wk tiles of 16 rows at a time; wave w
+// walks the chunks w % wk, w % wk + wk, ... of tile w / wk, kQAhead of them
+// multiplied while the kQAhead after them are loaded, on into the next tile.
+template <int DT, bool TR, int SS>
+__global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
+  constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
+  constexpr int NB = kQStageBytes / (16 * P) / kQWG;      // blocks per thread at most
+  extern __shared__ __align__(16) uint8_t s_x[];
+  __shared__ float s_red[2][kQWaves * 16];
+  __shared__ uint32_t s_max[kQWaves];
+  // the wave's number through readfirstlane: its tiles and chunks are scalars
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int row = lane & 15, quarter = lane >> 4;
+  const int wk = a.wk, tiles = kQWaves / wk, kw = wave % wk, tw = wave / wk;
+  const int nblk = a.nch * (kQChunk / 8);
+  const int ngroups = ((a.N + 15) / 16 + tiles - 1) / tiles;
+  const int spt = ((a.nch + wk - 1) / wk + kQAhead - 1) / kQAhead;      // steps per tile
+  const int nit = (ngroups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int64_t steps = (int64_t)nit * spt;
+
+  Raw<DT> raw[NB];
+  const __amdgpu_buffer_rsrc_t xv = x_view<DT>(a, 0, 1);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) load8<DT>(a, xv, 0, 8 * (tid + kQWG * i), true, raw[i]);
+  __builtin_amdgcn_sched_barrier(0);
+
+  // the codes of one step: step ld_i of the workgroup's ld_g-th tile group
+  int ld_g = blockIdx.x, ld_i = 0;
+  View v = view_rows<SS>(a, (ld_g * tiles + tw) * 16, 16, row, quarter);
+  auto load = [&](Unit (&u)[kQAhead]) {
+#pragma unroll
+    for (int i = 0; i < kQAhead; ++i) {
+      const int c = kw + wk * (ld_i * kQAhead + i);
+      load_unit<TR, SS>(a, v, 0, c, quarter, c < a.nch && ld_g < ngroups, u[i]);
+    }
+    if (++ld_i == spt) {
+      ld_i = 0;
+      ld_g += gridDim.x;
+      v = view_rows<SS>(a, (ld_g * tiles + tw) * 16, 16, row, quarter);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const Magic mg = magic();
+  Unit u0[kQAhead], u1[kQAhead];
+  load(u0);
+  load(u1);
+
+  float m = 1.0f, inv = 1.0f;
+  bool finite = true;
+  if (DT != MOE_DT_F16) {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) mx = raw_max<DT>(raw[i], mx);
+    mx = wave_umax(mx);
+    if (lane == 0) s_max[wave] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQWaves; ++w) mx = s_max[w] > mx ? s_max[w] : mx;
+    term_scale(mx, m, inv);
+    finite = mx < 0x7F800000u;
   }
 #pragma unroll
-  for (int t = 0; t < kQTok; ++t) {
-    float v = wave_sum(acc[t]);
-    if (lane == 0 && c0 + t < a.C) {
-      const int64_t i = (int64_t)(c0 + t) * a.y_pitch + n;
-      if (a.accumulate) v += ld<DT>(a.y, i);
-      st<DT>(a.y, i, v);
+  for (int i = 0; i < NB; ++i) {
+    const int b = tid + kQWG * i;
+    if (b >= nblk) continue;
+    half8 hi, lo;
+    make_terms<DT>(raw[i], m, finite, hi, lo);
+    *reinterpret_cast<half8*>(s_x + 16 * b) = hi;
+    if (P == 2) *reinterpret_cast<half8*>(s_x + 16 * (nblk + b)) = lo;
+  }
+  __syncthreads();
+
+  float acc[1] = {0.0f};
+  int cg = blockIdx.x, ci = 0, parity = 0;
+  auto compute = [&](const Unit (&u)[kQAhead]) {
+#pragma unroll
+    for (int i = 0; i < kQAhead; ++i) {
+      const int c = kw + wk * (ci * kQAhead + i);
+      if (c >= a.nch) continue;
+      multiply<P, 1, TR, SS>(a, mg, u[i], [&](int p, int j) {
+        return *reinterpret_cast<const half8*>(s_x + 16 * (p * nblk + c * (kQChunk / 8) + block_of<TR>(j, quarter)));
+      }, acc);
     }
+    if (++ci < spt) return;
+    // the tile is done: the waves that split its columns add up, in order
+    const int n0 = cg * tiles * 16;
+    float* red = s_red[parity];
+    parity ^= 1;
+    if (lane < 16) red[wave * 16 + lane] = acc[0];
+    if (wk > 1) __syncthreads();
+    const int tile = wk > 1 ? tid >> 4 : tw;
+    const int n = n0 + tile * 16 + (tid & 15);
+    if ((wk > 1 ? tid < tiles * 16 : lane < 16) && n < a.N) {
+      float s = 0.0f;
+      for (int w = 0; w < wk; ++w) s += red[(tile * wk + w) * 16 + (tid & 15)];
+      put(a, 0, n, s * inv);
+    }
+    acc[0] = 0.0f;
+    ci = 0;
+    cg += gridDim.x;
+  };
+  for (int64_t s = 0;; s += 2) {
+    compute(u0);
+    if (s + 1 >= steps) break;
+    load(u0);
+    compute(u1);
+    if (s + 2 >= steps) break;
+    load(u1);
   }
 }
 
+// ---------------------------------------------------------------------------
+// 2 .. 16 tokens
+// ---------------------------------------------------------------------------
+// Workgroup (rows, range): kQWaves * RT tiles of 16 rows, a range of column
+// slices of kQSlice chunks.  For each slice the workgroup makes the tokens'
+// terms in LDS, under a power of two per token and slice; its waves then walk
+// the slice's codes, each unit's next slice loaded as soon as it is used.
+constexpr int kQSlice = 8;
+constexpr int kQSliceCols = kQSlice * kQChunk;
+
+template <int DT, int TOK, bool TR, int SS>
+__global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
+  constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
+  constexpr int NR = TOK / 4;
+  constexpr int NB = TOK * kQSliceCols / 8 / kQWG;        // blocks of x per thread
+  constexpr int kBlocks = kQSliceCols / 8;
+  constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
+  extern __shared__ __align__(16) uint8_t s_x[];          // [P][blocks][TOK] of 16 bytes
+  __shared__ uint32_t s_max[kQWaves][TOK];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int row = lane & 15, quarter = lane >> 4;
+  const int n0 = (blockIdx.x * kQWaves + wave) * 16;
+  const int s0 = blockIdx.y * a.per_split;
+  const int nsl = (a.nch + kQSlice - 1) / kQSlice;
+  const int s1 = s0 + a.per_split < nsl ? s0 + a.per_split : nsl;
+  const int t = tid % TOK;                                // this thread's token
+  const __amdgpu_buffer_rsrc_t xv = x_view<DT>(a, 0, a.C);
+  const View v = view_rows<SS>(a, n0, 16, row, quarter);
+
+  Raw<DT> raw[NB];
+  auto load_x = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      load8<DT>(a, xv, (uint32_t)(t * (int)a.x_pitch * B), s * kQSliceCols + 8 * (tid / TOK + kQWG / TOK * i),
+                t < a.C && s < s1, raw[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const Magic mg = magic();
+  Unit u[kQSlice];
+  load_x(s0);
+#pragma unroll
+  for (int i = 0; i < kQSlice; ++i) {
+    const int c = s0 * kQSlice + i;
+    load_unit<TR, SS>(a, v, 0, c, quarter, c < a.nch, u[i]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  // the token of operand row `row`; rows beyond TOK tokens repeat one
+  const uint8_t* frag0 = s_x + 16 * (TOK == 4 ? row >> 2 : TOK == 8 ? (row >> 2) + 4 * (row & 1) : row_token(row));
+  float sum[NR];
+#pragma unroll
+  for (int r = 0; r < NR; ++r) sum[r] = 0.0f;
+  for (int s = s0; s < s1; ++s) {
+    float m = 1.0f, inv[NR];
+    bool finite = true;
+    uint32_t mx = 0;
+    if (DT != MOE_DT_F16) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) mx = raw_max<DT>(raw[i], mx);
+#pragma unroll
+      for (int w = TOK; w < 64; w <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)mx, w, 64);
+        mx = o > mx ? o : mx;
+      }
+      if (lane < TOK) s_max[wave][lane] = mx;
+    }
+    __syncthreads();                                      // and all are done with the last slice's terms
+    if (DT != MOE_DT_F16) {
+#pragma unroll
+      for (int w = 0; w < kQWaves; ++w) mx = s_max[w][t] > mx ? s_max[w][t] : mx;
+      float unused;
+      term_scale(mx, m, unused);
+      finite = mx < 0x7F800000u;
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      inv[r] = 1.0f;
+      if (DT != MOE_DT_F16) {
+        uint32_t q = 0;
+#pragma unroll
+        for (int w = 0; w < kQWaves; ++w) q = s_max[w][4 * r + quarter] > q ? s_max[w][4 * r + quarter] : q;
+        float unused;
+        term_scale(q, unused, inv[r]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      half8 hi, lo;
+      make_terms<DT>(raw[i], m, finite, hi, lo);
+      uint8_t* o = s_x + 16 * (size_t)(tid + kQWG * i);
+      *reinterpret_cast<half8*>(o) = hi;
+      if (P == 2) *reinterpret_cast<half8*>(o + 16 * kBlocks * TOK) = lo;
+    }
+    load_x(s + 1);
+    __syncthreads();
+    float acc[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) acc[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kQSlice; ++i) {
+      if (s * kQSlice + i < a.nch)
+        multiply<P, NR, TR, SS>(a, mg, u[i], [&](int p, int j) {
+          return *reinterpret_cast<const half8*>(
+              frag0 + 16 * TOK * (p * kBlocks + i * (kQChunk / 8) + block_of<TR>(j, quarter)));
+        }, acc);
+      const int c = (s + 1) * kQSlice + i;
+      load_unit<TR, SS>(a, v, 0, c, quarter, s + 1 < s1 && c < a.nch, u[i]);
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) sum[r] += inv[r] * acc[r];
+  }
+  const int n = n0 + row;
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    const int tok = 4 * r + quarter;
+    if (tok >= a.C || n >= a.N) continue;
+    if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.C + tok) * a.N + n] = sum[r];
+    else put(a, tok, n, sum[r]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Matrix kernel: 17 and more tokens
+// ---------------------------------------------------------------------------
+// TM token tiles of 16 per workgroup, WT waves along the tokens and the rest
+// along the rows, RT row tiles of 16 per wave.  A chunk's terms lie in LDS as
+// they lie in the workspace (loads go there directly, 1 KB a wave), the next
+// chunk's are loaded during the current one.
+template <int P, int TM, int WT, int RT, bool TR, int SS>
+__global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
+  constexpr int WR = kQWaves / WT, TW = TM / WT;
+  constexpr int kBuf = P * TM * kQTermBytes;
+  extern __shared__ __align__(16) uint8_t s_x[];      // two buffers
+  // the wave's number through readfirstlane: its tiles and chunks are scalars
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int row = lane & 15, quarter = lane >> 4;
+  const int wt = wave / WR, wr = wave % WR;
+  const int rg = blockIdx.x % a.row_groups, tg = blockIdx.x / a.row_groups;
+  const int ct = (a.C + 15) / 16;
+  const int c0 = blockIdx.y * a.per_split;
+  const int c1 = c0 + a.per_split < a.nch ? c0 + a.per_split : a.nch;
+  const int n0 = (rg * WR + wr) * RT * 16;
+
+  const View v = view_rows<SS>(a, n0, 16 * RT, row, quarter);
+  auto load = [&](int c, Unit (&u)[RT]) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) load_unit<TR, SS>(a, v, i, c, quarter, true, u[i]);
+  };
+  // piece i of a buffer (1 KB): term i / (4 TM), token tile (i / 4) % TM
+  auto stage = [&](int c, int buf) {
+#pragma unroll
+    for (int i0 = 0; i0 < P * TM * 4; i0 += kQWaves) {
+      const int i = i0 + wave;
+      const int p = i / (4 * TM);
+      int t = tg * TM + (i >> 2) % TM;
+      t = t < ct ? t : ct - 1;
+      const uint8_t* src = a.terms + (((int64_t)p * ct + t) * a.nch + c) * kQTermBytes + (i & 3) * 1024 + lane * 16;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                       (__attribute__((address_space(3))) void*)(s_x + buf * kBuf + i * 1024),
+                                       16, 0, 0);
+    }
+  };
+
+  float acc[TW][RT][4];
+#pragma unroll
+  for (int t = 0; t < TW; ++t)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[t][i][r] = 0.0f;
+
+  const Magic mg = magic();
+  Unit u[RT];
+  stage(c0, 0);
+  load(c0, u);
+  for (int c = c0; c < c1; ++c) {
+    const int buf = (c - c0) & 1;
+    Ready<TR> w[RT];
+    // the buffer's loads (and this chunk's codes) are complete in every wave,
+    // and every wave is done with the other buffer
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RT; ++i) ready<TR, SS>(a, u[i], w[i]);
+    if (c + 1 < c1) {
+      stage(c + 1, buf ^ 1);
+      load(c + 1, u);
+    }
+    const uint8_t* xs = s_x + buf * kBuf + wt * TW * kQTermBytes + row * 16;
+    float4v d[TW][RT];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      half8 b[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) b[i] = unpack8(mg, w[i].d[j], w[i].z[j]);
+#pragma unroll
+      for (int t = 0; t < TW; ++t) {
+        half8 x[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          x[p] = *reinterpret_cast<const half8*>(xs + (p * TM + t) * kQTermBytes + block_of<TR>(j, quarter) * 256);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          if (TR || j == 0) d[t][i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int p = 0; p < P; ++p) d[t][i] = mma(x[p], b[i], d[t][i]);
+          if (TR || j == 3) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[t][i][r] += w[i].s[j] * d[t][i][r];
+          }
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < TW; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int tok = (tg * TM + wt * TW + t) * 16 + 4 * r + quarter;
+      if (tok >= a.C) continue;
+      const float inv = a.inv[tok];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int n = n0 + 16 * i + row;
+        if (n >= a.N) continue;
+        if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.C + tok) * a.N + n] = acc[t][i][r] * inv;
+        else put(a, tok, n, acc[t][i][r] * inv);
+      }
+    }
+}
+
+__global__ __launch_bounds__(256) void k_qreduce(QArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t n = (int64_t)a.C * a.N;
+  if (i >= n) return;
+  float v = 0.0f;
+  for (int s = 0; s < a.splits; ++s) v += a.part[s * n + i];
+  put(a, (int)(i / a.N), (int)(i % a.N), v);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxPitch = 1 << 22, kMaxRow = 1 << 24;
 bool dtype_ok(int d) { return d == MOE_DT_F32 || d == MOE_DT_BF16 || d == MOE_DT_F16; }
 int64_t dtype_size(int d) { return d == MOE_DT_F32 ? 4 : 2; }
 
@@ -96,15 +814,131 @@ moe_status matrix_status(const moe_quant_matrix* m) {
     return MOE_ERR_INVALID_ARG;
   if (m->scale_pitch < ng || (uintptr_t)m->scales % dtype_size(m->scale_dtype)) return MOE_ERR_INVALID_ARG;
   if (m->zeros && m->zero_pitch < ng) return MOE_ERR_INVALID_ARG;
+  // a wave's rows (64 at most) are addressed by 32-bit offsets, and so are 16 rows of x
+  if (m->code_pitch > kMaxPitch || m->scale_pitch > kMaxPitch || (m->zeros && m->zero_pitch > kMaxPitch))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
+// How a call runs: one rule on its sizes.
+enum { kOne, kFew, kMany };
+struct QPlan {
+  int P, nch, ct;                      // terms, chunks, token tiles
+  int path;
+  bool wide;                           // the larger matrix tile
+  int row_groups, tok_groups, splits, per_split;
+  size_t inv, terms, part, total;
+};
+
+QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
+  QPlan p = {};
+  p.P = dtype == MOE_DT_F32 ? 2 : 1;
+  p.nch = (m->cols + kQChunk - 1) / kQChunk;
+  p.ct = (C + 15) / 16;
+  p.splits = 1;
+  p.tok_groups = 1;
+  p.per_split = p.nch;
+  p.path = C == 1 && (int64_t)p.nch * kQChunk * 2 * p.P <= kQStageBytes ? kOne
+           : C <= MOE_MAX_DECODE_TOKENS ? kFew : kMany;
+  if (p.path == kFew) {
+    p.row_groups = (m->rows + 16 * kQWaves - 1) / (16 * kQWaves);
+    const int nsl = (p.nch + kQSlice - 1) / kQSlice;
+    int s = 512 / p.row_groups;
+    s = s < 1 ? 1 : s > nsl ? nsl : s;
+    p.per_split = (nsl + s - 1) / s;
+    p.splits = (nsl + p.per_split - 1) / p.per_split;
+  } else if (p.path == kMany) {
+    p.wide = C > 64 && (int64_t)((C + 127) / 128) * ((m->rows + 255) / 256) >= 128;
+    p.tok_groups = p.wide ? (C + 127) / 128 : (C + 63) / 64;
+    p.row_groups = p.wide ? (m->rows + 255) / 256 : (m->rows + 127) / 128;
+    const int64_t wgs = (int64_t)p.tok_groups * p.row_groups;
+    if (!p.wide && wgs < 256) {
+      int s = (int)(512 / wgs);
+      if (s > p.nch / 4) s = p.nch / 4;
+      if (s > 1) {
+        p.per_split = (p.nch + s - 1) / s;
+        p.splits = (p.nch + p.per_split - 1) / p.per_split;
+      }
+    }
+  }
+  size_t o = 256;
+  p.inv = o; o = align256(o + (p.path == kMany ? (size_t)C * sizeof(float) : 0));
+  p.terms = o; o = align256(o + (p.path == kMany ? (size_t)p.P * p.ct * p.nch * kQTermBytes : 0));
+  p.part = o; o = align256(o + (p.splits > 1 ? (size_t)p.splits * C * m->rows * sizeof(float) : 0));
+  p.total = o;
+  return p;
+}
+
 template <int DT>
-void launch_row(const QArgs& a, int sdt, hipStream_t st) {
-  const dim3 grid((a.N + 3) / 4, (a.C + kQTok - 1) / kQTok);
-  if (sdt == MOE_DT_F32) hipLaunchKernelGGL((k_quant_row<DT, MOE_DT_F32>), grid, dim3(256), 0, st, a);
-  else if (sdt == MOE_DT_BF16) hipLaunchKernelGGL((k_quant_row<DT, MOE_DT_BF16>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((k_quant_row<DT, MOE_DT_F16>), grid, dim3(256), 0, st, a);
+void launch_one(const QArgs& a, bool tr, int ss, int grid, size_t lds, hipStream_t st) {
+  if (tr) {
+    if (ss == 4) hipLaunchKernelGGL((k_qone<DT, true, 4>), dim3(grid), dim3(kQWG), lds, st, a);
+    else hipLaunchKernelGGL((k_qone<DT, true, 2>), dim3(grid), dim3(kQWG), lds, st, a);
+  } else {
+    if (ss == 4) hipLaunchKernelGGL((k_qone<DT, false, 4>), dim3(grid), dim3(kQWG), lds, st, a);
+    else hipLaunchKernelGGL((k_qone<DT, false, 2>), dim3(grid), dim3(kQWG), lds, st, a);
+  }
+}
+
+template <int DT, int TOK, bool TR, int SS>
+moe_status launch_few_t(const QArgs& a, dim3 grid, hipStream_t st) {
+  constexpr int lds = (DT == MOE_DT_F32 ? 2 : 1) * 2 * kQSliceCols * TOK;
+  auto k = k_qfew<DT, TOK, TR, SS>;
+  if (lds + 1024 > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                                hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
+    return MOE_ERR_DEVICE;
+  hipLaunchKernelGGL(k, grid, dim3(kQWG), lds, st, a);
+  return MOE_OK;
+}
+template <int DT, int TOK>
+moe_status launch_few(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st) {
+  if (tr) return ss == 4 ? launch_few_t<DT, TOK, true, 4>(a, grid, st) : launch_few_t<DT, TOK, true, 2>(a, grid, st);
+  return ss == 4 ? launch_few_t<DT, TOK, false, 4>(a, grid, st) : launch_few_t<DT, TOK, false, 2>(a, grid, st);
+}
+
+template <int P, int TM, int WT, int RT, bool TR, int SS>
+moe_status launch_gemm_t(const QArgs& a, dim3 grid, hipStream_t st) {
+  constexpr int lds = 2 * P * TM * kQTermBytes;
+  auto k = k_qgemm<P, TM, WT, RT, TR, SS>;
+  if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         lds) != hipSuccess)
+    return MOE_ERR_DEVICE;
+  hipLaunchKernelGGL(k, grid, dim3(kQWG), lds, st, a);
+  return MOE_OK;
+}
+
+template <int P, int TM, int WT, int RT>
+moe_status launch_gemm(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st) {
+  if (tr) return ss == 4 ? launch_gemm_t<P, TM, WT, RT, true, 4>(a, grid, st) : launch_gemm_t<P, TM, WT, RT, true, 2>(a, grid, st);
+  return ss == 4 ? launch_gemm_t<P, TM, WT, RT, false, 4>(a, grid, st) : launch_gemm_t<P, TM, WT, RT, false, 2>(a, grid, st);
+}
+
+template <int DT>
+moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st) {
+  constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
+  moe_status s = MOE_OK;
+  if (p.path == kOne) {
+    // waves that split the columns of a tile: as many as it takes to give
+    // every CU's eight waves work, then tiles walked by a resident grid
+    const int nt = (a.N + 15) / 16;
+    a.wk = 8;
+    while (a.wk > 1 && (int64_t)nt * (a.wk / 2) >= 2048) a.wk /= 2;
+    const int groups = (nt + kQWaves / a.wk - 1) / (kQWaves / a.wk);
+    launch_one<DT>(a, tr, ss, groups < 512 ? groups : 512, (size_t)p.nch * kQChunk * 2 * P, st);
+  } else if (p.path == kFew) {
+    const dim3 grid((unsigned)p.row_groups, (unsigned)p.splits);
+    s = a.C <= 4 ? launch_few<DT, 4>(a, tr, ss, grid, st) : a.C <= 8 ? launch_few<DT, 8>(a, tr, ss, grid, st)
+                                                                     : launch_few<DT, 16>(a, tr, ss, grid, st);
+  } else {
+    hipLaunchKernelGGL((k_qterms<DT>), dim3(a.C), dim3(kTermWG), 0, st, a);
+    a.row_groups = p.row_groups;
+    const dim3 grid((unsigned)(p.row_groups * p.tok_groups), (unsigned)p.splits);
+    s = p.wide ? launch_gemm<P, 8, 2, 4>(a, tr, ss, grid, st) : launch_gemm<P, 4, 1, 1>(a, tr, ss, grid, st);
+  }
+  if (s != MOE_OK) return s;
+  if (p.splits > 1)
+    hipLaunchKernelGGL(k_qreduce, dim3((unsigned)(((int64_t)a.C * a.N + 255) / 256)), dim3(256), 0, st, a);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
 
 }  // namespace
@@ -116,7 +950,7 @@ extern "C" {
 
 size_t moe_quant_workspace_size(const moe_quant_matrix* m, int32_t dtype, int32_t C) {
   if (matrix_status(m) != MOE_OK || !dtype_ok(dtype) || C < 1 || C > MOE_MAX_TOKENS) return 0;
-  return 256;
+  return quant_plan(m, dtype, C).total;
 }
 
 moe_status moe_quant_linear(const moe_quant_matrix* m, int32_t dtype, const void* x,
@@ -126,21 +960,40 @@ moe_status moe_quant_linear(const moe_quant_matrix* m, int32_t dtype, const void
   if (ms != MOE_OK) return ms;
   if (!x || !y || x == y) return MOE_ERR_INVALID_ARG;
   if (!dtype_ok(dtype) || C < 1 || C > MOE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
-  if (x_pitch < m->cols || y_pitch < m->rows || (uintptr_t)x % dtype_size(dtype) ||
-      (uintptr_t)y % dtype_size(dtype))
+  const int64_t xs = dtype_size(dtype), ss = dtype_size(m->scale_dtype);
+  if (x_pitch > kMaxRow || y_pitch > kMaxRow) return MOE_ERR_UNSUPPORTED;
+  if (x_pitch < m->cols || y_pitch < m->rows || (uintptr_t)x % xs || (uintptr_t)y % xs)
     return MOE_ERR_INVALID_ARG;
-  if (!ws || (uintptr_t)ws % 256 || ws_bytes < moe_quant_workspace_size(m, dtype, C)) return MOE_ERR_WORKSPACE;
+  const QPlan p = quant_plan(m, dtype, C);
+  if (!ws || (uintptr_t)ws % 256 || ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
   QArgs a = {};
   a.codes = static_cast<const uint8_t*>(m->codes); a.code_pitch = m->code_pitch;
-  a.scales = m->scales; a.scale_pitch = m->scale_pitch;
-  a.zeros = m->zeros; a.zero_pitch = m->zero_pitch;
-  a.N = m->rows; a.K = m->cols; a.G = m->group;
-  a.x = x; a.x_pitch = x_pitch; a.C = C; a.y = y; a.y_pitch = y_pitch; a.accumulate = accumulate;
+  a.scales = static_cast<const uint8_t*>(m->scales); a.scale_pitch = m->scale_pitch * ss;
+  a.scale_bf16 = m->scale_dtype == MOE_DT_BF16;
+  a.zeros = m->zeros;
+  a.zero_pitch = m->zeros ? m->zero_pitch : 0;
+  a.zero_step = m->zeros ? 1 : 0;
+  a.N = m->rows; a.K = m->cols;
+  a.units = (m->cols + 31) / 32; a.nch = p.nch;
+  a.ng = (int)(((int64_t)m->cols + m->group - 1) / m->group);
+  const bool tr = m->group < 128;
+  a.gshift = m->group == 32 ? 5 : 6;
+  // groups of whole chunks: c < 2^10 chunks over gc chunks a group; the
+  // product's error c / 2^20 stays under the 1 / gc to the next quotient
+  const int gc = tr ? 1 : m->group / kQChunk < p.nch ? m->group / kQChunk : p.nch;
+  a.gmul = (1u << 20) / (uint32_t)gc + 1u;
+  a.x = x; a.x_pitch = x_pitch; a.x_dt = dtype;
+  a.x_vec = m->cols % 8 == 0 && (uintptr_t)x % 16 == 0 && (C == 1 || x_pitch * xs % 16 == 0);
+  a.C = C; a.y = y; a.y_pitch = y_pitch; a.accumulate = accumulate;
+  a.inv = reinterpret_cast<float*>(w8 + p.inv);
+  a.terms = w8 + p.terms;
+  a.part = reinterpret_cast<float*>(w8 + p.part);
+  a.splits = p.splits; a.per_split = p.per_split;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == MOE_DT_F32) launch_row<MOE_DT_F32>(a, m->scale_dtype, st);
-  else if (dtype == MOE_DT_BF16) launch_row<MOE_DT_BF16>(a, m->scale_dtype, st);
-  else launch_row<MOE_DT_F16>(a, m->scale_dtype, st);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+  if (dtype == MOE_DT_F32) return launch_quant<MOE_DT_F32>(a, p, tr, (int)ss, st);
+  if (dtype == MOE_DT_BF16) return launch_quant<MOE_DT_BF16>(a, p, tr, (int)ss, st);
+  return launch_quant<MOE_DT_F16>(a, p, tr, (int)ss, st);
 }
 
 }  // extern "C"
