@@ -355,66 +355,71 @@ class _Scratch:
         if nbytes == 0:
             raise MoeError(fn, MOE_ERR_UNSUPPORTED)
         self.tensor = torch.empty((nbytes + 255) // 256 * 64, dtype=torch.int32, device=device)
-        self.nbytes = self.tensor.numel() * 4
+        self.nbytes, self.device = self.tensor.numel() * 4, self.tensor.get_device()
         if init:
             with torch.cuda.device(self.tensor.device):
                 moe_workspace_init(self.tensor, stream)
 
+    def on(self, dev):
+        """Its pointer, on GPU `dev` only."""
+        if self.device != dev:
+            raise ValueError(f"workspace must be on cuda:{dev}, got {self.tensor.device}")
+        return self.tensor.data_ptr()
 
-class _Call:
-    """Checks the tensors of one call and launches it on their device: they
-    must all lie on one GPU, and the stream (by default that GPU's current
-    one) must be of that GPU too."""
 
-    __slots__ = ("device",)
+def _bad(t, dev, dtype, shape, name):
+    """The first thing wrong with a tensor argument."""
+    if not t.is_cuda:
+        return ValueError(f"{name} must be a device tensor")
+    if t.get_device() != dev:
+        return ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dtype != dtype:
+        return ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        return ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return ValueError(f"{name} must have dense rows, got strides {t.stride()}")
 
-    def __init__(self, tensor, name):
-        if not tensor.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
-        self.device = tensor.device
 
-    def ptr(self, t, dtype, shape, name):
-        """Device pointer of a contiguous tensor of this type and shape (None -> NULL)."""
-        if t is None:
-            return None
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+def _dense(t, dev, dtype, shape, name):
+    """Device pointer of a contiguous tensor of this type and shape on GPU `dev`."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous() or dev < 0:
+        raise _bad(t, dev, dtype, shape, name)
+    return t.data_ptr()
 
-    def rows(self, t, dtype, shape, name):
-        """(pointer, pitch in elements) of a matrix whose rows are dense."""
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        pitch, step = t.stride()
-        if (step != 1 and shape[1] > 1) or (pitch < shape[1] and shape[0] > 1):
-            raise ValueError(f"{name} must have dense rows, got strides {(pitch, step)}")
-        return t.data_ptr(), pitch if shape[0] > 1 else shape[1]
 
-    def __call__(self, fn, *args, stream=None):
-        import torch
-        dev = self.device
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"the stream must be of {dev}, got {stream.device}")
-        f = getattr(lib(), fn)
-        if torch.cuda.current_device() == dev.index:
-            status = f(*args, stream.cuda_stream)
-        else:
-            with torch.cuda.device(dev):
-                status = f(*args, stream.cuda_stream)
-        if status != MOE_OK:
-            raise MoeError(fn, status)
+def _maybe(t, dev, dtype, shape, name):
+    """The same, or NULL for None."""
+    return None if t is None else _dense(t, dev, dtype, shape, name)
+
+
+def _rows(t, dev, dtype, shape, name):
+    """(pointer, pitch in elements) of a matrix whose rows are dense."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or dev < 0:
+        raise _bad(t, dev, dtype, shape, name)
+    pitch, step = t.stride()
+    if (step != 1 and shape[1] > 1) or (pitch < shape[1] and shape[0] > 1):
+        raise _bad(t, dev, dtype, shape, name)
+    return t.data_ptr(), pitch if shape[0] > 1 else shape[1]
+
+
+def _launch(fn, dev, stream, *args):
+    """Calls an entry point on GPU `dev` and its stream (None: the current
+    one), whichever GPU is current."""
+    import torch
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream must be of cuda:{dev}, got {stream.device}")
+    else:
+        handle = stream.cuda_stream
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() == dev:
+        status = f(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, handle)
+    if status != MOE_OK:
+        raise MoeError(fn, status)
 
 
 def _moe_dtype(dtype):
@@ -436,10 +441,10 @@ class QuantMatrix:
         import torch
         if codes.dim() != 2 or K < 1 or group < 1:
             raise ValueError(f"codes must be a matrix and K, group >= 1, got {tuple(codes.shape)}, {K}, {group}")
-        call = _Call(codes, "codes")
+        dev = codes.get_device()
         N, ng = codes.shape[0], -(-K // group)
         units = -(-K // 32)
-        _, pitch = call.rows(codes, torch.uint8, codes.shape, "codes")
+        _, pitch = _rows(codes, dev, torch.uint8, codes.shape, "codes")
         if N == 1:
             pitch = 16 * units                       # no second row to be a pitch away
         if codes.shape[1] < -(-K // 2):
@@ -455,8 +460,8 @@ class QuantMatrix:
                 continue
             if t.dim() != 2 or t.shape[0] != N or t.shape[1] < ng:
                 raise ValueError(f"{name} must have shape {(N, ng)}, got {tuple(t.shape)}")
-            self.tables += call.rows(t, dtype, t.shape, name)
-        self.N, self.K, self.group, self.device = N, K, group, codes.device
+            self.tables += _rows(t, dev, dtype, t.shape, name)
+        self.N, self.K, self.group, self.device = N, K, group, dev
         self.keep = (codes, scales, zeros)
         self.struct = moe_quant_matrix(N, K, group, _moe_dtype(scales.dtype), codes.data_ptr(), pitch,
                                        *self.tables)
@@ -466,19 +471,17 @@ class QuantMatrix:
 class QuantWorkspace(_Scratch):
     def __init__(self, matrix: QuantMatrix, C: int, dtype):
         n = lib().moe_quant_workspace_size(matrix.ref, _moe_dtype(dtype), C)
-        super().__init__("moe_quant_workspace_size", n, matrix.device, False)
+        super().__init__("moe_quant_workspace_size", n, f"cuda:{matrix.device}", False)
 
 
 def moe_quant_linear(matrix: QuantMatrix, x, C, y, ws: QuantWorkspace, accumulate=False, stream=None):
     """y [C][N] = x [C][K] W^T (or y += with accumulate); x and y of one type,
     rows dense, any pitch."""
-    call = _Call(x, "x")
-    if matrix.device != call.device or ws.tensor.device != call.device:
-        raise ValueError(f"matrix and workspace must be on {call.device}")
-    xp, xs = call.rows(x, x.dtype, (C, matrix.K), "x")
-    yp, ys = call.rows(y, x.dtype, (C, matrix.N), "y")
-    call("moe_quant_linear", matrix.ref, _moe_dtype(x.dtype), xp, xs, C, yp, ys, int(accumulate),
-         ws.tensor.data_ptr(), ws.nbytes, stream=stream)
+    dev, dtype = matrix.device, x.dtype
+    xp, xs = _rows(x, dev, dtype, (C, matrix.K), "x")
+    yp, ys = _rows(y, dev, dtype, (C, matrix.N), "y")
+    _launch("moe_quant_linear", dev, stream, matrix.ref, _moe_dtype(dtype), xp, xs, C, yp, ys, accumulate,
+            ws.on(dev), ws.nbytes)
 
 
 # ---------------------------------------------------------------------------
@@ -494,12 +497,12 @@ def moe_expert_counts(topk_idx, C, E, k, counts, tokens=None, seq_offsets=None, 
                       accumulate=False, stream=None):
     """counts [S][E] (and tokens [S]) int32 of a selection topk_idx [C][k]."""
     import torch
-    call = _Call(topk_idx, "topk_idx")
-    call("moe_expert_counts", call.ptr(topk_idx, torch.int32, (C, k), "topk_idx"), C, k, E,
-         call.ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S,
-         call.ptr(token_mask, torch.uint8, (C,), "token_mask"),
-         call.ptr(counts, torch.int32, (S, E), "counts"),
-         call.ptr(tokens, torch.int32, (S,), "tokens"), int(accumulate), stream=stream)
+    dev, i32 = topk_idx.get_device(), torch.int32
+    _launch("moe_expert_counts", dev, stream, _dense(topk_idx, dev, i32, (C, k), "topk_idx"), C, k, E,
+            _maybe(seq_offsets, dev, i32, (S + 1,), "seq_offsets"), S,
+            _maybe(token_mask, dev, torch.uint8, (C,), "token_mask"),
+            _dense(counts, dev, i32, (S, E), "counts"), _maybe(tokens, dev, i32, (S,), "tokens"),
+            accumulate)
 
 
 class BalanceWorkspace(_Scratch):
@@ -514,17 +517,14 @@ def moe_balance_fwd(logits, topk_idx, C, E, k, alpha, counts, tokens, probs, los
     """The balance loss of a selection, with its counts [S][E], tokens [S] and
     mean shares probs [S][E]."""
     import torch
-    call = _Call(logits, "logits")
-    if ws.tensor.device != call.device:
-        raise ValueError(f"workspace must be on {call.device}")
-    call("moe_balance_fwd", call.ptr(logits, torch.float32, (C, E), "logits"),
-         call.ptr(topk_idx, torch.int32, (C, k), "topk_idx"), C, k, E,
-         call.ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S,
-         call.ptr(token_mask, torch.uint8, (C,), "token_mask"), _score(score), alpha,
-         call.ptr(counts, torch.int32, (S, E), "counts"),
-         call.ptr(tokens, torch.int32, (S,), "tokens"),
-         call.ptr(probs, torch.float32, (S, E), "probs"), call.ptr(loss, torch.float32, (1,), "loss"),
-         ws.tensor.data_ptr(), ws.nbytes, stream=stream)
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
+    _launch("moe_balance_fwd", dev, stream, _dense(logits, dev, f32, (C, E), "logits"),
+            _dense(topk_idx, dev, i32, (C, k), "topk_idx"), C, k, E,
+            _maybe(seq_offsets, dev, i32, (S + 1,), "seq_offsets"), S,
+            _maybe(token_mask, dev, torch.uint8, (C,), "token_mask"), _score(score), alpha,
+            _dense(counts, dev, i32, (S, E), "counts"), _dense(tokens, dev, i32, (S,), "tokens"),
+            _dense(probs, dev, f32, (S, E), "probs"), _dense(loss, dev, f32, (1,), "loss"),
+            ws.on(dev), ws.nbytes)
 
 
 def moe_balance_bwd(logits, counts, tokens, C, E, k, alpha, grad_loss, dlogits, score="sigmoid",
@@ -532,23 +532,22 @@ def moe_balance_bwd(logits, counts, tokens, C, E, k, alpha, grad_loss, dlogits, 
     """dlogits [C][E] of the balance loss, from what moe_balance_fwd wrote and
     grad_loss [1]."""
     import torch
-    call = _Call(logits, "logits")
-    call("moe_balance_bwd", call.ptr(logits, torch.float32, (C, E), "logits"),
-         call.ptr(counts, torch.int32, (S, E), "counts"),
-         call.ptr(tokens, torch.int32, (S,), "tokens"), C, k, E,
-         call.ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S,
-         call.ptr(token_mask, torch.uint8, (C,), "token_mask"), _score(score), alpha,
-         call.ptr(grad_loss, torch.float32, (1,), "grad_loss"),
-         call.ptr(dlogits, torch.float32, (C, E), "dlogits"), int(accumulate), stream=stream)
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
+    _launch("moe_balance_bwd", dev, stream, _dense(logits, dev, f32, (C, E), "logits"),
+            _dense(counts, dev, i32, (S, E), "counts"), _dense(tokens, dev, i32, (S,), "tokens"), C, k, E,
+            _maybe(seq_offsets, dev, i32, (S + 1,), "seq_offsets"), S,
+            _maybe(token_mask, dev, torch.uint8, (C,), "token_mask"), _score(score), alpha,
+            _dense(grad_loss, dev, f32, (1,), "grad_loss"), _dense(dlogits, dev, f32, (C, E), "dlogits"),
+            accumulate)
 
 
 def moe_route_bwd(logits, topk_idx, topk_dw, C, E, k, dlogits, token_mask=None, accumulate=False,
                   stream=None):
     """dlogits [C][E] from topk_dw [C][k], the gradient of moe_route's weights."""
     import torch
-    call = _Call(logits, "logits")
-    call("moe_route_bwd", call.ptr(logits, torch.float32, (C, E), "logits"),
-         call.ptr(topk_idx, torch.int32, (C, k), "topk_idx"),
-         call.ptr(topk_dw, torch.float32, (C, k), "topk_dw"), C, k, E,
-         call.ptr(token_mask, torch.uint8, (C,), "token_mask"),
-         call.ptr(dlogits, torch.float32, (C, E), "dlogits"), int(accumulate), stream=stream)
+    dev, f32 = logits.get_device(), torch.float32
+    _launch("moe_route_bwd", dev, stream, _dense(logits, dev, f32, (C, E), "logits"),
+            _dense(topk_idx, dev, torch.int32, (C, k), "topk_idx"),
+            _dense(topk_dw, dev, f32, (C, k), "topk_dw"), C, k, E,
+            _maybe(token_mask, dev, torch.uint8, (C,), "token_mask"),
+            _dense(dlogits, dev, f32, (C, E), "dlogits"), accumulate)

@@ -11,14 +11,17 @@
 //
 // Both passes over the logits are bound by reading them (the backward pass by
 // reading and writing C*E floats); a row of up to 1024 logits lies in one
-// wave's registers (16 a lane), so each pass reads it once.
+// wave's registers (16 a lane), so each pass reads it once.  A share costs one
+// exponential and one reciprocal (hardware, 1 unit each), so that arithmetic
+// stays below the memory time.
 //
 // Kernels:
 //   k_bal_part    a slot of up to TB tokens of one sequence: the slot's sums
-//                 of shares, its counts and its number of tokens
+//                 of shares, its counts and its number of tokens; a small
+//                 batch is one slot, whose workgroup goes on to the loss
 //   k_bal_final   per sequence and 64 experts: the slots added in order, the
 //                 loss from the last workgroup to arrive
-//   k_bal_bwd     one wave per token
+//   k_bal_bwd     a few consecutive tokens per wave
 //   k_count_fill / k_count   counts without logits
 //   k_route_bwd   one wave per token
 #include "common.h"
@@ -26,8 +29,11 @@
 namespace rf4 {
 namespace {
 
-constexpr int kBalWG = 256;           // four waves
+constexpr int kPartWG = 512;          // eight waves share a slot's tokens
+constexpr int kPartWaves = kPartWG / 64;
+constexpr int kBalWG = 256;           // backward kernels: four waves
 constexpr int kBalWaves = kBalWG / 64;
+constexpr int kOneSlot = 32;          // tokens up to which a single sequence is one slot
 
 // Sequence bounds from the device offsets, clipped to the batch so that no
 // content of seq_off makes a kernel leave its tensors.
@@ -48,10 +54,12 @@ __device__ __forceinline__ int seq_of(const int32_t* off, int t, int S, int C) {
   return (lo < S && seq_at(off, lo, S, C) <= t) ? lo : -1;
 }
 
-// Tokens per slot: about 256 slots for a prefill chunk and 1024 for a large
-// batch, whose partial sums (one row of E per slot) stay a small share of the
-// logits read.  A power of two, so that a sequence's first slot is a shift.
-__host__ __device__ inline int slot_shift(int C) {
+// Tokens per slot: 8 (one a wave) up to 8192 tokens, then as many as keep the
+// slots at about 1024, whose partial sums (one row of E per slot) stay a small
+// share of the logits read.  A power of two, so that a sequence's first slot
+// is a shift.
+__host__ __device__ inline int slot_shift(int C, int S) {
+  if (S == 1 && C <= kOneSlot) return 5;
   int s = 3;
   while (s < 10 && (C >> s) > 1024) ++s;
   return s;
@@ -59,7 +67,7 @@ __host__ __device__ inline int slot_shift(int C) {
 // Slots of sequence s: from (off[s] >> shift) + s, one per TB tokens.  The
 // next sequence's first slot is at least that many further on, so slots need
 // no prefix sum over the sequences.
-__host__ __device__ inline int num_slots(int C, int S) { return (C >> slot_shift(C)) + S; }
+__host__ __device__ inline int num_slots(int C, int S) { return (C >> slot_shift(C, S)) + S; }
 
 struct BalWs {
   size_t ctrl, psum, pcnt, ptok, dots, total;
@@ -99,13 +107,53 @@ struct BalArgs {
   const float* grad;
   float* dlogits;
   int accumulate;
+  int per;             // tokens per wave
+  int shift;           // slot_shift
+  bool one;            // one slot holds the batch
   bool vec;            // rows of logits (and dlogits) are 16-byte aligned
 };
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-  return v;
+// Reductions over the wave with DPP row shifts and row broadcasts (six adds;
+// through LDS permutes they took half of a row's time); every lane gets lane
+// 63's result.  Lanes a shift leaves without a source take the identity.
+template <int CTRL, int RMASK>
+__device__ __forceinline__ float dpp(float id, float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(id), __float_as_int(x), CTRL, RMASK, 0xF, false));
+}
+__device__ __forceinline__ float lane63(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp<0x111, 0xF>(0.0f, v);
+  v += dpp<0x112, 0xF>(0.0f, v);
+  v += dpp<0x114, 0xF>(0.0f, v);
+  v += dpp<0x118, 0xF>(0.0f, v);
+  v += dpp<0x142, 0xA>(0.0f, v);
+  v += dpp<0x143, 0xC>(0.0f, v);
+  return lane63(v);
+}
+__device__ __forceinline__ float row_max(float v) {
+  constexpr float lo = -INFINITY;
+  v = fmaxf(v, dpp<0x111, 0xF>(lo, v));
+  v = fmaxf(v, dpp<0x112, 0xF>(lo, v));
+  v = fmaxf(v, dpp<0x114, 0xF>(lo, v));
+  v = fmaxf(v, dpp<0x118, 0xF>(lo, v));
+  v = fmaxf(v, dpp<0x142, 0xA>(lo, v));
+  v = fmaxf(v, dpp<0x143, 0xC>(lo, v));
+  return lane63(v);
+}
+
+// e^x by the hardware's 2^y: y = x log2(e) is rounded, and what the rounding
+// (and log2(e) as an fp32 number) leaves out enters as a factor 1 + r ln 2.
+// x <= 0 or NaN here; -inf gives 0.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2e = 1.44269502162933349609f, kLog2eLo = 1.92596299112661746887e-8f;
+  constexpr float kLn2 = 0.69314718055994530942f;
+  x = x < -200.0f ? -200.0f : x;           // 0 already; keeps the remainder finite
+  const float y = x * kLog2e;
+  const float r = fmaf(x, kLog2eLo, fmaf(x, kLog2e, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fmaf(e, r * kLn2, e);
 }
 
 // A row of E logits over a wave: lane l holds experts 4 (l + 64 j) + c in
@@ -133,47 +181,71 @@ __device__ __forceinline__ void load_row(const float* row, int E, bool vec, floa
   }
 }
 
-// The shares of one row, in place of its logits, and for the sigmoid score
-// sigmoid(-l).  Sigmoid scores underflow where the whole row lies far below
-// zero; the shares are then formed from sigmoid(l) e^-m, m the largest logit,
-// which is e^(l - m) / (1 + e^l).  A row of -inf (m = -inf) has shares 0.
+// sigmoid(l) and sigmoid(-l)
+__device__ __forceinline__ void sigmoids(float l, float& s, float& neg) {
+  const float u = exp_neg(-fabsf(l));
+  const float r = __builtin_amdgcn_rcpf(1.0f + u);
+  const float ur = u * r;
+  s = l >= 0.0f ? r : ur;
+  neg = l >= 0.0f ? ur : r;
+}
+
+// A row's scores in place of its logits, and their sum; for the sigmoid score
+// also sigmoid(-l).  Where the whole row lies far below zero the sigmoids
+// underflow; the scores are then sigmoid(l) e^-m, m the largest logit, which is
+// e^(l - m) / (1 + e^l).  A row of -inf has scores 0.
 template <int NJ, bool SIG>
-__device__ __forceinline__ void shares(float (&v)[4 * NJ], float (&neg)[4 * NJ]) {
+__device__ __forceinline__ float scores(float (&v)[4 * NJ], float (&neg)[4 * NJ]) {
+  float z = 0.0f;
+  if (SIG) {
+    float l[4 * NJ];
+#pragma unroll
+    for (int i = 0; i < 4 * NJ; ++i) {
+      l[i] = v[i];
+      sigmoids(l[i], v[i], neg[i]);
+      z += v[i];
+    }
+    z = row_sum(z);
+    if (!(z < 1e-18f)) return z;            // NaN too
+#pragma unroll
+    for (int i = 0; i < 4 * NJ; ++i) v[i] = l[i];
+  }
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < 4 * NJ; ++i) m = fmaxf(m, v[i]);
-  m = wave_max(m);
-  float z = 0.0f;
+  m = row_max(m);
+  z = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4 * NJ; ++i) {
-    const float l = v[i];
-    if (SIG) {
-      const float u = expf(-fabsf(l));
-      const float r = 1.0f / (1.0f + u);
-      neg[i] = l >= 0.0f ? u * r : r;
-      v[i] = l >= 0.0f ? r : u * r;
-      if (m < -60.0f) v[i] = m == -INFINITY ? l - l : expf(l - m) * r;
-      if (m == -INFINITY && l == -INFINITY) v[i] = 0.0f;
-      // l != l: NaN in every term above
-    } else {
-      v[i] = m == -INFINITY && l == -INFINITY ? 0.0f : expf(l - m);
-    }
+    // -inf among finite logits: e^-inf; a row of it: no score at all
+    v[i] = v[i] == -INFINITY ? 0.0f : exp_neg(v[i] - m);
+    if (SIG) v[i] *= neg[i];                // 1 / (1 + e^l)
     z += v[i];
   }
-  z = wave_sum(z);
-  const float iz = z == 0.0f ? 0.0f : 1.0f / z;
+  return row_sum(z);
+}
+
+// The loss from the workgroups' sums of f . P, in order (a block of n threads).
+template <int WG>
+__device__ __forceinline__ float block_sum(float d, float* s_p) {
+  const int tid = threadIdx.x;
+  d = row_sum(d);
+  if ((tid & 63) == 0) s_p[tid >> 6] = d;
+  __syncthreads();
+  float v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4 * NJ; ++i) v[i] *= iz;
+  for (int w = 0; w < WG / 64; ++w) v += s_p[w];
+  return v;
 }
 
 template <int NJ, bool SIG>
-__global__ __launch_bounds__(kBalWG) void k_bal_part(BalArgs a) {
-  __shared__ float s_sum[MOE_MAX_EXPERTS];
-  __shared__ uint32_t s_cnt[MOE_MAX_EXPERTS];
+__global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
+  __shared__ float s_sum[kPartWaves][256 * NJ];
+  __shared__ uint32_t s_cnt[256 * NJ];
+  __shared__ float s_p[kPartWaves];
   __shared__ int s_tok;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int E = a.E, slot = blockIdx.x;
-  const int sh = slot_shift(a.C);
+  const int E = a.E, slot = blockIdx.x, sh = a.shift;
   // the sequence whose slots this one is among: largest s with
   // (off[s] >> sh) + s <= slot
   int lo = 0, hi = a.S - 1;
@@ -183,56 +255,72 @@ __global__ __launch_bounds__(kBalWG) void k_bal_part(BalArgs a) {
   }
   const int b = seq_at(a.off, lo, a.S, a.C), end = seq_at(a.off, lo + 1, a.S, a.C);
   const int first = slot - ((b >> sh) + lo);
-  if (first < 0) return;
   const int64_t t0 = b + ((int64_t)first << sh);
-  if (t0 >= end) return;
-  const int n = (int)(end - t0 < (1 << sh) ? end - t0 : (1 << sh));
+  if (first < 0 || t0 >= end) return;
+  const int n = end - t0 < (1 << sh) ? (int)(end - t0) : (1 << sh);
 
-  for (int e = tid; e < E; e += kBalWG) { s_sum[e] = 0.0f; s_cnt[e] = 0u; }
+  for (int e = tid; e < 256 * NJ; e += kPartWG) s_cnt[e] = 0u;
   if (tid == 0) s_tok = 0;
-  __syncthreads();
-  // counts (integers: any order gives the same)
-  for (int i = tid; i < n * a.k; i += kBalWG) {
-    const int t = i / a.k;
-    if (a.mask && !a.mask[t0 + t]) continue;
-    const int e = a.idx[t0 * a.k + i];
-    if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1u);
-  }
   // sums of shares: each wave its tokens in order, then the waves in order
   float acc[4 * NJ];
 #pragma unroll
   for (int i = 0; i < 4 * NJ; ++i) acc[i] = 0.0f;
   int live = 0;
-  for (int t = wave; t < n; t += kBalWaves) {
+  for (int t = wave; t < n; t += kPartWaves) {
     if (a.mask && !a.mask[t0 + t]) continue;
     ++live;
     float v[4 * NJ], neg[4 * NJ];
     load_row<NJ>(a.logits + (t0 + t) * E, E, a.vec, -INFINITY, v);
-    shares<NJ, SIG>(v, neg);
+    const float z = scores<NJ, SIG>(v, neg);
+    const float iz = z == 0.0f ? 0.0f : 1.0f / z;
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) acc[i] += v[i];
+    for (int i = 0; i < 4 * NJ; ++i) acc[i] = fmaf(v[i], iz, acc[i]);
   }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    *reinterpret_cast<float4*>(&s_sum[wave][4 * (lane + 64 * j)]) =
+        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+  __syncthreads();
   if (lane == 0 && live) atomicAdd(&s_tok, live);
-  for (int w = 0; w < kBalWaves; ++w) {
-    if (wave == w) {
+  // counts (integers: any order gives the same)
+  for (int i = tid; i < n * a.k; i += kPartWG) {
+    if (a.mask && !a.mask[t0 + i / a.k]) continue;
+    const int e = a.idx[t0 * a.k + i];
+    if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1u);
+  }
+  __syncthreads();
+  const int tok = s_tok;
+  const float it = tok > 0 ? 1.0f / (float)tok : 0.0f;
+  float d = 0.0f;
+  for (int e = tid; e < E; e += kPartWG) {
+    float p = s_sum[0][e];
 #pragma unroll
-      for (int i = 0; i < 4 * NJ; ++i) {
-        const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
-        if (e < E) s_sum[e] += acc[i];
-      }
+    for (int w = 1; w < kPartWaves; ++w) p += s_sum[w][e];
+    const int c = (int)s_cnt[e];
+    if (a.one) {
+      const float P = p * it;
+      a.probs[e] = P;
+      a.counts[e] = c;
+      d += (float)c * it * ((float)E / (float)a.k) * P;
+    } else {
+      a.psum[(size_t)slot * E + e] = p;
+      a.pcnt[(size_t)slot * E + e] = (uint16_t)c;         // at most 1024 tokens * 32 slots
     }
-    __syncthreads();
   }
-  for (int e = tid; e < E; e += kBalWG) {
-    a.psum[(size_t)slot * E + e] = s_sum[e];
-    a.pcnt[(size_t)slot * E + e] = (uint16_t)s_cnt[e];   // at most 1024 tokens * 32 slots
+  if (!a.one) {
+    if (tid == 0) a.ptok[slot] = tok;
+    return;
   }
-  if (tid == 0) a.ptok[slot] = s_tok;
+  d = block_sum<kPartWG>(d, s_p);
+  if (tid == 0) {
+    a.tokens[0] = tok;
+    a.loss[0] = a.alpha * d;
+  }
 }
 
 // Experts 64 x .. 64 x + 63 of sequence y: 16 threads per expert add every
-// 16th slot, then their sums in order.
-constexpr int kFinWG = 1024;
+// 16th slot, four loads in flight, then their sums in order.
+constexpr int kFinWG = 1024, kFinRows = kFinWG / 64;
 __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
   __shared__ float s_p[kFinWG];
   __shared__ int s_c[kFinWG];
@@ -240,25 +328,40 @@ __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
   __shared__ int s_flag;
   const int tid = threadIdx.x, le = tid & 63, row = tid >> 6;
   const int s = blockIdx.y, e = blockIdx.x * 64 + le, E = a.E;
-  const int sh = slot_shift(a.C), total = num_slots(a.C, a.S);
+  const int sh = a.shift, total = num_slots(a.C, a.S);
   const int b = seq_at(a.off, s, a.S, a.C), end = seq_at(a.off, s + 1, a.S, a.C);
   const int len = end > b ? end - b : 0;
   const int j0 = (b >> sh) + s;
   int n = (len + (1 << sh) - 1) >> sh;
   if (n > total - j0) n = total - j0;
+  const int ec = e < E ? e : E - 1;
+  const float* ps = a.psum + (size_t)j0 * E + ec;
+  const uint16_t* pc = a.pcnt + (size_t)j0 * E + ec;
   float p = 0.0f;
   int c = 0, t = 0;
-  for (int j = row; j < n; j += kFinWG / 64) {
-    if (e < E) {
-      p += a.psum[(size_t)(j0 + j) * E + e];
-      c += a.pcnt[(size_t)(j0 + j) * E + e];
+  int j = row;
+  for (; j + 3 * kFinRows < n; j += 4 * kFinRows) {
+    float q[4];
+    int k[4], u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const size_t at = (size_t)(j + i * kFinRows);
+      q[i] = ps[at * E];
+      k[i] = pc[at * E];
+      u[i] = a.ptok[j0 + at];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { p += q[i]; c += k[i]; t += u[i]; }
+  }
+  for (; j < n; j += kFinRows) {
+    p += ps[(size_t)j * E];
+    c += pc[(size_t)j * E];
     t += a.ptok[j0 + j];
   }
   s_p[tid] = p; s_c[tid] = c; s_t[tid] = t;
   __syncthreads();
   if (row == 0) {
-    for (int r = 1; r < kFinWG / 64; ++r) {
+    for (int r = 1; r < kFinRows; ++r) {
       p += s_p[64 * r + le];
       c += s_c[64 * r + le];
       t += s_t[64 * r + le];
@@ -270,7 +373,7 @@ __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
       a.probs[(size_t)s * E + e] = P;
       a.counts[(size_t)s * E + e] = c;
     }
-    const float d = wave_sum(e < E ? f * P : 0.0f);
+    const float d = row_sum(e < E ? f * P : 0.0f);
     if (le == 0) {
       if (blockIdx.x == 0) a.tokens[s] = t;
       store_coherent(a.dots + (size_t)s * gridDim.x + blockIdx.x, d);
@@ -282,54 +385,80 @@ __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
   const __amdgpu_buffer_rsrc_t v = coherent_view(a.dots, nb * 4u);
   float d = 0.0f;
   for (uint32_t i = tid; i < nb; i += kFinWG) d += coherent_ld(v, 4u * i);
-  s_p[tid] = d;
-  __syncthreads();
-  for (int w = kFinWG / 2; w >= 1; w >>= 1) {
-    if (tid < w) s_p[tid] += s_p[tid + w];
-    __syncthreads();
-  }
-  if (tid == 0) a.loss[0] = a.alpha / (float)a.S * s_p[0];
+  d = block_sum<kFinWG>(d, s_p);
+  if (tid == 0) a.loss[0] = a.alpha / (float)a.S * d;
 }
 
+// Each wave takes a.per consecutive tokens; g (the sequence's counts, scaled)
+// stays in registers from one token of a sequence to the next.
 template <int NJ, bool SIG>
 __global__ __launch_bounds__(kBalWG) void k_bal_bwd(BalArgs a) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int E = a.E;
-  const int64_t t = (int64_t)blockIdx.x * kBalWaves + wave;
-  if (t >= a.C) return;
-  const int s = seq_of(a.off, (int)t, a.S, a.C);
-  if (s < 0 || t >= seq_at(a.off, s + 1, a.S, a.C)) return;
-  float* out = a.dlogits + t * E;
-  float d[4 * NJ];
-  if (a.mask && !a.mask[t]) {
-    if (a.accumulate) return;
+  const int64_t base = ((int64_t)blockIdx.x * kBalWaves + wave) * a.per;
+  int end = -1;                              // of the sequence whose g is loaded
+  float g[4 * NJ];
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) d[i] = 0.0f;
-  } else {
-    float v[4 * NJ], neg[4 * NJ], g[4 * NJ];
-    load_row<NJ>(a.logits + t * E, E, a.vec, -INFINITY, v);
-    shares<NJ, SIG>(v, neg);
-    const int n = a.tokens[s];
-    const float it = n > 0 ? 1.0f / (float)n : 0.0f;
-    const float w = a.grad[0] * (a.alpha / (float)a.S) * it * it * ((float)E / (float)a.k);
-    float dot = 0.0f;
+  for (int i = 0; i < 4 * NJ; ++i) g[i] = 0.0f;
+  for (int64_t t = base; t < base + a.per && t < a.C; ++t) {
+    float v[4 * NJ], neg[4 * NJ];
+    const bool live = !a.mask || a.mask[t] != 0;
+    if (t >= end) {
+      const int s = seq_of(a.off, (int)t, a.S, a.C);
+      const int e1 = s < 0 ? -1 : seq_at(a.off, s + 1, a.S, a.C);
+      if (t >= e1) continue;                 // outside every sequence
+      end = e1;
+      const int n = a.tokens[s];
+      const float it = n > 0 ? 1.0f / (float)n : 0.0f;
+      const float w = a.grad[0] * (a.alpha / (float)a.S) * it * it * ((float)E / (float)a.k);
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) {
-      const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
-      g[i] = e < E ? w * (float)a.counts[(size_t)s * E + e] : 0.0f;
-      dot += v[i] * g[i];
+      for (int i = 0; i < 4 * NJ; ++i) {
+        const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
+        g[i] = e < E ? w * (float)a.counts[(size_t)s * E + e] : 0.0f;
+      }
     }
-    dot = wave_sum(dot);
+    if (!live) {
+      if (a.accumulate) continue;
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) {
-      d[i] = v[i] * (g[i] - dot);
-      if (SIG) d[i] *= neg[i];
+      for (int i = 0; i < 4 * NJ; ++i) v[i] = 0.0f;
+    } else {
+      load_row<NJ>(a.logits + t * E, E, a.vec, -INFINITY, v);
+      const float z = scores<NJ, SIG>(v, neg);
+      const float iz = z == 0.0f ? 0.0f : 1.0f / z;
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) {
+        v[i] *= iz;
+        dot = fmaf(v[i], g[i], dot);
+      }
+      dot = row_sum(dot);
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) {
+        v[i] *= g[i] - dot;
+        if (SIG) v[i] *= neg[i];
+      }
     }
-  }
+    float* out = a.dlogits + t * E;
+    if (a.vec) {
 #pragma unroll
-  for (int i = 0; i < 4 * NJ; ++i) {
-    const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
-    if (e < E) out[e] = a.accumulate ? out[e] + d[i] : d[i];
+      for (int j = 0; j < NJ; ++j) {
+        const int e = 4 * (lane + 64 * j);
+        if (e >= E) continue;
+        float4 d = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        float4* o = reinterpret_cast<float4*>(out + e);
+        if (a.accumulate) {
+          const float4 old = *o;
+          d.x += old.x; d.y += old.y; d.z += old.z; d.w += old.w;
+        }
+        *o = d;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) {
+        const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
+        if (e < E) out[e] = a.accumulate ? out[e] + v[i] : v[i];
+      }
+    }
   }
 }
 
@@ -345,33 +474,46 @@ __global__ __launch_bounds__(256) void k_count_fill(int32_t* counts, int32_t* to
 // Workgroup (s, j): the j-th of gridDim.x parts of sequence s.  One part:
 // the row is written (or added to) as a whole; more: the parts' integer
 // counts are added to the row by atomics, whose order does not matter.
-__global__ __launch_bounds__(256) void k_count(const int32_t* idx, const int32_t* off, const uint8_t* mask,
-                                               int C, int k, int E, int S, int32_t* counts,
-                                               int32_t* tokens, int accumulate) {
+// A part has at most 2^20 tokens: i / k of its i-th choice is the high word
+// of i * (2^32 / k + 1), whose error i / 2^32 stays under 1 / k.
+constexpr int kCntWG = 1024;
+__global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int32_t* off, const uint8_t* mask,
+                                                  int C, int k, uint32_t kmul, int E, int S, int32_t* counts,
+                                                  int32_t* tokens, int accumulate) {
   __shared__ int32_t s_cnt[MOE_MAX_EXPERTS];
   __shared__ int32_t s_tok;
   const int tid = threadIdx.x, s = blockIdx.y, parts = gridDim.x;
-  for (int e = tid; e < E; e += 256) s_cnt[e] = 0;
-  if (tid == 0) s_tok = 0;
-  __syncthreads();
   const int b = seq_at(off, s, S, C), end = seq_at(off, s + 1, S, C);
+  for (int e = tid; e < E; e += kCntWG) s_cnt[e] = 0;
+  if (tid == 0) s_tok = 0;
   const int len = end > b ? end - b : 0;
   const int per = (len + parts - 1) / parts;
-  const int t0 = b + (int)((int64_t)per * blockIdx.x < len ? per * blockIdx.x : len);
+  const int t0 = b + ((int64_t)per * blockIdx.x < len ? per * (int)blockIdx.x : len);
   const int t1 = t0 + per < end ? t0 + per : end;
-  for (int64_t i = (int64_t)t0 * k + tid; i < (int64_t)t1 * k; i += 256) {
-    if (mask && !mask[i / k]) continue;
-    const int e = idx[i];
-    if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+  const int n = (t1 - t0) * k;                 // at most 2^25
+  const int32_t* at = idx + (int64_t)t0 * k;
+  __syncthreads();
+  // four choices a thread in flight
+  for (int i0 = tid; i0 < n; i0 += 4 * kCntWG) {
+    int e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kCntWG;
+      e[j] = i < n ? at[i] : -1;
+      if (mask && i < n && !mask[t0 + (int)(k == 1 ? (uint32_t)i : __umulhi((uint32_t)i, kmul))]) e[j] = -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (e[j] >= 0 && e[j] < E) atomicAdd(&s_cnt[e[j]], 1);
   }
   if (tokens) {
     int live = 0;
-    for (int t = t0 + tid; t < t1; t += 256) live += mask ? mask[t] != 0 : 1;
+    for (int t = t0 + tid; t < t1; t += kCntWG) live += mask ? mask[t] != 0 : 1;
     if (live) atomicAdd(&s_tok, live);
   }
   __syncthreads();
   int32_t* row = counts + (size_t)s * E;
-  for (int e = tid; e < E; e += 256) {
+  for (int e = tid; e < E; e += kCntWG) {
     if (parts > 1) { if (s_cnt[e]) atomicAdd(&row[e], s_cnt[e]); }
     else row[e] = accumulate ? row[e] + s_cnt[e] : s_cnt[e];
   }
@@ -386,8 +528,9 @@ __global__ __launch_bounds__(256) void k_count(const int32_t* idx, const int32_t
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kBalWG) void k_route_bwd(const float* logits, const int32_t* idx,
                                                       const float* dw, int C, int k, int E,
-                                                      const uint8_t* mask, float* dlogits, int accumulate) {
-  __shared__ float s_row[kBalWaves][MOE_MAX_EXPERTS];
+                                                      const uint8_t* mask, float* dlogits, int accumulate,
+                                                      bool vec) {
+  __shared__ __align__(16) float s_row[kBalWaves][MOE_MAX_EXPERTS];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * kBalWaves + wave;
   if (t >= C) return;                       // whole waves: no barrier below
@@ -395,7 +538,7 @@ __global__ __launch_bounds__(kBalWG) void k_route_bwd(const float* logits, const
   if (!live && accumulate) return;
   float* srow = s_row[wave];
   if (!accumulate) {
-    for (int e = lane; e < E; e += 64) srow[e] = 0.0f;
+    for (int i = 4 * lane; i < E; i += 256) *reinterpret_cast<float4*>(srow + i) = make_float4(0, 0, 0, 0);
     wave_lds_fence();
   }
   int e = -1;
@@ -408,16 +551,14 @@ __global__ __launch_bounds__(kBalWG) void k_route_bwd(const float* logits, const
       d = dw[t * k + lane];
     }
   }
-  const float m = wave_max(l);
-  const float u = expf(-fabsf(l)), r = 1.0f / (1.0f + u);
-  const float neg = l >= 0.0f ? u * r : r;
-  float sg = l >= 0.0f ? r : u * r;
-  if (m < -60.0f) sg = m == -INFINITY ? 0.0f : expf(l - m) * r;   // every sigmoid underflows
+  float sg, neg;
+  sigmoids(l, sg, neg);
+  const float m = row_max(l);
+  if (m < -40.0f) sg = l == -INFINITY ? 0.0f : exp_neg(l - m) * neg;       // the sigmoids underflow
   if (e < 0) sg = 0.0f;
-  if (l != l) sg = l;
-  const float z = wave_sum(sg);
+  const float z = row_sum(sg);
   const float w = z == 0.0f ? 0.0f : sg / z;
-  const float dot = wave_sum(e >= 0 ? w * d : 0.0f);
+  const float dot = row_sum(e >= 0 ? w * d : 0.0f);
   const float dl = e >= 0 ? w * neg * (d - dot) : 0.0f;
   // slots that name one expert: the first adds them up, in slot order
   float mine = 0.0f;
@@ -436,7 +577,13 @@ __global__ __launch_bounds__(kBalWG) void k_route_bwd(const float* logits, const
   }
   if (firsts && lane < k) srow[e] = mine;
   wave_lds_fence();
-  for (int i = lane; i < E; i += 64) dlogits[t * E + i] = srow[i];
+  float* out = dlogits + t * E;
+  if (vec) {
+    for (int i = 4 * lane; i < E; i += 256)
+      *reinterpret_cast<float4*>(out + i) = *reinterpret_cast<const float4*>(srow + i);
+  } else {
+    for (int i = lane; i < E; i += 64) out[i] = srow[i];
+  }
 }
 
 bool batch_ok(int C, int k, int E) {
@@ -480,16 +627,17 @@ moe_status moe_expert_counts(const int32_t* topk_idx, int32_t C, int32_t k, int3
   if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
   if (!seq_ok(seq_off, S)) return MOE_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  // parts of about 4096 choices of an average sequence
-  int64_t parts = ((int64_t)C * k / S + 4095) / 4096;
-  if (parts < 1) parts = 1;
+  // one part per sequence (no zero fill, no atomics in memory) up to 32768
+  // choices of an average one; longer ones are shared out
+  int64_t parts = (int64_t)C * k / S <= 32768 ? 1 : ((int64_t)C * k / S + 8191) / 8192;
   if (parts > 256) parts = 256;
   if (parts > 1 && !accumulate) {
     const int64_t n = (int64_t)S * E;
     hipLaunchKernelGGL(k_count_fill, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, counts, tokens, n, S);
   }
-  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3(256), 0, st, topk_idx, seq_off, token_mask,
-                     C, k, E, S, counts, tokens, accumulate);
+  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3(kCntWG), 0, st, topk_idx, seq_off, token_mask,
+                     C, k, k == 1 ? 0u : (uint32_t)((1ull << 32) / (unsigned)k) + 1u, E, S, counts, tokens,
+                     accumulate);
   return launched();
 }
 
@@ -524,9 +672,11 @@ moe_status moe_balance_fwd(const float* logits, const int32_t* topk_idx, int32_t
   a.pcnt = reinterpret_cast<uint16_t*>(w8 + W.pcnt);
   a.ptok = reinterpret_cast<int32_t*>(w8 + W.ptok);
   a.dots = reinterpret_cast<float*>(w8 + W.dots);
+  a.shift = slot_shift(C, S);
+  a.one = S == 1 && C <= kOneSlot && !seq_off;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  RF4_BY_ROW(k_bal_part, E, score == MOE_SCORE_SIGMOID, dim3(num_slots(C, S)), kBalWG, st, a);
-  hipLaunchKernelGGL(k_bal_final, dim3(expert_blocks(E), S), dim3(kFinWG), 0, st, a);
+  RF4_BY_ROW(k_bal_part, E, score == MOE_SCORE_SIGMOID, dim3(a.one ? 1 : num_slots(C, S)), kPartWG, st, a);
+  if (!a.one) hipLaunchKernelGGL(k_bal_final, dim3(expert_blocks(E), S), dim3(kFinWG), 0, st, a);
   return launched();
 }
 
@@ -549,7 +699,10 @@ moe_status moe_balance_bwd(const float* logits, const int32_t* counts, const int
   a.counts = const_cast<int32_t*>(counts); a.tokens = const_cast<int32_t*>(tokens);
   a.grad = grad_loss; a.dlogits = dlogits; a.accumulate = accumulate;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  RF4_BY_ROW(k_bal_bwd, E, score == MOE_SCORE_SIGMOID, dim3((C + kBalWaves - 1) / kBalWaves), kBalWG, st, a);
+  // one token per wave until the chip is full of waves, then up to 8
+  a.per = C <= 8192 ? 1 : C >= 65536 ? 8 : C / 8192;
+  const int wg = kBalWaves * a.per;
+  RF4_BY_ROW(k_bal_bwd, E, score == MOE_SCORE_SIGMOID, dim3((C + wg - 1) / wg), kBalWG, st, a);
   return launched();
 }
 
@@ -562,7 +715,8 @@ moe_status moe_route_bwd(const float* logits, const int32_t* topk_idx, const flo
   if (!batch_ok(C, k, E)) return MOE_ERR_UNSUPPORTED;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipLaunchKernelGGL(k_route_bwd, dim3((C + kBalWaves - 1) / kBalWaves), dim3(kBalWG), 0, st, logits,
-                     topk_idx, topk_dw, C, k, E, token_mask, dlogits, accumulate);
+                     topk_idx, topk_dw, C, k, E, token_mask, dlogits, accumulate,
+                     E % 4 == 0 && (uintptr_t)dlogits % 16 == 0);
   return launched();
 }
 

@@ -113,6 +113,9 @@ CASES = [
     (1025, 64, 6, 13, False),
     (2048, 896, 16, 1, False),
     (3001, 448, 8, 2, True),
+    (17000, 36, 4, 9, True),
+    (32, 100, 7, 1, True),
+    (33, 100, 7, 1, True),
 ]
 
 
@@ -127,8 +130,9 @@ def test_balance_against_the_definition(case, score):
     r = ref.balance(logits, idx, alpha, score, seq, mask, S, grad)
     assert np.array_equal(t["counts"].cpu().numpy(), r["counts"])
     assert np.array_equal(t["tokens"].cpu().numpy(), r["tokens"])
-    # tokens per slot: 8 up to 8192 tokens
-    tp = tol_p(E, logits) + (2 + (C / 8 + S) / 16 + 24) * U
+    # tokens per slot: 8 up to 8192 tokens (32 in a single slot), then C / 1024 to the next power of two
+    slot = 8 if C <= 8192 else 2 * C / 1024
+    tp = tol_p(E, logits) + (max(4, slot / 8) + (C / slot + S) / 16 + 24) * U
     got = t["probs"].double().cpu().numpy()
     assert (np.abs(got - r["probs"]) <= tp * r["probs"] + 1e-44).all(), np.abs(got - r["probs"]).max()
     tl = tp + (8 + 6 + S * E / 64 / 1024 + 12) * U
