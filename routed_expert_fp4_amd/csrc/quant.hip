@@ -135,11 +135,9 @@ __device__ __forceinline__ View view_rows(const QArgs& a, int n0, int rows, int 
 // leaves the next step's in flight.
 constexpr uint32_t kOutside = 0x80000000u;
 template <bool TR, int SS>
-__device__ __forceinline__ void load_unit(const QArgs& a, const View& v, int i, int c, int quarter, bool live,
-                                          Unit& u) {
+__device__ __forceinline__ void load_scale(const QArgs& a, const View& v, int i, int c, int quarter, bool live,
+                                           uint32_t& s, uint32_t& z) {
   const uint32_t out = live ? 0u : kOutside;
-  u.q = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
-      v.codes, (int)(v.vc | out), 64 * c + 16 * i * (int)a.code_pitch, kCachePolicyNt));
   uint32_t os = v.vs | out, oz = v.vz | out;
   int g;
   if (TR) {
@@ -151,9 +149,16 @@ __device__ __forceinline__ void load_unit(const QArgs& a, const View& v, int i, 
     g = (int)(((uint32_t)c * a.gmul) >> 20);
   }
   const int ss = SS * g + 16 * i * (int)a.scale_pitch, sz = a.zero_step * g + 16 * i * (int)a.zero_pitch;
-  if (SS == 4) u.s = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)os, ss, 0);
-  else u.s = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)os, ss, 0);
-  u.z = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)oz, sz, 0);
+  if (SS == 4) s = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)os, ss, 0);
+  else s = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)os, ss, 0);
+  z = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)oz, sz, 0);
+}
+template <bool TR, int SS>
+__device__ __forceinline__ void load_unit(const QArgs& a, const View& v, int i, int c, int quarter, bool live,
+                                          Unit& u) {
+  u.q = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
+      v.codes, (int)(v.vc | (live ? 0u : kOutside)), 64 * c + 16 * i * (int)a.code_pitch, kCachePolicyNt));
+  load_scale<TR, SS>(a, v, i, c, quarter, live, u.s, u.z);
 }
 
 template <int SS>
@@ -680,40 +685,67 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
 // Matrix kernel: 17 and more tokens
 // ---------------------------------------------------------------------------
 // TM token tiles of 16 per workgroup, WT waves along the tokens and the rest
-// along the rows, RT row tiles of 16 per wave.  A chunk's terms lie in LDS as
-// they lie in the workspace (loads go there directly, 1 KB a wave), the next
-// chunk's are loaded during the current one.
+// along the rows, RT row tiles of 16 per wave.  A ring of three LDS buffers,
+// each a chunk's terms (as they lie in the workspace) and codes (64 bytes of
+// each row); loads go there directly, two chunks ahead of the products.
+template <int P, int TM, int WT, int RT>
+struct GemmTile {
+  static constexpr int WR = kQWaves / WT, TW = TM / WT, rows = WR * RT * 16;
+  static constexpr int terms = P * TM * kQTermBytes, codes = rows * 64, buffer = terms + codes;
+  static constexpr int ring = 3;
+  static constexpr int loads = buffer / 1024 / kQWaves;    // LDS loads per wave and chunk
+};
+
 template <int P, int TM, int WT, int RT, bool TR, int SS>
 __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
-  constexpr int WR = kQWaves / WT, TW = TM / WT;
-  constexpr int kBuf = P * TM * kQTermBytes;
-  extern __shared__ __align__(16) uint8_t s_x[];      // two buffers
-  // the wave's number through readfirstlane: its tiles and chunks are scalars
+  using G = GemmTile<P, TM, WT, RT>;
+  constexpr int WR = G::WR, TW = G::TW;
+  extern __shared__ __align__(16) uint8_t s_x[];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int row = lane & 15, quarter = lane >> 4;
   const int wt = wave / WR, wr = wave % WR;
-  const int rg = blockIdx.x % a.row_groups, tg = blockIdx.x / a.row_groups;
+  // workgroups b, b + 8, ... run on one XCD: a run of consecutive tiles (rows
+  // fastest) each, so that an XCD's L2 serves few token tiles and all rows
+  const int total = gridDim.x, xcd = blockIdx.x & 7, rem = total & 7;
+  const int tile = xcd * (total >> 3) + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+  const int tg = tile / a.row_groups, rg = tile - tg * a.row_groups;
   const int ct = (a.C + 15) / 16;
   const int c0 = blockIdx.y * a.per_split;
   const int c1 = c0 + a.per_split < a.nch ? c0 + a.per_split : a.nch;
-  const int n0 = (rg * WR + wr) * RT * 16;
-
+  const int nw = rg * G::rows;                             // the workgroup's rows
+  const int n0 = nw + wr * RT * 16;                        // the wave's
   const View v = view_rows<SS>(a, n0, 16 * RT, row, quarter);
-  auto load = [&](int c, Unit (&u)[RT]) {
+
+  struct Scales { uint32_t s[RT], z[RT]; };
+  auto load_scales = [&](int c, Scales& u) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) load_unit<TR, SS>(a, v, i, c, quarter, true, u[i]);
+    for (int i = 0; i < RT; ++i) load_scale<TR, SS>(a, v, i, c, quarter, true, u.s[i], u.z[i]);
   };
-  // piece i of a buffer (1 KB): term i / (4 TM), token tile (i / 4) % TM
+  // pieces of 1 KB: the terms' (term, token tile, quarter of it), then the
+  // codes' (16 rows each)
   auto stage = [&](int c, int buf) {
 #pragma unroll
-    for (int i0 = 0; i0 < P * TM * 4; i0 += kQWaves) {
+    for (int i0 = 0; i0 < G::terms / 1024; i0 += kQWaves) {
       const int i = i0 + wave;
       const int p = i / (4 * TM);
       int t = tg * TM + (i >> 2) % TM;
       t = t < ct ? t : ct - 1;
-      const uint8_t* src = a.terms + (((int64_t)p * ct + t) * a.nch + c) * kQTermBytes + (i & 3) * 1024 + lane * 16;
+      const uint8_t* src = a.terms + (((int64_t)p * ct + t) * a.nch + c) * kQTermBytes + (i & 3) * 1024;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + lane * 16),
+                                       (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + i * 1024),
+                                       16, 0, 0);
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < G::codes / 1024; i0 += kQWaves) {
+      const int i = i0 + wave;
+      int n = nw + 16 * i + (lane >> 2);
+      n = n < a.N ? n : a.N - 1;
+      int u = 4 * c + (lane & 3);
+      u = u < a.units ? u : a.units - 1;                   // x is zero past the last column
+      const uint8_t* src = a.codes + (int64_t)n * a.code_pitch + 16 * u;
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                       (__attribute__((address_space(3))) void*)(s_x + buf * kBuf + i * 1024),
+                                       (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + G::terms +
+                                                                                 i * 1024),
                                        16, 0, 0);
     }
   };
@@ -727,40 +759,60 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
       for (int r = 0; r < 4; ++r) acc[t][i][r] = 0.0f;
 
   const Magic mg = magic();
-  Unit u[RT];
-  stage(c0, 0);
-  load(c0, u);
-  for (int c = c0; c < c1; ++c) {
-    const int buf = (c - c0) & 1;
+  Scales u0, u1;
+  int buf = 0;
+  // One chunk: its loads are complete in every wave once each wave has waited
+  // for its own (loads complete in order, and the next chunk's LDS loads, the
+  // last ones issued, may stay in flight) and all have met; by then every wave
+  // is also done with the buffer before this one, which the loads of the chunk
+  // after next go into.  Past the last chunk that chunk is loaded again, so
+  // that the number of loads in flight is the same everywhere.
+  auto chunk = [&](int c, Scales& u) {
+    // (a plain barrier: __syncthreads would wait for every load in flight)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(G::loads) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
     Ready<TR> w[RT];
-    // the buffer's loads (and this chunk's codes) are complete in every wave,
-    // and every wave is done with the other buffer
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+    const uint8_t* base = s_x + buf * G::buffer;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) ready<TR, SS>(a, u[i], w[i]);
-    if (c + 1 < c1) {
-      stage(c + 1, buf ^ 1);
-      load(c + 1, u);
+    for (int i = 0; i < RT; ++i) {
+      Unit q;
+      q.q = *reinterpret_cast<const uint4v*>(base + G::terms + (wr * RT + i) * 1024 + row * 64 + quarter * 16);
+      q.s = u.s[i];
+      q.z = u.z[i];
+      ready<TR, SS>(a, q, w[i]);
     }
-    const uint8_t* xs = s_x + buf * kBuf + wt * TW * kQTermBytes + row * 16;
+    const int c2 = c + 2 < c1 ? c + 2 : c1 - 1;
+    load_scales(c2, u);
+    __builtin_amdgcn_sched_barrier(0);
+    stage(c2, buf == 0 ? 2 : buf - 1);
+    buf = buf == 2 ? 0 : buf + 1;
+    const uint8_t* xs = base + wt * TW * kQTermBytes + row * 16;
     float4v d[TW][RT];
+    half8 x[2][TW][P];
+    auto read = [&](int j) {
+#pragma unroll
+      for (int t = 0; t < TW; ++t)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          x[j & 1][t][p] =
+              *reinterpret_cast<const half8*>(xs + (p * TM + t) * kQTermBytes + block_of<TR>(j, quarter) * 256);
+    };
+    read(0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (j < 3) read(j + 1);
+      __builtin_amdgcn_sched_barrier(0);          // the next terms are read during these products
       half8 b[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) b[i] = unpack8(mg, w[i].d[j], w[i].z[j]);
 #pragma unroll
       for (int t = 0; t < TW; ++t) {
-        half8 x[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-          x[p] = *reinterpret_cast<const half8*>(xs + (p * TM + t) * kQTermBytes + block_of<TR>(j, quarter) * 256);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           if (TR || j == 0) d[t][i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int p = 0; p < P; ++p) d[t][i] = mma(x[p], b[i], d[t][i]);
+          for (int p = 0; p < P; ++p) d[t][i] = mma(x[j & 1][t][p], b[i], d[t][i]);
           if (TR || j == 3) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[t][i][r] += w[i].s[j] * d[t][i][r];
@@ -768,7 +820,22 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
         }
       }
     }
+  };
+  load_scales(c0, u0);
+  __builtin_amdgcn_sched_barrier(0);
+  stage(c0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  load_scales(c0 + 1 < c1 ? c0 + 1 : c0, u1);
+  __builtin_amdgcn_sched_barrier(0);
+  stage(c0 + 1 < c1 ? c0 + 1 : c0, 1);
+  for (int c = c0;; c += 2) {
+    chunk(c, u0);
+    if (c + 1 >= c1) break;
+    chunk(c + 1, u1);
+    if (c + 2 >= c1) break;
   }
+  // no load into LDS may be in flight when the workgroup gives its LDS up
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
 #pragma unroll
   for (int t = 0; t < TW; ++t)
@@ -848,8 +915,10 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
     p.per_split = (nsl + s - 1) / s;
     p.splits = (nsl + p.per_split - 1) / p.per_split;
   } else if (p.path == kMany) {
-    p.wide = C > 64 && (int64_t)((C + 127) / 128) * ((m->rows + 255) / 256) >= 128;
-    p.tok_groups = p.wide ? (C + 127) / 128 : (C + 63) / 64;
+    // the larger tile: 256 rows, and tokens whose terms fit the LDS ring
+    const int wide_tokens = p.P == 2 ? 64 : 128;
+    p.wide = C > 64 && (int64_t)((C + wide_tokens - 1) / wide_tokens) * ((m->rows + 255) / 256) >= 128;
+    p.tok_groups = p.wide ? (C + wide_tokens - 1) / wide_tokens : (C + 63) / 64;
     p.row_groups = p.wide ? (m->rows + 255) / 256 : (m->rows + 127) / 128;
     const int64_t wgs = (int64_t)p.tok_groups * p.row_groups;
     if (!p.wide && wgs < 256) {
@@ -898,7 +967,7 @@ moe_status launch_few(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st
 
 template <int P, int TM, int WT, int RT, bool TR, int SS>
 moe_status launch_gemm_t(const QArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int lds = 2 * P * TM * kQTermBytes;
+  constexpr int lds = GemmTile<P, TM, WT, RT>::ring * GemmTile<P, TM, WT, RT>::buffer;
   auto k = k_qgemm<P, TM, WT, RT, TR, SS>;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          lds) != hipSuccess)
@@ -933,7 +1002,8 @@ moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st
     hipLaunchKernelGGL((k_qterms<DT>), dim3(a.C), dim3(kTermWG), 0, st, a);
     a.row_groups = p.row_groups;
     const dim3 grid((unsigned)(p.row_groups * p.tok_groups), (unsigned)p.splits);
-    s = p.wide ? launch_gemm<P, 8, 2, 4>(a, tr, ss, grid, st) : launch_gemm<P, 4, 1, 1>(a, tr, ss, grid, st);
+    s = !p.wide ? launch_gemm<P, 4, 1, 1>(a, tr, ss, grid, st)
+        : P == 2 ? launch_gemm<2, 4, 1, 2>(a, tr, ss, grid, st) : launch_gemm<1, 8, 2, 4>(a, tr, ss, grid, st);
   }
   if (s != MOE_OK) return s;
   if (p.splits > 1)
