@@ -236,13 +236,10 @@ struct Ready {
   float s[4];
 };
 template <bool TR, int SS>
-__device__ __forceinline__ void ready(const QArgs& a, const Unit& u, Ready<TR>& r) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r.d[j] = u.q[j];
-  const float s = scale_of<SS>(a, u.s);
-  const uint32_t z = zero_pair(u.z);
+__device__ __forceinline__ void ready_scale(const QArgs& a, uint32_t us, uint32_t uz, Ready<TR>& r) {
+  const float s = scale_of<SS>(a, us);
+  const uint32_t z = zero_pair(uz);
   if (TR) {
-    transpose4(r.d);
     uint32_t t[4];
     spread4(__float_as_uint(s), t);
 #pragma unroll
@@ -252,6 +249,17 @@ __device__ __forceinline__ void ready(const QArgs& a, const Unit& u, Ready<TR>& 
 #pragma unroll
     for (int j = 0; j < 4; ++j) { r.s[j] = s; r.z[j] = z; }
   }
+}
+template <bool TR>
+__device__ __forceinline__ void ready_codes(uint4v q, Ready<TR>& r) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.d[j] = q[j];
+  if (TR) transpose4(r.d);
+}
+template <bool TR, int SS>
+__device__ __forceinline__ void ready(const QArgs& a, const Unit& u, Ready<TR>& r) {
+  ready_codes<TR>(u.q, r);
+  ready_scale<TR, SS>(a, u.s, u.z, r);
 }
 
 __device__ __forceinline__ float4v mma(half8 x, half8 w, float4v c) {
@@ -684,25 +692,35 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
 // ---------------------------------------------------------------------------
 // Matrix kernel: 17 and more tokens
 // ---------------------------------------------------------------------------
-// TM token tiles of 16 per workgroup, WT waves along the tokens and the rest
-// along the rows, RT row tiles of 16 per wave.  A ring of three LDS buffers,
-// each a chunk's terms (as they lie in the workspace) and codes (64 bytes of
-// each row); loads go there directly, two chunks ahead of the products.
-template <int P, int TM, int WT, int RT>
+// Products of 32 tokens x 32 rows x 16 columns.  A workgroup's waves are WT
+// along the tokens and the rest along the rows, each with TW x RT such tiles.
+// In LDS: a ring of three buffers, each a chunk's terms (as they lie in the
+// workspace) and codes (64 bytes of each row), which loads go to directly, two
+// to three chunks ahead of the products; and two tables of (scale, zero pair),
+// each for every row of four chunks (G >= 128: one group a chunk) or of a
+// chunk's four units.  The tables are there because a load of one scale per
+// row touches a cache line per row: taken chunk by chunk and wave by wave those
+// lines were more traffic than terms and codes together.
+template <int P, int WT, int TW, int RT, bool TR>
 struct GemmTile {
-  static constexpr int WR = kQWaves / WT, TW = TM / WT, rows = WR * RT * 16;
+  static constexpr int WR = kQWaves / WT, TM = WT * TW * 2, rows = WR * RT * 32;
   static constexpr int terms = P * TM * kQTermBytes, codes = rows * 64, buffer = terms + codes;
   static constexpr int ring = 3;
   static constexpr int loads = buffer / 1024 / kQWaves;    // LDS loads per wave and chunk
+  static constexpr int entries = rows * 4 / kQWG;          // table entries per thread
+  static constexpr int table = rows * 4 * 8;               // bytes
+  static constexpr int lds = ring * buffer + 2 * table;
 };
 
-template <int P, int TM, int WT, int RT, bool TR, int SS>
+typedef float float16v __attribute__((ext_vector_type(16)));
+
+template <int P, int WT, int TW, int RT, bool TR, int SS>
 __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
-  using G = GemmTile<P, TM, WT, RT>;
-  constexpr int WR = G::WR, TW = G::TW;
+  using G = GemmTile<P, WT, TW, RT, TR>;
+  constexpr int WR = G::WR, TM = G::TM;
   extern __shared__ __align__(16) uint8_t s_x[];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int row = lane & 15, quarter = lane >> 4;
+  const int row = lane & 31, half = lane >> 5;
   const int wt = wave / WR, wr = wave % WR;
   // workgroups b, b + 8, ... run on one XCD: a run of consecutive tiles (rows
   // fastest) each, so that an XCD's L2 serves few token tiles and all rows
@@ -713,16 +731,67 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   const int c0 = blockIdx.y * a.per_split;
   const int c1 = c0 + a.per_split < a.nch ? c0 + a.per_split : a.nch;
   const int nw = rg * G::rows;                             // the workgroup's rows
-  const int n0 = nw + wr * RT * 16;                        // the wave's
-  const View v = view_rows<SS>(a, n0, 16 * RT, row, quarter);
 
-  struct Scales { uint32_t s[RT], z[RT]; };
-  auto load_scales = [&](int c, Scales& u) {
+  // this thread's table entries: row tr, units or chunks te, te + 1, ...
+  constexpr int kPer = 4 / G::entries;
+  const int tr = tid / kPer, te = tid % kPer * G::entries;
+  const View v = view_rows<SS>(a, nw, G::rows, tr, 0);
+  uint32_t ts[G::entries], tz[G::entries], ns[G::entries], nz[G::entries];
+  // block kb's into ns, nz (live false: nothing is read)
+  auto load_table = [&](int kb, bool live) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) load_scale<TR, SS>(a, v, i, c, quarter, true, u.s[i], u.z[i]);
+    for (int e = 0; e < G::entries; ++e) {
+      int g;
+      if (TR) {
+        const int u = 4 * (kb < c1 ? kb : c1 - 1) + te + e;
+        g = u >> (a.gshift - 5);
+      } else {
+        const int c = 4 * kb + te + e;
+        g = (int)(((uint32_t)(c < a.nch ? c : a.nch - 1) * a.gmul) >> 20);
+      }
+      g = g < a.ng ? g : a.ng - 1;
+      const uint32_t out = live ? 0u : kOutside;
+      if (SS == 4) ns[e] = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
+      else ns[e] = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
+      nz[e] = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)((v.vz + a.zero_step * g) | out), 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
+  auto take_table = [&](bool yes) {
+#pragma unroll
+    for (int e = 0; e < G::entries; ++e) {
+      ts[e] = yes ? ns[e] : ts[e];
+      tz[e] = yes ? nz[e] : tz[e];
+    }
+  };
+  auto write_table = [&](int kb) {
+    uint8_t* t = s_x + G::ring * G::buffer + (kb & 1) * G::table;
+#pragma unroll
+    for (int e = 0; e < G::entries; ++e)
+      *reinterpret_cast<uint2*>(t + ((te + e) * G::rows + tr) * 8) =
+          make_uint2(__float_as_uint(scale_of<SS>(a, ts[e])), zero_pair(tz[e]));
+  };
+  // At every chunk c (just opened): the next block's table is written (a
+  // block's four chunks write the same, without a branch), and at a block's
+  // last chunk the table after it is loaded, to be taken at the next chunk.
+  // The table being written was last read a block ago.
+  auto step_table = [&](int c) {
+    const int kb = TR ? c : c >> 2;
+    take_table(TR || (c & 3) == 0);
+    write_table(kb + 1);
+    load_table(kb + 2, TR || (c & 3) == 3);
+  };
+
   // pieces of 1 KB: the terms' (term, token tile, quarter of it), then the
-  // codes' (16 rows each)
+  // codes' (16 rows each); scalar bases and 32-bit lane offsets
+  uint32_t vrow[G::codes / 1024 / kQWaves];
+#pragma unroll
+  for (int i = 0; i < G::codes / 1024 / kQWaves; ++i) {
+    const int n = nw + 16 * (kQWaves * i + wave) + (lane >> 2);
+    vrow[i] = (uint32_t)((n < a.N ? n : a.N - 1) - nw) * (uint32_t)a.code_pitch;
+  }
+  const uint8_t* cbase = a.codes + (int64_t)nw * a.code_pitch;
+  const int64_t plane = (int64_t)ct * a.nch * kQTermBytes;
   auto stage = [&](int c, int buf) {
 #pragma unroll
     for (int i0 = 0; i0 < G::terms / 1024; i0 += kQWaves) {
@@ -730,123 +799,184 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
       const int p = i / (4 * TM);
       int t = tg * TM + (i >> 2) % TM;
       t = t < ct ? t : ct - 1;
-      const uint8_t* src = a.terms + (((int64_t)p * ct + t) * a.nch + c) * kQTermBytes + (i & 3) * 1024;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + lane * 16),
-                                       (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + i * 1024),
-                                       16, 0, 0);
+      const uint8_t* src = a.terms + p * plane + ((int64_t)t * a.nch + c) * kQTermBytes + (i & 3) * 1024;
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(src + (uint32_t)(lane * 16)),
+          (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + i * 1024), 16, 0, 0);
     }
 #pragma unroll
-    for (int i0 = 0; i0 < G::codes / 1024; i0 += kQWaves) {
-      const int i = i0 + wave;
-      int n = nw + 16 * i + (lane >> 2);
-      n = n < a.N ? n : a.N - 1;
+    for (int i = 0; i < G::codes / 1024 / kQWaves; ++i) {
       int u = 4 * c + (lane & 3);
       u = u < a.units ? u : a.units - 1;                   // x is zero past the last column
-      const uint8_t* src = a.codes + (int64_t)n * a.code_pitch + 16 * u;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                       (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + G::terms +
-                                                                                 i * 1024),
-                                       16, 0, 0);
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(cbase + (vrow[i] + 16u * (uint32_t)u)),
+          (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + G::terms +
+                                                    (kQWaves * i + wave) * 1024),
+          16, 0, 0);
     }
   };
 
-  float acc[TW][RT][4];
-#pragma unroll
-  for (int t = 0; t < TW; ++t)
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[t][i][r] = 0.0f;
-
   const Magic mg = magic();
-  Scales u0, u1;
+  auto clamped = [&](int c) { return c < c1 ? c : c1 - 1; };
+  // The pipeline.  A chunk is eight steps of 16 columns; during a step's matrix
+  // instructions the next step's terms are read from LDS and its codes
+  // unpacked, and where a group's sums are complete (after the chunk, or for
+  // TR after each unit of two steps) the step after scales them into acc, so
+  // that vector instructions lie between the matrix instructions of the same
+  // wave (the waves of a workgroup run in step: what each does in phases, none
+  // overlaps).  The move to the next chunk comes before the last step: this
+  // chunk's LDS reads are complete by then, so one barrier both frees its
+  // buffer for the chunk three on and, each wave having waited for its own
+  // loads, opens the next chunk's.  Loads complete in order, and the newest
+  // (one chunk's LDS loads) may stay in flight; past the last chunk the last
+  // is loaded again, so that their number is the same everywhere.
+  float16v acc[TW][RT], d[TW][RT];
+  half8 x[2][TW][P], b[RT];
+  uint32_t w[RT][2][4];                                    // codes: unit 2 u + half (TR: swapped, see codes_of)
+  uint2 sz[2][RT];                                         // (scale, zero pair): TR unit & 1, else [0]
+  float sp[RT];                                            // scales of the sums in d
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    sp[i] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < TW; ++t) {
+      acc[t][i] = float16v(0.0f);
+      d[t][i] = float16v(0.0f);
+    }
+  }
   int buf = 0;
-  // One chunk: its loads are complete in every wave once each wave has waited
-  // for its own (loads complete in order, and the next chunk's LDS loads, the
-  // last ones issued, may stay in flight) and all have met; by then every wave
-  // is also done with the buffer before this one, which the loads of the chunk
-  // after next go into.  Past the last chunk that chunk is loaded again, so
-  // that the number of loads in flight is the same everywhere.
-  auto chunk = [&](int c, Scales& u) {
-    // (a plain barrier: __syncthreads would wait for every load in flight)
+  const uint8_t* tables = s_x + G::ring * G::buffer + (wr * RT * 32 + row) * 8;
+  // The block of 8 columns that a step takes in this half of the wave: TR
+  // step s is half of unit s / 2; else dword s % 4 of units 2 (s / 4) + half.
+  auto read = [&](int s) {
+    const uint8_t* xs = s_x + buf * G::buffer + (2 * wt * TW + (row >> 4)) * kQTermBytes + (row & 15) * 16 +
+                        (TR ? half : 4 * half) * 256;
+    const int block = TR ? 2 * s : 8 * (s >> 2) + (s & 3);
+#pragma unroll
+    for (int t = 0; t < TW; ++t)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        x[s & 1][t][p] = *reinterpret_cast<const half8*>(xs + (p * TM + 2 * t) * kQTermBytes + block * 256);
+  };
+  auto read_scales = [&](int c, int u) {
+    const uint8_t* t = tables + ((TR ? c : c >> 2) & 1) * G::table + (TR ? u : c & 3) * G::rows * 8;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) sz[TR ? u & 1 : 0][i] = *reinterpret_cast<const uint2*>(t + 32 * 8 * i);
+  };
+  // every wave's loads of buffer `buf` are complete, and so are its reads of
+  // the one before (a plain barrier: __syncthreads would wait for all loads)
+  auto open = [&](int c) {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(G::loads) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
-    Ready<TR> w[RT];
-    const uint8_t* base = s_x + buf * G::buffer;
+    const uint8_t* q = s_x + buf * G::buffer + G::terms + (wr * RT * 32 + row) * 64 + half * 16;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      Unit q;
-      q.q = *reinterpret_cast<const uint4v*>(base + G::terms + (wr * RT + i) * 1024 + row * 64 + quarter * 16);
-      q.s = u.s[i];
-      q.z = u.z[i];
-      ready<TR, SS>(a, q, w[i]);
-    }
-    const int c2 = c + 2 < c1 ? c + 2 : c1 - 1;
-    load_scales(c2, u);
-    __builtin_amdgcn_sched_barrier(0);
-    stage(c2, buf == 0 ? 2 : buf - 1);
-    buf = buf == 2 ? 0 : buf + 1;
-    const uint8_t* xs = base + wt * TW * kQTermBytes + row * 16;
-    float4v d[TW][RT];
-    half8 x[2][TW][P];
-    auto read = [&](int j) {
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int t = 0; t < TW; ++t)
+      for (int u = 0; u < 2; ++u) {
+        const uint4v v4 = *reinterpret_cast<const uint4v*>(q + i * 2048 + u * 32);
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-          x[j & 1][t][p] =
-              *reinterpret_cast<const half8*>(xs + (p * TM + t) * kQTermBytes + block_of<TR>(j, quarter) * 256);
-    };
+        for (int k = 0; k < 4; ++k) w[i][u][k] = v4[k];
+      }
     read(0);
+    read_scales(c, 0);
+  };
+  // TR: dwords 0 and 1 of unit 2 u come to lie in the two halves of w[u][0]
+  // and those of unit 2 u + 1 in w[u][1] (2 and 3 likewise)
+  auto codes_of = [&](int i) {
+    if (TR) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j < 3) read(j + 1);
-      __builtin_amdgcn_sched_barrier(0);          // the next terms are read during these products
-      half8 b[RT];
-#pragma unroll
-      for (int i = 0; i < RT; ++i) b[i] = unpack8(mg, w[i].d[j], w[i].z[j]);
-#pragma unroll
-      for (int t = 0; t < TW; ++t) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          if (TR || j == 0) d[t][i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int p = 0; p < P; ++p) d[t][i] = mma(x[j & 1][t][p], b[i], d[t][i]);
-          if (TR || j == 3) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[t][i][r] += w[i].s[j] * d[t][i][r];
-          }
-        }
+      for (int u = 0; u < 2; ++u) {
+        swap32(w[i][u][0], w[i][u][1]);
+        swap32(w[i][u][2], w[i][u][3]);
       }
     }
   };
-  load_scales(c0, u0);
-  __builtin_amdgcn_sched_barrier(0);
+  auto unpack = [&](int s, int i) {
+    const uint32_t code = TR ? w[i][s >> 2][2 * (s & 1) + ((s >> 1) & 1)] : w[i][s >> 2][s & 3];
+    b[i] = unpack8(mg, code, sz[TR ? (s >> 1) & 1 : 0][i].y);
+  };
+  const int k0 = TR ? c0 : c0 >> 2;
+  load_table(k0, true);
   stage(c0, 0);
-  __builtin_amdgcn_sched_barrier(0);
-  load_scales(c0 + 1 < c1 ? c0 + 1 : c0, u1);
-  __builtin_amdgcn_sched_barrier(0);
-  stage(c0 + 1 < c1 ? c0 + 1 : c0, 1);
-  for (int c = c0;; c += 2) {
-    chunk(c, u0);
-    if (c + 1 >= c1) break;
-    chunk(c + 1, u1);
-    if (c + 2 >= c1) break;
+  take_table(true);
+  write_table(k0);
+  load_table(k0 + 1, true);
+  stage(clamped(c0 + 1), 1);
+  take_table(true);
+  write_table(k0 + 1);
+  open(c0);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    codes_of(i);
+    unpack(0, i);
   }
+  __builtin_amdgcn_sched_barrier(0);
+  load_table(k0 + 2, TR || (c0 & 3) == 3);
+  stage(clamped(c0 + 2), 2);
+  // the matrix instructions of row tile i in step s
+  auto product = [&](int s, int i) {
+#pragma unroll
+    for (int t = 0; t < TW; ++t) {
+      if (s == 0 || (TR && s % 2 == 0)) {
+        acc[t][i] += sp[i] * d[t][i];
+        d[t][i] = float16v(0.0f);
+      }
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        d[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[s & 1][t][p], b[i], d[t][i], 0, 0, 0);
+    }
+    if (s == 0 || (TR && s % 2 == 0)) sp[i] = __uint_as_float(sz[TR ? (s >> 1) & 1 : 0][i].x);
+  };
+  for (int c = c0; c < c1; ++c) {
+#pragma unroll
+    for (int s = 0; s < 7; ++s) {
+      read(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        product(s, i);
+        unpack(s + 1, i);
+      }
+      if (TR && s % 2 == 0 && s < 6) read_scales(c, s / 2 + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const int done = buf;
+    buf = buf == 2 ? 0 : buf + 1;
+    open(c + 1);
+    step_table(c + 1);
+    stage(clamped(c + 3), done);
+    __builtin_amdgcn_sched_barrier(0);
+    // these first: the next codes are on their way from LDS
+#pragma unroll
+    for (int i = 0; i < RT; ++i) product(7, i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      codes_of(i);
+      unpack(0, i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int t = 0; t < TW; ++t) acc[t][i] += sp[i] * d[t][i];
   // no load into LDS may be in flight when the workgroup gives its LDS up
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
+  // register r of a product is its row 8 (r / 4) + 4 half + r % 4
 #pragma unroll
   for (int t = 0; t < TW; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int tok = (tg * TM + wt * TW + t) * 16 + 4 * r + quarter;
+    for (int r = 0; r < 16; ++r) {
+      const int m = 8 * (r >> 2) + 4 * half + (r & 3);
+      const int tok = (tg * TM + 2 * (wt * TW + t) + (m >> 4)) * 16 + row_token(m & 15);
       if (tok >= a.C) continue;
       const float inv = a.inv[tok];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const int n = n0 + 16 * i + row;
+        const int n = nw + (wr * RT + i) * 32 + row;
         if (n >= a.N) continue;
         if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.C + tok) * a.N + n] = acc[t][i][r] * inv;
         else put(a, tok, n, acc[t][i][r] * inv);
@@ -965,10 +1095,10 @@ moe_status launch_few(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st
   return ss == 4 ? launch_few_t<DT, TOK, false, 4>(a, grid, st) : launch_few_t<DT, TOK, false, 2>(a, grid, st);
 }
 
-template <int P, int TM, int WT, int RT, bool TR, int SS>
+template <int P, int WT, int TW, int RT, bool TR, int SS>
 moe_status launch_gemm_t(const QArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int lds = GemmTile<P, TM, WT, RT>::ring * GemmTile<P, TM, WT, RT>::buffer;
-  auto k = k_qgemm<P, TM, WT, RT, TR, SS>;
+  constexpr int lds = GemmTile<P, WT, TW, RT, TR>::lds;
+  auto k = k_qgemm<P, WT, TW, RT, TR, SS>;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          lds) != hipSuccess)
     return MOE_ERR_DEVICE;
@@ -976,10 +1106,10 @@ moe_status launch_gemm_t(const QArgs& a, dim3 grid, hipStream_t st) {
   return MOE_OK;
 }
 
-template <int P, int TM, int WT, int RT>
+template <int P, int WT, int TW, int RT>
 moe_status launch_gemm(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st) {
-  if (tr) return ss == 4 ? launch_gemm_t<P, TM, WT, RT, true, 4>(a, grid, st) : launch_gemm_t<P, TM, WT, RT, true, 2>(a, grid, st);
-  return ss == 4 ? launch_gemm_t<P, TM, WT, RT, false, 4>(a, grid, st) : launch_gemm_t<P, TM, WT, RT, false, 2>(a, grid, st);
+  if (tr) return ss == 4 ? launch_gemm_t<P, WT, TW, RT, true, 4>(a, grid, st) : launch_gemm_t<P, WT, TW, RT, true, 2>(a, grid, st);
+  return ss == 4 ? launch_gemm_t<P, WT, TW, RT, false, 4>(a, grid, st) : launch_gemm_t<P, WT, TW, RT, false, 2>(a, grid, st);
 }
 
 template <int DT>
@@ -1002,8 +1132,8 @@ moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st
     hipLaunchKernelGGL((k_qterms<DT>), dim3(a.C), dim3(kTermWG), 0, st, a);
     a.row_groups = p.row_groups;
     const dim3 grid((unsigned)(p.row_groups * p.tok_groups), (unsigned)p.splits);
-    s = !p.wide ? launch_gemm<P, 4, 1, 1>(a, tr, ss, grid, st)
-        : P == 2 ? launch_gemm<2, 4, 1, 2>(a, tr, ss, grid, st) : launch_gemm<1, 8, 2, 4>(a, tr, ss, grid, st);
+    s = !p.wide ? launch_gemm<P, 2, 1, 1>(a, tr, ss, grid, st)
+        : P == 2 ? launch_gemm<2, 1, 2, 1>(a, tr, ss, grid, st) : launch_gemm<1, 2, 2, 2>(a, tr, ss, grid, st);
   }
   if (s != MOE_OK) return s;
   if (p.splits > 1)
