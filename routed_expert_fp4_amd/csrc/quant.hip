@@ -79,9 +79,9 @@ struct QArgs {
   float* inv;                         // [C]: takes the terms' power of two out again
   uint8_t* terms;                     // [P][C / 16][nch][16 blocks][16 tokens][16 bytes]
   float* part;                        // [splits][C][N]
-  int wk;                             // stream: waves of a workgroup that split the columns
+  int ks, spt;                        // one token: 2^ks waves to a row tile, steps per tile
   int splits, per_split;              // matrix kernel: column ranges, chunks in each
-  int row_groups;
+  int row_groups;                     // one token: groups of row tiles; matrix kernel: row tiles
 };
 
 __device__ const uint8_t kEight[16] = {8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8};
@@ -95,11 +95,6 @@ __device__ __forceinline__ int row_token(int r) { return (r >> 2) + 4 * (r & 3);
 // ---------------------------------------------------------------------------
 // Codes
 // ---------------------------------------------------------------------------
-struct Unit {
-  uint4v q;         // 32 codes
-  uint32_t s, z;    // their group's scale (as stored) and zero point
-};
-
 // A wave's view of the codes, scales and zero points of the rows from n0 on:
 // buffer loads whose row and unit are a per-lane offset, and whose tile and
 // chunk are a scalar one.  Offsets past the last row's last unit read zeros.
@@ -127,38 +122,47 @@ __device__ __forceinline__ View view_rows(const QArgs& a, int n0, int rows, int 
   return v;
 }
 
-// Tile i (16 rows each) of the view, chunk c.  Units past the last column read
-// what lies there (a code is finite, and x is zero); their scale is the last
-// group's, since what lies behind a row of scales may be no number.  `live`
-// false: nothing is read.  The loads are always issued, so that the count of
-// loads in flight is the same on every path and a wait for one step's codes
-// leaves the next step's in flight.
-constexpr uint32_t kOutside = 0x80000000u;
-template <bool TR, int SS>
-__device__ __forceinline__ void load_scale(const QArgs& a, const View& v, int i, int c, int quarter, bool live,
-                                           uint32_t& s, uint32_t& z) {
-  const uint32_t out = live ? 0u : kOutside;
-  uint32_t os = v.vs | out, oz = v.vz | out;
-  int g;
-  if (TR) {
-    const int gl = (4 * c + quarter) >> (a.gshift - 5);
-    g = 0;
-    os += SS * (gl < a.ng ? gl : a.ng - 1);
-    oz += a.zero_step * (gl < a.ng ? gl : a.ng - 1);
-  } else {
-    g = (int)(((uint32_t)c * a.gmul) >> 20);
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every view
+
+// N (up to 4) of a wave's chunks, c, c + step, ...: codes, and as stored the
+// scales and zero points of all of them, for which a lane reads not its own
+// unit's but those of chunk number `quarter` (G >= 128: one; TR: of the
+// chunk's four units).  A load of one scale per row touches a cache line per
+// row, and the lines are gone by the row's next chunk; so each is touched once
+// for four chunks.
+template <int N, bool TR>
+struct Quad {
+  static constexpr int S = TR ? 4 : 1;
+  uint4v q[N];
+  uint32_t s[S], z[S];
+};
+
+// Units past the last column read what lies there (a code is finite, and x is
+// zero); their scale is the last group's, since what lies behind a row of
+// scales may be no number.  Chunks from nch on (or live false) are not read.
+// The loads are always issued, so that the count of loads in flight is the
+// same on every path and a wait for one step's codes leaves the next step's in
+// flight.
+template <int N, bool TR, int SS>
+__device__ __forceinline__ void load_quad(const QArgs& a, const View& v, int c, int step, int quarter, bool live,
+                                          Quad<N, TR>& u) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int ci = c + step * i;
+    u.q[i] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
+        v.codes, (int)(v.vc | (live && ci < a.nch ? 0u : kOutside)), 64 * ci, kCachePolicyNt));
   }
-  const int ss = SS * g + 16 * i * (int)a.scale_pitch, sz = a.zero_step * g + 16 * i * (int)a.zero_pitch;
-  if (SS == 4) s = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)os, ss, 0);
-  else s = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)os, ss, 0);
-  z = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)oz, sz, 0);
-}
-template <bool TR, int SS>
-__device__ __forceinline__ void load_unit(const QArgs& a, const View& v, int i, int c, int quarter, bool live,
-                                          Unit& u) {
-  u.q = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
-      v.codes, (int)(v.vc | (live ? 0u : kOutside)), 64 * c + 16 * i * (int)a.code_pitch, kCachePolicyNt));
-  load_scale<TR, SS>(a, v, i, c, quarter, live, u.s, u.z);
+  int cq = c + step * (quarter < N ? quarter : N - 1);
+  cq = cq < a.nch ? cq : a.nch - 1;
+  const uint32_t out = live ? 0u : kOutside;
+#pragma unroll
+  for (int e = 0; e < Quad<N, TR>::S; ++e) {
+    int g = TR ? (4 * cq + e) >> (a.gshift - 5) : (int)(((uint32_t)cq * a.gmul) >> 20);
+    if (TR) g = g < a.ng ? g : a.ng - 1;
+    if (SS == 4) u.s[e] = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
+    else u.s[e] = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
+    u.z[e] = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)((v.vz + a.zero_step * g) | out), 0, 0);
+  }
 }
 
 template <int SS>
@@ -229,37 +233,22 @@ __device__ __forceinline__ void spread4(uint32_t v, uint32_t (&o)[4]) {
   swap16(o[2], o[3]);
 }
 
-// A unit ready for its four products: dword j, scale and zero pair of product j.
-template <bool TR>
-struct Ready {
-  uint32_t d[4], z[4];
-  float s[4];
-};
-template <bool TR, int SS>
-__device__ __forceinline__ void ready_scale(const QArgs& a, uint32_t us, uint32_t uz, Ready<TR>& r) {
-  const float s = scale_of<SS>(a, us);
-  const uint32_t z = zero_pair(uz);
+// The scales and zero pairs of a quad: of chunk i in s[i], z[i], for TR those
+// of the lane's own unit.
+template <int N, bool TR, int SS>
+__device__ __forceinline__ void quad_scales(const QArgs& a, const Quad<N, TR>& u, uint32_t (&s)[4], uint32_t (&z)[4]) {
   if (TR) {
-    uint32_t t[4];
-    spread4(__float_as_uint(s), t);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.s[j] = __uint_as_float(t[j]);
-    spread4(z, r.z);
+    for (int e = 0; e < 4; ++e) {
+      s[e] = __float_as_uint(scale_of<SS>(a, u.s[e]));
+      z[e] = zero_pair(u.z[e]);
+    }
+    transpose4(s);
+    transpose4(z);
   } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) { r.s[j] = s; r.z[j] = z; }
+    spread4(__float_as_uint(scale_of<SS>(a, u.s[0])), s);
+    spread4(zero_pair(u.z[0]), z);
   }
-}
-template <bool TR>
-__device__ __forceinline__ void ready_codes(uint4v q, Ready<TR>& r) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r.d[j] = q[j];
-  if (TR) transpose4(r.d);
-}
-template <bool TR, int SS>
-__device__ __forceinline__ void ready(const QArgs& a, const Unit& u, Ready<TR>& r) {
-  ready_codes<TR>(u.q, r);
-  ready_scale<TR, SS>(a, u.s, u.z, r);
 }
 
 __device__ __forceinline__ float4v mma(half8 x, half8 w, float4v c) {
@@ -305,26 +294,34 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t x_view(const QArgs& a, int t, 
   return qview(static_cast<const uint8_t*>(a.x) + (int64_t)t * a.x_pitch * B, ((rows - 1) * a.x_pitch + a.K) * B);
 }
 template <int DT>
-__device__ __forceinline__ void load8(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
-                                      Raw<DT>& r) {
+__device__ __forceinline__ void load8v(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
+                                       Raw<DT>& r) {
   constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
-  if (a.x_vec) {
-    const uint32_t o = live && k < a.K ? row + (uint32_t)(k * B) : kOutside;
+  const uint32_t o = live && k < a.K ? row + (uint32_t)(k * B) : kOutside;
 #pragma unroll
-    for (int i = 0; i < B / 2; ++i)
-      r.v[i] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + 16 * i), 0, 0));
-  } else {
+  for (int i = 0; i < B / 2; ++i)
+    r.v[i] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + 16 * i), 0, 0));
+}
+template <int DT>
+__device__ __forceinline__ void load8e(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
+                                       Raw<DT>& r) {
+  constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t o = live && k + i < a.K ? row + (uint32_t)((k + i) * B) : kOutside;
-      if (DT == MOE_DT_F32) {
-        r.v[i >> 2][i & 3] = __builtin_amdgcn_raw_buffer_load_b32(x, (int)o, 0, 0);
-      } else {
-        const uint32_t h = __builtin_amdgcn_raw_buffer_load_b16(x, (int)o, 0, 0);
-        r.v[0][i >> 1] = (i & 1) ? r.v[0][i >> 1] | (h << 16) : h;
-      }
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t o = live && k + i < a.K ? row + (uint32_t)((k + i) * B) : kOutside;
+    if (DT == MOE_DT_F32) {
+      r.v[i >> 2][i & 3] = __builtin_amdgcn_raw_buffer_load_b32(x, (int)o, 0, 0);
+    } else {
+      const uint32_t h = __builtin_amdgcn_raw_buffer_load_b16(x, (int)o, 0, 0);
+      r.v[0][i >> 1] = (i & 1) ? r.v[0][i >> 1] | (h << 16) : h;
     }
   }
+}
+template <int DT>
+__device__ __forceinline__ void load8(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
+                                      Raw<DT>& r) {
+  if (a.x_vec) load8v<DT>(a, x, row, k, live, r);
+  else load8e<DT>(a, x, row, k, live, r);
 }
 
 template <int DT>
@@ -372,54 +369,86 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
   return v;
 }
 
-// Token blockIdx.x: its largest value, then its terms.
-constexpr int kTermWG = 256;
-template <int DT>
+// Four tokens whose operand rows are next to each other (t, t + 4, t + 8,
+// t + 12 of a tile), so that four lanes write 64 contiguous bytes: their
+// largest values, then their terms.  FITS: the rows (up to 8192 columns) stay
+// in registers between the two, else they are read twice.
+constexpr int kTermWG = 1024, kTermBlocks = kTermWG / 4;
+template <int DT, bool FITS>
 __global__ __launch_bounds__(kTermWG) void k_qterms(QArgs a) {
-  __shared__ uint32_t s_max[kTermWG / 64];
-  const int t = blockIdx.x, tid = threadIdx.x;
+  constexpr int B = DT == MOE_DT_F32 ? 4 : 2, NB = 4;
+  __shared__ uint32_t s_max[kTermWG / 64][4];
+  const int tid = threadIdx.x, lane = tid & 63, k = tid & 3;
+  const int t0 = blockIdx.x / 4 * 16, t = t0 + blockIdx.x % 4 + 4 * k;
+  const bool live = t < a.C;
   const int nblk = a.nch * (kQChunk / 8);
-  const __amdgpu_buffer_rsrc_t x = x_view<DT>(a, t, 1);
+  const __amdgpu_buffer_rsrc_t x = x_view<DT>(a, t0, a.C - t0 < 16 ? a.C - t0 : 16);
+  const uint32_t row = (uint32_t)((t - t0) * (int)a.x_pitch * B);
   float m = 1.0f, inv = 1.0f;
   bool finite = true;
+  Raw<DT> r[FITS ? NB : 1];
+  if (FITS) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) load8<DT>(a, x, row, 8 * ((tid >> 2) + kTermBlocks * i), live, r[i]);
+  }
   if (DT != MOE_DT_F16) {
     uint32_t mx = 0;
-    for (int b = tid; b < nblk; b += kTermWG) {
-      Raw<DT> r;
-      load8<DT>(a, x, 0, 8 * b, true, r);
-      mx = raw_max<DT>(r, mx);
+    if (FITS) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) mx = raw_max<DT>(r[i], mx);
+    } else {
+      for (int b = tid >> 2; b < nblk; b += kTermBlocks) {
+        load8<DT>(a, x, row, 8 * b, live, r[0]);
+        mx = raw_max<DT>(r[0], mx);
+      }
     }
-    mx = wave_umax(mx);
-    if ((tid & 63) == 0) s_max[tid >> 6] = mx;
+#pragma unroll
+    for (int w = 4; w < 64; w <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)mx, w, 64);
+      mx = o > mx ? o : mx;
+    }
+    if (lane < 4) s_max[tid >> 6][lane] = mx;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kTermWG / 64; ++w) mx = s_max[w] > mx ? s_max[w] : mx;
+    for (int w = 0; w < kTermWG / 64; ++w) mx = s_max[w][k] > mx ? s_max[w][k] : mx;
     term_scale(mx, m, inv);
     finite = mx < 0x7F800000u;
   }
-  if (tid == 0) a.inv[t] = inv;
+  if (!live) return;
+  if (tid < 4) a.inv[t] = inv;
   const int ct = (a.C + 15) / 16;
   const int64_t plane = (int64_t)ct * a.nch * kQTermBytes;
   uint8_t* out = a.terms + (int64_t)(t >> 4) * a.nch * kQTermBytes + token_row(t & 15) * 16;
-  for (int b = tid; b < nblk; b += kTermWG) {
-    Raw<DT> r;
-    load8<DT>(a, x, 0, 8 * b, true, r);
+  auto write = [&](int b, const Raw<DT>& v) {
     half8 hi, lo;
-    make_terms<DT>(r, m, finite, hi, lo);
+    make_terms<DT>(v, m, finite, hi, lo);
     *reinterpret_cast<half8*>(out + (int64_t)b * 256) = hi;
     if (DT == MOE_DT_F32) *reinterpret_cast<half8*>(out + plane + (int64_t)b * 256) = lo;
+  };
+  if (FITS) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int b = (tid >> 2) + kTermBlocks * i;
+      if (b < nblk) write(b, r[i]);
+    }
+  } else {
+    for (int b = tid >> 2; b < nblk; b += kTermBlocks) {
+      load8<DT>(a, x, row, 8 * b, live, r[0]);
+      write(b, r[0]);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Results
 // ---------------------------------------------------------------------------
+template <int DT>
 __device__ __forceinline__ void put(const QArgs& a, int t, int n, float v) {
   const int64_t i = (int64_t)t * a.y_pitch + n;
-  if (a.x_dt == MOE_DT_F32) {
+  if (DT == MOE_DT_F32) {
     float* y = static_cast<float*>(a.y) + i;
     *y = a.accumulate ? *y + v : v;
-  } else if (a.x_dt == MOE_DT_BF16) {
+  } else if (DT == MOE_DT_BF16) {
     __hip_bfloat16* y = static_cast<__hip_bfloat16*>(a.y) + i;
     *y = __float2bfloat16(a.accumulate ? __bfloat162float(*y) + v : v);
   } else {
@@ -427,25 +456,37 @@ __device__ __forceinline__ void put(const QArgs& a, int t, int n, float v) {
     *y = __float2half(a.accumulate ? __half2float(*y) + v : v);
   }
 }
+__device__ __forceinline__ void put(const QArgs& a, int t, int n, float v) {
+  if (a.x_dt == MOE_DT_F32) put<MOE_DT_F32>(a, t, n, v);
+  else if (a.x_dt == MOE_DT_BF16) put<MOE_DT_BF16>(a, t, n, v);
+  else put<MOE_DT_F16>(a, t, n, v);
+}
 
 // ---------------------------------------------------------------------------
 // One unit's four products
 // ---------------------------------------------------------------------------
-// acc[r] += the chunk's scaled sums; frag(p, j) gives x's term p of product j.
-template <int P, int NR, bool TR, int SS, class F>
-__device__ __forceinline__ void multiply(const QArgs& a, const Magic& mg, const Unit& u, F frag, float (&acc)[NR]) {
-  Ready<TR> w;
-  ready<TR, SS>(a, u, w);
-  float4v d = {0.0f, 0.0f, 0.0f, 0.0f};
+// acc[r] += a chunk's scaled sums; frag(p, j) gives x's term p of product j.
+// The terms' sums are chains of their own: none waits for the other.
+template <int P, int NR, bool TR, class F>
+__device__ __forceinline__ void multiply(const Magic& mg, uint4v q, uint32_t s, uint32_t z, F frag, float (&acc)[NR]) {
+  uint32_t d[4] = {q[0], q[1], q[2], q[3]}, sj[4], zj[4];
+  if (TR) {
+    transpose4(d);
+    spread4(s, sj);
+    spread4(z, zj);
+  }
+  float4v sum[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) sum[p] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const half8 b = unpack8(mg, w.d[j], w.z[j]);
-    if (TR) d = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    const half8 b = unpack8(mg, d[j], TR ? zj[j] : z);
 #pragma unroll
-    for (int p = 0; p < P; ++p) d = mma(frag(p, j), b, d);
+    for (int p = 0; p < P; ++p) sum[p] = mma(frag(p, j), b, TR ? float4v{0.0f, 0.0f, 0.0f, 0.0f} : sum[p]);
     if (TR || j == 3) {
+      const float f = __uint_as_float(TR ? sj[j] : s);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) acc[r] += w.s[j] * d[r];
+      for (int r = 0; r < NR; ++r) acc[r] += f * (P == 2 ? sum[0][r] + sum[P - 1][r] : sum[0][r]);
     }
   }
 }
@@ -453,13 +494,13 @@ __device__ __forceinline__ void multiply(const QArgs& a, const Magic& mg, const 
 // ---------------------------------------------------------------------------
 // One token
 // ---------------------------------------------------------------------------
-constexpr int kQAhead = 4;            // chunks a wave loads together, twice in flight
-
 // The workgroup makes the token's terms in LDS ([P][blocks] of 16 bytes) while
 // the first codes are on their way (x's loads are issued before theirs: loads
-// complete in order).  It takes kQWaves / wk tiles of 16 rows at a time; wave w
-// walks the chunks w % wk, w % wk + wk, ... of tile w / wk, kQAhead of them
-// multiplied while the kQAhead after them are loaded, on into the next tile.
+// complete in order).  It takes kQWaves >> ks tiles of 16 rows at a time, 2^ks
+// waves to a tile; a wave walks its tile's chunks kw, kw + 2^ks, ... in steps
+// of eight, each quad's next step loaded as soon as it is multiplied, on into
+// the next tile.  Short code matters here as much as bytes: a call for a few
+// thousand rows lasts about as long as fetching a straight-line kernel does.
 template <int DT, bool TR, int SS>
 __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
   constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
@@ -470,46 +511,50 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
   // the wave's number through readfirstlane: its tiles and chunks are scalars
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int row = lane & 15, quarter = lane >> 4;
-  const int wk = a.wk, tiles = kQWaves / wk, kw = wave % wk, tw = wave / wk;
+  const int ks = a.ks, wk = 1 << ks, kw = wave & (wk - 1), tw = wave >> ks, tiles = kQWaves >> ks;
   const int nblk = a.nch * (kQChunk / 8);
-  const int ngroups = ((a.N + 15) / 16 + tiles - 1) / tiles;
-  const int spt = ((a.nch + wk - 1) / wk + kQAhead - 1) / kQAhead;      // steps per tile
-  const int nit = (ngroups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int64_t steps = (int64_t)nit * spt;
 
   Raw<DT> raw[NB];
   const __amdgpu_buffer_rsrc_t xv = x_view<DT>(a, 0, 1);
+  if (a.x_vec) {
 #pragma unroll
-  for (int i = 0; i < NB; ++i) load8<DT>(a, xv, 0, 8 * (tid + kQWG * i), true, raw[i]);
+    for (int i = 0; i < NB; ++i) load8v<DT>(a, xv, 0, 8 * (tid + kQWG * i), true, raw[i]);
+  }
   __builtin_amdgcn_sched_barrier(0);
 
   // the codes of one step: step ld_i of the workgroup's ld_g-th tile group
   int ld_g = blockIdx.x, ld_i = 0;
   View v = view_rows<SS>(a, (ld_g * tiles + tw) * 16, 16, row, quarter);
-  auto load = [&](Unit (&u)[kQAhead]) {
-#pragma unroll
-    for (int i = 0; i < kQAhead; ++i) {
-      const int c = kw + wk * (ld_i * kQAhead + i);
-      load_unit<TR, SS>(a, v, 0, c, quarter, c < a.nch && ld_g < ngroups, u[i]);
-    }
-    if (++ld_i == spt) {
+  Quad<4, TR> u[2];
+  auto load = [&](int k) {
+    load_quad<4, TR, SS>(a, v, kw + ((8 * ld_i + 4 * k) << ks), wk, quarter, ld_g < a.row_groups, u[k]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto advance = [&]() {
+    if (++ld_i == a.spt) {
       ld_i = 0;
       ld_g += gridDim.x;
       v = view_rows<SS>(a, (ld_g * tiles + tw) * 16, 16, row, quarter);
     }
-    __builtin_amdgcn_sched_barrier(0);
   };
   const Magic mg = magic();
-  Unit u0[kQAhead], u1[kQAhead];
-  load(u0);
-  load(u1);
+  load(0);
+  load(1);
+  advance();
 
   float m = 1.0f, inv = 1.0f;
   bool finite = true;
   if (DT != MOE_DT_F16) {
     uint32_t mx = 0;
+    if (a.x_vec) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) mx = raw_max<DT>(raw[i], mx);
+      for (int i = 0; i < NB; ++i) mx = raw_max<DT>(raw[i], mx);
+    } else {
+      for (int b = tid; b < nblk; b += kQWG) {
+        load8e<DT>(a, xv, 0, 8 * b, true, raw[0]);
+        mx = raw_max<DT>(raw[0], mx);
+      }
+    }
     mx = wave_umax(mx);
     if (lane == 0) s_max[wave] = mx;
     __syncthreads();
@@ -518,78 +563,86 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
     term_scale(mx, m, inv);
     finite = mx < 0x7F800000u;
   }
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int b = tid + kQWG * i;
-    if (b >= nblk) continue;
+  auto write = [&](int b, const Raw<DT>& r) {
     half8 hi, lo;
-    make_terms<DT>(raw[i], m, finite, hi, lo);
+    make_terms<DT>(r, m, finite, hi, lo);
     *reinterpret_cast<half8*>(s_x + 16 * b) = hi;
     if (P == 2) *reinterpret_cast<half8*>(s_x + 16 * (nblk + b)) = lo;
+  };
+  if (a.x_vec) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if (tid + kQWG * i < nblk) write(tid + kQWG * i, raw[i]);
+  } else {
+    for (int b = tid; b < nblk; b += kQWG) {
+      load8e<DT>(a, xv, 0, 8 * b, true, raw[0]);
+      write(b, raw[0]);
+    }
   }
   __syncthreads();
 
-  float acc[1] = {0.0f};
-  int cg = blockIdx.x, ci = 0, parity = 0;
-  auto compute = [&](const Unit (&u)[kQAhead]) {
+  int parity = 0;
+  for (int cg = blockIdx.x; cg < a.row_groups; cg += gridDim.x) {
+    float acc[1] = {0.0f};
+    for (int ci = 0; ci < a.spt; ++ci) {
 #pragma unroll
-    for (int i = 0; i < kQAhead; ++i) {
-      const int c = kw + wk * (ci * kQAhead + i);
-      if (c >= a.nch) continue;
-      multiply<P, 1, TR, SS>(a, mg, u[i], [&](int p, int j) {
-        return *reinterpret_cast<const half8*>(s_x + 16 * (p * nblk + c * (kQChunk / 8) + block_of<TR>(j, quarter)));
-      }, acc);
+      for (int k = 0; k < 2; ++k) {
+        uint32_t sc[4], zp[4];
+        quad_scales<4, TR, SS>(a, u[k], sc, zp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = kw + ((8 * ci + 4 * k + i) << ks);
+          if (c >= a.nch) continue;
+          const uint8_t* xc = s_x + c * (2 * kQChunk) + (TR ? 1 : 4) * 16 * quarter;
+          multiply<P, 1, TR>(mg, u[k].q[i], sc[i], zp[i], [&](int p, int j) {
+            return *reinterpret_cast<const half8*>(xc + 16 * (p * nblk + (TR ? 4 : 1) * j));
+          }, acc);
+        }
+        load(k);
+      }
+      advance();
     }
-    if (++ci < spt) return;
     // the tile is done: the waves that split its columns add up, in order
-    const int n0 = cg * tiles * 16;
     float* red = s_red[parity];
     parity ^= 1;
     if (lane < 16) red[wave * 16 + lane] = acc[0];
-    if (wk > 1) __syncthreads();
-    const int tile = wk > 1 ? tid >> 4 : tw;
-    const int n = n0 + tile * 16 + (tid & 15);
-    if ((wk > 1 ? tid < tiles * 16 : lane < 16) && n < a.N) {
+    if (ks) __syncthreads();
+    const int tile = ks ? tid >> 4 : tw;
+    const int n = (cg * tiles + tile) * 16 + (tid & 15);
+    if ((ks ? tid < tiles * 16 : lane < 16) && n < a.N) {
       float s = 0.0f;
-      for (int w = 0; w < wk; ++w) s += red[(tile * wk + w) * 16 + (tid & 15)];
-      put(a, 0, n, s * inv);
+      for (int w = 0; w < wk; ++w) s += red[((tile << ks) + w) * 16 + (tid & 15)];
+      put<DT>(a, 0, n, s * inv);
     }
-    acc[0] = 0.0f;
-    ci = 0;
-    cg += gridDim.x;
-  };
-  for (int64_t s = 0;; s += 2) {
-    compute(u0);
-    if (s + 1 >= steps) break;
-    load(u0);
-    compute(u1);
-    if (s + 2 >= steps) break;
-    load(u1);
   }
 }
 
 // ---------------------------------------------------------------------------
 // 2 .. 16 tokens
 // ---------------------------------------------------------------------------
-// Workgroup (rows, range): kQWaves * RT tiles of 16 rows, a range of column
+// Workgroup (rows, range): kQWaves / WK tiles of 16 rows, a range of column
 // slices of kQSlice chunks.  For each slice the workgroup makes the tokens'
 // terms in LDS, under a power of two per token and slice; its waves then walk
-// the slice's codes, each unit's next slice loaded as soon as it is used.
+// the slice's codes (WK waves share a tile's chunks), the next slice's loaded
+// as soon as these are used.  Small matrices take a large WK: more workgroups,
+// each with less to do after its loads have arrived.
 constexpr int kQSlice = 8;
 constexpr int kQSliceCols = kQSlice * kQChunk;
 
-template <int DT, int TOK, bool TR, int SS>
+template <int DT, int TOK, int WK, bool TR, int SS>
 __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
   constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
   constexpr int NR = TOK / 4;
   constexpr int NB = TOK * kQSliceCols / 8 / kQWG;        // blocks of x per thread
   constexpr int kBlocks = kQSliceCols / 8;
   constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
+  constexpr int NU = kQSlice / WK, NQ = NU > 4 ? 4 : NU, QN = NU / NQ;   // a wave's chunks, as quads
   extern __shared__ __align__(16) uint8_t s_x[];          // [P][blocks][TOK] of 16 bytes
   __shared__ uint32_t s_max[kQWaves][TOK];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int row = lane & 15, quarter = lane >> 4;
-  const int n0 = (blockIdx.x * kQWaves + wave) * 16;
+  const int kw = wave % WK;
+  const int n0 = (blockIdx.x * (kQWaves / WK) + wave / WK) * 16;
   const int s0 = blockIdx.y * a.per_split;
   const int nsl = (a.nch + kQSlice - 1) / kQSlice;
   const int s1 = s0 + a.per_split < nsl ? s0 + a.per_split : nsl;
@@ -599,24 +652,30 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
 
   Raw<DT> raw[NB];
   auto load_x = [&](int s) {
+    const uint32_t xrow = (uint32_t)(t * (int)a.x_pitch * B);
+    const int k = s * kQSliceCols + 8 * (tid / TOK);
+    if (a.x_vec) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-      load8<DT>(a, xv, (uint32_t)(t * (int)a.x_pitch * B), s * kQSliceCols + 8 * (tid / TOK + kQWG / TOK * i),
-                t < a.C && s < s1, raw[i]);
+      for (int i = 0; i < NB; ++i) load8v<DT>(a, xv, xrow, k + 8 * (kQWG / TOK) * i, t < a.C && s < s1, raw[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) load8e<DT>(a, xv, xrow, k + 8 * (kQWG / TOK) * i, t < a.C && s < s1, raw[i]);
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
   const Magic mg = magic();
-  Unit u[kQSlice];
+  Quad<NQ, TR> u[QN];
+  auto load = [&](int s, int k) {
+    load_quad<NQ, TR, SS>(a, v, s * kQSlice + kw + WK * NQ * k, WK, quarter, s < s1, u[k]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
   load_x(s0);
 #pragma unroll
-  for (int i = 0; i < kQSlice; ++i) {
-    const int c = s0 * kQSlice + i;
-    load_unit<TR, SS>(a, v, 0, c, quarter, c < a.nch, u[i]);
-  }
-  __builtin_amdgcn_sched_barrier(0);
+  for (int k = 0; k < QN; ++k) load(s0, k);
 
   // the token of operand row `row`; rows beyond TOK tokens repeat one
-  const uint8_t* frag0 = s_x + 16 * (TOK == 4 ? row >> 2 : TOK == 8 ? (row >> 2) + 4 * (row & 1) : row_token(row));
+  const uint8_t* frag0 = s_x + 16 * (TOK == 8 ? (row >> 2) + 4 * (row & 1) : row_token(row)) +
+                         16 * TOK * (TR ? 1 : 4) * quarter;
   float sum[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) sum[r] = 0.0f;
@@ -661,31 +720,51 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
       *reinterpret_cast<half8*>(o) = hi;
       if (P == 2) *reinterpret_cast<half8*>(o + 16 * kBlocks * TOK) = lo;
     }
-    load_x(s + 1);
+    if (s + 1 < s1) load_x(s + 1);
     __syncthreads();
     float acc[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[r] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kQSlice; ++i) {
-      if (s * kQSlice + i < a.nch)
-        multiply<P, NR, TR, SS>(a, mg, u[i], [&](int p, int j) {
-          return *reinterpret_cast<const half8*>(
-              frag0 + 16 * TOK * (p * kBlocks + i * (kQChunk / 8) + block_of<TR>(j, quarter)));
+    for (int k = 0; k < QN; ++k) {
+      uint32_t sc[4], zp[4];
+      quad_scales<NQ, TR, SS>(a, u[k], sc, zp);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int c = kw + WK * (NQ * k + i);             // in the slice
+        if (s * kQSlice + c >= a.nch) continue;
+        const uint8_t* xc = frag0 + c * (16 * TOK * (kQChunk / 8));
+        multiply<P, NR, TR>(mg, u[k].q[i], sc[i], zp[i], [&](int p, int j) {
+          return *reinterpret_cast<const half8*>(xc + 16 * TOK * (p * kBlocks + (TR ? 4 : 1) * j));
         }, acc);
-      const int c = (s + 1) * kQSlice + i;
-      load_unit<TR, SS>(a, v, 0, c, quarter, s + 1 < s1 && c < a.nch, u[i]);
+      }
+      load(s + 1, k);
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) sum[r] += inv[r] * acc[r];
   }
-  const int n = n0 + row;
+  auto out = [&](int tok, int n, float val) {
+    if (tok >= a.C || n >= a.N) return;
+    if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.C + tok) * a.N + n] = val;
+    else put<DT>(a, tok, n, val);
+  };
+  if (WK == 1) {
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int tok = 4 * r + quarter;
-    if (tok >= a.C || n >= a.N) continue;
-    if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.C + tok) * a.N + n] = sum[r];
-    else put(a, tok, n, sum[r]);
+    for (int r = 0; r < NR; ++r) out(4 * r + quarter, n0 + row, sum[r]);
+  } else {
+    // the waves that shared a tile's chunks add up, in order
+    float* red = reinterpret_cast<float*>(s_x);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) red[(wave * NR + r) * 64 + lane] = sum[r];
+    __syncthreads();
+    for (int i = tid; i < kQWaves / WK * NR * 64; i += kQWG) {
+      const int l = i & 63, r = (i >> 6) % NR, tile = (i >> 6) / NR;
+      float val = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) val += red[((tile * WK + w) * NR + r) * 64 + l];
+      out(4 * r + (l >> 4), (blockIdx.x * (kQWaves / WK) + tile) * 16 + (l & 15), val);
+    }
   }
 }
 
@@ -1023,6 +1102,7 @@ struct QPlan {
   int P, nch, ct;                      // terms, chunks, token tiles
   int path;
   bool wide;                           // the larger matrix tile
+  int wk;                              // few tokens: waves to a row tile
   int row_groups, tok_groups, splits, per_split;
   size_t inv, terms, part, total;
 };
@@ -1038,8 +1118,13 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
   p.path = C == 1 && (int64_t)p.nch * kQChunk * 2 * p.P <= kQStageBytes ? kOne
            : C <= MOE_MAX_DECODE_TOKENS ? kFew : kMany;
   if (p.path == kFew) {
-    p.row_groups = (m->rows + 16 * kQWaves - 1) / (16 * kQWaves);
+    // the fewest waves to a row tile that give every CU a workgroup
     const int nsl = (p.nch + kQSlice - 1) / kQSlice;
+    for (p.wk = 1;; p.wk = p.wk == 1 ? 2 : 8) {
+      const int rows = 16 * kQWaves / p.wk;
+      p.row_groups = (m->rows + rows - 1) / rows;
+      if (p.wk == 8 || (int64_t)p.row_groups * nsl >= 256) break;
+    }
     int s = 512 / p.row_groups;
     s = s < 1 ? 1 : s > nsl ? nsl : s;
     p.per_split = (nsl + s - 1) / s;
@@ -1079,20 +1164,26 @@ void launch_one(const QArgs& a, bool tr, int ss, int grid, size_t lds, hipStream
   }
 }
 
-template <int DT, int TOK, bool TR, int SS>
+template <int DT, int TOK, int WK, bool TR, int SS>
 moe_status launch_few_t(const QArgs& a, dim3 grid, hipStream_t st) {
   constexpr int lds = (DT == MOE_DT_F32 ? 2 : 1) * 2 * kQSliceCols * TOK;
-  auto k = k_qfew<DT, TOK, TR, SS>;
+  auto k = k_qfew<DT, TOK, WK, TR, SS>;
   if (lds + 1024 > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return MOE_ERR_DEVICE;
   hipLaunchKernelGGL(k, grid, dim3(kQWG), lds, st, a);
   return MOE_OK;
 }
+template <int DT, int TOK, int WK>
+moe_status launch_few_w(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st) {
+  if (tr) return ss == 4 ? launch_few_t<DT, TOK, WK, true, 4>(a, grid, st) : launch_few_t<DT, TOK, WK, true, 2>(a, grid, st);
+  return ss == 4 ? launch_few_t<DT, TOK, WK, false, 4>(a, grid, st) : launch_few_t<DT, TOK, WK, false, 2>(a, grid, st);
+}
 template <int DT, int TOK>
-moe_status launch_few(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st) {
-  if (tr) return ss == 4 ? launch_few_t<DT, TOK, true, 4>(a, grid, st) : launch_few_t<DT, TOK, true, 2>(a, grid, st);
-  return ss == 4 ? launch_few_t<DT, TOK, false, 4>(a, grid, st) : launch_few_t<DT, TOK, false, 2>(a, grid, st);
+moe_status launch_few(const QArgs& a, bool tr, int ss, int wk, dim3 grid, hipStream_t st) {
+  if (wk == 1) return launch_few_w<DT, TOK, 1>(a, tr, ss, grid, st);
+  if (wk == 2) return launch_few_w<DT, TOK, 2>(a, tr, ss, grid, st);
+  return launch_few_w<DT, TOK, 8>(a, tr, ss, grid, st);
 }
 
 template <int P, int WT, int TW, int RT, bool TR, int SS>
@@ -1117,19 +1208,21 @@ moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st
   constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
   moe_status s = MOE_OK;
   if (p.path == kOne) {
-    // waves that split the columns of a tile: as many as it takes to give
-    // every CU's eight waves work, then tiles walked by a resident grid
+    // waves to a row tile: as many as it takes to give every CU's eight
+    // waves work; tiles walked by a resident grid
     const int nt = (a.N + 15) / 16;
-    a.wk = 8;
-    while (a.wk > 1 && (int64_t)nt * (a.wk / 2) >= 2048) a.wk /= 2;
-    const int groups = (nt + kQWaves / a.wk - 1) / (kQWaves / a.wk);
-    launch_one<DT>(a, tr, ss, groups < 512 ? groups : 512, (size_t)p.nch * kQChunk * 2 * P, st);
+    a.ks = 3;
+    while (a.ks > 0 && ((int64_t)nt << (a.ks - 1)) >= 2048) --a.ks;
+    a.row_groups = (nt + (kQWaves >> a.ks) - 1) / (kQWaves >> a.ks);
+    a.spt = (((a.nch + (1 << a.ks) - 1) >> a.ks) + 7) / 8;
+    launch_one<DT>(a, tr, ss, a.row_groups < 512 ? a.row_groups : 512, (size_t)p.nch * kQChunk * 2 * P, st);
   } else if (p.path == kFew) {
     const dim3 grid((unsigned)p.row_groups, (unsigned)p.splits);
-    s = a.C <= 4 ? launch_few<DT, 4>(a, tr, ss, grid, st) : a.C <= 8 ? launch_few<DT, 8>(a, tr, ss, grid, st)
-                                                                     : launch_few<DT, 16>(a, tr, ss, grid, st);
+    s = a.C <= 8 ? launch_few<DT, 8>(a, tr, ss, p.wk, grid, st) : launch_few<DT, 16>(a, tr, ss, p.wk, grid, st);
   } else {
-    hipLaunchKernelGGL((k_qterms<DT>), dim3(a.C), dim3(kTermWG), 0, st, a);
+    const dim3 tgrid((unsigned)p.ct * 4);
+    if (p.nch <= 4 * kTermBlocks * 8 / kQChunk) hipLaunchKernelGGL((k_qterms<DT, true>), tgrid, dim3(kTermWG), 0, st, a);
+    else hipLaunchKernelGGL((k_qterms<DT, false>), tgrid, dim3(kTermWG), 0, st, a);
     a.row_groups = p.row_groups;
     const dim3 grid((unsigned)(p.row_groups * p.tok_groups), (unsigned)p.splits);
     s = !p.wide ? launch_gemm<P, 2, 1, 1>(a, tr, ss, grid, st)

@@ -96,6 +96,23 @@ CASES = [
     (129, 300, 640, 384, "bf16", "f16", True),
     (300, 129, 4096, 64, "f32", "f32", True),
     (4096, 40, 256, 32, "bf16", "bf16", False),
+    # wider than a token's terms keep in registers or in LDS
+    (20, 48, 8200, 32, "f32", "f32", True),
+    (18, 33, 9001, 128, "bf16", "bf16", True),
+    (1, 20, 12289, 128, "f32", "bf16", True),
+    (1, 20, 24577, 64, "f16", "f16", False),
+    # waves that share a row tile: none, two, eight; several slices to a workgroup
+    (6, 4096, 8192, 128, "bf16", "bf16", False),
+    (12, 4000, 4096, 64, "f32", "bf16", True),
+    (3, 33000, 2100, 256, "f32", "f16", True),
+    # one token: eight, four, two and one wave to a row tile
+    (1, 5000, 640, 128, "bf16", "f32", True),
+    (1, 9000, 700, 64, "f32", "f16", False),
+    (1, 17000, 300, 32, "f16", "bf16", True),
+    (1, 40000, 260, 128, "f32", "bf16", True),
+    # the larger matrix tile
+    (300, 16384, 272, 32, "f32", "bf16", True),
+    (520, 8200, 300, 128, "bf16", "f32", True),
 ]
 
 
