@@ -331,10 +331,10 @@ moe_status moe_quant_linear(const moe_quant_matrix *m, int32_t dtype, const void
  *             device array of S + 1 int32, non-decreasing, in [0, C]: sequence
  *             s is the tokens seq_off[s] .. seq_off[s+1] - 1, and may be
  *             empty.  Tokens outside every sequence take no part: their rows
- *             of logits are not read and their rows of dlogits are left as
+ *             of logits have no effect and their rows of dlogits are left as
  *             they were.  1 <= S <= MOE_MAX_SEQUENCES.
  *  token_mask NULL, or [C] bytes: a token whose byte is 0 is padding.  Its
- *             logits and selection are not read, it counts nowhere, and its
+ *             logits and selection have no effect, it counts nowhere, and its
  *             row of dlogits is written as zeros (left alone where the call
  *             accumulates).
  *  score      how a token's logits become its shares p over the experts:

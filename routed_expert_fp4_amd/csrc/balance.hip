@@ -23,13 +23,13 @@
 //                 loss from the last workgroup to arrive
 //   k_bal_bwd     a few consecutive tokens per wave
 //   k_count_fill / k_count   counts without logits
-//   k_route_bwd   one wave per token
+//   k_route_bwd   two, four or eight tokens per wave
 #include "common.h"
 
 namespace rf4 {
 namespace {
 
-constexpr int kPartWG = 512;          // eight waves share a slot's tokens
+constexpr int kPartWG = 512;          // up to eight waves share a slot's tokens
 constexpr int kPartWaves = kPartWG / 64;
 constexpr int kBalWG = 256;           // backward kernels: four waves
 constexpr int kBalWaves = kBalWG / 64;
@@ -110,6 +110,7 @@ struct BalArgs {
   int per;             // tokens per wave
   int shift;           // slot_shift
   bool one;            // one slot holds the batch
+  bool vec_counts;     // and rows of counts
   bool vec;            // rows of logits (and dlogits) are 16-byte aligned
 };
 
@@ -225,16 +226,14 @@ __device__ __forceinline__ float scores(float (&v)[4 * NJ], float (&neg)[4 * NJ]
   return row_sum(z);
 }
 
-// The loss from the workgroups' sums of f . P, in order (a block of n threads).
-template <int WG>
-__device__ __forceinline__ float block_sum(float d, float* s_p) {
+// The sum over a workgroup, its waves' sums in order.
+__device__ __forceinline__ float block_sum(float d, float* s_p, int waves) {
   const int tid = threadIdx.x;
   d = row_sum(d);
   if ((tid & 63) == 0) s_p[tid >> 6] = d;
   __syncthreads();
   float v = 0.0f;
-#pragma unroll
-  for (int w = 0; w < WG / 64; ++w) v += s_p[w];
+  for (int w = 0; w < waves; ++w) v += s_p[w];
   return v;
 }
 
@@ -245,6 +244,7 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
   __shared__ float s_p[kPartWaves];
   __shared__ int s_tok;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int threads = blockDim.x, waves = threads >> 6;
   const int E = a.E, slot = blockIdx.x, sh = a.shift;
   // the sequence whose slots this one is among: largest s with
   // (off[s] >> sh) + s <= slot
@@ -259,22 +259,34 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
   if (first < 0 || t0 >= end) return;
   const int n = end - t0 < (1 << sh) ? (int)(end - t0) : (1 << sh);
 
-  for (int e = tid; e < 256 * NJ; e += kPartWG) s_cnt[e] = 0u;
+  for (int e = tid; e < 256 * NJ; e += threads) s_cnt[e] = 0u;
   if (tid == 0) s_tok = 0;
   // sums of shares: each wave its tokens in order, then the waves in order
   float acc[4 * NJ];
 #pragma unroll
   for (int i = 0; i < 4 * NJ; ++i) acc[i] = 0.0f;
   int live = 0;
-  for (int t = wave; t < n; t += kPartWaves) {
-    if (a.mask && !a.mask[t0 + t]) continue;
-    ++live;
-    float v[4 * NJ], neg[4 * NJ];
-    load_row<NJ>(a.logits + (t0 + t) * E, E, a.vec, -INFINITY, v);
-    const float z = scores<NJ, SIG>(v, neg);
-    const float iz = z == 0.0f ? 0.0f : 1.0f / z;
+  // 64 of the wave's tokens at a time: which are live, in one load of the
+  // mask; a token's row is loaded while the one before it is worked on
+  for (int base = wave; base < n; base += 64 * waves) {
+    const int mine = base + waves * lane;
+    uint64_t left = __ballot(mine < n && (!a.mask || a.mask[t0 + mine] != 0));
+    live += __popcll(left);
+    if (!left) continue;
+    float v[4 * NJ], neg[4 * NJ], next[4 * NJ];
+    load_row<NJ>(a.logits + (t0 + base + waves * (__ffsll((long long)left) - 1)) * E, E, a.vec, -INFINITY, next);
+    while (left) {
+      left &= left - 1;
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) acc[i] = fmaf(v[i], iz, acc[i]);
+      for (int i = 0; i < 4 * NJ; ++i) v[i] = next[i];
+      if (left)
+        load_row<NJ>(a.logits + (t0 + base + waves * (__ffsll((long long)left) - 1)) * E, E, a.vec, -INFINITY,
+                     next);
+      const float z = scores<NJ, SIG>(v, neg);
+      const float iz = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) acc[i] = fmaf(v[i], iz, acc[i]);
+    }
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
@@ -283,7 +295,7 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
   __syncthreads();
   if (lane == 0 && live) atomicAdd(&s_tok, live);
   // counts (integers: any order gives the same)
-  for (int i = tid; i < n * a.k; i += kPartWG) {
+  for (int i = tid; i < n * a.k; i += threads) {
     if (a.mask && !a.mask[t0 + i / a.k]) continue;
     const int e = a.idx[t0 * a.k + i];
     if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1u);
@@ -292,10 +304,9 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
   const int tok = s_tok;
   const float it = tok > 0 ? 1.0f / (float)tok : 0.0f;
   float d = 0.0f;
-  for (int e = tid; e < E; e += kPartWG) {
+  for (int e = tid; e < E; e += threads) {
     float p = s_sum[0][e];
-#pragma unroll
-    for (int w = 1; w < kPartWaves; ++w) p += s_sum[w][e];
+    for (int w = 1; w < waves; ++w) p += s_sum[w][e];
     const int c = (int)s_cnt[e];
     if (a.one) {
       const float P = p * it;
@@ -311,7 +322,7 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
     if (tid == 0) a.ptok[slot] = tok;
     return;
   }
-  d = block_sum<kPartWG>(d, s_p);
+  d = block_sum(d, s_p, waves);
   if (tid == 0) {
     a.tokens[0] = tok;
     a.loss[0] = a.alpha * d;
@@ -361,6 +372,7 @@ __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
   s_p[tid] = p; s_c[tid] = c; s_t[tid] = t;
   __syncthreads();
   if (row == 0) {
+#pragma unroll
     for (int r = 1; r < kFinRows; ++r) {
       p += s_p[64 * r + le];
       c += s_c[64 * r + le];
@@ -385,7 +397,7 @@ __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
   const __amdgpu_buffer_rsrc_t v = coherent_view(a.dots, nb * 4u);
   float d = 0.0f;
   for (uint32_t i = tid; i < nb; i += kFinWG) d += coherent_ld(v, 4u * i);
-  d = block_sum<kFinWG>(d, s_p);
+  d = block_sum(d, s_p, kFinRows);
   if (tid == 0) a.loss[0] = a.alpha / (float)a.S * d;
 }
 
@@ -402,6 +414,7 @@ __global__ __launch_bounds__(kBalWG) void k_bal_bwd(BalArgs a) {
   for (int i = 0; i < 4 * NJ; ++i) g[i] = 0.0f;
   for (int64_t t = base; t < base + a.per && t < a.C; ++t) {
     float v[4 * NJ], neg[4 * NJ];
+    load_row<NJ>(a.logits + t * E, E, a.vec, -INFINITY, v);     // in flight while g is formed
     const bool live = !a.mask || a.mask[t] != 0;
     if (t >= end) {
       const int s = seq_of(a.off, (int)t, a.S, a.C);
@@ -411,18 +424,15 @@ __global__ __launch_bounds__(kBalWG) void k_bal_bwd(BalArgs a) {
       const int n = a.tokens[s];
       const float it = n > 0 ? 1.0f / (float)n : 0.0f;
       const float w = a.grad[0] * (a.alpha / (float)a.S) * it * it * ((float)E / (float)a.k);
+      load_row<NJ>(reinterpret_cast<const float*>(a.counts) + (size_t)s * E, E, a.vec_counts, 0.0f, g);
 #pragma unroll
-      for (int i = 0; i < 4 * NJ; ++i) {
-        const int e = 4 * (lane + 64 * (i >> 2)) + (i & 3);
-        g[i] = e < E ? w * (float)a.counts[(size_t)s * E + e] : 0.0f;
-      }
+      for (int i = 0; i < 4 * NJ; ++i) g[i] = w * (float)__float_as_int(g[i]);      // 0.0f is the integer 0
     }
     if (!live) {
       if (a.accumulate) continue;
 #pragma unroll
       for (int i = 0; i < 4 * NJ; ++i) v[i] = 0.0f;
     } else {
-      load_row<NJ>(a.logits + t * E, E, a.vec, -INFINITY, v);
       const float z = scores<NJ, SIG>(v, neg);
       const float iz = z == 0.0f ? 0.0f : 1.0f / z;
       float dot = 0.0f;
@@ -482,9 +492,9 @@ __global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int3
                                                   int32_t* tokens, int accumulate) {
   __shared__ int32_t s_cnt[MOE_MAX_EXPERTS];
   __shared__ int32_t s_tok;
-  const int tid = threadIdx.x, s = blockIdx.y, parts = gridDim.x;
+  const int tid = threadIdx.x, threads = blockDim.x, s = blockIdx.y, parts = gridDim.x;
   const int b = seq_at(off, s, S, C), end = seq_at(off, s + 1, S, C);
-  for (int e = tid; e < E; e += kCntWG) s_cnt[e] = 0;
+  for (int e = tid; e < E; e += threads) s_cnt[e] = 0;
   if (tid == 0) s_tok = 0;
   const int len = end > b ? end - b : 0;
   const int per = (len + parts - 1) / parts;
@@ -494,11 +504,11 @@ __global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int3
   const int32_t* at = idx + (int64_t)t0 * k;
   __syncthreads();
   // four choices a thread in flight
-  for (int i0 = tid; i0 < n; i0 += 4 * kCntWG) {
+  for (int i0 = tid; i0 < n; i0 += 4 * threads) {
     int e[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * kCntWG;
+      const int i = i0 + j * threads;
       e[j] = i < n ? at[i] : -1;
       if (mask && i < n && !mask[t0 + (int)(k == 1 ? (uint32_t)i : __umulhi((uint32_t)i, kmul))]) e[j] = -1;
     }
@@ -508,12 +518,12 @@ __global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int3
   }
   if (tokens) {
     int live = 0;
-    for (int t = t0 + tid; t < t1; t += kCntWG) live += mask ? mask[t] != 0 : 1;
+    for (int t = t0 + tid; t < t1; t += threads) live += mask ? mask[t] != 0 : 1;
     if (live) atomicAdd(&s_tok, live);
   }
   __syncthreads();
   int32_t* row = counts + (size_t)s * E;
-  for (int e = tid; e < E; e += kCntWG) {
+  for (int e = tid; e < E; e += threads) {
     if (parts > 1) { if (s_cnt[e]) atomicAdd(&row[e], s_cnt[e]); }
     else row[e] = accumulate ? row[e] + s_cnt[e] : s_cnt[e];
   }
@@ -526,63 +536,88 @@ __global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int3
 // ---------------------------------------------------------------------------
 // Gradient of the routing weights
 // ---------------------------------------------------------------------------
+// Sum and maximum over the KP lanes of a group, in every lane of it: DPP
+// permutes inside 4, 8 and 16 lanes, one LDS permute across 16.
+template <int KP, class F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+  v = f(v, dpp<0xB1, 0xF>(0.0f, v));         // lanes 1 0 3 2
+  v = f(v, dpp<0x4E, 0xF>(0.0f, v));         // lanes 2 3 0 1
+  v = f(v, dpp<0x141, 0xF>(0.0f, v));        // mirrored in 8
+  if (KP >= 16) v = f(v, dpp<0x140, 0xF>(0.0f, v));   // mirrored in 16
+  if (KP >= 32) v = f(v, __shfl_xor(v, 16, 64));
+  return v;
+}
+
+// KP lanes (k rounded up to 8, 16 or 32) per token, so that a wave has 64 / KP
+// tokens' loads and sums in flight together; then their rows, one after the
+// other through a row of zeros in LDS that each token's values are put into
+// and taken out of again.  Bound by writing the rows.
+template <int KP>
 __global__ __launch_bounds__(kBalWG) void k_route_bwd(const float* logits, const int32_t* idx,
                                                       const float* dw, int C, int k, int E,
                                                       const uint8_t* mask, float* dlogits, int accumulate,
                                                       bool vec) {
+  constexpr int TPW = 64 / KP;
   __shared__ __align__(16) float s_row[kBalWaves][MOE_MAX_EXPERTS];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * kBalWaves + wave;
-  if (t >= C) return;                       // whole waves: no barrier below
-  const bool live = !mask || mask[t] != 0;
-  if (!live && accumulate) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, slot = lane % KP;
+  const int64_t t0 = ((int64_t)blockIdx.x * kBalWaves + wave) * TPW, t = t0 + lane / KP;
+  if (t0 >= C) return;                      // whole waves: no barrier below
   float* srow = s_row[wave];
   if (!accumulate) {
     for (int i = 4 * lane; i < E; i += 256) *reinterpret_cast<float4*>(srow + i) = make_float4(0, 0, 0, 0);
-    wave_lds_fence();
   }
   int e = -1;
   float l = -INFINITY, d = 0.0f;
-  if (live && lane < k) {
-    e = idx[t * k + lane];
+  if (t < C && slot < k && (!mask || mask[t] != 0)) {
+    e = idx[t * k + slot];
     if (e < 0 || e >= E) e = -1;
     if (e >= 0) {
       l = logits[t * E + e];
-      d = dw[t * k + lane];
+      d = dw[t * k + slot];
     }
   }
+  auto add = [](float x, float y) { return x + y; };
+  auto larger = [](float x, float y) { return fmaxf(x, y); };
   float sg, neg;
   sigmoids(l, sg, neg);
-  const float m = row_max(l);
+  const float m = group_reduce<KP>(l, larger);
   if (m < -40.0f) sg = l == -INFINITY ? 0.0f : exp_neg(l - m) * neg;       // the sigmoids underflow
   if (e < 0) sg = 0.0f;
-  const float z = row_sum(sg);
+  const float z = group_reduce<KP>(sg, add);
   const float w = z == 0.0f ? 0.0f : sg / z;
-  const float dot = row_sum(e >= 0 ? w * d : 0.0f);
+  const float dot = group_reduce<KP>(e >= 0 ? w * d : 0.0f, add);
   const float dl = e >= 0 ? w * neg * (d - dot) : 0.0f;
   // slots that name one expert: the first adds them up, in slot order
   float mine = 0.0f;
-  bool firsts = e >= 0;
+  bool first = e >= 0;
   for (int s = 0; s < k; ++s) {
-    const int es = __builtin_amdgcn_readlane(e, s);
-    const float ds = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(dl), s));
+    const int es = __shfl(e, s, KP);
+    const float ds = __shfl(dl, s, KP);
     if (es == e) {
-      if (s < lane) firsts = false;
+      if (s < slot) first = false;
       mine += ds;
     }
   }
   if (accumulate) {
-    if (firsts && lane < k) dlogits[t * E + e] += mine;
+    if (first) dlogits[t * E + e] += mine;
     return;
   }
-  if (firsts && lane < k) srow[e] = mine;
   wave_lds_fence();
-  float* out = dlogits + t * E;
-  if (vec) {
-    for (int i = 4 * lane; i < E; i += 256)
-      *reinterpret_cast<float4*>(out + i) = *reinterpret_cast<const float4*>(srow + i);
-  } else {
-    for (int i = lane; i < E; i += 64) out[i] = srow[i];
+#pragma unroll
+  for (int i = 0; i < TPW; ++i) {
+    if (t0 + i >= C) return;
+    const bool here = first && lane / KP == i;
+    if (here) srow[e] = mine;
+    wave_lds_fence();
+    float* out = dlogits + (t0 + i) * E;
+    if (vec) {
+      for (int c = 4 * lane; c < E; c += 256)
+        *reinterpret_cast<float4*>(out + c) = *reinterpret_cast<const float4*>(srow + c);
+    } else {
+      for (int c = lane; c < E; c += 64) out[c] = srow[c];
+    }
+    wave_lds_fence();
+    if (here) srow[e] = 0.0f;
   }
 }
 
@@ -627,15 +662,16 @@ moe_status moe_expert_counts(const int32_t* topk_idx, int32_t C, int32_t k, int3
   if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
   if (!seq_ok(seq_off, S)) return MOE_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  // one part per sequence (no zero fill, no atomics in memory) up to 32768
-  // choices of an average one; longer ones are shared out
-  int64_t parts = (int64_t)C * k / S <= 32768 ? 1 : ((int64_t)C * k / S + 8191) / 8192;
+  // one part per sequence (no zero fill, no atomics in memory) up to 4096
+  // choices of an average one; longer ones are shared out, however uneven they
+  // are
+  int64_t parts = (int64_t)C * k / S <= 4096 ? 1 : ((int64_t)C * k / S + 2047) / 2048;
   if (parts > 256) parts = 256;
   if (parts > 1 && !accumulate) {
     const int64_t n = (int64_t)S * E;
     hipLaunchKernelGGL(k_count_fill, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, counts, tokens, n, S);
   }
-  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3(kCntWG), 0, st, topk_idx, seq_off, token_mask,
+  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3((int64_t)C * k / S <= 1024 ? 256 : kCntWG), 0, st, topk_idx, seq_off, token_mask,
                      C, k, k == 1 ? 0u : (uint32_t)((1ull << 32) / (unsigned)k) + 1u, E, S, counts, tokens,
                      accumulate);
   return launched();
@@ -675,7 +711,10 @@ moe_status moe_balance_fwd(const float* logits, const int32_t* topk_idx, int32_t
   a.shift = slot_shift(C, S);
   a.one = S == 1 && C <= kOneSlot && !seq_off;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  RF4_BY_ROW(k_bal_part, E, score == MOE_SCORE_SIGMOID, dim3(a.one ? 1 : num_slots(C, S)), kPartWG, st, a);
+  // eight waves to a slot while that leaves room for every slot at once; then
+  // four (65536 tokens, 1061 slots: the last ones would wait for a second round)
+  const int slots = a.one ? 1 : num_slots(C, S);
+  RF4_BY_ROW(k_bal_part, E, score == MOE_SCORE_SIGMOID, dim3(slots), slots <= 768 ? kPartWG : kPartWG / 2, st, a);
   if (!a.one) hipLaunchKernelGGL(k_bal_final, dim3(expert_blocks(E), S), dim3(kFinWG), 0, st, a);
   return launched();
 }
@@ -696,6 +735,7 @@ moe_status moe_balance_bwd(const float* logits, const int32_t* counts, const int
   a.logits = logits; a.off = seq_off; a.mask = token_mask;
   a.C = C; a.k = k; a.E = E; a.S = S; a.alpha = alpha;
   a.vec = E % 4 == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)dlogits % 16 == 0;
+  a.vec_counts = E % 4 == 0 && (uintptr_t)counts % 16 == 0;
   a.counts = const_cast<int32_t*>(counts); a.tokens = const_cast<int32_t*>(tokens);
   a.grad = grad_loss; a.dlogits = dlogits; a.accumulate = accumulate;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -714,9 +754,12 @@ moe_status moe_route_bwd(const float* logits, const int32_t* topk_idx, const flo
     return MOE_ERR_INVALID_ARG;
   if (!batch_ok(C, k, E)) return MOE_ERR_UNSUPPORTED;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(k_route_bwd, dim3((C + kBalWaves - 1) / kBalWaves), dim3(kBalWG), 0, st, logits,
-                     topk_idx, topk_dw, C, k, E, token_mask, dlogits, accumulate,
-                     E % 4 == 0 && (uintptr_t)dlogits % 16 == 0);
+  const bool vec = E % 4 == 0 && (uintptr_t)dlogits % 16 == 0;
+  const int per = kBalWaves * (k <= 8 ? 8 : k <= 16 ? 4 : 2);
+  const dim3 grid((C + per - 1) / per);
+  if (k <= 8) hipLaunchKernelGGL(k_route_bwd<8>, grid, dim3(kBalWG), 0, st, logits, topk_idx, topk_dw, C, k, E, token_mask, dlogits, accumulate, vec);
+  else if (k <= 16) hipLaunchKernelGGL(k_route_bwd<16>, grid, dim3(kBalWG), 0, st, logits, topk_idx, topk_dw, C, k, E, token_mask, dlogits, accumulate, vec);
+  else hipLaunchKernelGGL(k_route_bwd<32>, grid, dim3(kBalWG), 0, st, logits, topk_idx, topk_dw, C, k, E, token_mask, dlogits, accumulate, vec);
   return launched();
 }
 
