@@ -407,7 +407,8 @@ def _launch(fn, dev, stream, *args):
     one), whichever GPU is current."""
     import torch
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of a Stream object's time
+        handle = raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
     elif stream.device.index != dev:
         raise ValueError(f"the stream must be of cuda:{dev}, got {stream.device}")
     else:

@@ -15,6 +15,10 @@
 // exponential and one reciprocal (hardware, 1 unit each), so that arithmetic
 // stays below the memory time.
 //
+// A slot or part has at most 2^20 tokens of k <= 32 choices: i / k of its i-th
+// choice is the high word of i * kmul, kmul = 2^32 / k + 1, whose error
+// i / 2^32 stays under 1 / k.
+//
 // Kernels:
 //   k_bal_part    a slot of up to TB tokens of one sequence: the slot's sums
 //                 of shares, its counts and its number of tokens; a small
@@ -42,16 +46,31 @@ __device__ __forceinline__ int seq_at(const int32_t* off, int i, int S, int C) {
   return v < 0 ? 0 : v > C ? C : v;
 }
 
+// The largest i in [0, n) whose key is at most x, keys rising and key(0) <= x:
+// 64 candidates a step, one per lane, since a binary search waits for memory
+// once per halving (65535 sequences take three steps).  Whatever the keys are,
+// the result lies in [0, n).
+template <class K>
+__device__ __forceinline__ int wave_search(int n, int x, K key) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int64_t i = (int64_t)lane * step;
+    const int c = __popcll(__ballot(i < n && key(lo + (int)i) <= x));
+    const int k = c > 1 ? (c - 1) * step : 0;
+    lo += k;
+    n = n - k < step ? n - k : step;
+  }
+  return lo;
+}
+
 // The sequence that token t lies in (the last one that starts at or before
 // t, so empty ones are passed over), or -1.
 __device__ __forceinline__ int seq_of(const int32_t* off, int t, int S, int C) {
   if (!off) return 0;
-  int lo = 0, hi = S;                 // largest i in [0, S] with off[i] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (seq_at(off, mid, S, C) <= t) lo = mid; else hi = mid - 1;
-  }
-  return (lo < S && seq_at(off, lo, S, C) <= t) ? lo : -1;
+  const int s = wave_search(S + 1, t, [&](int i) { return seq_at(off, i, S, C); });
+  return s < S && seq_at(off, s, S, C) <= t ? s : -1;
 }
 
 // Tokens per slot: 8 (one a wave) up to 8192 tokens, then as many as keep the
@@ -108,6 +127,7 @@ struct BalArgs {
   float* dlogits;
   int accumulate;
   int per;             // tokens per wave
+  uint32_t kmul;       // see above
   int shift;           // slot_shift
   bool one;            // one slot holds the batch
   bool vec_counts;     // and rows of counts
@@ -215,11 +235,11 @@ __device__ __forceinline__ float scores(float (&v)[4 * NJ], float (&neg)[4 * NJ]
 #pragma unroll
   for (int i = 1; i < 4 * NJ; ++i) m = fmaxf(m, v[i]);
   m = row_max(m);
+  m = m == -INFINITY ? 0.0f : m;            // a row of -inf: every score is e^-inf
   z = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4 * NJ; ++i) {
-    // -inf among finite logits: e^-inf; a row of it: no score at all
-    v[i] = v[i] == -INFINITY ? 0.0f : exp_neg(v[i] - m);
+    v[i] = exp_neg(v[i] - m);
     if (SIG) v[i] *= neg[i];                // 1 / (1 + e^l)
     z += v[i];
   }
@@ -248,11 +268,7 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
   const int E = a.E, slot = blockIdx.x, sh = a.shift;
   // the sequence whose slots this one is among: largest s with
   // (off[s] >> sh) + s <= slot
-  int lo = 0, hi = a.S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((seq_at(a.off, mid, a.S, a.C) >> sh) + mid <= slot) lo = mid; else hi = mid - 1;
-  }
+  const int lo = wave_search(a.S, slot, [&](int i) { return (seq_at(a.off, i, a.S, a.C) >> sh) + i; });
   const int b = seq_at(a.off, lo, a.S, a.C), end = seq_at(a.off, lo + 1, a.S, a.C);
   const int first = slot - ((b >> sh) + lo);
   const int64_t t0 = b + ((int64_t)first << sh);
@@ -261,45 +277,58 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
 
   for (int e = tid; e < 256 * NJ; e += threads) s_cnt[e] = 0u;
   if (tid == 0) s_tok = 0;
+  __syncthreads();
   // sums of shares: each wave its tokens in order, then the waves in order
   float acc[4 * NJ];
 #pragma unroll
   for (int i = 0; i < 4 * NJ; ++i) acc[i] = 0.0f;
   int live = 0;
   // 64 of the wave's tokens at a time: which are live, in one load of the
-  // mask; a token's row is loaded while the one before it is worked on
-  for (int base = wave; base < n; base += 64 * waves) {
+  // mask; two tokens' rows are loaded while the two before are worked on
+  for (int base = wave; base < n || base == wave; base += 64 * waves) {
     const int mine = base + waves * lane;
     uint64_t left = __ballot(mine < n && (!a.mask || a.mask[t0 + mine] != 0));
     live += __popcll(left);
-    if (!left) continue;
-    float v[4 * NJ], neg[4 * NJ], next[4 * NJ];
-    load_row<NJ>(a.logits + (t0 + base + waves * (__ffsll((long long)left) - 1)) * E, E, a.vec, -INFINITY, next);
-    while (left) {
+    const float* row0 = a.logits + (t0 + base) * E;
+    float next[2][4 * NJ];
+    auto take = [&](float (&v)[4 * NJ]) {      // the row of the lowest token left, which leaves
+      if (!left) return;
+      load_row<NJ>(row0 + (int64_t)waves * (__ffsll((long long)left) - 1) * E, E, a.vec, -INFINITY, v);
       left &= left - 1;
+    };
+    int todo = __popcll(left);
+    take(next[0]);
+    take(next[1]);
+    if (base == wave) {
+      // counts, while the first rows are on their way (integers: any order
+      // gives the same)
+      for (int i = tid; i < n * a.k; i += threads) {
+        const int e = a.idx[t0 * a.k + i];
+        const bool on = !a.mask || a.mask[t0 + (a.k == 1 ? i : (int)__umulhi((uint32_t)i, a.kmul))] != 0;
+        if (on && e >= 0 && e < E) atomicAdd(&s_cnt[e], 1u);
+      }
+    }
+    for (; todo > 0; todo -= 2) {
+      float v[2][4 * NJ], neg[4 * NJ];
 #pragma unroll
-      for (int i = 0; i < 4 * NJ; ++i) v[i] = next[i];
-      if (left)
-        load_row<NJ>(a.logits + (t0 + base + waves * (__ffsll((long long)left) - 1)) * E, E, a.vec, -INFINITY,
-                     next);
-      const float z = scores<NJ, SIG>(v, neg);
-      const float iz = z == 0.0f ? 0.0f : 1.0f / z;
+      for (int i = 0; i < 4 * NJ; ++i) { v[0][i] = next[0][i]; v[1][i] = next[1][i]; }
+      take(next[0]);
+      take(next[1]);
 #pragma unroll
-      for (int i = 0; i < 4 * NJ; ++i) acc[i] = fmaf(v[i], iz, acc[i]);
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && todo == 1) break;
+        const float z = scores<NJ, SIG>(v[h], neg);
+        const float iz = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+        for (int i = 0; i < 4 * NJ; ++i) acc[i] = fmaf(v[h][i], iz, acc[i]);
+      }
     }
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
     *reinterpret_cast<float4*>(&s_sum[wave][4 * (lane + 64 * j)]) =
         make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-  __syncthreads();
   if (lane == 0 && live) atomicAdd(&s_tok, live);
-  // counts (integers: any order gives the same)
-  for (int i = tid; i < n * a.k; i += threads) {
-    if (a.mask && !a.mask[t0 + i / a.k]) continue;
-    const int e = a.idx[t0 * a.k + i];
-    if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1u);
-  }
   __syncthreads();
   const int tok = s_tok;
   const float it = tok > 0 ? 1.0f / (float)tok : 0.0f;
@@ -409,13 +438,19 @@ __global__ __launch_bounds__(kBalWG) void k_bal_bwd(BalArgs a) {
   const int E = a.E;
   const int64_t base = ((int64_t)blockIdx.x * kBalWaves + wave) * a.per;
   int end = -1;                              // of the sequence whose g is loaded
-  float g[4 * NJ];
+  float g[4 * NJ], next[4 * NJ];
 #pragma unroll
   for (int i = 0; i < 4 * NJ; ++i) g[i] = 0.0f;
-  for (int64_t t = base; t < base + a.per && t < a.C; ++t) {
+  // which of the tokens are live, in one load of the mask; a live token's row
+  // is loaded while the one before it is worked on
+  const uint64_t live = __ballot(lane < a.per && base + lane < a.C && (!a.mask || a.mask[base + lane] != 0));
+  if (live & 1) load_row<NJ>(a.logits + base * E, E, a.vec, -INFINITY, next);
+  for (int k = 0; k < a.per && base + k < a.C; ++k) {
+    const int64_t t = base + k;
     float v[4 * NJ], neg[4 * NJ];
-    load_row<NJ>(a.logits + t * E, E, a.vec, -INFINITY, v);     // in flight while g is formed
-    const bool live = !a.mask || a.mask[t] != 0;
+#pragma unroll
+    for (int i = 0; i < 4 * NJ; ++i) v[i] = next[i];
+    if (live >> k >> 1 & 1) load_row<NJ>(a.logits + (t + 1) * E, E, a.vec, -INFINITY, next);
     if (t >= end) {
       const int s = seq_of(a.off, (int)t, a.S, a.C);
       const int e1 = s < 0 ? -1 : seq_at(a.off, s + 1, a.S, a.C);
@@ -428,7 +463,7 @@ __global__ __launch_bounds__(kBalWG) void k_bal_bwd(BalArgs a) {
 #pragma unroll
       for (int i = 0; i < 4 * NJ; ++i) g[i] = w * (float)__float_as_int(g[i]);      // 0.0f is the integer 0
     }
-    if (!live) {
+    if (!(live >> k & 1)) {
       if (a.accumulate) continue;
 #pragma unroll
       for (int i = 0; i < 4 * NJ; ++i) v[i] = 0.0f;
@@ -484,8 +519,6 @@ __global__ __launch_bounds__(256) void k_count_fill(int32_t* counts, int32_t* to
 // Workgroup (s, j): the j-th of gridDim.x parts of sequence s.  One part:
 // the row is written (or added to) as a whole; more: the parts' integer
 // counts are added to the row by atomics, whose order does not matter.
-// A part has at most 2^20 tokens: i / k of its i-th choice is the high word
-// of i * (2^32 / k + 1), whose error i / 2^32 stays under 1 / k.
 constexpr int kCntWG = 1024;
 __global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int32_t* off, const uint8_t* mask,
                                                   int C, int k, uint32_t kmul, int E, int S, int32_t* counts,
@@ -621,6 +654,7 @@ __global__ __launch_bounds__(kBalWG) void k_route_bwd(const float* logits, const
   }
 }
 
+uint32_t division(int k) { return k == 1 ? 0u : (uint32_t)((1ull << 32) / (unsigned)k) + 1u; }
 bool batch_ok(int C, int k, int E) {
   return C >= 1 && C <= MOE_MAX_BATCH_TOKENS && E >= 1 && E <= MOE_MAX_EXPERTS && k >= 1 &&
          k <= MOE_MAX_TOPK && k <= E;
@@ -672,7 +706,7 @@ moe_status moe_expert_counts(const int32_t* topk_idx, int32_t C, int32_t k, int3
     hipLaunchKernelGGL(k_count_fill, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, counts, tokens, n, S);
   }
   hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3((int64_t)C * k / S <= 1024 ? 256 : kCntWG), 0, st, topk_idx, seq_off, token_mask,
-                     C, k, k == 1 ? 0u : (uint32_t)((1ull << 32) / (unsigned)k) + 1u, E, S, counts, tokens,
+                     C, k, division(k), E, S, counts, tokens,
                      accumulate);
   return launched();
 }
@@ -709,6 +743,7 @@ moe_status moe_balance_fwd(const float* logits, const int32_t* topk_idx, int32_t
   a.ptok = reinterpret_cast<int32_t*>(w8 + W.ptok);
   a.dots = reinterpret_cast<float*>(w8 + W.dots);
   a.shift = slot_shift(C, S);
+  a.kmul = division(k);
   a.one = S == 1 && C <= kOneSlot && !seq_off;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   // eight waves to a slot while that leaves room for every slot at once; then
