@@ -870,21 +870,23 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
     vrow[i] = (uint32_t)((n < a.N ? n : a.N - 1) - nw) * (uint32_t)a.code_pitch;
   }
   const uint8_t* cbase = a.codes + (int64_t)nw * a.code_pitch;
-  const int64_t plane = (int64_t)ct * a.nch * kQTermBytes;
-  auto stage = [&](int c, int buf) {
+  constexpr int kTermPieces = G::terms / 1024 / kQWaves, kPieces = G::loads;
+  const uint8_t* tbase[kTermPieces];                       // chunk 0's pieces
 #pragma unroll
-    for (int i0 = 0; i0 < G::terms / 1024; i0 += kQWaves) {
-      const int i = i0 + wave;
-      const int p = i / (4 * TM);
-      int t = tg * TM + (i >> 2) % TM;
-      t = t < ct ? t : ct - 1;
-      const uint8_t* src = a.terms + p * plane + ((int64_t)t * a.nch + c) * kQTermBytes + (i & 3) * 1024;
+  for (int k = 0; k < kTermPieces; ++k) {
+    const int i = k * kQWaves + wave;
+    int t = tg * TM + (i >> 2) % TM;
+    t = t < ct ? t : ct - 1;
+    tbase[k] = a.terms + ((int64_t)(i / (4 * TM) * ct + t) * a.nch) * kQTermBytes + (i & 3) * 1024;
+  }
+  auto stage_piece = [&](int c, int buf, int k) {
+    if (k < kTermPieces) {
       __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(src + (uint32_t)(lane * 16)),
-          (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + i * 1024), 16, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < G::codes / 1024 / kQWaves; ++i) {
+          (const __attribute__((address_space(1))) void*)(tbase[k] + (uint32_t)c * (uint32_t)kQTermBytes +
+                                                          (uint32_t)(lane * 16)),
+          (__attribute__((address_space(3))) void*)(s_x + buf * G::buffer + (k * kQWaves + wave) * 1024), 16, 0, 0);
+    } else {
+      const int i = k - kTermPieces;
       int u = 4 * c + (lane & 3);
       u = u < a.units ? u : a.units - 1;                   // x is zero past the last column
       __builtin_amdgcn_global_load_lds(
@@ -893,6 +895,10 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
                                                     (kQWaves * i + wave) * 1024),
           16, 0, 0);
     }
+  };
+  auto stage = [&](int c, int buf) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) stage_piece(c, buf, k);
   };
 
   const Magic mg = magic();
@@ -977,11 +983,11 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   };
   const int k0 = TR ? c0 : c0 >> 2;
   load_table(k0, true);
-  stage(c0, 0);
   take_table(true);
-  write_table(k0);
   load_table(k0 + 1, true);
+  stage(c0, 0);
   stage(clamped(c0 + 1), 1);
+  write_table(k0);
   take_table(true);
   write_table(k0 + 1);
   open(c0);
@@ -992,7 +998,6 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   }
   __builtin_amdgcn_sched_barrier(0);
   load_table(k0 + 2, TR || (c0 & 3) == 3);
-  stage(clamped(c0 + 2), 2);
   // the matrix instructions of row tile i in step s
   auto product = [&](int s, int i) {
 #pragma unroll
@@ -1007,11 +1012,17 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
     }
     if (s == 0 || (TR && s % 2 == 0)) sp[i] = __uint_as_float(sz[TR ? (s >> 1) & 1 : 0][i].x);
   };
+  // The loads of the chunk two on are issued one by one between the products:
+  // together, right after the barrier, they kept both waves of a SIMD from
+  // their products for a quarter of the chunk.
   for (int c = c0; c < c1; ++c) {
+    const int c2 = clamped(c + 2), free = buf == 0 ? 2 : buf - 1;
 #pragma unroll
     for (int s = 0; s < 7; ++s) {
       read(s + 1);
       __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = s * kPieces / 7; k < (s + 1) * kPieces / 7; ++k) stage_piece(c2, free, k);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         product(s, i);
@@ -1020,16 +1031,12 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
       if (TR && s % 2 == 0 && s < 6) read_scales(c, s / 2 + 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    const int done = buf;
     buf = buf == 2 ? 0 : buf + 1;
     open(c + 1);
-    step_table(c + 1);
-    stage(clamped(c + 3), done);
-    __builtin_amdgcn_sched_barrier(0);
     // these first: the next codes are on their way from LDS
 #pragma unroll
     for (int i = 0; i < RT; ++i) product(7, i);
-    __builtin_amdgcn_sched_barrier(0);
+    step_table(c + 1);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       codes_of(i);
@@ -1044,23 +1051,40 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   // no load into LDS may be in flight when the workgroup gives its LDS up
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
-  // register r of a product is its row 8 (r / 4) + 4 half + r % 4
+  // Register r of a product is its row 8 (r / 4) + 4 half + r % 4.  The
+  // tokens' powers of two are all loaded before the first result is stored: a
+  // load behind a store would wait for it, once per register.
+  auto token = [&](int t, int r) {
+    const int m = 8 * (r >> 2) + 4 * half + (r & 3);
+    return (tg * TM + 2 * (wt * TW + t) + (m >> 4)) * 16 + row_token(m & 15);
+  };
+  float inv[TW][16];
 #pragma unroll
   for (int t = 0; t < TW; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int m = 8 * (r >> 2) + 4 * half + (r & 3);
-      const int tok = (tg * TM + 2 * (wt * TW + t) + (m >> 4)) * 16 + row_token(m & 15);
-      if (tok >= a.C) continue;
-      const float inv = a.inv[tok];
+    for (int r = 0; r < 16; ++r) inv[t][r] = token(t, r) < a.C ? a.inv[token(t, r)] : 0.0f;
+  auto store = [&](auto put1) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int n = nw + (wr * RT + i) * 32 + row;
-        if (n >= a.N) continue;
-        if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.C + tok) * a.N + n] = acc[t][i][r] * inv;
-        else put(a, tok, n, acc[t][i][r] * inv);
+    for (int t = 0; t < TW; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int tok = token(t, r);
+        if (tok >= a.C) continue;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const int n = nw + (wr * RT + i) * 32 + row;
+          if (n < a.N) put1(tok, n, acc[t][i][r] * inv[t][r]);
+        }
       }
-    }
+  };
+  if (a.splits > 1)
+    store([&](int t, int n, float v) { a.part[((int64_t)blockIdx.y * a.C + t) * a.N + n] = v; });
+  else if (P == 2)
+    store([&](int t, int n, float v) { put<MOE_DT_F32>(a, t, n, v); });
+  else if (a.x_dt == MOE_DT_BF16)
+    store([&](int t, int n, float v) { put<MOE_DT_BF16>(a, t, n, v); });
+  else
+    store([&](int t, int n, float v) { put<MOE_DT_F16>(a, t, n, v); });
 }
 
 __global__ __launch_bounds__(256) void k_qreduce(QArgs a) {
