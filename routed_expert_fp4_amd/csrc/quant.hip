@@ -904,19 +904,19 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   const Magic mg = magic();
   auto clamped = [&](int c) { return c < c1 ? c : c1 - 1; };
   // The pipeline.  A chunk is eight steps of 16 columns; during a step's matrix
-  // instructions the next step's terms are read from LDS and its codes
-  // unpacked, and where a group's sums are complete (after the chunk, or for
+  // instructions the terms of the step two on are read from LDS and the next
+  // step's codes unpacked, and where a group's sums are complete (after the chunk, or for
   // TR after each unit of two steps) the step after scales them into acc, so
   // that vector instructions lie between the matrix instructions of the same
   // wave (the waves of a workgroup run in step: what each does in phases, none
-  // overlaps).  The move to the next chunk comes before the last step: this
+  // overlaps).  The move to the next chunk comes before the last two steps: this
   // chunk's LDS reads are complete by then, so one barrier both frees its
   // buffer for the chunk three on and, each wave having waited for its own
   // loads, opens the next chunk's.  Loads complete in order, and the newest
   // (one chunk's LDS loads) may stay in flight; past the last chunk the last
   // is loaded again, so that their number is the same everywhere.
   float16v acc[TW][RT], d[TW][RT];
-  half8 x[2][TW][P], b[RT];
+  half8 x[4][TW][P], b[RT];                                // step s's terms in x[s & 3]
   uint32_t w[RT][2][4];                                    // codes: unit 2 u + half (TR: swapped, see codes_of)
   uint2 sz[2][RT];                                         // (scale, zero pair): TR unit & 1, else [0]
   float sp[RT];                                            // scales of the sums in d
@@ -941,7 +941,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
     for (int t = 0; t < TW; ++t)
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        x[s & 1][t][p] = *reinterpret_cast<const half8*>(xs + (p * TM + 2 * t) * kQTermBytes + block * 256);
+        x[s & 3][t][p] = *reinterpret_cast<const half8*>(xs + (p * TM + 2 * t) * kQTermBytes + block * 256);
   };
   auto read_scales = [&](int c, int u) {
     const uint8_t* t = tables + ((TR ? c : c >> 2) & 1) * G::table + (TR ? u : c & 3) * G::rows * 8;
@@ -964,6 +964,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
         for (int k = 0; k < 4; ++k) w[i][u][k] = v4[k];
       }
     read(0);
+    read(1);
     read_scales(c, 0);
   };
   // TR: dwords 0 and 1 of unit 2 u come to lie in the two halves of w[u][0]
@@ -977,10 +978,8 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
       }
     }
   };
-  auto unpack = [&](int s, int i) {
-    const uint32_t code = TR ? w[i][s >> 2][2 * (s & 1) + ((s >> 1) & 1)] : w[i][s >> 2][s & 3];
-    b[i] = unpack8(mg, code, sz[TR ? (s >> 1) & 1 : 0][i].y);
-  };
+  auto code = [&](int s, int i) { return TR ? w[i][s >> 2][2 * (s & 1) + ((s >> 1) & 1)] : w[i][s >> 2][s & 3]; };
+  auto unpack = [&](int s, int i) { b[i] = unpack8(mg, code(s, i), sz[TR ? (s >> 1) & 1 : 0][i].y); };
   const int k0 = TR ? c0 : c0 >> 2;
   load_table(k0, true);
   take_table(true);
@@ -1008,7 +1007,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
       }
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        d[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[s & 1][t][p], b[i], d[t][i], 0, 0, 0);
+        d[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[s & 3][t][p], b[i], d[t][i], 0, 0, 0);
     }
     if (s == 0 || (TR && s % 2 == 0)) sp[i] = __uint_as_float(sz[TR ? (s >> 1) & 1 : 0][i].x);
   };
@@ -1017,23 +1016,35 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   // their products for a quarter of the chunk.
   for (int c = c0; c < c1; ++c) {
     const int c2 = clamped(c + 2), free = buf == 0 ? 2 : buf - 1;
+    uint32_t code7[RT], z7[RT];
 #pragma unroll
-    for (int s = 0; s < 7; ++s) {
-      read(s + 1);
+    for (int s = 0; s < 6; ++s) {
+      read(s + 2);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int k = s * kPieces / 7; k < (s + 1) * kPieces / 7; ++k) stage_piece(c2, free, k);
+      for (int k = s * kPieces / 6; k < (s + 1) * kPieces / 6; ++k) stage_piece(c2, free, k);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         product(s, i);
         unpack(s + 1, i);
       }
-      if (TR && s % 2 == 0 && s < 6) read_scales(c, s / 2 + 1);
+      if (TR && s % 2 == 0) read_scales(c, s / 2 + 1);
       __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      code7[i] = code(7, i);
+      z7[i] = sz[TR ? 1 : 0][i].y;
     }
     buf = buf == 2 ? 0 : buf + 1;
     open(c + 1);
-    // these first: the next codes are on their way from LDS
+    // two steps left: the next chunk's codes are on their way from LDS
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      product(6, i);
+      b[i] = unpack8(mg, code7[i], z7[i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < RT; ++i) product(7, i);
     step_table(c + 1);
