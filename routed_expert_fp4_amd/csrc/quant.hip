@@ -75,6 +75,7 @@ struct QArgs {
   int C;
   void* y;
   int64_t y_pitch;
+  int y_vec;                          // rows of y are aligned to four of its elements
   int accumulate;
   float* inv;                         // [C]: takes the terms' power of two out again
   uint8_t* terms;                     // [P][C / 16][nch][16 blocks][16 tokens][16 bytes]
@@ -460,6 +461,34 @@ __device__ __forceinline__ void put(const QArgs& a, int t, int n, float v) {
   if (a.x_dt == MOE_DT_F32) put<MOE_DT_F32>(a, t, n, v);
   else if (a.x_dt == MOE_DT_BF16) put<MOE_DT_BF16>(a, t, n, v);
   else put<MOE_DT_F16>(a, t, n, v);
+}
+
+// Four results of a token, rows n .. n + 3 (n % 4 == 0).
+template <int DT>
+__device__ __forceinline__ void put4(const QArgs& a, int t, int n, float4 v) {
+  if (a.y_vec && n + 3 < a.N && !a.accumulate) {
+    const int64_t i = (int64_t)t * a.y_pitch + n;
+    if (DT == MOE_DT_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.y) + i) = v;
+    } else if (DT == MOE_DT_BF16) {
+      const __hip_bfloat16 h[4] = {__float2bfloat16(v.x), __float2bfloat16(v.y), __float2bfloat16(v.z),
+                                   __float2bfloat16(v.w)};
+      __builtin_memcpy(__builtin_assume_aligned(static_cast<__hip_bfloat16*>(a.y) + i, 8), h, 8);
+    } else {
+      const __half h[4] = {__float2half(v.x), __float2half(v.y), __float2half(v.z), __float2half(v.w)};
+      __builtin_memcpy(__builtin_assume_aligned(static_cast<__half*>(a.y) + i, 8), h, 8);
+    }
+    return;
+  }
+  const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) put<DT>(a, t, n + i, e[i]);
+}
+__device__ __forceinline__ void put4(const QArgs& a, int t, int n, float4 v) {
+  if (a.x_dt == MOE_DT_F32) put4<MOE_DT_F32>(a, t, n, v);
+  else if (a.x_dt == MOE_DT_BF16) put4<MOE_DT_BF16>(a, t, n, v);
+  else put4<MOE_DT_F16>(a, t, n, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -963,9 +992,8 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[i][u][k] = v4[k];
       }
-    read(0);
-    read(1);
     read_scales(c, 0);
+    read(0);
   };
   // TR: dwords 0 and 1 of unit 2 u come to lie in the two halves of w[u][0]
   // and those of unit 2 u + 1 in w[u][1] (2 and 3 likewise)
@@ -996,6 +1024,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
     unpack(0, i);
   }
   __builtin_amdgcn_sched_barrier(0);
+  read(1);
   load_table(k0 + 2, TR || (c0 & 3) == 3);
   // the matrix instructions of row tile i in step s
   auto product = [&](int s, int i) {
@@ -1045,6 +1074,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
       b[i] = unpack8(mg, code7[i], z7[i]);
     }
     __builtin_amdgcn_sched_barrier(0);
+    read(1);
 #pragma unroll
     for (int i = 0; i < RT; ++i) product(7, i);
     step_table(c + 1);
@@ -1062,40 +1092,46 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   // no load into LDS may be in flight when the workgroup gives its LDS up
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
 
-  // Register r of a product is its row 8 (r / 4) + 4 half + r % 4.  The
-  // tokens' powers of two are all loaded before the first result is stored: a
-  // load behind a store would wait for it, once per register.
-  auto token = [&](int t, int r) {
-    const int m = 8 * (r >> 2) + 4 * half + (r & 3);
-    return (tg * TM + 2 * (wt * TW + t) + (m >> 4)) * 16 + row_token(m & 15);
-  };
-  float inv[TW][16];
+  // The results through LDS, so that a wave stores a token's consecutive rows
+  // (as they lie in registers, a store held two tokens' 32 rows each, and 64 of
+  // them took a tenth of the kernel).  Register r of a product is its row
+  // 8 (r / 4) + 4 half + r % 4.
+  constexpr int kPitch = G::rows + 32;
+  static_assert(kPitch * TM * 16 * 4 <= G::lds, "the results fit the LDS");
+  float* res = reinterpret_cast<float*>(s_x);
+  __syncthreads();
 #pragma unroll
   for (int t = 0; t < TW; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) inv[t][r] = token(t, r) < a.C ? a.inv[token(t, r)] : 0.0f;
-  auto store = [&](auto put1) {
+    for (int r = 0; r < 16; ++r) {
+      const int m = 8 * (r >> 2) + 4 * half + (r & 3);
+      const int tok = 16 * (2 * (wt * TW + t) + (m >> 4)) + row_token(m & 15);
 #pragma unroll
-    for (int t = 0; t < TW; ++t)
+      for (int i = 0; i < RT; ++i) res[tok * kPitch + (wr * RT + i) * 32 + row] = acc[t][i][r];
+    }
+  __syncthreads();
+  for (int k = wave; k < TM * 16; k += kQWaves) {
+    const int tok = tg * TM * 16 + k, c = 4 * lane;
+    if (tok >= a.C) break;
+    if (c >= G::rows) continue;
+    const float inv = a.inv[tok];
+    float4 v = *reinterpret_cast<const float4*>(res + k * kPitch + c);
+    v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+    const int n = nw + c;
+    if (a.splits > 1) {
+      float* o = a.part + ((int64_t)blockIdx.y * a.C + tok) * a.N + n;
+      if (a.N % 4 == 0 && n < a.N) {
+        *reinterpret_cast<float4*>(o) = v;
+      } else {
+        const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int tok = token(t, r);
-        if (tok >= a.C) continue;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const int n = nw + (wr * RT + i) * 32 + row;
-          if (n < a.N) put1(tok, n, acc[t][i][r] * inv[t][r]);
-        }
+        for (int i = 0; i < 4; ++i)
+          if (n + i < a.N) o[i] = e[i];
       }
-  };
-  if (a.splits > 1)
-    store([&](int t, int n, float v) { a.part[((int64_t)blockIdx.y * a.C + t) * a.N + n] = v; });
-  else if (P == 2)
-    store([&](int t, int n, float v) { put<MOE_DT_F32>(a, t, n, v); });
-  else if (a.x_dt == MOE_DT_BF16)
-    store([&](int t, int n, float v) { put<MOE_DT_BF16>(a, t, n, v); });
-  else
-    store([&](int t, int n, float v) { put<MOE_DT_F16>(a, t, n, v); });
+    } else {
+      put4(a, tok, n, v);
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void k_qreduce(QArgs a) {
@@ -1314,6 +1350,7 @@ moe_status moe_quant_linear(const moe_quant_matrix* m, int32_t dtype, const void
   a.x = x; a.x_pitch = x_pitch; a.x_dt = dtype;
   a.x_vec = m->cols % 8 == 0 && (uintptr_t)x % 16 == 0 && (C == 1 || x_pitch * xs % 16 == 0);
   a.C = C; a.y = y; a.y_pitch = y_pitch; a.accumulate = accumulate;
+  a.y_vec = (uintptr_t)y % (4 * xs) == 0 && y_pitch % 4 == 0;
   a.inv = reinterpret_cast<float*>(w8 + p.inv);
   a.terms = w8 + p.terms;
   a.part = reinterpret_cast<float*>(w8 + p.part);
