@@ -348,17 +348,16 @@ def moe_expert_fwd_mx_mma(bank: Bank, x, C, k, topk_idx, topk_w, out, terms: int
 # Dense matrices in 4-bit codes with group scales
 # ---------------------------------------------------------------------------
 class _Scratch:
-    """A device workspace of `nbytes`, zero-initialised where `init`."""
+    """A zero-initialised device workspace of `nbytes`."""
 
-    def __init__(self, fn: str, nbytes: int, device, init: bool, stream=None):
+    def __init__(self, fn: str, nbytes: int, device, stream=None):
         import torch
         if nbytes == 0:
             raise MoeError(fn, MOE_ERR_UNSUPPORTED)
         self.tensor = torch.empty((nbytes + 255) // 256 * 64, dtype=torch.int32, device=device)
         self.nbytes, self.device = self.tensor.numel() * 4, self.tensor.get_device()
-        if init:
-            with torch.cuda.device(self.tensor.device):
-                moe_workspace_init(self.tensor, stream)
+        with torch.cuda.device(self.tensor.device):
+            moe_workspace_init(self.tensor, stream)
 
     def on(self, dev):
         """Its pointer, on GPU `dev` only."""
@@ -470,9 +469,9 @@ class QuantMatrix:
 
 
 class QuantWorkspace(_Scratch):
-    def __init__(self, matrix: QuantMatrix, C: int, dtype):
+    def __init__(self, matrix: QuantMatrix, C: int, dtype, stream=None):
         n = lib().moe_quant_workspace_size(matrix.ref, _moe_dtype(dtype), C)
-        super().__init__("moe_quant_workspace_size", n, f"cuda:{matrix.device}", False)
+        super().__init__("moe_quant_workspace_size", n, f"cuda:{matrix.device}", stream)
 
 
 def moe_quant_linear(matrix: QuantMatrix, x, C, y, ws: QuantWorkspace, accumulate=False, stream=None):
@@ -509,7 +508,7 @@ def moe_expert_counts(topk_idx, C, E, k, counts, tokens=None, seq_offsets=None, 
 class BalanceWorkspace(_Scratch):
     def __init__(self, C: int, E: int, S: int = 1, device="cuda", stream=None):
         super().__init__("moe_balance_workspace_size", lib().moe_balance_workspace_size(C, E, S),
-                         device, True, stream)
+                         device, stream)
 
 
 def moe_balance_fwd(logits, topk_idx, C, E, k, alpha, counts, tokens, probs, loss,

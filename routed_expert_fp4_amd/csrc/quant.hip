@@ -29,8 +29,8 @@
 //              by every workgroup, whose waves split the rows, the columns of
 //              a row tile, or both
 //   k_qfew     2 .. 16 tokens: workgroups take rows x column slices, make the
-//              slice's terms in LDS and stream its codes; k_qreduce adds the
-//              ranges of slices
+//              slice's terms in LDS and stream its codes; the last of a group
+//              of rows to finish adds the ranges of slices
 //   k_qterms   x to fp16 terms in the workspace, in the operand order
 //   k_qgemm    17 and more tokens: workgroup tiles of tokens x rows, x's terms
 //              through LDS (loaded there directly, two buffers), the codes
@@ -80,6 +80,7 @@ struct QArgs {
   float* inv;                         // [C]: takes the terms' power of two out again
   uint8_t* terms;                     // [P][C / 16][nch][16 blocks][16 tokens][16 bytes]
   float* part;                        // [splits][C][N]
+  uint32_t* tickets;                  // few tokens: arrivals per group of rows, left at zero
   int ks, spt;                        // one token: 2^ks waves to a row tile, steps per tile
   int splits, per_split;              // matrix kernel: column ranges, chunks in each
   int row_groups;                     // one token: groups of row tiles; matrix kernel: row tiles
@@ -284,8 +285,8 @@ __device__ __forceinline__ void split_term(float v, bool finite, _Float16& hi, _
 }
 
 // Eight columns of a row of x as stored (0 past the last column), through a
-// buffer view of x whose loads outside it give zeros.  vec: every row starts
-// 16-byte aligned and has a multiple of 8 columns; else element by element.
+// buffer view of x whose loads outside it give zeros: 16 bytes at a time
+// (load8v) where every row starts 16-byte aligned, else element by element.
 template <int DT>
 struct Raw { uint4v v[DT == MOE_DT_F32 ? 2 : 1]; };
 
@@ -293,15 +294,6 @@ template <int DT>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t x_view(const QArgs& a, int t, int rows) {
   constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
   return qview(static_cast<const uint8_t*>(a.x) + (int64_t)t * a.x_pitch * B, ((rows - 1) * a.x_pitch + a.K) * B);
-}
-template <int DT>
-__device__ __forceinline__ void load8v(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
-                                       Raw<DT>& r) {
-  constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
-  const uint32_t o = live && k < a.K ? row + (uint32_t)(k * B) : kOutside;
-#pragma unroll
-  for (int i = 0; i < B / 2; ++i)
-    r.v[i] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + 16 * i), 0, 0));
 }
 template <int DT>
 __device__ __forceinline__ void load8e(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
@@ -317,6 +309,16 @@ __device__ __forceinline__ void load8e(const QArgs& a, __amdgpu_buffer_rsrc_t x,
       r.v[0][i >> 1] = (i & 1) ? r.v[0][i >> 1] | (h << 16) : h;
     }
   }
+}
+template <int DT>
+__device__ __forceinline__ void load8v(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
+                                       Raw<DT>& r) {
+  constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
+  const uint32_t o = live && k + 8 <= a.K ? row + (uint32_t)(k * B) : kOutside;
+#pragma unroll
+  for (int i = 0; i < B / 2; ++i)
+    r.v[i] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(x, (int)(o + 16 * i), 0, 0));
+  if (live && k < a.K && k + 8 > a.K) load8e<DT>(a, x, row, k, live, r);   // a row's last columns
 }
 template <int DT>
 __device__ __forceinline__ void load8(const QArgs& a, __amdgpu_buffer_rsrc_t x, uint32_t row, int k, bool live,
@@ -774,7 +776,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
   }
   auto out = [&](int tok, int n, float val) {
     if (tok >= a.C || n >= a.N) return;
-    if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.C + tok) * a.N + n] = val;
+    if (a.splits > 1) store_coherent(a.part + ((int64_t)blockIdx.y * a.C + tok) * a.N + n, val);
     else put<DT>(a, tok, n, val);
   };
   if (WK == 1) {
@@ -794,6 +796,22 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
       for (int w = 0; w < WK; ++w) val += red[((tile * WK + w) * NR + r) * 64 + l];
       out(4 * r + (l >> 4), (blockIdx.x * (kQWaves / WK) + tile) * 16 + (l & 15), val);
     }
+  }
+  // the last of the rows' workgroups to arrive adds their ranges up, in order
+  // (a launch of its own for that took 2 us and the gap before it)
+  if (a.splits == 1) return;
+  __shared__ int s_last;
+  uint32_t* ticket = a.tickets + blockIdx.x;
+  if (!last_to_arrive(ticket, (uint32_t)a.splits, &s_last)) return;
+  if (tid == 0) reset_ticket(ticket);
+  constexpr int kRows = 16 * kQWaves / WK;
+  const __amdgpu_buffer_rsrc_t pv = coherent_view(a.part, (uint32_t)a.splits * a.C * a.N * 4u);
+  for (int i = tid; i < a.C * kRows; i += kQWG) {
+    const int tok = i / kRows, n = blockIdx.x * kRows + i % kRows;
+    if (n >= a.N) continue;
+    float val = 0.0f;
+    for (int s = 0; s < a.splits; ++s) val += coherent_ld(pv, 4u * (uint32_t)((s * a.C + tok) * a.N + n));
+    put<DT>(a, tok, n, val);
   }
 }
 
@@ -1049,7 +1067,6 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
 #pragma unroll
     for (int s = 0; s < 6; ++s) {
       read(s + 2);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int k = s * kPieces / 6; k < (s + 1) * kPieces / 6; ++k) stage_piece(c2, free, k);
 #pragma unroll
@@ -1058,6 +1075,13 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
         unpack(s + 1, i);
       }
       if (TR && s % 2 == 0) read_scales(c, s / 2 + 1);
+      // a matrix instruction, then a few vector ones and an LDS read
+#pragma unroll
+      for (int k = 0; k < TW * RT * P; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -1169,6 +1193,7 @@ moe_status matrix_status(const moe_quant_matrix* m) {
 
 // How a call runs: one rule on its sizes.
 enum { kOne, kFew, kMany };
+constexpr size_t kTicketBytes = 256 * sizeof(uint32_t);
 struct QPlan {
   int P, nch, ct;                      // terms, chunks, token tiles
   int path;
@@ -1216,7 +1241,9 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
       }
     }
   }
-  size_t o = 256;
+  // the tickets come first in every plan (ranges are only split for up to 256
+  // groups of rows), so that calls of other shapes leave them at zero
+  size_t o = kTicketBytes;
   p.inv = o; o = align256(o + (p.path == kMany ? (size_t)C * sizeof(float) : 0));
   p.terms = o; o = align256(o + (p.path == kMany ? (size_t)p.P * p.ct * p.nch * kQTermBytes : 0));
   p.part = o; o = align256(o + (p.splits > 1 ? (size_t)p.splits * C * m->rows * sizeof(float) : 0));
@@ -1300,7 +1327,7 @@ moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st
         : P == 2 ? launch_gemm<2, 1, 2, 1>(a, tr, ss, grid, st) : launch_gemm<1, 2, 2, 2>(a, tr, ss, grid, st);
   }
   if (s != MOE_OK) return s;
-  if (p.splits > 1)
+  if (p.path == kMany && p.splits > 1)
     hipLaunchKernelGGL(k_qreduce, dim3((unsigned)(((int64_t)a.C * a.N + 255) / 256)), dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
@@ -1348,12 +1375,13 @@ moe_status moe_quant_linear(const moe_quant_matrix* m, int32_t dtype, const void
   const int gc = tr ? 1 : m->group / kQChunk < p.nch ? m->group / kQChunk : p.nch;
   a.gmul = (1u << 20) / (uint32_t)gc + 1u;
   a.x = x; a.x_pitch = x_pitch; a.x_dt = dtype;
-  a.x_vec = m->cols % 8 == 0 && (uintptr_t)x % 16 == 0 && (C == 1 || x_pitch * xs % 16 == 0);
+  a.x_vec = (uintptr_t)x % 16 == 0 && (C == 1 || x_pitch * xs % 16 == 0);
   a.C = C; a.y = y; a.y_pitch = y_pitch; a.accumulate = accumulate;
   a.y_vec = (uintptr_t)y % (4 * xs) == 0 && y_pitch % 4 == 0;
   a.inv = reinterpret_cast<float*>(w8 + p.inv);
   a.terms = w8 + p.terms;
   a.part = reinterpret_cast<float*>(w8 + p.part);
+  a.tickets = reinterpret_cast<uint32_t*>(w8);
   a.splits = p.splits; a.per_split = p.per_split;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (dtype == MOE_DT_F32) return launch_quant<MOE_DT_F32>(a, p, tr, (int)ss, st);

@@ -103,6 +103,7 @@ CASES = [
     (1, 20, 24577, 64, "f16", "f16", False),
     # waves that share a row tile: none, two, eight; several slices to a workgroup
     (6, 4096, 8192, 128, "bf16", "bf16", False),
+    (16, 130, 8195, 32, "bf16", "f32", True),
     (12, 4000, 4096, 64, "f32", "bf16", True),
     (3, 33000, 2100, 256, "f32", "f16", True),
     # one token: eight, four, two and one wave to a row tile
@@ -254,6 +255,25 @@ def test_codes_past_four_gigabytes(C):
     check(y[:, at], want, tol, "rows")
     del codes, m
     torch.cuda.empty_cache()
+
+
+def test_one_workspace_for_several_shapes():
+    """Every path in turn over one workspace, twice: none leaves anything
+    behind that another takes for its own."""
+    import routed_expert_fp4_amd as rf
+    shapes = [(16, 300, 4100, 64, "f32"), (80, 500, 1300, 128, "f32"), (1, 900, 700, 32, "bf16"),
+              (5, 2000, 3000, 128, "bf16"), (33, 260, 2050, 64, "f16"), (9, 64, 9000, 32, "f16")]
+    work = []
+    for j, (C, N, K, G, xt) in enumerate(shapes):
+        codes, scales, z, x, y = make(C, N, K, G, xt, "f16", True, 20 + j)
+        m = rf.QuantMatrix(codes, scales, K, G, z)
+        work.append((m, x, y, rf.QuantWorkspace(m, C, x.dtype), expect(codes, scales, z, x, K, G)))
+    ws = max((w[3] for w in work), key=lambda w: w.nbytes)
+    for _ in range(2):
+        for (m, x, y, _, (want, tol)), shape in zip(work, shapes):
+            y.fill_(float("nan"))
+            rf.moe_quant_linear(m, x, x.shape[0], y, ws)
+            check(y, want, tol, shape)
 
 
 def test_refused_tensors():
