@@ -359,12 +359,12 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
 }
 
 // Experts 64 x .. 64 x + 63 of sequence y: 16 threads per expert add every
-// 16th slot, four loads in flight, then their sums in order.
+// 16th slot, eight of them in flight, then their sums in order.
 constexpr int kFinWG = 1024, kFinRows = kFinWG / 64;
 __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
   __shared__ float s_p[kFinWG];
   __shared__ int s_c[kFinWG];
-  __shared__ int s_t[kFinWG];
+  __shared__ float s_t[kFinRows];
   __shared__ int s_flag;
   const int tid = threadIdx.x, le = tid & 63, row = tid >> 6;
   const int s = blockIdx.y, e = blockIdx.x * 64 + le, E = a.E;
@@ -377,35 +377,33 @@ __global__ __launch_bounds__(kFinWG) void k_bal_final(BalArgs a) {
   const int ec = e < E ? e : E - 1;
   const float* ps = a.psum + (size_t)j0 * E + ec;
   const uint16_t* pc = a.pcnt + (size_t)j0 * E + ec;
-  float p = 0.0f;
-  int c = 0, t = 0;
+  float p = 0.0f, live = 0.0f;
+  int c = 0;
+  for (int j = tid; j < n; j += kFinWG) live += (float)a.ptok[j0 + j];
   int j = row;
-  for (; j + 3 * kFinRows < n; j += 4 * kFinRows) {
-    float q[4];
-    int k[4], u[4];
+  for (; j + 7 * kFinRows < n; j += 8 * kFinRows) {
+    float q[8];
+    int k[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const size_t at = (size_t)(j + i * kFinRows);
-      q[i] = ps[at * E];
-      k[i] = pc[at * E];
-      u[i] = a.ptok[j0 + at];
+    for (int i = 0; i < 8; ++i) {
+      q[i] = ps[(size_t)(j + i * kFinRows) * E];
+      k[i] = pc[(size_t)(j + i * kFinRows) * E];
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { p += q[i]; c += k[i]; t += u[i]; }
+    for (int i = 0; i < 8; ++i) { p += q[i]; c += k[i]; }
   }
   for (; j < n; j += kFinRows) {
     p += ps[(size_t)j * E];
     c += pc[(size_t)j * E];
-    t += a.ptok[j0 + j];
   }
-  s_p[tid] = p; s_c[tid] = c; s_t[tid] = t;
-  __syncthreads();
+  s_p[tid] = p; s_c[tid] = c;
+  // at most 2^20 tokens: exact in fp32
+  const int t = (int)block_sum(live, s_t, kFinRows);
   if (row == 0) {
 #pragma unroll
     for (int r = 1; r < kFinRows; ++r) {
       p += s_p[64 * r + le];
       c += s_c[64 * r + le];
-      t += s_t[64 * r + le];
     }
     const float it = t > 0 ? 1.0f / (float)t : 0.0f;
     const float P = p * it;

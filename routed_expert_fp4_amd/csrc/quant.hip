@@ -277,11 +277,12 @@ __device__ __forceinline__ void term_scale(uint32_t maxbits, float& m, float& in
 // v (scaled) as hi + lo.  A token with an infinity or NaN is not scaled: its
 // finite values are held within fp16's range (its results are infinite or NaN
 // whatever they are), and the infinity itself has no second term.
-__device__ __forceinline__ void split_term(float v, bool finite, _Float16& hi, _Float16& lo) {
-  if (!finite && fabsf(v) < INFINITY) v = fminf(fmaxf(v, -65504.0f), 65504.0f);
+template <bool FINITE>
+__device__ __forceinline__ void split_term(float v, _Float16& hi, _Float16& lo) {
+  if (!FINITE && fabsf(v) < INFINITY) v = fminf(fmaxf(v, -65504.0f), 65504.0f);
   hi = (_Float16)v;
   lo = (_Float16)(v - (float)hi);
-  if (!finite && !(fabsf(v) < INFINITY)) lo = (_Float16)0.0f;
+  if (!FINITE && !(fabsf(v) < INFINITY)) lo = (_Float16)0.0f;
 }
 
 // Eight columns of a row of x as stored (0 past the last column), through a
@@ -344,9 +345,11 @@ __device__ __forceinline__ uint32_t raw_max(const Raw<DT>& r, uint32_t m) {
   return m;
 }
 
-// The block's terms in the operand order.
-template <int DT>
-__device__ __forceinline__ void make_terms(const Raw<DT>& r, float m, bool finite, half8& hi, half8& lo) {
+// The block's terms in the operand order.  Tokens that are not finite are set
+// apart by a branch of the wave: selecting in every element cost as much as the
+// split itself.
+template <int DT, bool FINITE>
+__device__ __forceinline__ void make_terms_of(const Raw<DT>& r, float m, half8& hi, half8& lo) {
   constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -356,11 +359,16 @@ __device__ __forceinline__ void make_terms(const Raw<DT>& r, float m, bool finit
       hi[i] = __builtin_bit_cast(_Float16, (uint16_t)((k & 1) ? w >> 16 : w));
     } else {
       _Float16 h, l;
-      split_term(raw_f32<DT>(r, k) * m, finite, h, l);
+      split_term<FINITE>(raw_f32<DT>(r, k) * m, h, l);
       hi[i] = h;
       if (DT == MOE_DT_F32) lo[i] = l;
     }
   }
+}
+template <int DT>
+__device__ __forceinline__ void make_terms(const Raw<DT>& r, float m, bool finite, half8& hi, half8& lo) {
+  if (DT == MOE_DT_F16 || __ballot(!finite) == 0) make_terms_of<DT, true>(r, m, hi, lo);
+  else make_terms_of<DT, false>(r, m, hi, lo);
 }
 
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
