@@ -8,7 +8,7 @@
 // product is exact and only fp32 sums round; the group's scale multiplies its
 // fp32 sum.  fp16 x is taken as it is.  bf16 x (8 bits) is one fp16 term under
 // a power of two per token that puts the token's largest value below 2^15:
-// exact down to 2^-29 of that value, and off by at most 2^-39 of it below.
+// exact down to 2^-28 of that value, and off by at most 2^-38 of it below.
 // fp32 x is two such terms (22 bits).
 //
 // Codes become fp16 without conversions: a nibble OR-ed into the fp16 1024 is
@@ -63,6 +63,7 @@ struct QArgs {
   int64_t zero_pitch;
   int zero_step;                      // 0 where one byte (8) serves every group
   int scale_bf16;                     // 16-bit scales: bf16, else fp16
+  int scales_vec;                     // G 32, 64: a chunk's scales and zero points can be loaded together
   int N, K;
   int units;                          // 16-byte units of a row
   int nch;                            // chunks of a row
@@ -157,6 +158,39 @@ __device__ __forceinline__ void load_quad(const QArgs& a, const View& v, int c, 
   int cq = c + step * (quarter < N ? quarter : N - 1);
   cq = cq < a.nch ? cq : a.nch - 1;
   const uint32_t out = live ? 0u : kOutside;
+  if (TR && a.scales_vec) {
+    // the chunk's four (G 32) or two scales and zero points in one load each
+    if (a.gshift == 5) {
+      const int os = (int)((v.vs + 4 * SS * cq) | out);
+      if (SS == 4) {
+        const auto s = __builtin_amdgcn_raw_buffer_load_b128(v.scales, os, 0, 0);
+#pragma unroll
+        for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = s[e];
+      } else {
+        const auto s = __builtin_amdgcn_raw_buffer_load_b64(v.scales, os, 0, 0);
+#pragma unroll
+        for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = (e & 1) ? s[e >> 1] >> 16 : s[e >> 1] & 0xFFFFu;
+      }
+      const uint32_t z = __builtin_amdgcn_raw_buffer_load_b32(v.zeros, (int)((v.vz + 4 * a.zero_step * cq) | out), 0, 0);
+#pragma unroll
+      for (int e = 0; e < Quad<N, TR>::S; ++e) u.z[e] = (z >> (8 * e)) & 0xFFu;
+    } else {
+      const int os = (int)((v.vs + 2 * SS * cq) | out);
+      if (SS == 4) {
+        const auto s = __builtin_amdgcn_raw_buffer_load_b64(v.scales, os, 0, 0);
+#pragma unroll
+        for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = s[e >> 1];
+      } else {
+        const uint32_t s = __builtin_amdgcn_raw_buffer_load_b32(v.scales, os, 0, 0);
+#pragma unroll
+        for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = e >> 1 ? s >> 16 : s & 0xFFFFu;
+      }
+      const uint32_t z = __builtin_amdgcn_raw_buffer_load_b16(v.zeros, (int)((v.vz + 2 * a.zero_step * cq) | out), 0, 0);
+#pragma unroll
+      for (int e = 0; e < Quad<N, TR>::S; ++e) u.z[e] = e >> 1 ? z >> 8 : z & 0xFFu;
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < Quad<N, TR>::S; ++e) {
     int g = TR ? (4 * cq + e) >> (a.gshift - 5) : (int)(((uint32_t)cq * a.gmul) >> 20);
@@ -335,8 +369,19 @@ __device__ __forceinline__ float raw_f32(const Raw<DT>& r, int i) {
   return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);        // bf16
 }
 
+// The largest |x| so far as fp32 bits (NaN above infinity above the rest).
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
 template <int DT>
 __device__ __forceinline__ uint32_t raw_max(const Raw<DT>& r, uint32_t m) {
+  if (DT == MOE_DT_BF16) {
+    // pairs of bf16: their bits rise with |x|
+    ushort2v p = __builtin_bit_cast(ushort2v, r.v[0][0] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      p = __builtin_elementwise_max(p, __builtin_bit_cast(ushort2v, r.v[0][i] & 0x7FFF7FFFu));
+    const uint32_t b = (uint32_t)(p[0] > p[1] ? p[0] : p[1]) << 16;
+    return b > m ? b : m;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t b = __float_as_uint(raw_f32<DT>(r, i)) & 0x7FFFFFFFu;
@@ -351,6 +396,16 @@ __device__ __forceinline__ uint32_t raw_max(const Raw<DT>& r, uint32_t m) {
 template <int DT, bool FINITE>
 __device__ __forceinline__ void make_terms_of(const Raw<DT>& r, float m, half8& hi, half8& lo) {
   constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+  if (DT == MOE_DT_BF16 && FINITE) {
+    // two at a time, toward zero: exact wherever fp16 is normal
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto h = __builtin_amdgcn_cvt_pkrtz(raw_f32<DT>(r, i) * m, raw_f32<DT>(r, i + 4) * m);
+      hi[2 * i] = h[0];
+      hi[2 * i + 1] = h[1];
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int k = order[i];
@@ -663,15 +718,16 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
 // slices of kQSlice chunks.  For each slice the workgroup makes the tokens'
 // terms in LDS, under a power of two per token and slice; its waves then walk
 // the slice's codes (WK waves share a tile's chunks), the next slice's loaded
-// as soon as these are used.  Small matrices take a large WK: more workgroups,
-// each with less to do after its loads have arrived.
-constexpr int kQSlice = 8;
-constexpr int kQSliceCols = kQSlice * kQChunk;
+// as soon as these are used.  Small matrices take a larger WK (and with eight as
+// long a slice as 64 KB of terms hold): more workgroups, each with less to do
+// after its loads have arrived.
+constexpr int few_slice(int P, int TOK, int WK) { return WK == 8 ? 65536 / (P * TOK * 2 * kQChunk) : 8; }
 
 template <int DT, int TOK, int WK, bool TR, int SS>
 __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
   constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
   constexpr int NR = TOK / 4;
+  constexpr int kQSlice = few_slice(P, TOK, WK), kQSliceCols = kQSlice * kQChunk;
   constexpr int NB = TOK * kQSliceCols / 8 / kQWG;        // blocks of x per thread
   constexpr int kBlocks = kQSliceCols / 8;
   constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
@@ -1222,14 +1278,20 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
   p.path = C == 1 && (int64_t)p.nch * kQChunk * 2 * p.P <= kQStageBytes ? kOne
            : C <= MOE_MAX_DECODE_TOKENS ? kFew : kMany;
   if (p.path == kFew) {
-    // the fewest waves to a row tile that give every CU a workgroup
-    const int nsl = (p.nch + kQSlice - 1) / kQSlice;
+    // the fewest waves to a row tile that give every CU a workgroup: a
+    // workgroup of fewer rows makes the same terms for less (7 tokens, bf16,
+    // 7168 x 3584: 13.6 us with two, 15.8 with eight; 1001 x 4099, 16 tokens,
+    // fp32: 18.1 with two, 11.4 with eight)
+    const int tok = C <= 8 ? 8 : 16;
+    int nsl = 1, s = 1;
     for (p.wk = 1;; p.wk = p.wk == 1 ? 2 : 8) {
-      const int rows = 16 * kQWaves / p.wk;
+      const int rows = 16 * kQWaves / p.wk, slice = few_slice(p.P, tok, p.wk);
+      nsl = (p.nch + slice - 1) / slice;
       p.row_groups = (m->rows + rows - 1) / rows;
       if (p.wk == 8 || (int64_t)p.row_groups * nsl >= 256) break;
     }
-    int s = 512 / p.row_groups;
+    // ranges of slices while there are fewer than two workgroups a CU
+    s = 512 / p.row_groups;
     s = s < 1 ? 1 : s > nsl ? nsl : s;
     p.per_split = (nsl + s - 1) / s;
     p.splits = (nsl + p.per_split - 1) / p.per_split;
@@ -1272,7 +1334,7 @@ void launch_one(const QArgs& a, bool tr, int ss, int grid, size_t lds, hipStream
 
 template <int DT, int TOK, int WK, bool TR, int SS>
 moe_status launch_few_t(const QArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int lds = (DT == MOE_DT_F32 ? 2 : 1) * 2 * kQSliceCols * TOK;
+  constexpr int P = DT == MOE_DT_F32 ? 2 : 1, lds = P * 2 * few_slice(P, TOK, WK) * kQChunk * TOK;
   auto k = k_qfew<DT, TOK, WK, TR, SS>;
   if (lds + 1024 > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
@@ -1377,6 +1439,9 @@ moe_status moe_quant_linear(const moe_quant_matrix* m, int32_t dtype, const void
   a.units = (m->cols + 31) / 32; a.nch = p.nch;
   a.ng = (int)(((int64_t)m->cols + m->group - 1) / m->group);
   const bool tr = m->group < 128;
+  // whole chunks, and rows of scales and zero points at multiples of 4 bytes
+  a.scales_vec = m->cols % kQChunk == 0 && (uintptr_t)m->scales % 4 == 0 && a.scale_pitch % 4 == 0 &&
+                 (uintptr_t)m->zeros % 4 == 0 && a.zero_pitch % 4 == 0;
   a.gshift = m->group == 32 ? 5 : 6;
   // groups of whole chunks: c < 2^10 chunks over gc chunks a group; the
   // product's error c / 2^20 stays under the 1 / gc to the next quotient
