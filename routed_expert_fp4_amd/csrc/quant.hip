@@ -33,7 +33,7 @@
 //              of rows to finish adds the ranges of slices
 //   k_qterms   x to fp16 terms in the workspace, in the operand order
 //   k_qgemm    17 and more tokens: workgroup tiles of tokens x rows, x's terms
-//              through LDS (loaded there directly, two buffers), the codes
+//              through LDS (loaded there directly, three buffers), the codes
 //              from memory to registers; k_qreduce adds split column ranges
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
@@ -1279,9 +1279,9 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
            : C <= MOE_MAX_DECODE_TOKENS ? kFew : kMany;
   if (p.path == kFew) {
     // the fewest waves to a row tile that give every CU a workgroup: a
-    // workgroup of fewer rows makes the same terms for less (7 tokens, bf16,
-    // 7168 x 3584: 13.6 us with two, 15.8 with eight; 1001 x 4099, 16 tokens,
-    // fp32: 18.1 with two, 11.4 with eight)
+    // workgroup of fewer rows makes the same terms for less (us with one, two,
+    // eight: 7 tokens, bf16, 7168 x 3584 14.7, 13.0, 13.1; 16384 x 4096 15.3,
+    // 16.4, 19.7; 16 tokens, fp32, 1001 x 4099 23.8, 17.7, 16.8)
     const int tok = C <= 8 ? 8 : 16;
     int nsl = 1, s = 1;
     for (p.wk = 1;; p.wk = p.wk == 1 ? 2 : 8) {
@@ -1290,8 +1290,12 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
       p.row_groups = (m->rows + rows - 1) / rows;
       if (p.wk == 8 || (int64_t)p.row_groups * nsl >= 256) break;
     }
-    // ranges of slices while there are fewer than two workgroups a CU
-    s = 512 / p.row_groups;
+    // ranges of slices: two workgroups a CU (7 tokens, bf16, 7168 x 3584: 12.9
+    // us in four ranges, 13.8 in two; 16, fp32, 1001 x 4099: 17.0 in five, 20.6
+    // in three); for more than 8 tokens in slices of several chunks a wave one,
+    // whose partial results are half as many (16, fp32, 3584 x 7168: 17.0 in
+    // four, 20.9 in seven)
+    s = (tok == 8 || p.wk == 8 ? 512 : 256) / p.row_groups;
     s = s < 1 ? 1 : s > nsl ? nsl : s;
     p.per_split = (nsl + s - 1) / s;
     p.splits = (nsl + p.per_split - 1) / p.per_split;
