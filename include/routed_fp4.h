@@ -277,8 +277,8 @@ moe_status moe_layer_fwd_noalloc(const moe_bank *bank, const float *w_router, co
  * MOE_MAX_QUANT_COLS; group 32, 64 or a multiple of 128; codes and code_pitch
  * multiples of 16, code_pitch >= cols / 2 rounded up; scale_pitch and (where
  * zeros are given) zero_pitch >= the number of groups; pitches of at most
- * 2^22; scales aligned to their type.  A row's bytes are read in units of 16, so rows * code_pitch
- * bytes, or up to the end of the last row's last unit, must be readable. */
+ * 2^22; scales aligned to their type.  A row's bytes are read in units of 16,
+ * so up to the end of the last row's last unit must be readable. */
 typedef enum { MOE_DT_F32 = 1, MOE_DT_BF16 = 2, MOE_DT_F16 = 3 } moe_dtype;
 
 #define MOE_MAX_QUANT_ROWS (1 << 22)
@@ -300,17 +300,18 @@ typedef struct {
 /* Workspace bytes of moe_quant_linear for C tokens of the type `dtype` (at
  * least 256; 0 outside the supported range).  It must be initialised once with
  * moe_workspace_init, and one workspace serves every matrix, type and number of
- * tokens that it is large enough for. */
+ * tokens that it is large enough for, one call at a time; it serves
+ * moe_quant_linear alone, since it keeps state between calls. */
 size_t moe_quant_workspace_size(const moe_quant_matrix *m, int32_t dtype, int32_t C);
 
 /* y[c][n] = sum_k x[c][k] W[n][k], or y += where `accumulate` is not 0, for
  * 1 <= C <= MOE_MAX_TOKENS tokens.
  *  x [C][x_pitch], y [C][y_pitch]: both of `dtype` (moe_dtype), pitches in
  *  elements (x_pitch >= cols, y_pitch >= rows, at most 2^24), aligned to
- *  their type, any row alignment; y may not alias x.  Elements behind a row are neither read
- *  nor written.  Products are exact and sums are fp32; y (with accumulate,
- *  the sum with the old y) is rounded once to its type.  fp32 and bf16
- *  activations enter as fp16 terms under a power-of-two scale per token and
+ *  their type, any row alignment; y may not alias x.  Elements behind a row
+ *  are neither read nor written.  Products are exact and sums are fp32; y (with
+ *  accumulate, the sum with the old y) is rounded once to its type.  fp32 and
+ *  bf16 activations enter as fp16 terms under a power-of-two scale per token and
  *  slab of columns (two terms for fp32: an element keeps 22 bits, and at
  *  least 2^-38 of its slab's largest).  The result does not depend on what
  *  ran before: the same call gives the same bits. */
@@ -359,7 +360,8 @@ moe_status moe_expert_counts(const int32_t *topk_idx, int32_t C, int32_t k, int3
                              int32_t *counts, int32_t *tokens, int32_t accumulate, void *stream);
 
 /* Workspace of moe_balance_fwd (0 outside the supported range); it must be
- * initialised once with moe_workspace_init. */
+ * initialised once with moe_workspace_init, serves every call that it is large
+ * enough for, one at a time, and moe_balance_fwd alone. */
 size_t moe_balance_workspace_size(int32_t C, int32_t E, int32_t S);
 
 /* The balance loss of a selection:

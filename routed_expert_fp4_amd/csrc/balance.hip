@@ -33,7 +33,7 @@
 namespace rf4 {
 namespace {
 
-constexpr int kPartWG = 512;          // up to eight waves share a slot's tokens
+constexpr int kPartWG = 512;          // eight waves share a slot's tokens
 constexpr int kPartWaves = kPartWG / 64;
 constexpr int kBalWG = 256;           // backward kernels: four waves
 constexpr int kBalWaves = kBalWG / 64;
@@ -73,14 +73,18 @@ __device__ __forceinline__ int seq_of(const int32_t* off, int t, int S, int C) {
   return s < S && seq_at(off, s, S, C) <= t ? s : -1;
 }
 
-// Tokens per slot: 8 (one a wave) up to 8192 tokens, then as many as keep the
-// slots at about 1024, whose partial sums (one row of E per slot) stay a small
-// share of the logits read.  A power of two, so that a sequence's first slot
-// is a shift.
+// Tokens per slot, a power of two, so that a sequence's first slot is a shift:
+// 8 (one a wave) while that makes a slot a CU, then up to 32 (8192 tokens x 896,
+// both passes, with 8, 16, 32, 64: 38.8, 37.1, 32.6, 36.4 us), then as many as
+// keep the slots at 1024, whose partial sums (a row of E per slot) stay a small
+// share of the logits read (65536 x 448 with 16, 32, 64, 128: 103.6, 96.2, 95.1,
+// 93.4 us).  One slot for up to 32 tokens, whose workgroup writes the loss (16
+// tokens: 11.1 us in one slot, 13.7 in two; 32: 13.9 and 13.8; 64: 19.2 and
+// 14.0).
 __host__ __device__ inline int slot_shift(int C, int S) {
   if (S == 1 && C <= kOneSlot) return 5;
   int s = 3;
-  while (s < 10 && (C >> s) > 1024) ++s;
+  while (s < 10 && (C >> s) > (s < 5 ? 256 : 1024)) ++s;
   return s;
 }
 // Slots of sequence s: from (off[s] >> shift) + s, one per TB tokens.  The
@@ -264,7 +268,7 @@ __global__ __launch_bounds__(kPartWG) void k_bal_part(BalArgs a) {
   __shared__ float s_p[kPartWaves];
   __shared__ int s_tok;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int threads = blockDim.x, waves = threads >> 6;
+  constexpr int threads = kPartWG, waves = kPartWaves;
   const int E = a.E, slot = blockIdx.x, sh = a.shift;
   // the sequence whose slots this one is among: largest s with
   // (off[s] >> sh) + s <= slot
@@ -694,18 +698,23 @@ moe_status moe_expert_counts(const int32_t* topk_idx, int32_t C, int32_t k, int3
   if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
   if (!seq_ok(seq_off, S)) return MOE_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  // one part per sequence (no zero fill, no atomics in memory) up to 4096
-  // choices of an average one; longer ones are shared out, however uneven they
-  // are
-  int64_t parts = (int64_t)C * k / S <= 4096 ? 1 : ((int64_t)C * k / S + 2047) / 2048;
-  if (parts > 256) parts = 256;
+  // one part per sequence (no zero fill, no atomics in memory) up to 8192
+  // choices of an average one (512 tokens x 16: 5.8 us, 7.1 in four parts; 2048:
+  // 9.3, 7.3 in 16); longer ones are shared out, however uneven they are, to
+  // workgroups that run at once (61 sequences of 17190: 10.8 us in 8 parts, 12.4
+  // in 9; one of 2^20: 10.5 in 64, 11.8 in 256)
+  const int64_t choices = (int64_t)C * k / S, at_once = 512 / S > 4 ? 512 / S : 4;
+  int64_t parts = choices <= 8192 ? 1 : (choices + 2047) / 2048;
+  if (parts > at_once) parts = at_once;
+  if (parts > 64) parts = 64;
   if (parts > 1 && !accumulate) {
     const int64_t n = (int64_t)S * E;
     hipLaunchKernelGGL(k_count_fill, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, counts, tokens, n, S);
   }
-  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3((int64_t)C * k / S <= 1024 ? 256 : kCntWG), 0, st, topk_idx, seq_off, token_mask,
-                     C, k, division(k), E, S, counts, tokens,
-                     accumulate);
+  // small workgroups for short sequences (1000 of 64 choices: 5.7 us, 8.0 with
+  // large ones; one of 8192: 7.5 and 5.7)
+  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3(choices <= 1024 ? 256 : kCntWG), 0, st, topk_idx,
+                     seq_off, token_mask, C, k, division(k), E, S, counts, tokens, accumulate);
   return launched();
 }
 
@@ -744,10 +753,8 @@ moe_status moe_balance_fwd(const float* logits, const int32_t* topk_idx, int32_t
   a.kmul = division(k);
   a.one = S == 1 && C <= kOneSlot && !seq_off;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  // eight waves to a slot while that leaves room for every slot at once; then
-  // four (65536 tokens, 1061 slots: the last ones would wait for a second round)
   const int slots = a.one ? 1 : num_slots(C, S);
-  RF4_BY_ROW(k_bal_part, E, score == MOE_SCORE_SIGMOID, dim3(slots), slots <= 768 ? kPartWG : kPartWG / 2, st, a);
+  RF4_BY_ROW(k_bal_part, E, score == MOE_SCORE_SIGMOID, dim3(slots), kPartWG, st, a);
   if (!a.one) hipLaunchKernelGGL(k_bal_final, dim3(expert_blocks(E), S), dim3(kFinWG), 0, st, a);
   return launched();
 }
@@ -772,8 +779,10 @@ moe_status moe_balance_bwd(const float* logits, const int32_t* counts, const int
   a.counts = const_cast<int32_t*>(counts); a.tokens = const_cast<int32_t*>(tokens);
   a.grad = grad_loss; a.dlogits = dlogits; a.accumulate = accumulate;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  // one token per wave until the chip is full of waves, then up to 8
-  a.per = C <= 8192 ? 1 : C >= 65536 ? 8 : C / 8192;
+  // one token per wave until the chip is half full of waves, then up to 4 (both
+  // passes with 1, 2, 4, 8: 2048 tokens x 896 18.7, 18.7, 22.3, 27.7 us; 8192
+  // 38.7, 35.9, 36.9, 40.4; 65536 x 448 98.0, 97.8, 93.9, 95.0)
+  a.per = C < 8192 ? 1 : C >= 16384 ? 4 : 2;
   const int wg = kBalWaves * a.per;
   RF4_BY_ROW(k_bal_bwd, E, score == MOE_SCORE_SIGMOID, dim3((C + wg - 1) / wg), kBalWG, st, a);
   return launched();

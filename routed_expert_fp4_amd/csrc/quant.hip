@@ -438,7 +438,8 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 // Four tokens whose operand rows are next to each other (t, t + 4, t + 8,
 // t + 12 of a tile), so that four lanes write 64 contiguous bytes: their
 // largest values, then their terms.  FITS: the rows (up to 8192 columns) stay
-// in registers between the two, else they are read twice.
+// in registers between the two, else they are read twice (2048 tokens x 7168
+// in fp32: 12 us more).
 constexpr int kTermWG = 1024, kTermBlocks = kTermWG / 4;
 template <int DT, bool FITS>
 __global__ __launch_bounds__(kTermWG) void k_qterms(QArgs a) {
@@ -1249,7 +1250,8 @@ moe_status matrix_status(const moe_quant_matrix* m) {
     return MOE_ERR_INVALID_ARG;
   if (m->scale_pitch < ng || (uintptr_t)m->scales % dtype_size(m->scale_dtype)) return MOE_ERR_INVALID_ARG;
   if (m->zeros && m->zero_pitch < ng) return MOE_ERR_INVALID_ARG;
-  // a wave's rows (64 at most) are addressed by 32-bit offsets, and so are 16 rows of x
+  // a workgroup's rows (256 at most, of up to 2^24 bytes) are addressed by
+  // 32-bit offsets, and so are 16 rows of x
   if (m->code_pitch > kMaxPitch || m->scale_pitch > kMaxPitch || (m->zeros && m->zero_pitch > kMaxPitch))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -1300,15 +1302,24 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
     p.per_split = (nsl + s - 1) / s;
     p.splits = (nsl + p.per_split - 1) / p.per_split;
   } else if (p.path == kMany) {
-    // the larger tile: 256 rows, and tokens whose terms fit the LDS ring
+    // the larger tile (256 rows, and tokens whose terms fit the LDS ring) where
+    // its workgroups fill half the CUs (us without, with it, bf16: 2048 tokens x
+    // 3584 x 7168, 224 workgroups, 176, 121; 1024 tokens, 112 of them, 94, 105;
+    // 1024 tokens in fp32, 224, 141, 113; 512, 112, 85, 89)
     const int wide_tokens = p.P == 2 ? 64 : 128;
     p.wide = C > 64 && (int64_t)((C + wide_tokens - 1) / wide_tokens) * ((m->rows + 255) / 256) >= 128;
     p.tok_groups = p.wide ? (C + wide_tokens - 1) / wide_tokens : (C + 63) / 64;
     p.row_groups = p.wide ? (m->rows + 255) / 256 : (m->rows + 127) / 128;
     const int64_t wgs = (int64_t)p.tok_groups * p.row_groups;
     if (!p.wide && wgs < 256) {
-      int s = (int)(512 / wgs);
-      if (s > p.nch / 4) s = p.nch / 4;
+      // column ranges: a workgroup a CU as long as a range keeps four chunks,
+      // two as long as it keeps eight (us in one, this many and twice as many
+      // ranges, bf16, 3584 x 7168: 64 tokens 54.8, 22.8 in 9, 25.7 in 18; 256
+      // tokens 54.6, 37.5 in 4, 45.1 in 8; fp32, 1001 x 4099, 64 tokens 46.3,
+      // 23.8 in 8, 22.8 in 16)
+      const int64_t once = 256 / wgs < p.nch / 4 ? 256 / wgs : p.nch / 4;
+      const int64_t most = once > p.nch / 8 ? once : p.nch / 8;
+      const int s = (int)(512 / wgs < most ? 512 / wgs : most);
       if (s > 1) {
         p.per_split = (p.nch + s - 1) / s;
         p.splits = (p.nch + p.per_split - 1) / p.per_split;
@@ -1380,11 +1391,14 @@ moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st
   constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
   moe_status s = MOE_OK;
   if (p.path == kOne) {
-    // waves to a row tile: as many as it takes to give every CU's eight
-    // waves work; tiles walked by a resident grid
+    // waves to a row tile: the power of two that comes nearest to eight waves
+    // a CU (us with 2, 4, 8 waves, fp32: 3584 x 7168 17.4, 11.8, 9.0; 7168 x
+    // 3584 11.3, 8.7, 9.8; 16384 x 7168 20.0, 20.1, 21.0); tiles walked by a
+    // resident grid, whose terms are made once (any grid from 512 to 8192
+    // takes the 55 us that 65536 x 7168 is read in)
     const int nt = (a.N + 15) / 16;
     a.ks = 3;
-    while (a.ks > 0 && ((int64_t)nt << (a.ks - 1)) >= 2048) --a.ks;
+    while (a.ks > 0 && ((int64_t)nt << (a.ks - 1)) >= 1536) --a.ks;
     a.row_groups = (nt + (kQWaves >> a.ks) - 1) / (kQWaves >> a.ks);
     a.spt = (((a.nch + (1 << a.ks) - 1) >> a.ks) + 7) / 8;
     launch_one<DT>(a, tr, ss, a.row_groups < 512 ? a.row_groups : 512, (size_t)p.nch * kQChunk * 2 * P, st);
