@@ -282,6 +282,177 @@ def test_one_workspace_for_several_shapes():
             check(y, want, tol, shape)
 
 
+def test_largest_matrix_and_row():
+    """The most rows a matrix may have, and the most columns."""
+    import routed_expert_fp4_amd as rf
+    N, K = rf.MOE_MAX_QUANT_ROWS, 40
+    for C in (1, 2, 18):
+        say(f"[quant] {N} rows, {C} tokens")
+        codes, scales, z, x, y = make(C, 64, K, 32, "bf16", "bf16", True, 30)
+        copies = N // 64
+        many = [t.repeat(copies, 1) for t in (codes, scales, z)]
+        y = torch.full((C, N), float("nan"), dtype=x.dtype, device="cuda")
+        run(*many, x, y, K, 32)
+        want, tol = expect(codes, scales, z, x, K, 32)
+        check(y[:, :64], want, tol, C)
+        assert bool((y.reshape(C, copies, 64) == y[:, None, :64]).all())
+    K = rf.MOE_MAX_QUANT_COLS
+    for C, xt in ((1, "f32"), (9, "bf16"), (33, "f16")):
+        say(f"[quant] {K} columns, {C} tokens")
+        codes, scales, z, x, y = make(C, 37, K, 64, xt, "f32", True, 31)
+        run(codes, scales, z, x, y, K, 64)
+        want, tol = expect(codes, scales, z, x, K, 64)
+        check(y, want, tol, C, rel=False)
+
+
+@pytest.mark.parametrize("C", [3, 21])
+def test_largest_pitches(C):
+    """Rows of x and y 2^24 elements apart, rows of codes, scales and zero
+    points 2^22."""
+    N, K, G = 20, 200, 64
+    codes, scales, z, x, y = make(C, N, K, G, "f32", "f32", True, 32)
+    want, tol = expect(codes, scales, z, x, K, G)
+
+    def spread(t, pitch):
+        wide = torch.empty((t.shape[0], pitch), dtype=t.dtype, device="cuda")[:, :t.shape[1]]
+        wide.copy_(t)
+        return wide
+
+    codes, scales, z = (spread(t, 1 << 22) for t in (codes, scales, z))
+    x, y = spread(x, 1 << 24), spread(y, 1 << 24)
+    run(codes, scales, z, x, y, K, G)
+    check(y, want, tol, C)
+    torch.cuda.empty_cache()
+
+
+def test_scales_past_two_gigabytes_of_a_workgroup():
+    """The larger matrix tile's 256 rows of fp32 scales, 2^22 elements apart."""
+    C, N, K, G = 4096, 512, 160, 32
+    codes, scales, z, x, y = make(C, N, K, G, "f32", "f32", False, 33)
+    wide = torch.empty((N, 1 << 22), device="cuda")[:, :scales.shape[1]]
+    wide.copy_(scales)
+    run(codes, wide, z, x, y, K, G)
+    at = torch.arange(0, C, 97)
+    want, tol = expect(codes, scales, z, x[at], K, G)
+    check(y[at], want, tol, "wide")
+    del wide
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_drawn_calls(seed):
+    """Sizes, types, pitches, alignments and accumulation drawn together."""
+    rng = np.random.default_rng(1000 + seed)
+    C = int(rng.choice([1, 2, 4, 8, 11, 16, 17, 40, 64, 100, 200, 600]))
+    N, K = int(rng.integers(1, 1200)), int(rng.integers(1, 5000))
+    if rng.random() < 0.4:
+        K = max(32, K // 128 * 128)
+    G = int(rng.choice([32, 64, 128, 256, 640]))
+    xt, st = (str(rng.choice(["f32", "bf16", "f16"])) for _ in range(2))
+    zeros, acc = bool(rng.random() < 0.5), bool(rng.random() < 0.3)
+    pads = [int(rng.choice([0, 0, 1, 3, 8])) for _ in range(2)]
+    say(f"[quant] C={C} N={N} K={K} G={G} x={xt} scales={st} zeros={zeros} accumulate={acc} pads={pads}")
+    codes, scales, z, x, y = make(C, N, K, G, xt, st, zeros, seed, 16 * int(rng.integers(0, 3)), *pads)
+    shift = int(rng.integers(0, 4))                 # x from any element on
+    flat = torch.zeros(x.numel() + C * pads[0] + 8, dtype=x.dtype, device="cuda")
+    moved = flat[shift:].as_strided(x.shape, (K + pads[0], 1), shift)
+    moved.copy_(x)
+    y.copy_(torch.randn(y.shape, device="cuda"))
+    old, part = y.clone(), y[:, :N]
+    run(codes, scales, z, moved, part, K, G, accumulate=acc)
+    want, tol = expect(codes, scales, z, x, K, G)
+    if acc:
+        want = want + old[:, :N].double().cpu().numpy()
+        tol = tol + ref.U * np.abs(want)
+    check(part, want, tol, seed, rel=False)
+    assert torch.equal(y[:, N:], old[:, N:])
+
+
+@pytest.mark.parametrize("C", [1, 12, 40])
+def test_two_graphs_share_a_workspace(C):
+    """Two captured calls of different shapes over one workspace, replayed in
+    turn with eager calls between them."""
+    import routed_expert_fp4_amd as rf
+    calls = []
+    for j, (N, K, G) in enumerate(((300, 4100, 64), (700, 1300, 128))):
+        codes, scales, z, x, y = make(C, N, K, G, "f32", "f16", True, 40 + j)
+        m = rf.QuantMatrix(codes, scales, K, G, z)
+        calls.append([m, x, y, expect(codes, scales, z, x, K, G)])
+    ws = max((rf.QuantWorkspace(m, C, x.dtype) for m, x, _, _ in calls), key=lambda w: w.nbytes)
+    for call in calls:
+        m, x, y, _ = call
+        rf.moe_quant_linear(m, x, C, y, ws)
+        torch.cuda.synchronize()
+        call.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(call[4]):
+            rf.moe_quant_linear(m, x, C, y, ws)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for j in order:
+            m, x, y, (want, tol), graph = calls[j]
+            y.fill_(float("nan"))
+            graph.replay()
+            check(y, want, tol, (C, order, j))
+            y.fill_(float("nan"))
+            rf.moe_quant_linear(m, x, C, y, ws)
+            check(y, want, tol, (C, order, j))
+
+
+@pytest.mark.parametrize("C", [1, 5, 16])
+def test_together_as_a_latent_layer(C):
+    """A latent layer whose dense steps are held in 4 bits: router, routed_down
+    by the dense product, routed experts, RMS norm, routed_up by the dense
+    product onto the shared experts' sum; against moe_latent_layer_fwd with the
+    same weights in bf16 (integers times powers of two: exact) and the oracle.
+    Bars as for the layer itself, whose experts both share."""
+    import oracle
+    import routed_expert_fp4_amd as rf
+    import synth
+    from gpu_util import assert_close, cached_bank, to_dev
+    oracle.build()
+    wl = synth.LatentWorkload("lat_quant", synth.FMT_MX, 64, 8, 1024, 512, 512, 2, 1024, C, gamma_scale=2.0 ** 17)
+    Wr, x, _, _, gamma = synth.latent_inputs(wl, 0, C=C)
+    rng = np.random.default_rng(50)
+    mats, bits = [], []
+    for N, K, G in ((wl.L, wl.H, 128), (wl.H, wl.L, 32)):
+        codes = rng.integers(0, 256, (N, K // 2), np.uint8)
+        scales = np.ldexp(1.0, rng.integers(-9, -6, (N, K // G))).astype(np.float32)
+        zeros = rng.integers(6, 10, (N, K // G), np.uint8)
+        W = ref.quant_weights(codes, scales, zeros, K, G).astype(np.float32)
+        b = W.view(np.uint32)
+        assert not (b & 0xFFFF).any()
+        bits.append((b >> 16).astype(np.uint16))
+        mats.append(rf.QuantMatrix(to_dev(codes), to_dev(scales), K, G, to_dev(zeros)))
+    routed, shared = cached_bank(wl.routed_bank()), cached_bank(wl.shared_bank())
+    gd, xd, wd = to_dev(gamma), to_dev(x), to_dev(Wr)
+
+    layer = rf.LatentLayer(wd, to_dev(bits[0].view(np.int16)), gd, wl.eps, to_dev(bits[1].view(np.int16)),
+                           routed, shared)
+    whole = torch.empty((C, wl.H), device="cuda")
+    chosen = torch.empty((C, wl.k), dtype=torch.int32, device="cuda")
+    rf.moe_latent_layer_fwd(layer, xd, C, wl.k, whole, chosen, None, rf.LatentWorkspace(layer, wl.k, C))
+
+    logits = torch.empty((C, wl.E), device="cuda")
+    idx, w = torch.empty_like(chosen), torch.empty((C, wl.k), device="cuda")
+    rf.moe_route(xd, wd, logits, C, wl.H, wl.E, wl.k, idx, w, rf.Workspace(wl.E, wl.H, 512, wl.k, C))
+    lat, mixed = torch.empty((C, wl.L), device="cuda"), torch.empty((C, wl.L), device="cuda")
+    out = torch.empty((C, wl.H), device="cuda")
+    ws = max((rf.QuantWorkspace(m, C, torch.float32) for m in mats), key=lambda s: s.nbytes)
+    rf.moe_quant_linear(mats[0], xd, C, lat, ws)
+    rf.moe_expert_fwd(routed, lat, C, wl.k, idx, w, mixed, rf.Workspace(routed.E, wl.L, routed.I, wl.k, C))
+    normed = gd * mixed / torch.sqrt((mixed * mixed).mean(dim=1, keepdim=True) + wl.eps)
+    every = torch.arange(shared.E, dtype=torch.int32, device="cuda").repeat(C, 1)
+    rf.moe_expert_fwd(shared, xd, C, shared.E, every, torch.ones((C, shared.E), device="cuda"), out,
+                      rf.Workspace(shared.E, wl.H, shared.I, shared.E, C))
+    before = out.clone()
+    rf.moe_quant_linear(mats[1], normed.contiguous(), C, out, ws, accumulate=True)
+    torch.cuda.synchronize()
+    assert torch.equal(idx, chosen)
+    assert float((out - before).norm()) > 0.1 * float(before.norm())     # the routed part counts
+    assert_close(out.cpu().numpy(), whole.cpu().numpy(), f"against the bf16 layer, C={C}")
+    want = oracle.latent_layer(wl, Wr, x, bits[0], bits[1], gamma, idx=idx.cpu().numpy())
+    assert_close(out.cpu().numpy(), want["out"], f"against the oracle, C={C}")
+
+
 def test_refused_tensors():
     import routed_expert_fp4_amd as rf
     codes, scales, z, x, y = make(4, 32, 128, 64, "f32", "f32", True, 1)
