@@ -892,7 +892,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
 // chunk's four units.  The tables are there because a load of one scale per
 // row touches a cache line per row: taken chunk by chunk and wave by wave those
 // lines were more traffic than terms and codes together.
-template <int P, int WT, int TW, int RT, bool TR>
+template <int P, int WT, int TW, int RT>
 struct GemmTile {
   static constexpr int WR = kQWaves / WT, TM = WT * TW * 2, rows = WR * RT * 32;
   static constexpr int terms = P * TM * kQTermBytes, codes = rows * 64, buffer = terms + codes;
@@ -905,9 +905,12 @@ struct GemmTile {
 
 typedef float float16v __attribute__((ext_vector_type(16)));
 
-template <int P, int WT, int TW, int RT, bool TR, int SS>
+// UG: units (of 32 columns) to a group for G 32 and 64, else 0.
+template <int P, int WT, int TW, int RT, int UG, int SS>
 __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
-  using G = GemmTile<P, WT, TW, RT, TR>;
+  using G = GemmTile<P, WT, TW, RT>;
+  constexpr bool TR = UG > 0;
+  constexpr int kGroupSteps = TR ? 2 * UG : 8;             // steps of 16 columns to a scale
   constexpr int WR = G::WR, TM = G::TM;
   extern __shared__ __align__(16) uint8_t s_x[];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -1018,7 +1021,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   // The pipeline.  A chunk is eight steps of 16 columns; during a step's matrix
   // instructions the terms of the step two on are read from LDS and the next
   // step's codes unpacked, and where a group's sums are complete (after the chunk, or for
-  // TR after each unit of two steps) the step after scales them into acc, so
+  // TR after each group's units of two steps) the step after scales them into acc, so
   // that vector instructions lie between the matrix instructions of the same
   // wave (the waves of a workgroup run in step: what each does in phases, none
   // overlaps).  The move to the next chunk comes before the last two steps: this
@@ -1030,7 +1033,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   float16v acc[TW][RT], d[TW][RT];
   half8 x[4][TW][P], b[RT];                                // step s's terms in x[s & 3]
   uint32_t w[RT][2][4];                                    // codes: unit 2 u + half (TR: swapped, see codes_of)
-  uint2 sz[2][RT];                                         // (scale, zero pair): TR unit & 1, else [0]
+  uint2 sz[2][RT];                                         // (scale, zero pair): TR group & 1, else [0]
   float sp[RT];                                            // scales of the sums in d
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
@@ -1058,7 +1061,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   auto read_scales = [&](int c, int u) {
     const uint8_t* t = tables + ((TR ? c : c >> 2) & 1) * G::table + (TR ? u : c & 3) * G::rows * 8;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) sz[TR ? u & 1 : 0][i] = *reinterpret_cast<const uint2*>(t + 32 * 8 * i);
+    for (int i = 0; i < RT; ++i) sz[TR ? u / (kGroupSteps / 2) & 1 : 0][i] = *reinterpret_cast<const uint2*>(t + 32 * 8 * i);
   };
   // every wave's loads of buffer `buf` are complete, and so are its reads of
   // the one before (a plain barrier: __syncthreads would wait for all loads)
@@ -1090,7 +1093,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
     }
   };
   auto code = [&](int s, int i) { return TR ? w[i][s >> 2][2 * (s & 1) + ((s >> 1) & 1)] : w[i][s >> 2][s & 3]; };
-  auto unpack = [&](int s, int i) { b[i] = unpack8(mg, code(s, i), sz[TR ? (s >> 1) & 1 : 0][i].y); };
+  auto unpack = [&](int s, int i) { b[i] = unpack8(mg, code(s, i), sz[TR ? s / kGroupSteps & 1 : 0][i].y); };
   const int k0 = TR ? c0 : c0 >> 2;
   load_table(k0, true);
   take_table(true);
@@ -1113,7 +1116,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   auto product = [&](int s, int i) {
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
-      if (s == 0 || (TR && s % 2 == 0)) {
+      if (s % kGroupSteps == 0) {
         acc[t][i] += sp[i] * d[t][i];
         d[t][i] = float16v(0.0f);
       }
@@ -1121,7 +1124,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
       for (int p = 0; p < P; ++p)
         d[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[s & 3][t][p], b[i], d[t][i], 0, 0, 0);
     }
-    if (s == 0 || (TR && s % 2 == 0)) sp[i] = __uint_as_float(sz[TR ? (s >> 1) & 1 : 0][i].x);
+    if (s % kGroupSteps == 0) sp[i] = __uint_as_float(sz[TR ? s / kGroupSteps & 1 : 0][i].x);
   };
   // The loads of the chunk two on are issued one by one between the products:
   // together, right after the barrier, they kept both waves of a SIMD from
@@ -1139,7 +1142,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
         product(s, i);
         unpack(s + 1, i);
       }
-      if (TR && s % 2 == 0) read_scales(c, s / 2 + 1);
+      if (TR && s % kGroupSteps == kGroupSteps - 2) read_scales(c, s / 2 + 1);
       // a matrix instruction, then a few vector ones and an LDS read
 #pragma unroll
       for (int k = 0; k < TW * RT * P; ++k) {
@@ -1280,17 +1283,19 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
   p.path = C == 1 && (int64_t)p.nch * kQChunk * 2 * p.P <= kQStageBytes ? kOne
            : C <= MOE_MAX_DECODE_TOKENS ? kFew : kMany;
   if (p.path == kFew) {
-    // the fewest waves to a row tile that give every CU a workgroup: a
-    // workgroup of fewer rows makes the same terms for less (us with one, two,
-    // eight: 7 tokens, bf16, 7168 x 3584 14.7, 13.0, 13.1; 16384 x 4096 15.3,
-    // 16.4, 19.7; 16 tokens, fp32, 1001 x 4099 23.8, 17.7, 16.8)
+    // the fewest waves to a row tile that give every CU a workgroup, eight only
+    // up to a workgroup of 16 rows a CU: a workgroup of fewer rows makes the same
+    // terms for less (us with one, two, eight: 7 tokens, bf16, 7168 x 3584 14.7,
+    // 13.0, 13.1; 16384 x 4096 15.3, 16.4, 19.7; 2 tokens, 14917 x 832 6.7, 5.8,
+    // 13.4; 4 tokens, 3000 x 2000 13.4, 10.6, 8.7; 6000 x 2000 9.9, 8.2, 9.2; 16
+    // tokens, fp32, 1001 x 4099 23.8, 17.7, 16.8)
     const int tok = C <= 8 ? 8 : 16;
     int nsl = 1, s = 1;
     for (p.wk = 1;; p.wk = p.wk == 1 ? 2 : 8) {
       const int rows = 16 * kQWaves / p.wk, slice = few_slice(p.P, tok, p.wk);
       nsl = (p.nch + slice - 1) / slice;
       p.row_groups = (m->rows + rows - 1) / rows;
-      if (p.wk == 8 || (int64_t)p.row_groups * nsl >= 256) break;
+      if (p.wk == 8 || (int64_t)p.row_groups * nsl >= 256 || (p.wk == 2 && m->rows > 4096)) break;
     }
     // ranges of slices: two workgroups a CU (7 tokens, bf16, 7168 x 3584: 12.9
     // us in four ranges, 13.8 in two; 16, fp32, 1001 x 4099: 17.0 in five, 20.6
@@ -1302,12 +1307,17 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
     p.per_split = (nsl + s - 1) / s;
     p.splits = (nsl + p.per_split - 1) / p.per_split;
   } else if (p.path == kMany) {
-    // the larger tile (256 rows, and tokens whose terms fit the LDS ring) where
-    // its workgroups fill half the CUs (us without, with it, bf16: 2048 tokens x
-    // 3584 x 7168, 224 workgroups, 176, 121; 1024 tokens, 112 of them, 94, 105;
-    // 1024 tokens in fp32, 224, 141, 113; 512, 112, 85, 89)
+    // the larger tile (256 rows, and tokens whose terms fit the LDS ring): with
+    // two terms where its workgroups, one a CU, fill half the CUs (us without,
+    // with it, 7168 columns: 512 tokens x 3584, 112 workgroups, 85, 89; 1024
+    // tokens, 224, 141, 113); with one, whose smaller tile runs two workgroups a
+    // CU and so is the faster as long as all of those run at once, where they do
+    // not (3136 columns: 1024 tokens x 4096, 512 small ones, 49.7, 55.0; 1100
+    // tokens, 576, 67.9, 56.6)
     const int wide_tokens = p.P == 2 ? 64 : 128;
-    p.wide = C > 64 && (int64_t)((C + wide_tokens - 1) / wide_tokens) * ((m->rows + 255) / 256) >= 128;
+    const int64_t wide = (int64_t)((C + wide_tokens - 1) / wide_tokens) * ((m->rows + 255) / 256);
+    const int64_t narrow = (int64_t)((C + 63) / 64) * ((m->rows + 127) / 128);
+    p.wide = C > 64 && (p.P == 2 ? wide >= 128 : narrow > 512);
     p.tok_groups = p.wide ? (C + wide_tokens - 1) / wide_tokens : (C + 63) / 64;
     p.row_groups = p.wide ? (m->rows + 255) / 256 : (m->rows + 127) / 128;
     const int64_t wgs = (int64_t)p.tok_groups * p.row_groups;
@@ -1369,10 +1379,10 @@ moe_status launch_few(const QArgs& a, bool tr, int ss, int wk, dim3 grid, hipStr
   return launch_few_w<DT, TOK, 8>(a, tr, ss, grid, st);
 }
 
-template <int P, int WT, int TW, int RT, bool TR, int SS>
+template <int P, int WT, int TW, int RT, int UG, int SS>
 moe_status launch_gemm_t(const QArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int lds = GemmTile<P, WT, TW, RT, TR>::lds;
-  auto k = k_qgemm<P, WT, TW, RT, TR, SS>;
+  constexpr int lds = GemmTile<P, WT, TW, RT>::lds;
+  auto k = k_qgemm<P, WT, TW, RT, UG, SS>;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          lds) != hipSuccess)
     return MOE_ERR_DEVICE;
@@ -1380,10 +1390,14 @@ moe_status launch_gemm_t(const QArgs& a, dim3 grid, hipStream_t st) {
   return MOE_OK;
 }
 
+template <int P, int WT, int TW, int RT, int UG>
+moe_status launch_gemm_u(const QArgs& a, int ss, dim3 grid, hipStream_t st) {
+  return ss == 4 ? launch_gemm_t<P, WT, TW, RT, UG, 4>(a, grid, st) : launch_gemm_t<P, WT, TW, RT, UG, 2>(a, grid, st);
+}
 template <int P, int WT, int TW, int RT>
 moe_status launch_gemm(const QArgs& a, bool tr, int ss, dim3 grid, hipStream_t st) {
-  if (tr) return ss == 4 ? launch_gemm_t<P, WT, TW, RT, true, 4>(a, grid, st) : launch_gemm_t<P, WT, TW, RT, true, 2>(a, grid, st);
-  return ss == 4 ? launch_gemm_t<P, WT, TW, RT, false, 4>(a, grid, st) : launch_gemm_t<P, WT, TW, RT, false, 2>(a, grid, st);
+  if (!tr) return launch_gemm_u<P, WT, TW, RT, 0>(a, ss, grid, st);
+  return a.gshift == 5 ? launch_gemm_u<P, WT, TW, RT, 1>(a, ss, grid, st) : launch_gemm_u<P, WT, TW, RT, 2>(a, ss, grid, st);
 }
 
 template <int DT>
