@@ -146,6 +146,9 @@ struct Quad {
 // The loads are always issued, so that the count of loads in flight is the
 // same on every path and a wait for one step's codes leaves the next step's in
 // flight.
+// Codes are not loaded as non-temporal, though a call reads them once: 64 bytes
+// of a row are half a cache line, and the other half is the next chunk's (65536
+// x 7168, one token: 58.5 us non-temporal, 52.6 not).
 template <int N, bool TR, int SS>
 __device__ __forceinline__ void load_quad(const QArgs& a, const View& v, int c, int step, int quarter, bool live,
                                           Quad<N, TR>& u) {
@@ -153,7 +156,7 @@ __device__ __forceinline__ void load_quad(const QArgs& a, const View& v, int c, 
   for (int i = 0; i < N; ++i) {
     const int ci = c + step * i;
     u.q[i] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
-        v.codes, (int)(v.vc | (live && ci < a.nch ? 0u : kOutside)), 64 * ci, kCachePolicyNt));
+        v.codes, (int)(v.vc | (live && ci < a.nch ? 0u : kOutside)), 64 * ci, 0));
   }
   int cq = c + step * (quarter < N ? quarter : N - 1);
   cq = cq < a.nch ? cq : a.nch - 1;
@@ -1322,14 +1325,15 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
     p.row_groups = p.wide ? (m->rows + 255) / 256 : (m->rows + 127) / 128;
     const int64_t wgs = (int64_t)p.tok_groups * p.row_groups;
     if (!p.wide && wgs < 256) {
-      // column ranges: a workgroup a CU as long as a range keeps four chunks,
-      // two as long as it keeps eight (us in one, this many and twice as many
-      // ranges, bf16, 3584 x 7168: 64 tokens 54.8, 22.8 in 9, 25.7 in 18; 256
-      // tokens 54.6, 37.5 in 4, 45.1 in 8; fp32, 1001 x 4099, 64 tokens 46.3,
-      // 23.8 in 8, 22.8 in 16)
+      // column ranges: a workgroup a CU as long as a range keeps four chunks;
+      // with one term, where two workgroups fit a CU, two as long as it keeps
+      // twelve (us in 1, 2, 4, 7 ranges, 3584 x 7168: fp32, 128 tokens, 56
+      // workgroups, 63.7, 43.1, 32.8, 39.2; 200 tokens, 112 of them, 64.9, 47.1,
+      // 51.9, 66.5; bf16, 128 tokens 54.1, 36.7, 27.3, 28.4; 256 tokens in 2, 4, 9
+      // ranges 40.0, 37.5, 45.1)
       const int64_t once = 256 / wgs < p.nch / 4 ? 256 / wgs : p.nch / 4;
-      const int64_t most = once > p.nch / 8 ? once : p.nch / 8;
-      const int s = (int)(512 / wgs < most ? 512 / wgs : most);
+      const int64_t twice = p.P == 2 ? 0 : 512 / wgs < p.nch / 12 ? 512 / wgs : p.nch / 12;
+      const int s = (int)(once > twice ? once : twice);
       if (s > 1) {
         p.per_split = (p.nch + s - 1) / s;
         p.splits = (p.nch + p.per_split - 1) / p.per_split;
@@ -1406,10 +1410,11 @@ moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st
   moe_status s = MOE_OK;
   if (p.path == kOne) {
     // waves to a row tile: the power of two that comes nearest to eight waves
-    // a CU (us with 2, 4, 8 waves, fp32: 3584 x 7168 17.4, 11.8, 9.0; 7168 x
-    // 3584 11.3, 8.7, 9.8; 16384 x 7168 20.0, 20.1, 21.0); tiles walked by a
-    // resident grid, whose terms are made once (any grid from 512 to 8192
-    // takes the 55 us that 65536 x 7168 is read in)
+    // a CU (us with 1, 2, 4, 8 waves: fp32, 3584 x 7168 25.9, 16.5, 11.2, 9.0;
+    // 7168 x 3584 15.7, 10.8, 8.5, 9.3; 16384 x 7168 26.5, 18.2, 17.9, 17.7;
+    // bf16, 65536 x 7168 50.8, 54.0, 52.6, 56.2); tiles walked by a resident
+    // grid, whose terms are made once (65536 x 7168: 50.5 us from 512 workgroups,
+    // 51.3 from 8192)
     const int nt = (a.N + 15) / 16;
     a.ks = 3;
     while (a.ks > 0 && ((int64_t)nt << (a.ks - 1)) >= 1536) --a.ks;
