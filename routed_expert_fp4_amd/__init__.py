@@ -401,21 +401,35 @@ def _rows(t, dev, dtype, shape, name):
     return t.data_ptr(), pitch if shape[0] > 1 else shape[1]
 
 
+_cuda = None      # torch's raw current stream of a GPU, and its current GPU
+
+
+def _bind_cuda():
+    """The two queries without the Python around them: a quarter of a
+    microsecond less per call."""
+    global _cuda
+    import torch
+    _cuda = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+             (lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+             getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
+    return _cuda
+
+
 def _launch(fn, dev, stream, *args):
     """Calls an entry point on GPU `dev` and its stream (None: the current
     one), whichever GPU is current."""
-    import torch
+    raw_stream, current = _cuda or _bind_cuda()
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of a Stream object's time
-        handle = raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+        handle = raw_stream(dev)
     elif stream.device.index != dev:
         raise ValueError(f"the stream must be of cuda:{dev}, got {stream.device}")
     else:
         handle = stream.cuda_stream
     f = getattr(_lib or lib(), fn)
-    if torch.cuda.current_device() == dev:
+    if current() == dev:
         status = f(*args, handle)
     else:
+        import torch
         with torch.cuda.device(dev):
             status = f(*args, handle)
     if status != MOE_OK:
