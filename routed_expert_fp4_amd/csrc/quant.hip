@@ -141,8 +141,8 @@ struct Quad {
 };
 
 // Units past the last column read what lies there (a code is finite, and x is
-// zero); their scale is the last group's, since what lies behind a row of
-// scales may be no number.  Chunks from nch on (or live false) are not read.
+// zero); their scale is 0, since what lies behind a row of scales may be no
+// number, and the last group's may be infinite.  Chunks from nch on (or live false) are not read.
 // The loads are always issued, so that the count of loads in flight is the
 // same on every path and a wait for one step's codes leaves the next step's in
 // flight.
@@ -197,10 +197,10 @@ __device__ __forceinline__ void load_quad(const QArgs& a, const View& v, int c, 
 #pragma unroll
   for (int e = 0; e < Quad<N, TR>::S; ++e) {
     int g = TR ? (4 * cq + e) >> (a.gshift - 5) : (int)(((uint32_t)cq * a.gmul) >> 20);
-    if (TR) g = g < a.ng ? g : a.ng - 1;
-    if (SS == 4) u.s[e] = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
-    else u.s[e] = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
-    u.z[e] = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)((v.vz + a.zero_step * g) | out), 0, 0);
+    const uint32_t skip = TR && 4 * cq + e >= a.units ? kOutside : out;
+    if (SS == 4) u.s[e] = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)((v.vs + SS * g) | skip), 0, 0);
+    else u.s[e] = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)((v.vs + SS * g) | skip), 0, 0);
+    u.z[e] = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)((v.vz + a.zero_step * g) | skip), 0, 0);
   }
 }
 
@@ -946,8 +946,8 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
         const int c = 4 * kb + te + e;
         g = (int)(((uint32_t)(c < a.nch ? c : a.nch - 1) * a.gmul) >> 20);
       }
-      g = g < a.ng ? g : a.ng - 1;
-      const uint32_t out = live ? 0u : kOutside;
+      // past the last group (units past the last column): a scale of 0
+      const uint32_t out = live && (!TR || g < a.ng) ? 0u : kOutside;
       if (SS == 4) ns[e] = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
       else ns[e] = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
       nz[e] = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)((v.vz + a.zero_step * g) | out), 0, 0);

@@ -178,6 +178,26 @@ def test_masked_and_outside_tokens_are_not_read(score):
     assert (got[inner] == 0.0).all() and np.isfinite(got[3:80]).all()
 
 
+@pytest.mark.parametrize("C", [5, 32, 33, 700])
+def test_one_sequence_by_its_offsets(C):
+    """One sequence that does not begin at the first token nor end at the last."""
+    E, k = 70, 6
+    logits, idx, _, mask = make(C, E, k, 1, True, seed=12)
+    seq = np.array([1, C - 2], np.int32)
+    r = ref.balance(logits, idx, 0.1, "sigmoid", seq, mask, 1)
+    t, _ = fwd(logits, idx, E, 0.1, "sigmoid", seq, mask, 1)
+    assert np.array_equal(t["counts"].cpu().numpy(), r["counts"]) and int(t["tokens"]) == r["tokens"][0]
+    tp = tol_p(E, logits) + (4 + (C / 8 + 1) / 16 + 24) * U
+    assert (np.abs(t["probs"].double().cpu().numpy() - r["probs"]) <= tp * r["probs"] + 1e-44).all()
+    assert abs(float(t["loss"]) - r["loss"]) <= (tp + 30 * U) * r["loss"] + 1e-44
+    d = torch.full((C, E), 5.0, device="cuda")
+    bwd(t, C, E, k, 0.1, 1.0, "sigmoid", 1, d)
+    got = d.double().cpu().numpy()
+    assert (got[:1] == 5.0).all() and (got[C - 2:] == 5.0).all()
+    tol = grad_tol(r, logits, 0.1, 1.0, "sigmoid", seq, mask, 1, E, k)
+    assert (np.abs(got - r["dlogits"]) <= tol)[1:C - 2].all()
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_no_token_at_all(score):
     C, E, k, S = 12, 40, 4, 3

@@ -195,6 +195,54 @@ def test_infinities_and_nan_stay_in_their_token(C, xt):
         check(y[2:], want, tol, (C, xt))
 
 
+@pytest.mark.parametrize("C", [1, 5, 40, 70])
+@pytest.mark.parametrize("K,G", [(33, 32), (65, 64), (200, 64), (300, 128)])
+def test_infinite_scales_stay_in_their_row(C, K, G):
+    """A row whose last, partial group has an infinite scale: its results are
+    infinite (NaN where the group's sum is 0), and no other row changes."""
+    codes, scales, z, x, y = make(C, 50, K, G, "f32", "f32", False, 51)
+    codes |= 0x11                                   # no code is 8: no weight is 0
+    x[:, K // G * G:] = x[:, K // G * G:].abs() + 1
+    codes[7] = 0xFF                                 # every weight 7 scales
+    scales[7, -1] = float("inf")
+    scales[9, 0] = float("nan")
+    run(codes, scales, z, x, y, K, G)
+    assert bool((y[:, 7] == float("inf")).all()) and bool(torch.isnan(y[:, 9]).all())
+    rows = [n for n in range(50) if n not in (7, 9)]
+    want, tol = expect(codes[rows], scales[rows], None, x, K, G)
+    check(y[:, rows], want, tol, (C, K, G))
+
+
+@pytest.mark.parametrize("C", [1, 7, 16, 50])
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_every_zero_point(C, G):
+    """Zero points are bytes: all 256 of them, not the codes' range alone."""
+    N, K = 64, 1000
+    codes, scales, z, x, y = make(C, N, K, G, "f32", "f16", True, 52)
+    z.copy_((torch.arange(z.numel(), device="cuda") % 256).to(torch.uint8).view(z.shape))
+    run(codes, scales, z, x, y, K, G)
+    want, tol = expect(codes, scales, z, x, K, G)
+    check(y, want, tol, (C, G), rel=False)
+
+
+@pytest.mark.parametrize("C", [1, 9, 40])
+def test_two_streams_at_once(C):
+    """Calls that overlap, each stream with a workspace of its own."""
+    import routed_expert_fp4_amd as rf
+    codes, scales, z, x, y = make(C, 2000, 4000, 128, "f32", "bf16", True, 53)
+    m, _ = run(codes, scales, z, x, y, 4000, 128)
+    lanes = []
+    for _ in range(3):
+        lanes.append((torch.cuda.Stream(), torch.zeros_like(y), rf.QuantWorkspace(m, C, x.dtype)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for stream, out, ws in lanes:
+            rf.moe_quant_linear(m, x, C, out, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, out, _ in lanes:
+        assert torch.equal(out, y)
+
+
 def test_constant_sign_activations_lose_nothing():
     """All activations positive: sums of q alone would be far larger than the
     result."""
