@@ -440,13 +440,15 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 
 // Four tokens whose operand rows are next to each other (t, t + 4, t + 8,
 // t + 12 of a tile), so that four lanes write 64 contiguous bytes: their
-// largest values, then their terms.  FITS: the rows (up to 8192 columns) stay
-// in registers between the two, else they are read twice (2048 tokens x 7168
-// in fp32: 12 us more).
+// largest values, then their terms.  NB blocks of 8 columns a thread (0: any
+// number): the rows, up to 8192 or 16384 columns, stay in registers between the
+// two, else they are read twice (2048 tokens x 7168 in fp32: 12 us more; 64
+// unaligned tokens x 10001: 11.6 us, 9.0 in registers).
 constexpr int kTermWG = 1024, kTermBlocks = kTermWG / 4;
-template <int DT, bool FITS>
+template <int DT, int NB>
 __global__ __launch_bounds__(kTermWG) void k_qterms(QArgs a) {
-  constexpr int B = DT == MOE_DT_F32 ? 4 : 2, NB = 4;
+  constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
+  constexpr bool FITS = NB > 0;
   __shared__ uint32_t s_max[kTermWG / 64][4];
   const int tid = threadIdx.x, lane = tid & 63, k = tid & 3;
   const int t0 = blockIdx.x / 4 * 16, t = t0 + blockIdx.x % 4 + 4 * k;
@@ -1233,8 +1235,22 @@ __global__ __launch_bounds__(256) void k_qreduce(QArgs a) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t n = (int64_t)a.C * a.N;
   if (i >= n) return;
+  // eight ranges in flight, added in order (500 x 100 results of 19 ranges: 6.6
+  // us one by one, 4.2)
   float v = 0.0f;
-  for (int s = 0; s < a.splits; ++s) v += a.part[s * n + i];
+  int s = 0;
+  for (; s + 8 <= a.splits; s += 8) {
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = a.part[(s + j) * n + i];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v += q[j];
+  }
+  float q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = s + j < a.splits ? a.part[(s + j) * n + i] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v += q[j];
   put(a, (int)(i / a.N), (int)(i % a.N), v);
 }
 
@@ -1426,8 +1442,10 @@ moe_status launch_quant(QArgs a, const QPlan& p, bool tr, int ss, hipStream_t st
     s = a.C <= 8 ? launch_few<DT, 8>(a, tr, ss, p.wk, grid, st) : launch_few<DT, 16>(a, tr, ss, p.wk, grid, st);
   } else {
     const dim3 tgrid((unsigned)p.ct * 4);
-    if (p.nch <= 4 * kTermBlocks * 8 / kQChunk) hipLaunchKernelGGL((k_qterms<DT, true>), tgrid, dim3(kTermWG), 0, st, a);
-    else hipLaunchKernelGGL((k_qterms<DT, false>), tgrid, dim3(kTermWG), 0, st, a);
+    constexpr int kTermChunks = kTermBlocks * 8 / kQChunk;         // of one block a thread
+    if (p.nch <= 4 * kTermChunks) hipLaunchKernelGGL((k_qterms<DT, 4>), tgrid, dim3(kTermWG), 0, st, a);
+    else if (p.nch <= 8 * kTermChunks) hipLaunchKernelGGL((k_qterms<DT, 8>), tgrid, dim3(kTermWG), 0, st, a);
+    else hipLaunchKernelGGL((k_qterms<DT, 0>), tgrid, dim3(kTermWG), 0, st, a);
     a.row_groups = p.row_groups;
     const dim3 grid((unsigned)(p.row_groups * p.tok_groups), (unsigned)p.splits);
     s = !p.wide ? launch_gemm<P, 2, 1, 1>(a, tr, ss, grid, st)

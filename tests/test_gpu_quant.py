@@ -99,6 +99,8 @@ CASES = [
     # wider than a token's terms keep in registers or in LDS
     (20, 48, 8200, 32, "f32", "f32", True),
     (18, 33, 9001, 128, "bf16", "bf16", True),
+    (20, 40, 16500, 64, "f32", "f32", True),
+    (19, 30, 17001, 128, "bf16", "bf16", False),
     (1, 20, 12289, 128, "f32", "bf16", True),
     (1, 20, 24577, 64, "f16", "f16", False),
     # waves that share a row tile: eight, none, two; one or several slices to a
