@@ -125,7 +125,7 @@ __device__ __forceinline__ View view_rows(const QArgs& a, int n0, int rows, int 
   return v;
 }
 
-constexpr uint32_t kOutside = 0x80000000u;   // an offset past every view
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every view of 16 rows
 
 // N (up to 4) of a wave's chunks, c, c + step, ...: codes, and as stored the
 // scales and zero points of all of them, for which a lane reads not its own
@@ -954,11 +954,14 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
         const int c = 4 * kb + te + e;
         g = (int)(((uint32_t)(c < a.nch ? c : a.nch - 1) * a.gmul) >> 20);
       }
-      // past the last group (units past the last column): a scale of 0
-      const uint32_t out = live && (!TR || g < a.ng) ? 0u : kOutside;
-      if (SS == 4) ns[e] = __builtin_amdgcn_raw_buffer_load_b32(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
-      else ns[e] = __builtin_amdgcn_raw_buffer_load_b16(v.scales, (int)((v.vs + SS * g) | out), 0, 0);
-      nz[e] = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, (int)((v.vz + a.zero_step * g) | out), 0, 0);
+      // past the last group (units past the last column): a scale of 0.  A view
+      // of 256 rows may pass 2^31 bytes, but not this offset
+      constexpr uint32_t nowhere = 0xFFFFFFFCu;
+      const bool there = live && (!TR || g < a.ng);
+      const int os = (int)(there ? v.vs + SS * g : nowhere), oz = (int)(there ? v.vz + a.zero_step * g : nowhere);
+      if (SS == 4) ns[e] = __builtin_amdgcn_raw_buffer_load_b32(v.scales, os, 0, 0);
+      else ns[e] = __builtin_amdgcn_raw_buffer_load_b16(v.scales, os, 0, 0);
+      nz[e] = __builtin_amdgcn_raw_buffer_load_b8(v.zeros, oz, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };

@@ -364,7 +364,8 @@ def test_largest_pitches(C):
     want, tol = expect(codes, scales, z, x, K, G)
 
     def spread(t, pitch):
-        wide = torch.empty((t.shape[0], pitch), dtype=t.dtype, device="cuda")[:, :t.shape[1]]
+        behind = float("nan") if t.is_floating_point() else 255
+        wide = torch.full((t.shape[0], pitch), behind, dtype=t.dtype, device="cuda")[:, :t.shape[1]]
         wide.copy_(t)
         return wide
 
@@ -379,7 +380,8 @@ def test_scales_past_two_gigabytes_of_a_workgroup():
     """The larger matrix tile's 256 rows of fp32 scales, 2^22 elements apart."""
     C, N, K, G = 4096, 512, 160, 32
     codes, scales, z, x, y = make(C, N, K, G, "f32", "f32", False, 33)
-    wide = torch.empty((N, 1 << 22), device="cuda")[:, :scales.shape[1]]
+    # what lies between the rows of scales is no number
+    wide = torch.full((N, 1 << 22), float("nan"), device="cuda")[:, :scales.shape[1]]
     wide.copy_(scales)
     run(codes, wide, z, x, y, K, G)
     at = torch.arange(0, C, 97)
