@@ -313,7 +313,10 @@ size_t moe_quant_workspace_size(const moe_quant_matrix *m, int32_t dtype, int32_
  *  accumulate, the sum with the old y) is rounded once to its type.  fp32 and
  *  bf16 activations enter as fp16 terms under a power-of-two scale per token and
  *  slab of columns (two terms for fp32: an element keeps 22 bits, and at
- *  least 2^-38 of its slab's largest).  The result does not depend on what
+ *  least 2^-38 of its slab's largest).  However large the scales and small the
+ *  activations, what fp32 can hold is not lost to that power: a sum that leaves
+ *  fp32's range under it is formed anew in 64 bits (slower, where it happens:
+ *  scales past about 2^88).  The result does not depend on what
  *  ran before: the same call gives the same bits. */
 moe_status moe_quant_linear(const moe_quant_matrix *m, int32_t dtype, const void *x,
                             int64_t x_pitch, int32_t C, void *y, int64_t y_pitch,

@@ -37,6 +37,7 @@
 //              from memory to registers; k_qreduce adds split column ranges
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
+#include <limits.h>
 
 #include "common.h"
 
@@ -78,7 +79,8 @@ struct QArgs {
   int64_t y_pitch;
   int y_vec;                          // rows of y are aligned to four of its elements
   int accumulate;
-  float* inv;                         // [C]: takes the terms' power of two out again
+  float* inv;                         // [C]: takes the terms' power of two out again; a token
+                                      // that is not finite: -1 (its terms are not scaled)
   uint8_t* terms;                     // [P][C / 16][nch][16 blocks][16 tokens][16 bytes]
   float* part;                        // [splits][C][N]
   uint32_t* tickets;                  // few tokens: arrivals per group of rows, left at zero
@@ -163,32 +165,37 @@ __device__ __forceinline__ void load_quad(const QArgs& a, const View& v, int c, 
   const uint32_t out = live ? 0u : kOutside;
   if (TR && a.scales_vec) {
     // the chunk's four (G 32) or two scales and zero points in one load each
+    // (the zero points' first: what follows waits for the scales)
     if (a.gshift == 5) {
       const int os = (int)((v.vs + 4 * SS * cq) | out);
+      const uint32_t z = __builtin_amdgcn_raw_buffer_load_b32(v.zeros, (int)((v.vz + 4 * a.zero_step * cq) | out), 0, 0);
       if (SS == 4) {
         const auto s = __builtin_amdgcn_raw_buffer_load_b128(v.scales, os, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = s[e];
       } else {
         const auto s = __builtin_amdgcn_raw_buffer_load_b64(v.scales, os, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = (e & 1) ? s[e >> 1] >> 16 : s[e >> 1] & 0xFFFFu;
       }
-      const uint32_t z = __builtin_amdgcn_raw_buffer_load_b32(v.zeros, (int)((v.vz + 4 * a.zero_step * cq) | out), 0, 0);
 #pragma unroll
       for (int e = 0; e < Quad<N, TR>::S; ++e) u.z[e] = (z >> (8 * e)) & 0xFFu;
     } else {
       const int os = (int)((v.vs + 2 * SS * cq) | out);
+      const uint32_t z = __builtin_amdgcn_raw_buffer_load_b16(v.zeros, (int)((v.vz + 2 * a.zero_step * cq) | out), 0, 0);
       if (SS == 4) {
         const auto s = __builtin_amdgcn_raw_buffer_load_b64(v.scales, os, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = s[e >> 1];
       } else {
         const uint32_t s = __builtin_amdgcn_raw_buffer_load_b32(v.scales, os, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int e = 0; e < Quad<N, TR>::S; ++e) u.s[e] = e >> 1 ? s >> 16 : s & 0xFFFFu;
       }
-      const uint32_t z = __builtin_amdgcn_raw_buffer_load_b16(v.zeros, (int)((v.vz + 2 * a.zero_step * cq) | out), 0, 0);
 #pragma unroll
       for (int e = 0; e < Quad<N, TR>::S; ++e) u.z[e] = e >> 1 ? z >> 8 : z & 0xFFu;
     }
@@ -205,11 +212,11 @@ __device__ __forceinline__ void load_quad(const QArgs& a, const View& v, int c, 
 }
 
 template <int SS>
-__device__ __forceinline__ float scale_of(const QArgs& a, uint32_t s) {
+__device__ __forceinline__ float scale_of(int bf16, uint32_t s) {
   if (SS == 4) return __uint_as_float(s);
   // both readings and a mask: a branch would cost more
   const uint32_t h = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)s));
-  const uint32_t b = a.scale_bf16 ? 0xFFFFFFFFu : 0u;
+  const uint32_t b = bf16 ? 0xFFFFFFFFu : 0u;
   return __uint_as_float(((s << 16) & b) | (h & ~b));
 }
 
@@ -279,13 +286,13 @@ __device__ __forceinline__ void quad_scales(const QArgs& a, const Quad<N, TR>& u
   if (TR) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      s[e] = __float_as_uint(scale_of<SS>(a, u.s[e]));
+      s[e] = __float_as_uint(scale_of<SS>(a.scale_bf16, u.s[e]));
       z[e] = zero_pair(u.z[e]);
     }
     transpose4(s);
     transpose4(z);
   } else {
-    spread4(__float_as_uint(scale_of<SS>(a, u.s[0])), s);
+    spread4(__float_as_uint(scale_of<SS>(a.scale_bf16, u.s[0])), s);
     spread4(zero_pair(u.z[0]), z);
   }
 }
@@ -487,7 +494,7 @@ __global__ __launch_bounds__(kTermWG) void k_qterms(QArgs a) {
     finite = mx < 0x7F800000u;
   }
   if (!live) return;
-  if (tid < 4) a.inv[t] = inv;
+  if (tid < 4) a.inv[t] = finite ? inv : -1.0f;
   const int ct = (a.C + 15) / 16;
   const int64_t plane = (int64_t)ct * a.nch * kQTermBytes;
   uint8_t* out = a.terms + (int64_t)(t >> 4) * a.nch * kQTermBytes + token_row(t & 15) * 16;
@@ -560,6 +567,69 @@ __device__ __forceinline__ void put4(const QArgs& a, int t, int n, float4 v) {
   if (a.x_dt == MOE_DT_F32) put4<MOE_DT_F32>(a, t, n, v);
   else if (a.x_dt == MOE_DT_BF16) put4<MOE_DT_BF16>(a, t, n, v);
   else put4<MOE_DT_F16>(a, t, n, v);
+}
+
+// ---------------------------------------------------------------------------
+// Results beyond the scaled sums' range
+// ---------------------------------------------------------------------------
+// The sums are scaled while their activations are raised to just below 2^15, and
+// the token's power of two is taken out last.  Very small activations (raised by
+// up to 2^126) against very large scales so leave fp32's range with a result
+// inside it.  Every kernel looks at its results, and where one of a finite token
+// is not finite this forms its columns k0 (a multiple of 8) to k1 - 1 anew, in 64
+// bits: fp32 inputs neither overflow nor vanish there, and what is still infinite
+// or NaN comes of infinite scales or of a sum past fp32.  Folding the power into
+// the scale instead would lose small scales, and doing so per token would cost a
+// product per result and group.
+//
+// The arguments are read from the kernel's own argument segment (every kernel has
+// QArgs first), by a pointer that the compiler cannot see through: kept in scalar
+// registers over the whole kernel for this they took those of its loop.
+typedef const __attribute__((address_space(4))) QArgs* QArgsPtr;
+__device__ __forceinline__ QArgsPtr args_again() {
+  QArgsPtr a = (QArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(a));
+  return a;
+}
+template <int DT, bool TR, int SS>
+__device__ __forceinline__ float sum_in_f64(int t, int n, int k0, int k1) {
+  const QArgsPtr a = args_again();
+  const uint8_t* code = a->codes + (int64_t)n * a->code_pitch;
+  const uint8_t* scale = a->scales + (int64_t)n * a->scale_pitch;
+  const uint8_t* zero = a->zeros ? a->zeros + (int64_t)n * a->zero_pitch : nullptr;
+  const int64_t row = (int64_t)t * a->x_pitch;
+  const bool wide = DT == 0 ? a->x_dt == MOE_DT_F32 : DT == MOE_DT_F32;
+  k1 = k1 < a->K ? k1 : a->K;
+  double y = 0.0;
+#pragma unroll 1
+  for (int k = k0; k < k1; k += 8) {            // eight codes: one group
+    const int g = TR ? k >> a->gshift : (int)(((uint32_t)(k / kQChunk) * a->gmul) >> 20);
+    const uint32_t s = SS == 4 ? reinterpret_cast<const uint32_t*>(scale)[g] : reinterpret_cast<const uint16_t*>(scale)[g];
+    const int z = zero ? zero[g] : 8;
+    const uint32_t q = *reinterpret_cast<const uint32_t*>(code + k / 2);   // up to the end of a 16-byte unit
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = row + (k + i < k1 ? k + i : k1 - 1);
+      const float x = wide ? static_cast<const float*>(a->x)[at]
+                           : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a->x)[at] << 16);
+      if (k + i < k1) sum += (double)x * (double)((int)((q >> (4 * i)) & 15u) - z);
+    }
+    y += (double)scale_of<SS>(a->scale_bf16, s) * sum;
+  }
+  return (float)y;
+}
+// v unless it has left the range (`spoilt`: the token is not finite; asked only
+// then).  fp16 activations are not raised: theirs stays.  DT 0: as the call says.
+// The branch is the wave's: one scalar test where nothing has.
+template <int DT, bool TR, int SS, class F>
+__device__ __forceinline__ float in_range(float v, F spoilt, int t, int n, int k0, int k1) {
+  if (DT == MOE_DT_F16) return v;
+  const bool left = !(fabsf(v) < INFINITY);
+  if (__builtin_expect(__ballot(left) != 0, 0)) {
+    if (left && !spoilt()) v = sum_in_f64<DT, TR, SS>(t, n, k0, k1);
+  }
+  return v;
 }
 
 // ---------------------------------------------------------------------------
@@ -664,6 +734,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
     for (int w = 0; w < kQWaves; ++w) mx = s_max[w] > mx ? s_max[w] : mx;
     term_scale(mx, m, inv);
     finite = mx < 0x7F800000u;
+    inv = finite ? inv : -inv;                            // its sign is kept for the results
   }
   auto write = [&](int b, const Raw<DT>& r) {
     half8 hi, lo;
@@ -684,7 +755,10 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
   __syncthreads();
 
   int parity = 0;
-  for (int cg = blockIdx.x; cg < a.row_groups; cg += gridDim.x) {
+  // bit i: this thread's result in the workgroup's i-th tile group left the range
+  // (at most 64 of them: 2^22 rows over 512 workgroups of 128)
+  uint64_t left = 0, bit = 1;
+  for (int cg = blockIdx.x; cg < a.row_groups; cg += gridDim.x, bit <<= 1) {
     float acc[1] = {0.0f};
     for (int ci = 0; ci < a.spt; ++ci) {
 #pragma unroll
@@ -714,8 +788,21 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
     if ((ks ? tid < tiles * 16 : lane < 16) && n < a.N) {
       float s = 0.0f;
       for (int w = 0; w < wk; ++w) s += red[((tile << ks) + w) * 16 + (tid & 15)];
-      put<DT>(a, 0, n, s * inv);
+      s *= fabsf(inv);
+      if (DT != MOE_DT_F16 && !(fabsf(s) < INFINITY) && inv > 0.0f) left |= bit;
+      else put<DT>(a, 0, n, s);
     }
+  }
+  if (DT == MOE_DT_F16 || __ballot(left != 0) == 0) return;
+  // behind the loop, whose scalars this code would spill
+  const QArgsPtr b = args_again();
+  for (; left; left &= left - 1) {
+    const int cg = blockIdx.x + (__ffsll((long long)left) - 1) * gridDim.x;
+    const int n = (cg * (kQWaves >> b->ks) + (b->ks ? tid >> 4 : tid >> 6)) * 16 + (tid & 15);
+    const float s = sum_in_f64<DT, TR, SS>(0, n, 0, INT_MAX);
+    QArgs c;
+    c.y = b->y; c.y_pitch = b->y_pitch; c.accumulate = b->accumulate;
+    put<DT>(c, 0, n, s);
   }
 }
 
@@ -731,10 +818,11 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
 // after its loads have arrived.  7 tokens, bf16, 7168 x 3584 in groups of 32:
 // 11.5 us, of which unpacking and transposing are 3.3, and latencies (x, terms,
 // the hand-off of ranges) most of the rest.
+// Eight waves to a row tile are for two workgroups a CU: four waves to a SIMD.
 constexpr int few_slice(int P, int TOK, int WK) { return WK == 8 ? 65536 / (P * TOK * 2 * kQChunk) : 8; }
 
 template <int DT, int TOK, int WK, bool TR, int SS>
-__global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
+__global__ __launch_bounds__(kQWG, WK == 8 ? 4 : 2) void k_qfew(QArgs a) {
   constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
   constexpr int NR = TOK / 4;
   constexpr int kQSlice = few_slice(P, TOK, WK), kQSliceCols = kQSlice * kQChunk;
@@ -744,6 +832,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
   constexpr int NU = kQSlice / WK, NQ = NU > 4 ? 4 : NU, QN = NU / NQ;   // a wave's chunks, as quads
   extern __shared__ __align__(16) uint8_t s_x[];          // [P][blocks][TOK] of 16 bytes
   __shared__ uint32_t s_max[kQWaves][TOK];
+  __shared__ bool s_spoilt[TOK];                          // tokens that are not finite in these slices
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int row = lane & 15, quarter = lane >> 4;
   const int kw = wave % WK;
@@ -781,6 +870,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
   // the token of operand row `row`; rows beyond TOK tokens repeat one
   const uint8_t* frag0 = s_x + 16 * (TOK == 8 ? (row >> 2) + 4 * (row & 1) : row_token(row)) +
                          16 * TOK * (TR ? 1 : 4) * quarter;
+  bool spoilt = false;
   float sum[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) sum[r] = 0.0f;
@@ -805,6 +895,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
       float unused;
       term_scale(mx, m, unused);
       finite = mx < 0x7F800000u;
+      spoilt |= !finite;
     }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -848,14 +939,19 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) sum[r] += inv[r] * acc[r];
   }
-  auto out = [&](int tok, int n, float val) {
+  if (tid < TOK) s_spoilt[tid] = spoilt;
+  if (WK == 1) __syncthreads();
+  const int k0 = s0 * kQSliceCols, k1 = s1 * kQSliceCols;
+  auto out = [&](int r, int n, float val) {               // of token 4 r + quarter
+    const int tok = 4 * r + quarter;
     if (tok >= a.C || n >= a.N) return;
+    val = in_range<DT, TR, SS>(val, [&] { return s_spoilt[tok]; }, tok, n, k0, k1);
     if (a.splits > 1) store_coherent(a.part + ((int64_t)blockIdx.y * a.C + tok) * a.N + n, val);
     else put<DT>(a, tok, n, val);
   };
   if (WK == 1) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) out(4 * r + quarter, n0 + row, sum[r]);
+    for (int r = 0; r < NR; ++r) out(r, n0 + row, sum[r]);
   } else {
     // the waves that shared a tile's chunks add up, in order
     float* red = reinterpret_cast<float*>(s_x);
@@ -864,11 +960,11 @@ __global__ __launch_bounds__(kQWG, 2) void k_qfew(QArgs a) {
     for (int r = 0; r < NR; ++r) red[(wave * NR + r) * 64 + lane] = sum[r];
     __syncthreads();
     for (int i = tid; i < kQWaves / WK * NR * 64; i += kQWG) {
-      const int l = i & 63, r = (i >> 6) % NR, tile = (i >> 6) / NR;
+      const int r = (i >> 6) % NR, tile = (i >> 6) / NR;  // i % 64 is the lane
       float val = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WK; ++w) val += red[((tile * WK + w) * NR + r) * 64 + l];
-      out(4 * r + (l >> 4), (blockIdx.x * (kQWaves / WK) + tile) * 16 + (l & 15), val);
+      for (int w = 0; w < WK; ++w) val += red[((tile * WK + w) * NR + r) * 64 + lane];
+      out(r, (blockIdx.x * (kQWaves / WK) + tile) * 16 + row, val);
     }
   }
   // the last of the rows' workgroups to arrive adds their ranges up, in order
@@ -977,7 +1073,7 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
 #pragma unroll
     for (int e = 0; e < G::entries; ++e)
       *reinterpret_cast<uint2*>(t + ((te + e) * G::rows + tr) * 8) =
-          make_uint2(__float_as_uint(scale_of<SS>(a, ts[e])), zero_pair(tz[e]));
+          make_uint2(__float_as_uint(scale_of<SS>(a.scale_bf16, ts[e])), zero_pair(tz[e]));
   };
   // At every chunk c (just opened): the next block's table is written (a
   // block's four chunks write the same, without a branch), and at a block's
@@ -1222,8 +1318,19 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
     if (c >= G::rows) continue;
     const float inv = a.inv[tok];
     float4 v = *reinterpret_cast<const float4*>(res + k * kPitch + c);
-    v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+    const float up = fabsf(inv);
+    v.x *= up; v.y *= up; v.z *= up; v.w *= up;
     const int n = nw + c;
+    // infinite or NaN among them
+    if (__builtin_expect(__ballot(0.0f * v.x + 0.0f * v.y + 0.0f * v.z + 0.0f * v.w != 0.0f) != 0, 0)) {
+      const int k0 = c0 * kQChunk, k1 = c1 * kQChunk;
+#pragma unroll 1
+      for (int i = 0; i < 4 && n + i < a.N; ++i) {
+        const float e = in_range<0, TR, SS>(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w,
+                                         [&] { return inv < 0.0f || a.x_dt == MOE_DT_F16; }, tok, n + i, k0, k1);
+        v = make_float4(i == 0 ? e : v.x, i == 1 ? e : v.y, i == 2 ? e : v.z, i == 3 ? e : v.w);
+      }
+    }
     if (a.splits > 1) {
       float* o = a.part + ((int64_t)blockIdx.y * a.C + tok) * a.N + n;
       if (a.N % 4 == 0 && n < a.N) {
