@@ -297,11 +297,11 @@ typedef struct {
   int64_t zero_pitch;    /* bytes between rows                                */
 } moe_quant_matrix;
 
-/* Workspace bytes of moe_quant_linear for C tokens of the type `dtype` (at
- * least 256; 0 outside the supported range).  It must be initialised once with
- * moe_workspace_init, and one workspace serves every matrix, type and number of
- * tokens that it is large enough for, one call at a time; it serves
- * moe_quant_linear alone, since it keeps state between calls. */
+/* Workspace bytes of moe_quant_linear for up to C tokens of the type `dtype` (at
+ * least 256; 0 outside the supported range): it never falls as C rises.  The
+ * workspace must be initialised once with moe_workspace_init, and one serves every
+ * matrix, type and number of tokens that it is large enough for, one call at a
+ * time; it serves moe_quant_linear alone, since it keeps state between calls. */
 size_t moe_quant_workspace_size(const moe_quant_matrix *m, int32_t dtype, int32_t C);
 
 /* y[c][n] = sum_k x[c][k] W[n][k], or y += where `accumulate` is not 0, for

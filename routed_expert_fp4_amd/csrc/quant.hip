@@ -1482,6 +1482,19 @@ QPlan quant_plan(const moe_quant_matrix* m, int dtype, int C) {
   return p;
 }
 
+// The most that any number of tokens up to C needs.  A plan's partial results come
+// and go with its ranges, so fewer tokens may need more than C (bf16, 7168 x 3584:
+// 256 tokens 16.5 MB, 257 2 MB).  From 17 tokens on tile and ranges depend on the
+// tiles of 64 tokens alone, so that among equal ones the most tokens need the most.
+size_t quant_workspace(const moe_quant_matrix* m, int dtype, int C) {
+  size_t most = quant_plan(m, dtype, C).total;
+  for (int c = 1; c < C; c = c < MOE_MAX_DECODE_TOKENS ? c + 1 : c / 64 * 64 + 64) {
+    const size_t n = quant_plan(m, dtype, c).total;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
 template <int DT>
 void launch_one(const QArgs& a, bool tr, int ss, int grid, size_t lds, hipStream_t st) {
   if (tr) {
@@ -1582,7 +1595,7 @@ extern "C" {
 
 size_t moe_quant_workspace_size(const moe_quant_matrix* m, int32_t dtype, int32_t C) {
   if (matrix_status(m) != MOE_OK || !dtype_ok(dtype) || C < 1 || C > MOE_MAX_TOKENS) return 0;
-  return quant_plan(m, dtype, C).total;
+  return quant_workspace(m, dtype, C);
 }
 
 moe_status moe_quant_linear(const moe_quant_matrix* m, int32_t dtype, const void* x,
