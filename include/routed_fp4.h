@@ -362,7 +362,8 @@ moe_status moe_expert_counts(const int32_t *topk_idx, int32_t C, int32_t k, int3
                              const int32_t *seq_off, int32_t S, const uint8_t *token_mask,
                              int32_t *counts, int32_t *tokens, int32_t accumulate, void *stream);
 
-/* Workspace of moe_balance_fwd (0 outside the supported range); it must be
+/* Workspace of moe_balance_fwd for up to C tokens, E experts and S sequences (0
+ * outside the supported range): it never falls as one of them rises.  It must be
  * initialised once with moe_workspace_init, serves every call that it is large
  * enough for, one at a time, and moe_balance_fwd alone. */
 size_t moe_balance_workspace_size(int32_t C, int32_t E, int32_t S);

@@ -82,16 +82,27 @@ __device__ __forceinline__ int seq_of(const int32_t* off, int t, int S, int C) {
 // 93.4 us).  One slot for up to 32 tokens, whose workgroup writes the loss (16
 // tokens: 11.1 us in one slot, 13.7 in two; 32: 13.9 and 13.8; 64: 19.2 and
 // 14.0).
+__host__ __device__ inline int slot_limit(int s) { return s < 5 ? 256 : 1024; }
 __host__ __device__ inline int slot_shift(int C, int S) {
   if (S == 1 && C <= kOneSlot) return 5;
   int s = 3;
-  while (s < 10 && (C >> s) > (s < 5 ? 256 : 1024)) ++s;
+  while (s < 10 && (C >> s) > slot_limit(s)) ++s;
   return s;
 }
 // Slots of sequence s: from (off[s] >> shift) + s, one per TB tokens.  The
 // next sequence's first slot is at least that many further on, so slots need
 // no prefix sum over the sequences.
 __host__ __device__ inline int num_slots(int C, int S) { return (C >> slot_shift(C, S)) + S; }
+// The most slots of a batch of up to C tokens, which a workspace is sized by: they
+// fall where the slots grow (32799 tokens are 1024 full slots, 32800 are 512).
+inline int most_slots(int C, int S) {
+  int n = num_slots(C, S);
+  for (int s = 3; s < 10; ++s) {
+    const int last = ((slot_limit(s) + 1) << s) - 1;       // the most tokens in slots of 2^s
+    if (last < C && num_slots(last, S) > n) n = num_slots(last, S);
+  }
+  return n;
+}
 
 // Tickets of k_bal_final, each in a cache line of its own: one for up to twice
 // kTickets workgroups; for more, kTickets that they share out among them and one
@@ -107,7 +118,7 @@ inline int expert_blocks(int E) { return (E + 63) / 64; }
 inline BalWs bal_ws(int C, int E, int S) {
   BalWs W;
   size_t o = 0;
-  const size_t n = (size_t)num_slots(C, S);
+  const size_t n = (size_t)most_slots(C, S);
   W.ctrl = o; o = align256(o + (1 + kTickets) * kTicketStride * sizeof(uint32_t));
   W.psum = o; o = align256(o + n * E * sizeof(float));
   W.pcnt = o; o = align256(o + n * E * sizeof(uint16_t));

@@ -3,6 +3,7 @@ the same bits as a workspace of each call's own."""
 import pytest
 
 from gpu_util import say
+from test_gpu_load import fwd, make as make_load
 from test_gpu_quant import make, run
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +33,19 @@ def test_dense_product_of_fewer_tokens(N, K, G, xt, largest):
         own = torch.full_like(y[:C], float("nan"))
         run(codes, scales, z, x[:C], own, K, G)
         assert torch.equal(y[:C], own), C
+
+
+def test_balance_of_other_batches():
+    """Batches of one slot and of many, and both sides of the number of
+    workgroups from which arrivals are shared out over several tickets."""
+    import routed_expert_fp4_amd as rf
+    E, k = 896, 4
+    ws = rf.BalanceWorkspace(40000, E, 60)
+    for C, S in [(40000, 1), (32768, 1), (300, 47), (20, 1), (2047, 8), (900, 60), (2056, 9), (1000, 10), (32, 1),
+                 (4111, 47), (33, 2), (40000, 1), (300, 47)]:
+        say(f"[balance] {C} tokens, {S} sequences")
+        logits, idx, seq, mask = make_load(C, E, k, S, True, seed=C)
+        a, _ = fwd(logits, idx, E, 0.1, "sigmoid", seq, mask, S, ws)
+        b, _ = fwd(logits, idx, E, 0.1, "sigmoid", seq, mask, S)
+        for n in ("counts", "tokens", "probs", "loss"):
+            assert torch.equal(a[n], b[n]), (C, S, n)

@@ -1,5 +1,5 @@
 """A workspace for a number of tokens serves every smaller number: the sizes
-never fall as tokens rise (no GPU)."""
+never fall as tokens, sequences or experts rise (no GPU)."""
 import ctypes
 import os
 
@@ -28,3 +28,25 @@ def test_dense_product(rf, N, K, G):
             n = rf.lib().moe_quant_workspace_size(ctypes.byref(m), dtype, C)
             assert n >= last, f"{C} tokens need {n} bytes, {C - 1} {last} (type {dtype})"
             last = n
+
+
+@pytest.mark.parametrize("E", [1, 64, 896, 1024])
+@pytest.mark.parametrize("S", [1, 2, 61, 5000, 65535])
+def test_balance_by_tokens(rf, E, S):
+    sizes = list(range(1, 5000)) + list(range(5000, 70000, 7)) + [1 << 17, (1 << 20) - 1, 1 << 20]
+    sizes += [(limit << s) + d for s in range(3, 11) for limit in (256, 1024) for d in (-1, 0, (1 << s) - 1, 1 << s)]
+    last, before = 1, 0
+    for C in sorted(c for c in set(sizes) if c <= rf.MOE_MAX_BATCH_TOKENS):
+        n = rf.lib().moe_balance_workspace_size(C, E, S)
+        assert n >= last, f"{C} tokens need {n} bytes, {before} {last}"
+        last, before = n, C
+
+
+@pytest.mark.parametrize("C", [1, 32, 33, 2056, 40000, 1 << 20])
+def test_balance_by_sequences_and_experts(rf, C):
+    size = rf.lib().moe_balance_workspace_size
+    for E in (1, 64, 65, 1024):
+        at = [size(C, E, S) for S in (1, 2, 3, 128, 65535)]
+        assert at == sorted(at)
+    at = [size(C, E, 9) for E in range(1, 1025)]
+    assert at == sorted(at)
