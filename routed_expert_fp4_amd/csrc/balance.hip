@@ -26,7 +26,8 @@
 //   k_bal_final   per sequence and 64 experts: the slots added in order, the
 //                 loss from the last workgroup to arrive
 //   k_bal_bwd     a few consecutive tokens per wave
-//   k_count_fill / k_count   counts without logits
+//   k_count       counts without logits: a workgroup per sequence, or several
+//   k_count_fill / k_count_slots   counts of large packed batches, in slots
 //   k_route_bwd   two, four or eight tokens per wave
 // 65536 tokens x 448, both passes: 84 us, three passes over 117 MB at 4.2 TB/s.
 #include "common.h"
@@ -551,28 +552,18 @@ __global__ __launch_bounds__(256) void k_count_fill(int32_t* counts, int32_t* to
   if (tokens && i < S) tokens[i] = 0;
 }
 
-// Workgroup (s, j): the j-th of gridDim.x parts of sequence s.  One part:
-// the row is written (or added to) as a whole; more: the parts' integer
-// counts are added to the row by atomics, whose order does not matter.  Bound
-// by atomics in LDS on popular experts (65536 tokens x 16 over 896: 7.5 us).
+// A workgroup's tokens t0 .. t1 - 1 (k times their number at most 2^25): their
+// choices into s_cnt, the live ones into s_tok (where TOK).  Each choice waits for
+// its mask byte.
 constexpr int kCntWG = 1024;
-__global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int32_t* off, const uint8_t* mask,
-                                                  int C, int k, uint32_t kmul, int E, int S, int32_t* counts,
-                                                  int32_t* tokens, int accumulate) {
-  __shared__ int32_t s_cnt[MOE_MAX_EXPERTS];
-  __shared__ int32_t s_tok;
-  const int tid = threadIdx.x, threads = blockDim.x, s = blockIdx.y, parts = gridDim.x;
-  const int b = seq_at(off, s, S, C), end = seq_at(off, s + 1, S, C);
+__device__ __forceinline__ void count_tokens(const int32_t* idx, const uint8_t* mask, int t0, int t1, int k, uint32_t kmul,
+                                             int E, bool tok, int32_t* s_cnt, int32_t* s_tok) {
+  const int tid = threadIdx.x, threads = blockDim.x;
   for (int e = tid; e < E; e += threads) s_cnt[e] = 0;
-  if (tid == 0) s_tok = 0;
-  const int len = end > b ? end - b : 0;
-  const int per = (len + parts - 1) / parts;
-  const int t0 = b + ((int64_t)per * blockIdx.x < len ? per * (int)blockIdx.x : len);
-  const int t1 = t0 + per < end ? t0 + per : end;
-  const int n = (t1 - t0) * k;                 // at most 2^25
+  if (tid == 0) *s_tok = 0;
+  const int n = (t1 - t0) * k;
   const int32_t* at = idx + (int64_t)t0 * k;
   __syncthreads();
-  // four choices a thread in flight
   for (int i0 = tid; i0 < n; i0 += 4 * threads) {
     int e[4];
 #pragma unroll
@@ -585,21 +576,70 @@ __global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int3
     for (int j = 0; j < 4; ++j)
       if (e[j] >= 0 && e[j] < E) atomicAdd(&s_cnt[e[j]], 1);
   }
-  if (tokens) {
+  if (tok) {
     int live = 0;
     for (int t = t0 + tid; t < t1; t += threads) live += mask ? mask[t] != 0 : 1;
-    if (live) atomicAdd(&s_tok, live);
+    if (live) atomicAdd(s_tok, live);
   }
   __syncthreads();
+}
+// The workgroup's counts added to a row by atomics (integers: any order gives
+// the same).
+__device__ __forceinline__ void add_counts(const int32_t* s_cnt, int s_tok, int E, int32_t* row, int32_t* tok) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  for (int e = tid; e < E; e += threads)
+    if (s_cnt[e]) atomicAdd(&row[e], s_cnt[e]);
+  if (tok && tid == 0 && s_tok) atomicAdd(tok, s_tok);
+}
+
+// Workgroup (s, j): the j-th of gridDim.x parts of sequence s.  One part:
+// the row is written (or added to) as a whole.
+__global__ __launch_bounds__(kCntWG) void k_count(const int32_t* idx, const int32_t* off, const uint8_t* mask,
+                                                  int C, int k, uint32_t kmul, int E, int S, int32_t* counts,
+                                                  int32_t* tokens, int accumulate) {
+  __shared__ int32_t s_cnt[MOE_MAX_EXPERTS];
+  __shared__ int32_t s_tok;
+  const int tid = threadIdx.x, threads = blockDim.x, s = blockIdx.y, parts = gridDim.x;
+  const int b = seq_at(off, s, S, C), end = seq_at(off, s + 1, S, C);
+  const int len = end > b ? end - b : 0;
+  const int per = (len + parts - 1) / parts;
+  const int t0 = b + ((int64_t)per * blockIdx.x < len ? per * (int)blockIdx.x : len);
+  const int t1 = t0 + per < b + len ? t0 + per : b + len;
+  count_tokens(idx, mask, t0, t1, k, kmul, E, tokens != nullptr, s_cnt, &s_tok);
   int32_t* row = counts + (size_t)s * E;
-  for (int e = tid; e < E; e += threads) {
-    if (parts > 1) { if (s_cnt[e]) atomicAdd(&row[e], s_cnt[e]); }
-    else row[e] = accumulate ? row[e] + s_cnt[e] : s_cnt[e];
+  if (parts > 1) {
+    add_counts(s_cnt, s_tok, E, row, tokens ? tokens + s : nullptr);
+    return;
   }
-  if (tokens && tid == 0) {
-    if (parts > 1) atomicAdd(&tokens[s], s_tok);
-    else tokens[s] = accumulate ? tokens[s] + s_tok : s_tok;
+  for (int e = tid; e < E; e += threads) row[e] = accumulate ? row[e] + s_cnt[e] : s_cnt[e];
+  if (tokens && tid == 0) tokens[s] = accumulate ? tokens[s] + s_tok : s_tok;
+}
+
+// Slots of up to 2^sh tokens of one sequence, numbered as k_bal_part numbers
+// its own: however uneven the sequences are, no workgroup has more than a slot.
+// A slot that holds all of its sequence writes the row (zeroed before, unless the
+// call accumulates) without atomics.
+__global__ __launch_bounds__(kCntWG) void k_count_slots(const int32_t* idx, const int32_t* off, const uint8_t* mask,
+                                                        int C, int k, uint32_t kmul, int E, int S, int sh,
+                                                        int32_t* counts, int32_t* tokens, int accumulate) {
+  __shared__ int32_t s_cnt[MOE_MAX_EXPERTS];
+  __shared__ int32_t s_tok;
+  const int slot = blockIdx.x;
+  const int s = wave_search(S, slot, [&](int i) { return (seq_at(off, i, S, C) >> sh) + i; });
+  const int b = seq_at(off, s, S, C), end = seq_at(off, s + 1, S, C);
+  const int first = slot - ((b >> sh) + s);
+  const int64_t t0 = b + ((int64_t)first << sh);
+  if (first < 0 || t0 >= end) return;
+  const int t1 = end - t0 < (1 << sh) ? end : (int)t0 + (1 << sh);
+  count_tokens(idx, mask, (int)t0, t1, k, kmul, E, tokens != nullptr, s_cnt, &s_tok);
+  int32_t* row = counts + (size_t)s * E;
+  if (t0 > b || t1 < end) {
+    add_counts(s_cnt, s_tok, E, row, tokens ? tokens + s : nullptr);
+    return;
   }
+  for (int e = threadIdx.x; e < E; e += blockDim.x)
+    if (s_cnt[e]) row[e] = accumulate ? row[e] + s_cnt[e] : s_cnt[e];
+  if (tokens && threadIdx.x == 0) tokens[s] = accumulate ? tokens[s] + s_tok : s_tok;
 }
 
 // ---------------------------------------------------------------------------
@@ -733,23 +773,39 @@ moe_status moe_expert_counts(const int32_t* topk_idx, int32_t C, int32_t k, int3
   if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
   if (!seq_ok(seq_off, S)) return MOE_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  // one part per sequence (no zero fill, no atomics in memory) up to 8192
-  // choices of an average one (512 tokens x 16: 5.8 us, 7.1 in four parts; 2048:
-  // 9.3, 7.3 in 16); longer ones are shared out, however uneven they are, to
-  // workgroups that run at once (61 sequences of 17190: 10.8 us in 8 parts, 12.4
-  // in 9; one of 2^20: 10.5 in 64, 11.8 in 256)
-  const int64_t choices = (int64_t)C * k / S, at_once = 512 / S > 4 ? 512 / S : 4;
-  int64_t parts = choices <= 8192 ? 1 : (choices + 2047) / 2048;
-  if (parts > at_once) parts = at_once;
-  if (parts > 64) parts = 64;
-  if (parts > 1 && !accumulate) {
+  const int64_t choices = (int64_t)C * k;
+  // How long a sequence is only the device knows, so the rule is on the choices of
+  // the whole batch.  Up to 65536 of them, one workgroup per sequence, which writes
+  // its row without zero fill or atomics: at worst one sequence has them all (us,
+  // even sequences and all in one, here and in slots: 16 of 4096 choices 5.5, 12.2
+  // and 7.4, 7.6; 1000 of 64 5.0, 22.5 and 8.2, 10.1).  More are shared out in slots
+  // (128 of 8192 here 6.0, 145.6, in slots 9.1, 12.1), about 256 of at least 2048
+  // choices (61 sequences, 2^20 choices: 9.0, in 512 slots 10.4); one sequence in
+  // parts, which need no search (2^20 choices: 10.5 in 64, 11.8 in 256).
+  const bool slots = S > 1 && choices > 65536;
+  int64_t parts = 1;
+  if (S == 1 && choices > 8192) {
+    parts = (choices + 2047) / 2048;
+    if (parts > 64) parts = 64;
+  }
+  if ((slots || parts > 1) && !accumulate) {
     const int64_t n = (int64_t)S * E;
     hipLaunchKernelGGL(k_count_fill, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, counts, tokens, n, S);
   }
-  // small workgroups for short sequences (1000 of 64 choices: 5.7 us, 8.0 with
-  // large ones; one of 8192: 7.5 and 5.7)
-  hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3(choices <= 1024 ? 256 : kCntWG), 0, st, topk_idx,
-                     seq_off, token_mask, C, k, division(k), E, S, counts, tokens, accumulate);
+  if (slots) {
+    int sh = 0;
+    while (((int64_t)k << sh) < 2048 || (C >> sh) > 256) ++sh;
+    // workgroups as large as lets all of them run at once (1000 sequences of 524
+    // choices: 9.1 us with 256 threads, 18.0 with 1024; 16 of 8192: 8.2 and 7.7)
+    const int wgs = (C >> sh) + S, wg = wgs <= 512 ? kCntWG : wgs <= 1024 ? 512 : 256;
+    hipLaunchKernelGGL(k_count_slots, dim3((unsigned)wgs), dim3(wg), 0, st, topk_idx, seq_off, token_mask, C, k,
+                       division(k), E, S, sh, counts, tokens, accumulate);
+  } else {
+    // small workgroups for short sequences (1000 of 64 choices: 5.7 us, 8.0 with
+    // large ones; one of 8192: 7.5 and 5.7)
+    hipLaunchKernelGGL(k_count, dim3((unsigned)parts, S), dim3(choices / S <= 1024 ? 256 : kCntWG), 0, st, topk_idx,
+                       seq_off, token_mask, C, k, division(k), E, S, counts, tokens, accumulate);
+  }
   return launched();
 }
 
