@@ -308,16 +308,16 @@ size_t moe_quant_workspace_size(const moe_quant_matrix *m, int32_t dtype, int32_
  * 1 <= C <= MOE_MAX_TOKENS tokens.
  *  x [C][x_pitch], y [C][y_pitch]: both of `dtype` (moe_dtype), pitches in
  *  elements (x_pitch >= cols, y_pitch >= rows, at most 2^24), aligned to
- *  their type, any row alignment; y may not alias x.  Elements behind a row
- *  are neither read nor written.  Products are exact and sums are fp32; y (with
- *  accumulate, the sum with the old y) is rounded once to its type.  fp32 and
- *  bf16 activations enter as fp16 terms under a power-of-two scale per token and
- *  slab of columns (two terms for fp32: an element keeps 22 bits, and at
- *  least 2^-38 of its slab's largest).  However large the scales and small the
- *  activations, what fp32 can hold is not lost to that power: a sum that leaves
- *  fp32's range under it is formed anew in 64 bits (slower, where it happens:
- *  scales past about 2^88).  The result does not depend on what
- *  ran before: the same call gives the same bits. */
+ *  their type, any row alignment; no row of y may overlap one of x (checked).
+ *  Elements behind a row are neither read nor written.  Products are exact and
+ *  sums are fp32; y (with accumulate, the sum with the old y) is rounded once to
+ *  its type.  fp32 and bf16 activations enter as fp16 terms under a power-of-two
+ *  scale per token and slab of columns (two terms for fp32: an element keeps 22
+ *  bits, and at least 2^-38 of its slab's largest).  However large the scales and
+ *  small the activations, what fp32 can hold is not lost to that power: a sum that
+ *  leaves fp32's range under it is formed anew in 64 bits (slower, where it
+ *  happens: scales past about 2^88).  The result does not depend on what ran
+ *  before: the same call gives the same bits. */
 moe_status moe_quant_linear(const moe_quant_matrix *m, int32_t dtype, const void *x,
                             int64_t x_pitch, int32_t C, void *y, int64_t y_pitch,
                             int32_t accumulate, void *ws, size_t ws_bytes, void *stream);
@@ -384,7 +384,8 @@ moe_status moe_balance_fwd(const float *logits, const int32_t *topk_idx, int32_t
  *   g_e = grad_loss * alpha / (S tokens[s]) * f[s][e],
  *   dlogits_e = p_e (g_e - sum_j p_j g_j) * (sigmoid(-l_e) for MOE_SCORE_SIGMOID, else 1).
  *  counts and tokens as moe_balance_fwd wrote them; grad_loss: a device fp32.
- *  dlogits [C][E] fp32 is written, or added to where accumulate is not 0. */
+ *  dlogits [C][E] fp32 is written, or added to where accumulate is not 0; it may
+ *  not overlap the logits (checked). */
 moe_status moe_balance_bwd(const float *logits, const int32_t *counts, const int32_t *tokens,
                            int32_t C, int32_t k, int32_t E, const int32_t *seq_off, int32_t S,
                            const uint8_t *token_mask, int32_t score, float alpha,
@@ -398,7 +399,8 @@ moe_status moe_balance_bwd(const float *logits, const int32_t *counts, const int
  *  written (zeros where nothing was chosen), or added to at the chosen
  *  experts where accumulate is not 0.  Slots that name one expert add up; an
  *  index outside [0, E) is skipped.  A token whose chosen logits are all -inf
- *  has a zero gradient.  The selection itself is held constant. */
+ *  has a zero gradient.  The selection itself is held constant.  dlogits may not
+ *  overlap another tensor of the call (checked). */
 moe_status moe_route_bwd(const float *logits, const int32_t *topk_idx, const float *topk_dw,
                          int32_t C, int32_t k, int32_t E, const uint8_t *token_mask,
                          float *dlogits, int32_t accumulate, void *stream);

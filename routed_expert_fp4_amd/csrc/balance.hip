@@ -855,13 +855,15 @@ moe_status moe_balance_bwd(const float* logits, const int32_t* counts, const int
                            const uint8_t* token_mask, int32_t score, float alpha,
                            const float* grad_loss, float* dlogits, int32_t accumulate,
                            void* stream) {
-  if (!logits || !counts || !tokens || !grad_loss || !dlogits || logits == dlogits) return MOE_ERR_INVALID_ARG;
+  if (!logits || !counts || !tokens || !grad_loss || !dlogits) return MOE_ERR_INVALID_ARG;
   if (!aligned4(logits) || !aligned4(dlogits) || !aligned4(counts) || !aligned4(tokens) ||
       !aligned4(grad_loss) || !aligned4(seq_off))
     return MOE_ERR_INVALID_ARG;
   if (!batch_ok(C, k, E) || S < 1 || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED;
   if (!seq_ok(seq_off, S) || (score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SOFTMAX))
     return MOE_ERR_INVALID_ARG;
+  const int64_t bytes = (int64_t)C * E * 4;
+  if (overlap(logits, bytes, dlogits, bytes)) return MOE_ERR_INVALID_ARG;
   BalArgs a = {};
   a.logits = logits; a.off = seq_off; a.mask = token_mask;
   a.C = C; a.k = k; a.E = E; a.S = S; a.alpha = alpha;
@@ -882,10 +884,14 @@ moe_status moe_balance_bwd(const float* logits, const int32_t* counts, const int
 moe_status moe_route_bwd(const float* logits, const int32_t* topk_idx, const float* topk_dw,
                          int32_t C, int32_t k, int32_t E, const uint8_t* token_mask,
                          float* dlogits, int32_t accumulate, void* stream) {
-  if (!logits || !topk_idx || !topk_dw || !dlogits || logits == dlogits) return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_idx || !topk_dw || !dlogits) return MOE_ERR_INVALID_ARG;
   if (!aligned4(logits) || !aligned4(topk_idx) || !aligned4(topk_dw) || !aligned4(dlogits))
     return MOE_ERR_INVALID_ARG;
   if (!batch_ok(C, k, E)) return MOE_ERR_UNSUPPORTED;
+  const int64_t bytes = (int64_t)C * E * 4, chosen = (int64_t)C * k * 4;
+  if (overlap(logits, bytes, dlogits, bytes) || overlap(topk_dw, chosen, dlogits, bytes) ||
+      overlap(topk_idx, chosen, dlogits, bytes))
+    return MOE_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const bool vec = E % 4 == 0 && (uintptr_t)dlogits % 16 == 0;
   const int per = kBalWaves * (k <= 8 ? 8 : k <= 16 ? 4 : 2);

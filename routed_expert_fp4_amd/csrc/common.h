@@ -288,6 +288,24 @@ __device__ __forceinline__ float route_weight(float l, int lane, int k) {
   return sg / wave_sum(sg);
 }
 
+// Whether n rows of `ra` bytes, pa apart, share a byte with n rows of rb bytes, pb
+// apart (rows of one tensor do not overlap).  Slices of one buffer may lie between
+// each other's rows, so overlapping spans are compared row by row.
+inline bool rows_overlap(const void* a, int64_t ra, int64_t pa, const void* b, int64_t rb, int64_t pb, int64_t n) {
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  if (a0 + (uint64_t)((n - 1) * pa + ra) <= b0 || b0 + (uint64_t)((n - 1) * pb + rb) <= a0) return false;
+  for (int64_t i = 0, j = 0; i < n && j < n;) {
+    const uintptr_t x = a0 + (uint64_t)(i * pa), y = b0 + (uint64_t)(j * pb);
+    if (x + (uint64_t)ra <= y) ++i;
+    else if (y + (uint64_t)rb <= x) ++j;
+    else return true;
+  }
+  return false;
+}
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  return (uintptr_t)a < (uintptr_t)b + (uint64_t)nb && (uintptr_t)b < (uintptr_t)a + (uint64_t)na;
+}
+
 // Shapes the batched path is built for: K stages of 256 elements taken in
 // pairs, row tiles of 128 (gate/up) and 256 (down) rows, scale tensors at
 // 4-byte aligned offsets (their words are loaded whole).

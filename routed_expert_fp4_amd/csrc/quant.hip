@@ -1603,12 +1603,13 @@ moe_status moe_quant_linear(const moe_quant_matrix* m, int32_t dtype, const void
                             int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
   const moe_status ms = matrix_status(m);
   if (ms != MOE_OK) return ms;
-  if (!x || !y || x == y) return MOE_ERR_INVALID_ARG;
+  if (!x || !y) return MOE_ERR_INVALID_ARG;
   if (!dtype_ok(dtype) || C < 1 || C > MOE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
   const int64_t xs = dtype_size(dtype), ss = dtype_size(m->scale_dtype);
   if (x_pitch > kMaxRow || y_pitch > kMaxRow) return MOE_ERR_UNSUPPORTED;
   if (x_pitch < m->cols || y_pitch < m->rows || (uintptr_t)x % xs || (uintptr_t)y % xs)
     return MOE_ERR_INVALID_ARG;
+  if (rows_overlap(x, m->cols * xs, x_pitch * xs, y, m->rows * xs, y_pitch * xs, C)) return MOE_ERR_INVALID_ARG;
   const QPlan p = quant_plan(m, dtype, C);
   if (!ws || (uintptr_t)ws % 256 || ws_bytes < p.total) return MOE_ERR_WORKSPACE;
   uint8_t* w8 = static_cast<uint8_t*>(ws);
