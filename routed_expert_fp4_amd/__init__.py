@@ -359,11 +359,15 @@ class _Scratch:
         with torch.cuda.device(self.tensor.device):
             moe_workspace_init(self.tensor, stream)
 
-    def on(self, dev):
-        """Its pointer, on GPU `dev` only."""
-        if self.device != dev:
-            raise ValueError(f"workspace must be on cuda:{dev}, got {self.tensor.device}")
-        return self.tensor.data_ptr()
+
+def _scratch(ws, kind, dev):
+    """Pointer and bytes of a workspace of this kind on GPU `dev`: each keeps its
+    own state between calls."""
+    if not isinstance(ws, kind):
+        raise ValueError(f"ws must be a {kind.__name__}, got {type(ws).__name__}")
+    if ws.device != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}, got {ws.tensor.device}")
+    return ws.tensor.data_ptr(), ws.nbytes
 
 
 def _bad(t, dev, dtype, shape, name):
@@ -495,7 +499,7 @@ def moe_quant_linear(matrix: QuantMatrix, x, C, y, ws: QuantWorkspace, accumulat
     xp, xs = _rows(x, dev, dtype, (C, matrix.K), "x")
     yp, ys = _rows(y, dev, dtype, (C, matrix.N), "y")
     _launch("moe_quant_linear", dev, stream, matrix.ref, _moe_dtype(dtype), xp, xs, C, yp, ys, accumulate,
-            ws.on(dev), ws.nbytes)
+            *_scratch(ws, QuantWorkspace, dev))
 
 
 # ---------------------------------------------------------------------------
@@ -538,7 +542,7 @@ def moe_balance_fwd(logits, topk_idx, C, E, k, alpha, counts, tokens, probs, los
             _maybe(token_mask, dev, torch.uint8, (C,), "token_mask"), _score(score), alpha,
             _dense(counts, dev, i32, (S, E), "counts"), _dense(tokens, dev, i32, (S,), "tokens"),
             _dense(probs, dev, f32, (S, E), "probs"), _dense(loss, dev, f32, (1,), "loss"),
-            ws.on(dev), ws.nbytes)
+            *_scratch(ws, BalanceWorkspace, dev))
 
 
 def moe_balance_bwd(logits, counts, tokens, C, E, k, alpha, grad_loss, dlogits, score="sigmoid",
