@@ -9,7 +9,9 @@
 // fp32 sum.  fp16 x is taken as it is.  bf16 x (8 bits) is one fp16 term under
 // a power of two per token that puts the token's largest value below 2^15:
 // exact down to 2^-28 of that value, and off by at most 2^-38 of it below.
-// fp32 x is two such terms (22 bits).
+// fp32 x is two such terms (22 bits): a third would make half as many matrix
+// instructions again, for an error that fp32 sums cover (7168 columns against 64
+// bits: 1e-7, a library's fp32 product 7e-7).
 //
 // Codes become fp16 without conversions: a nibble OR-ed into the fp16 1024 is
 // 1024 + q, one in the next four bits of the fp16 64 is 64 + q, and one packed
@@ -591,6 +593,12 @@ __device__ __forceinline__ QArgsPtr args_again() {
   asm volatile("" : "+s"(a));
   return a;
 }
+__device__ __forceinline__ double readlane_f64(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, readlane_u64(u, l));
+}
+// Result (t, n), the same in every lane that is active, by all of these together:
+// one column after the other a lane took 0.5 ms for 7168 of them.
 template <int DT, bool TR, int SS>
 __device__ __forceinline__ float sum_in_f64(int t, int n, int k0, int k1) {
   const QArgsPtr a = args_again();
@@ -600,24 +608,57 @@ __device__ __forceinline__ float sum_in_f64(int t, int n, int k0, int k1) {
   const int64_t row = (int64_t)t * a->x_pitch;
   const bool wide = DT == 0 ? a->x_dt == MOE_DT_F32 : DT == MOE_DT_F32;
   k1 = k1 < a->K ? k1 : a->K;
-  double y = 0.0;
-#pragma unroll 1
-  for (int k = k0; k < k1; k += 8) {            // eight codes: one group
-    const int g = TR ? k >> a->gshift : (int)(((uint32_t)(k / kQChunk) * a->gmul) >> 20);
+  const uint64_t on = __ballot(1);
+  const int lanes = __popcll(on), rank = __popcll(on & ((1ull << (threadIdx.x & 63)) - 1ull));
+  auto total = [&](double v) {                             // in the order of the lanes
+    double sum = 0.0;
+    for (uint64_t m = on; m; m &= m - 1) sum += readlane_f64(v, __ffsll((long long)m) - 1);
+    return sum;
+  };
+  auto group = [&](int k) { return TR ? k >> a->gshift : (int)(((uint32_t)(k / kQChunk) * a->gmul) >> 20); };
+  auto scale_at = [&](int k) {
+    const int g = group(k);
     const uint32_t s = SS == 4 ? reinterpret_cast<const uint32_t*>(scale)[g] : reinterpret_cast<const uint16_t*>(scale)[g];
-    const int z = zero ? zero[g] : 8;
+    return scale_of<SS>(a->scale_bf16, s);
+  };
+  auto eight = [&](int k, int end) {                       // columns k .. k + 7, one group
     const uint32_t q = *reinterpret_cast<const uint32_t*>(code + k / 2);   // up to the end of a 16-byte unit
+    const int z = zero ? zero[group(k)] : 8;
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t at = row + (k + i < k1 ? k + i : k1 - 1);
+      const int64_t at = row + (k + i < end ? k + i : end - 1);
       const float x = wide ? static_cast<const float*>(a->x)[at]
                            : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a->x)[at] << 16);
-      if (k + i < k1) sum += (double)x * (double)((int)((q >> (4 * i)) & 15u) - z);
+      if (k + i < end) sum += (double)x * (double)((int)((q >> (4 * i)) & 15u) - z);
     }
-    y += (double)scale_of<SS>(a->scale_bf16, s) * sum;
+    return sum;
+  };
+  double y = 0.0;
+  // infinite and NaN scales first, each times its group's sum (of a chunk, in
+  // groups of several): beside them the other groups make no difference
+  bool only = false;
+  const int step = TR ? 1 << a->gshift : kQChunk;
+#pragma unroll 1
+  for (int base = k0; base < k1; base += step * lanes) {
+    const int k = base + step * rank;
+    const float s = k < k1 ? scale_at(k) : 0.0f;
+#pragma unroll 1
+    for (uint64_t m = __ballot(!(fabsf(s) < INFINITY)); m; m &= m - 1) {
+      const int l = __ffsll((long long)m) - 1, kb = __builtin_amdgcn_readlane(k, l);
+      const int end = kb + step < k1 ? kb + step : k1;
+      double sum = 0.0;
+#pragma unroll 1
+      for (int c = kb + 8 * rank; c < end; c += 8 * lanes) sum += eight(c, end);
+      y += (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(s), l)) * total(sum);
+      only = true;
+      if (y != y) return (float)y;
+    }
   }
-  return (float)y;
+  if (only) return (float)y;
+#pragma unroll 1
+  for (int k = k0 + 8 * rank; k < k1; k += 8 * lanes) y += (double)scale_at(k) * eight(k, k1);
+  return (float)total(y);
 }
 // v unless it has left the range (`spoilt`: the token is not finite; asked only
 // then).  fp16 activations are not raised: theirs stays.  DT 0: as the call says.
@@ -627,7 +668,12 @@ __device__ __forceinline__ float in_range(float v, F spoilt, int t, int n, int k
   if (DT == MOE_DT_F16) return v;
   const bool left = !(fabsf(v) < INFINITY);
   if (__builtin_expect(__ballot(left) != 0, 0)) {
-    if (left && !spoilt()) v = sum_in_f64<DT, TR, SS>(t, n, k0, k1);
+#pragma unroll 1
+    for (uint64_t m = __ballot(left && !spoilt()); m; m &= m - 1) {
+      const int l = __ffsll((long long)m) - 1;
+      const float y = sum_in_f64<DT, TR, SS>(__builtin_amdgcn_readlane(t, l), __builtin_amdgcn_readlane(n, l), k0, k1);
+      if ((int)(threadIdx.x & 63) == l) v = y;
+    }
   }
   return v;
 }
@@ -796,13 +842,16 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
   if (DT == MOE_DT_F16 || __ballot(left != 0) == 0) return;
   // behind the loop, whose scalars this code would spill
   const QArgsPtr b = args_again();
-  for (; left; left &= left - 1) {
-    const int cg = blockIdx.x + (__ffsll((long long)left) - 1) * gridDim.x;
+  for (int cg = blockIdx.x; cg < b->row_groups; cg += gridDim.x, left >>= 1) {
     const int n = (cg * (kQWaves >> b->ks) + (b->ks ? tid >> 4 : tid >> 6)) * 16 + (tid & 15);
-    const float s = sum_in_f64<DT, TR, SS>(0, n, 0, INT_MAX);
-    QArgs c;
-    c.y = b->y; c.y_pitch = b->y_pitch; c.accumulate = b->accumulate;
-    put<DT>(c, 0, n, s);
+#pragma unroll 1
+    for (uint64_t m = __ballot(left & 1); m; m &= m - 1) {
+      const int l = __ffsll((long long)m) - 1;
+      const float s = sum_in_f64<DT, TR, SS>(0, __builtin_amdgcn_readlane(n, l), 0, INT_MAX);
+      QArgs c;
+      c.y = b->y; c.y_pitch = b->y_pitch; c.accumulate = b->accumulate;
+      if (lane == l) put<DT>(c, 0, n, s);
+    }
   }
 }
 
@@ -816,13 +865,14 @@ __global__ __launch_bounds__(kQWG, 2) void k_qone(QArgs a) {
 // as soon as these are used.  Small matrices take a larger WK (and with eight as
 // long a slice as 64 KB of terms hold): more workgroups, each with less to do
 // after its loads have arrived.  7 tokens, bf16, 7168 x 3584 in groups of 32:
-// 11.5 us, of which unpacking and transposing are 3.3, and latencies (x, terms,
-// the hand-off of ranges) most of the rest.
-// Eight waves to a row tile are for two workgroups a CU: four waves to a SIMD.
+// 11.6 us, of which unpacking and transposing are 3.3, and latencies (x, terms,
+// the ranges added one load after the other) most of the rest.
+// Calls of up to 8 tokens and eight waves to a row tile are for two workgroups a
+// CU: four waves to a SIMD (8 tokens x 16384 x 4096, fp32: 25.3 us with three).
 constexpr int few_slice(int P, int TOK, int WK) { return WK == 8 ? 65536 / (P * TOK * 2 * kQChunk) : 8; }
 
 template <int DT, int TOK, int WK, bool TR, int SS>
-__global__ __launch_bounds__(kQWG, WK == 8 ? 4 : 2) void k_qfew(QArgs a) {
+__global__ __launch_bounds__(kQWG, WK == 8 || TOK == 8 ? 4 : 2) void k_qfew(QArgs a) {
   constexpr int P = DT == MOE_DT_F32 ? 2 : 1;
   constexpr int NR = TOK / 4;
   constexpr int kQSlice = few_slice(P, TOK, WK), kQSliceCols = kQSlice * kQChunk;
@@ -997,8 +1047,12 @@ __global__ __launch_bounds__(kQWG, WK == 8 ? 4 : 2) void k_qfew(QArgs a) {
 // chunk's four units.  The tables are there because a load of one scale per
 // row touches a cache line per row: taken chunk by chunk and wave by wave those
 // lines were more traffic than terms and codes together.  2048 tokens x 3584 x
-// 7168, bf16: 106 us, 1.0 PFLOP/s (a large library fp16 product reaches 1.4),
-// bound by issue: the vector work of unpacking beside the matrix instructions.
+// 7168, bf16, in groups of 128: a call takes 120 us one behind the other, of which
+// the terms are about 11, so 0.97 PFLOP/s (a large library fp16 product reaches
+// 1.4); under a profiler, with the kernels apart, 121 to 148.  The matrix cores
+// are busy for 40% of that time and the vector units for 43% (unpacking), and a
+// wave waits for 31% of its own: neither bounds it alone (see the waits below; 224
+// workgroups on 256 CUs).
 template <int P, int WT, int TW, int RT>
 struct GemmTile {
   static constexpr int WR = kQWaves / WT, TM = WT * TW * 2, rows = WR * RT * 32;
@@ -1137,9 +1191,14 @@ __global__ __launch_bounds__(kQWG, 2) void k_qgemm(QArgs a) {
   // overlaps).  The move to the next chunk comes before the last two steps: this
   // chunk's LDS reads are complete by then, so one barrier both frees its
   // buffer for the chunk three on and, each wave having waited for its own
-  // loads, opens the next chunk's.  Loads complete in order, and the newest
-  // (one chunk's LDS loads) may stay in flight; past the last chunk the last
-  // is loaded again, so that their number is the same everywhere.
+  // loads, opens the next chunk's.  Loads complete in order, and the barrier lets
+  // the newest (one chunk's LDS loads) stay in flight; past the last chunk the
+  // last is loaded again, so that their number is the same everywhere.  As compiled
+  // they do not stay there for long: the LDS reads behind the barrier are taken to
+  // depend on the loads into LDS and wait for all of them, and the next chunk's
+  // first step waits for the table's loads; groups of 32 and 64 wait so two or
+  // three times more in the middle of a chunk, and for groups of 64 the larger tile
+  // of one term keeps a few registers in scratch memory.
   float16v acc[TW][RT], d[TW][RT];
   half8 x[4][TW][P], b[RT];                                // step s's terms in x[s & 3]
   uint32_t w[RT][2][4];                                    // codes: unit 2 u + half (TR: swapped, see codes_of)

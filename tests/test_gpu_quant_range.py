@@ -81,3 +81,36 @@ def test_results_past_the_largest_number(C, xt):
     assert bool((y[:, 0::4] == float("inf")).all()) and bool((y[:, 2::4] == float("-inf")).all())
     want, tol = expect(codes[1::2], scales[1::2], None, x, 300, 128)
     check(y[:, 1::2], want, tol, C, rel=False)
+
+
+@pytest.mark.parametrize("C", [1, 5, 16, 40, 200])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+def test_an_infinite_scale_multiplies_its_groups_sum(C, G, xt):
+    """Beside finite groups, and beside very large ones: the infinity of the
+    group's sum, with its sign, and a NaN scale's row is NaN."""
+    N, K = 60, 700
+    codes, scales, z, x, y = make(C, N, K, G, xt, "f32", True, 5)
+    scales[1::5] *= 1e38                                     # left the range without an infinity too
+    x *= 1e-33
+    scales[2::5, 3] = float("inf")
+    scales[1::5, 2] = float("-inf")
+    scales[3::5, 1] = float("nan")
+    run(codes, scales, z, x, y, K, G)
+    got, xd = y.double().cpu().numpy(), x.double().cpu().numpy()
+    q = np.empty((N, 2 * codes.shape[1]))
+    c = codes.cpu().numpy()
+    q[:, 0::2], q[:, 1::2] = c & 15, c >> 4
+    for first, g, sign in ((2, 3, 1.0), (1, 2, -1.0)):
+        at = slice(g * G, (g + 1) * G)
+        w = q[first::5, at] - z.cpu().numpy()[first::5, g:g + 1]
+        sums = xd[:, at] @ w.T
+        # a sum within its own roundings of zero may have either sign, or be zero
+        clear = np.abs(sums) > 170 * 2.0 ** -24 * (np.abs(xd[:, at]) @ np.abs(w).T)
+        assert clear.mean() > 0.9                            # of twelve rows at least eleven
+        assert np.array_equal(got[:, first::5][clear], (sign * np.sign(sums) * np.inf)[clear])
+        assert not np.isfinite(got[:, first::5]).any()
+    assert np.isnan(got[:, 3::5]).all()
+    rows = [n for n in range(N) if n % 5 not in (1, 2, 3)]
+    want, tol = expect(codes[rows], scales[rows], z[rows], x, K, G)
+    check(y[:, rows], want, tol, (C, G, xt), rel=False)
