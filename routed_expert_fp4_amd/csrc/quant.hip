@@ -578,7 +578,7 @@ __device__ __forceinline__ void put4(const QArgs& a, int t, int n, float4 v) {
 // the token's power of two is taken out last.  Very small activations (raised by
 // up to 2^126) against very large scales so leave fp32's range with a result
 // inside it.  Every kernel looks at its results, and where one of a finite token
-// is not finite this forms its columns k0 (a multiple of 8) to k1 - 1 anew, in 64
+// is not finite this forms its columns k0 (a chunk's first) to k1 - 1 anew, in 64
 // bits: fp32 inputs neither overflow nor vanish there, and what is still infinite
 // or NaN comes of infinite scales or of a sum past fp32.  Folding the power into
 // the scale instead would lose small scales, and doing so per token would cost a
