@@ -114,3 +114,22 @@ def test_an_infinite_scale_multiplies_its_groups_sum(C, G, xt):
     rows = [n for n in range(N) if n % 5 not in (1, 2, 3)]
     want, tol = expect(codes[rows], scales[rows], z[rows], x, K, G)
     check(y[:, rows], want, tol, (C, G, xt), rel=False)
+
+
+@pytest.mark.parametrize("C", [1, 7, 16, 40])
+def test_captured_into_a_graph(C):
+    import routed_expert_fp4_amd as rf
+    N, K, G = 300, 2100, 64
+    codes, scales, z, x, y = extreme(C, N, K, G, "f32")
+    m, ws = run(codes, scales, z, x, y, K, G)
+    graph, again = torch.cuda.CUDAGraph(), torch.zeros_like(y)
+    with torch.cuda.graph(graph):
+        rf.moe_quant_linear(m, x, C, again, ws)
+    for r in range(4):
+        x.copy_(torch.randn_like(x) * 1e-33)
+        again.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        rf.moe_quant_linear(m, x, C, y, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y, again) and bool(torch.isfinite(y).all()), r
