@@ -405,6 +405,145 @@ moe_status moe_route_bwd(const float *logits, const int32_t *topk_idx, const flo
                          int32_t C, int32_t k, int32_t E, const uint8_t *token_mask,
                          float *dlogits, int32_t accumulate, void *stream);
 
+/* Dropout whose mask is never stored: whether element (c, k) is kept follows from
+ * a seed, an offset, c and k alone, so that a backward pass (the same call on the
+ * gradient) forms it again.
+ *   y[c][k] = base[c][k] + (kept(c, k) ? x[c][k] / (1 - p') : 0)
+ *  dtype    moe_dtype of x [C][x_pitch], base [C][base_pitch] (NULL: zeros) and
+ *           y [C][y_pitch]; 1 <= C <= MOE_MAX_BATCH_TOKENS, 1 <= K <=
+ *           MOE_MAX_QUANT_COLS, pitches in elements, at least K and at most 2^24 (one
+ *           row's is not used).  y may be x or base themselves (the same rows);
+ *           other overlaps are refused.
+ *  p        in [0, 1], taken to the nearest multiple p' of 2^-16; 1: all dropped.
+ *  rng      two device uint64, seed and offset, read when the call runs (so that a
+ *           captured call takes what is there at its replay); may be NULL at p' = 0.
+ * A dropped element adds 0 whatever x holds there.  The numbers: Philox 4x32 in ten
+ * rounds under the key (seed, low word first), of the counter (offset low, offset
+ * high, k / 8, c); element k takes the low half of word (k % 8) / 2 for even k, the
+ * high half for odd, and is kept where that is at least 65536 p'.  Another offset
+ * or seed gives another mask; a training loop takes a new offset for every use.
+ * Computed in fp32 and rounded once. */
+moe_status moe_dropout(int32_t dtype, const void *x, int64_t x_pitch, int32_t C, int32_t K,
+                       const void *base, int64_t base_pitch, void *y, int64_t y_pitch, double p,
+                       const uint64_t *rng, void *stream);
+
+/* Low-rank adapters beside a shared projection from `cols` to `rows` (a dense
+ * 4-bit product, routed_down, routed_up, ...), many of them at once: token c of a
+ * request that uses adapter a adds
+ *   t_c = A_a d(x_c),   y_c = base_c + scales[a] B_a t_c
+ * with d dropout of x in training (kept as moe_dropout keeps element (c, k) of x)
+ * and the identity else.  A token without adapter has y_c = base_c.  t and every
+ * sum are fp32, y is rounded once.
+ * Requirements (checked): 1 .. MOE_MAX_ADAPTERS adapters of one rank 1 ..
+ * MOE_MAX_RANK (fill up smaller ones with zero rows of A), cols and rows up to
+ * MOE_MAX_QUANT_COLS; rows of a matrix apart by their pitch (at most 2^24 elements),
+ * matrices by their stride, both at least what they hold; everything aligned to its
+ * type and no more. */
+#define MOE_MAX_ADAPTERS 1024
+#define MOE_MAX_RANK 128
+typedef struct {
+  int32_t adapters;
+  int32_t rank;
+  int32_t cols;          /* K: inputs                                         */
+  int32_t rows;          /* N: outputs                                        */
+  int32_t dtype;         /* moe_dtype of a, b, x, y and their gradients       */
+  const void *a;         /* [adapters][rank][cols]                            */
+  int64_t a_stride;      /* elements between adapters                         */
+  int64_t a_pitch;       /* elements between rows                             */
+  const void *b;         /* [adapters][rows][rank]                            */
+  int64_t b_stride;
+  int64_t b_pitch;
+  const float *scales;   /* [adapters], or NULL: 1                            */
+} moe_adapter_bank;
+
+/* The order in which a batch's tokens are taken: one plan serves every bank with
+ * that many adapters, so a step makes it once for all of its projections.
+ *  token_adapter [C] device int32: a token's adapter; a value outside [0, adapters)
+ *  means none.  plan: moe_adapter_plan_size bytes, 256-byte aligned, written by the
+ *  call (no initialisation) and read by the ones below; a plan made for another C or
+ *  number of adapters is found out on the device: such a call writes nothing. */
+size_t moe_adapter_plan_size(int32_t C, int32_t adapters);
+moe_status moe_adapter_plan(const int32_t *token_adapter, int32_t C, int32_t adapters, void *plan,
+                            size_t plan_bytes, void *stream);
+
+/* Workspace of both directions for up to C tokens (0 outside the supported range):
+ * no initialisation, nothing is kept in it between calls, one call at a time. */
+size_t moe_adapter_workspace_size(const moe_adapter_bank *bank, int32_t C);
+
+/* y [C][y_pitch] from x [C][x_pitch] and base [C][base_pitch] (NULL: zeros; y may be
+ * base itself, other overlaps of an output are refused), 1 <= C <=
+ * MOE_MAX_BATCH_TOKENS.  hidden: NULL, or [C][rank] fp32 that receives t (zeros for a
+ * token without adapter), which the backward pass takes.  p, rng: dropout of x as in
+ * moe_dropout (0: none). */
+moe_status moe_adapter_fwd(const moe_adapter_bank *bank, const void *plan, size_t plan_bytes,
+                           const void *x, int64_t x_pitch, int32_t C, const void *base,
+                           int64_t base_pitch, void *y, int64_t y_pitch, float *hidden, double p,
+                           const uint64_t *rng, void *ws, size_t ws_bytes, void *stream);
+
+/* The gradients for dy [C][dy_pitch] (that of base is dy itself), with u_c =
+ * scales[a] B_a^T dy_c:
+ *   dx_c = base_c + d'(A_a^T u_c)    [C][dx_pitch], rounded once; base as above (the
+ *                                    gradient that other users of x have given it)
+ *   da_a = sum_c u_c d(x_c)^T        [adapters][rank][cols] fp32, dense
+ *   db_a = scales[a] sum_c dy_c t_c^T [adapters][rows][rank] fp32, dense
+ * Each of dx, da, db may be NULL (not all); x is needed for da, hidden (as the
+ * forward pass wrote it) for db.  accumulate: da and db are added to.  An adapter
+ * without tokens has zero gradients.  p and rng as in the forward pass.  The sums'
+ * order is fixed: the same call gives the same bits. */
+moe_status moe_adapter_bwd(const moe_adapter_bank *bank, const void *plan, size_t plan_bytes,
+                           const void *x, int64_t x_pitch, const float *hidden, const void *dy,
+                           int64_t dy_pitch, int32_t C, const void *base, int64_t base_pitch,
+                           void *dx, int64_t dx_pitch, float *da, float *db, int32_t accumulate,
+                           double p, const uint64_t *rng, void *ws, size_t ws_bytes, void *stream);
+
+/* The gated block of a dense layer or of shared experts whose weights are held in 16
+ * or 32 bits:
+ *   g = x w_gate^T, u = x w_up^T, h = act(g) * u       (all products in fp32, h
+ *                                                        rounded once)
+ *   MOE_ACT_SILU  act(g) = g sigmoid(g)
+ *   MOE_ACT_GELU  act(g) = g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)), the tanh form
+ * Requirements (checked): sizes up to MOE_MAX_QUANT_COLS; rows apart by their pitch (at
+ * most 2^24 elements), aligned to their type and no more.  (More than 32 tokens, and the
+ * gradients, take x and the weights as they are where rows start and end at multiples of
+ * 16 bytes; others are copied to the workspace first.) */
+#define MOE_MAX_FFN_TOKENS (1 << 17)
+typedef enum { MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 } moe_act;
+typedef struct {
+  int32_t hidden;        /* H                                                 */
+  int32_t inter;         /* I                                                 */
+  int32_t dtype;         /* moe_dtype of the weights, x, h and the gradients  */
+  int32_t act;           /* moe_act                                           */
+  const void *w_gate;    /* [inter][hidden]                                   */
+  int64_t gate_pitch;    /* elements between rows                             */
+  const void *w_up;      /* [inter][hidden]                                   */
+  int64_t up_pitch;
+} moe_ffn;
+
+/* Workspace of both directions for up to C tokens (0 outside the supported range): no
+ * initialisation, nothing is kept in it between calls, one call at a time. */
+size_t moe_ffn_workspace_size(const moe_ffn *f, int32_t C);
+
+/* h [C][h_pitch] from x [C][x_pitch], 1 <= C <= MOE_MAX_FFN_TOKENS.  gate, up
+ * [C][..pitch]: NULL both, or they receive g and u, rounded to the type, for the
+ * backward pass.  An output may overlap nothing else (checked). */
+moe_status moe_ffn_fwd(const moe_ffn *f, const void *x, int64_t x_pitch, int32_t C, void *h,
+                       int64_t h_pitch, void *gate, int64_t gate_pitch, void *up,
+                       int64_t up_pitch, void *ws, size_t ws_bytes, void *stream);
+
+/* Its gradients for dh [C][dh_pitch], from gate and up as the forward pass wrote them:
+ *   du = dh act(g), dg = dh u act'(g)    formed in fp32, rounded to the type
+ *   dx = dg w_gate + du w_up             [C][dx_pitch], of the type
+ *   dw_gate = dg^T x, dw_up = du^T x     [inter][..pitch], of grad_dtype: the type, or
+ *                                        MOE_DT_F32
+ * fp32 sums, rounded once.  dx may be NULL, and dw_gate and dw_up both; x is needed for
+ * those alone.  accumulate: all of them are added to (the sum rounded once). */
+moe_status moe_ffn_bwd(const moe_ffn *f, const void *x, int64_t x_pitch, const void *gate,
+                       int64_t gate_pitch, const void *up, int64_t up_pitch, const void *dh,
+                       int64_t dh_pitch, int32_t C, void *dx, int64_t dx_pitch,
+                       int32_t grad_dtype, void *dw_gate, int64_t dw_gate_pitch, void *dw_up,
+                       int64_t dw_up_pitch, int32_t accumulate, void *ws, size_t ws_bytes,
+                       void *stream);
+
 /* Test export: dequantise one matrix of one expert to fp32.
  *  matrix 0 = gate [I][H], 1 = up [I][H], 2 = down [H][I].
  *  MXFP4: w = e2m1 * 2^(b-127), exact (IEEE denormals kept).

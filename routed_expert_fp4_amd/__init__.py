@@ -29,11 +29,18 @@ EXPORTS = ("moe_version", "moe_status_string", "moe_bank_layout", "moe_workspace
            "moe_latent_workspace_size", "moe_latent_layer_fwd", "moe_mx_mma_workspace_size",
            "moe_expert_fwd_mx_mma", "moe_layer_fwd_noalloc", "moe_quant_workspace_size",
            "moe_quant_linear", "moe_expert_counts", "moe_balance_workspace_size",
-           "moe_balance_fwd", "moe_balance_bwd", "moe_route_bwd")
+           "moe_balance_fwd", "moe_balance_bwd", "moe_route_bwd", "moe_dropout",
+           "moe_adapter_plan_size", "moe_adapter_plan", "moe_adapter_workspace_size",
+           "moe_adapter_fwd", "moe_adapter_bwd", "moe_ffn_workspace_size", "moe_ffn_fwd",
+           "moe_ffn_bwd")
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 1, 2, 3
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 1, 2
 MOE_MAX_QUANT_ROWS, MOE_MAX_QUANT_COLS = 1 << 22, 1 << 17
 MOE_MAX_BATCH_TOKENS, MOE_MAX_SEQUENCES = 1 << 20, 65535
+MOE_MAX_ADAPTERS, MOE_MAX_RANK = 1024, 128
+MOE_ACT_SILU, MOE_ACT_GELU = 1, 2
+MOE_MAX_FFN_TOKENS = 1 << 17
+ACTIVATIONS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
 SCORES = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 
 
@@ -65,6 +72,19 @@ class moe_quant_matrix(ctypes.Structure):
                 ("zero_pitch", ctypes.c_int64)]
 
 
+class moe_adapter_bank(ctypes.Structure):
+    _fields_ = [("adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("dtype", ctypes.c_int32), ("a", ctypes.c_void_p),
+                ("a_stride", ctypes.c_int64), ("a_pitch", ctypes.c_int64), ("b", ctypes.c_void_p),
+                ("b_stride", ctypes.c_int64), ("b_pitch", ctypes.c_int64), ("scales", ctypes.c_void_p)]
+
+
+class moe_ffn(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("w_gate", ctypes.c_void_p), ("gate_pitch", ctypes.c_int64),
+                ("w_up", ctypes.c_void_p), ("up_pitch", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -77,7 +97,7 @@ def lib() -> ctypes.CDLL:
                                "(or routed_expert_fp4_amd.build.build_library()) first")
         L = ctypes.CDLL(LIB_PATH)
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-        f32 = ctypes.c_float
+        f32, f64 = ctypes.c_float, ctypes.c_double
         sig = {
             "moe_version": ([], i32),
             "moe_status_string": ([i32], ctypes.c_char_p),
@@ -100,6 +120,17 @@ def lib() -> ctypes.CDLL:
             "moe_balance_fwd": ([P, P, i32, i32, i32, P, i32, P, i32, f32, P, P, P, P, P, sz, P], i32),
             "moe_balance_bwd": ([P, P, P, i32, i32, i32, P, i32, P, i32, f32, P, P, i32, P], i32),
             "moe_route_bwd": ([P, P, P, i32, i32, i32, P, P, i32, P], i32),
+            "moe_dropout": ([i32, P, i64, i32, i32, P, i64, P, i64, f64, P, P], i32),
+            "moe_adapter_plan_size": ([i32, i32], sz),
+            "moe_adapter_plan": ([P, i32, i32, P, sz, P], i32),
+            "moe_adapter_workspace_size": ([P, i32], sz),
+            "moe_adapter_fwd": ([P, P, sz, P, i64, i32, P, i64, P, i64, P, f64, P, P, sz, P], i32),
+            "moe_adapter_bwd": ([P, P, sz, P, i64, P, P, i64, i32, P, i64, P, i64, P, P, i32, f64, P, P, sz, P],
+                                i32),
+            "moe_ffn_workspace_size": ([P, i32], sz),
+            "moe_ffn_fwd": ([P, P, i64, i32, P, i64, P, i64, P, i64, P, sz, P], i32),
+            "moe_ffn_bwd": ([P, P, i64, P, i64, P, i64, P, i64, i32, P, i64, i32, P, i64, P, i64, i32, P, sz, P],
+                            i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -569,3 +600,183 @@ def moe_route_bwd(logits, topk_idx, topk_dw, C, E, k, dlogits, token_mask=None, 
             _dense(topk_dw, dev, f32, (C, k), "topk_dw"), C, k, E,
             _maybe(token_mask, dev, torch.uint8, (C,), "token_mask"),
             _dense(dlogits, dev, f32, (C, E), "dlogits"), accumulate)
+
+
+# ---------------------------------------------------------------------------
+# Dropout, and low-rank adapters beside a shared projection
+# ---------------------------------------------------------------------------
+def _rows_or_none(t, dev, dtype, shape, name):
+    """(pointer, pitch), or (NULL, 0) for None."""
+    return (None, 0) if t is None else _rows(t, dev, dtype, shape, name)
+
+
+def _rng(rng, dev, name="rng"):
+    """Seed and offset: a device tensor of two int64 (None: no dropout)."""
+    import torch
+    return None if rng is None else _dense(rng, dev, torch.int64, (2,), name)
+
+
+def moe_dropout(x, p, rng, y, base=None, stream=None):
+    """y [C][K] = base + dropout(x), the mask formed from rng (int64 [2]: seed,
+    offset) and an element's place; the same call on a gradient is its backward
+    pass.  Rows dense, any pitch; y may be x or base."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be a matrix, got shape {tuple(x.shape)}")
+    dev, dtype, (C, K) = x.get_device(), x.dtype, x.shape
+    _launch("moe_dropout", dev, stream, _moe_dtype(dtype), *_rows(x, dev, dtype, (C, K), "x"), C, K,
+            *_rows_or_none(base, dev, dtype, (C, K), "base"), *_rows(y, dev, dtype, (C, K), "y"), p,
+            _rng(rng, dev))
+
+
+class AdapterBank:
+    """The device tensors of adapters A [n][r][K], B [n][N][r] and scales [n] fp32
+    (None: 1), and their moe_adapter_bank struct; rows dense, any pitch."""
+
+    def __init__(self, A, B, scales=None):
+        import torch
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+            raise ValueError(f"A and B must have shapes (n, r, K) and (n, N, r), got {tuple(A.shape)}, {tuple(B.shape)}")
+        dev, dtype = A.get_device(), A.dtype
+        if B.get_device() != dev or B.dtype != dtype:
+            raise ValueError(f"A and B must be of one type on one GPU, got {A.dtype} on {A.device}, {B.dtype} on {B.device}")
+        (n, r, K), N = A.shape, B.shape[1]
+        where = []
+        for t, name in ((A, "A"), (B, "B")):
+            if t.shape[0] == 0:
+                raise ValueError(f"{name} holds no adapter")
+            ptr, pitch = _rows(t[0], dev, dtype, t.shape[1:], name)
+            where += [ptr, t.stride(0) if n > 1 else 0, pitch]
+        self.n, self.r, self.K, self.N, self.dtype, self.device = n, r, K, N, dtype, dev
+        self.keep = (A, B, scales)
+        self.struct = moe_adapter_bank(n, r, K, N, _moe_dtype(dtype), *where,
+                                       _maybe(scales, dev, torch.float32, (n,), "scales"))
+        self.ref = ctypes.byref(self.struct)
+
+
+class AdapterPlan:
+    """The order of a batch's tokens by their adapters (int32 [C], outside [0, n):
+    none); update() makes it anew for another batch of as many tokens."""
+
+    def __init__(self, token_adapter, n, stream=None):
+        import torch
+        self.C, self.n, self.device = token_adapter.shape[0], n, token_adapter.get_device()
+        nbytes = lib().moe_adapter_plan_size(self.C, n)
+        if nbytes == 0:
+            raise MoeError("moe_adapter_plan_size", MOE_ERR_UNSUPPORTED)
+        self.tensor = torch.empty(nbytes // 4, dtype=torch.int32, device=token_adapter.device)
+        self.nbytes = nbytes
+        self.update(token_adapter, stream)
+
+    def update(self, token_adapter, stream=None):
+        moe_adapter_plan(token_adapter, self.C, self.n, self, stream)
+
+
+def moe_adapter_plan(token_adapter, C, n, plan: AdapterPlan, stream=None):
+    import torch
+    dev = plan.device
+    _launch("moe_adapter_plan", dev, stream, _dense(token_adapter, dev, torch.int32, (C,), "token_adapter"), C, n,
+            plan.tensor.data_ptr(), plan.nbytes)
+
+
+class AdapterWorkspace:
+    """Device memory of the adapters' calls for up to C tokens; nothing is kept in
+    it between calls."""
+
+    def __init__(self, bank: AdapterBank, C: int):
+        import torch
+        self.nbytes, self.device = lib().moe_adapter_workspace_size(bank.ref, C), bank.device
+        if self.nbytes == 0:
+            raise MoeError("moe_adapter_workspace_size", MOE_ERR_UNSUPPORTED)
+        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=f"cuda:{bank.device}")
+
+
+def _adapter_plan(plan, bank, C):
+    if plan.device != bank.device or plan.C != C or plan.n != bank.n:
+        raise ValueError(f"the plan is of {plan.C} tokens and {plan.n} adapters on cuda:{plan.device}, the call of "
+                         f"{C} and {bank.n} on cuda:{bank.device}")
+    return plan.tensor.data_ptr(), plan.nbytes
+
+
+def moe_adapter_fwd(bank: AdapterBank, plan: AdapterPlan, x, C, y, ws: AdapterWorkspace, base=None, hidden=None,
+                    dropout=None, stream=None):
+    """y [C][N] = base + s_a B_a (A_a x) for tokens x [C][K]; hidden [C][r] fp32
+    receives A_a x; dropout: (p, rng) of x, as in moe_dropout."""
+    import torch
+    dev, dtype = bank.device, bank.dtype
+    p, rng = dropout or (0.0, None)
+    xp, xs = _rows(x, dev, dtype, (C, bank.K), "x")
+    _launch("moe_adapter_fwd", dev, stream, bank.ref, *_adapter_plan(plan, bank, C), xp, xs, C,
+            *_rows_or_none(base, dev, dtype, (C, bank.N), "base"), *_rows(y, dev, dtype, (C, bank.N), "y"),
+            _maybe(hidden, dev, torch.float32, (C, bank.r), "hidden"), p, _rng(rng, dev),
+            *_scratch(ws, AdapterWorkspace, dev))
+
+
+def moe_adapter_bwd(bank: AdapterBank, plan: AdapterPlan, x, hidden, dy, C, dx, dA, dB, ws: AdapterWorkspace,
+                    base=None, dropout=None, accumulate=False, stream=None):
+    """dx [C][K] = base + the gradient by x, dA [n][r][K] and dB [n][N][r] fp32 for
+    dy [C][N]; each of them may be None, x where dA is, hidden where dB is."""
+    import torch
+    dev, dtype, f32 = bank.device, bank.dtype, torch.float32
+    p, rng = dropout or (0.0, None)
+    xp, xs = _rows_or_none(x, dev, dtype, (C, bank.K), "x")
+    dp, ds = _rows(dy, dev, dtype, (C, bank.N), "dy")
+    _launch("moe_adapter_bwd", dev, stream, bank.ref, *_adapter_plan(plan, bank, C), xp, xs,
+            _maybe(hidden, dev, f32, (C, bank.r), "hidden"), dp, ds, C,
+            *_rows_or_none(base, dev, dtype, (C, bank.K), "base"), *_rows_or_none(dx, dev, dtype, (C, bank.K), "dx"),
+            _maybe(dA, dev, f32, (bank.n, bank.r, bank.K), "dA"), _maybe(dB, dev, f32, (bank.n, bank.N, bank.r), "dB"),
+            accumulate, p, _rng(rng, dev), *_scratch(ws, AdapterWorkspace, dev))
+
+
+# ---------------------------------------------------------------------------
+# The gated feed-forward block with dense weights
+# ---------------------------------------------------------------------------
+class FfnBlock:
+    """The device tensors of a gated block, w_gate and w_up [I][H] (rows dense, any
+    pitch), and their moe_ffn struct; activation "silu" or "gelu" (tanh form)."""
+
+    def __init__(self, w_gate, w_up, activation="silu"):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+        if w_gate.dim() != 2:
+            raise ValueError(f"w_gate must be a matrix, got shape {tuple(w_gate.shape)}")
+        dev, dtype, (I, H) = w_gate.get_device(), w_gate.dtype, w_gate.shape
+        self.H, self.I, self.dtype, self.device = H, I, dtype, dev
+        self.keep = (w_gate, w_up)
+        self.struct = moe_ffn(H, I, _moe_dtype(dtype), ACTIVATIONS[activation],
+                              *_rows(w_gate, dev, dtype, (I, H), "w_gate"), *_rows(w_up, dev, dtype, (I, H), "w_up"))
+        self.ref = ctypes.byref(self.struct)
+
+
+class FfnWorkspace:
+    """Device memory of a gated block's calls for up to C tokens; nothing is kept in
+    it between calls."""
+
+    def __init__(self, block: FfnBlock, C: int):
+        import torch
+        self.nbytes, self.device = lib().moe_ffn_workspace_size(block.ref, C), block.device
+        if self.nbytes == 0:
+            raise MoeError("moe_ffn_workspace_size", MOE_ERR_UNSUPPORTED)
+        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=f"cuda:{block.device}")
+
+
+def moe_ffn_fwd(block: FfnBlock, x, C, h, ws: FfnWorkspace, gate=None, up=None, stream=None):
+    """h [C][I] = act(x w_gate^T) * (x w_up^T); gate and up [C][I] receive the two
+    products for the backward pass."""
+    dev, dtype = block.device, block.dtype
+    xp, xs = _rows(x, dev, dtype, (C, block.H), "x")
+    _launch("moe_ffn_fwd", dev, stream, block.ref, xp, xs, C, *_rows(h, dev, dtype, (C, block.I), "h"),
+            *_rows_or_none(gate, dev, dtype, (C, block.I), "gate"), *_rows_or_none(up, dev, dtype, (C, block.I), "up"),
+            *_scratch(ws, FfnWorkspace, dev))
+
+
+def moe_ffn_bwd(block: FfnBlock, x, gate, up, dh, C, dx, dw_gate, dw_up, ws: FfnWorkspace, accumulate=False,
+                stream=None):
+    """dx [C][H], dw_gate and dw_up [I][H] (of the block's type, or fp32) for dh
+    [C][I]; dx, or both of the others (and then x), may be None."""
+    dev, dtype, H, I = block.device, block.dtype, block.H, block.I
+    gd = dtype if dw_gate is None else dw_gate.dtype
+    _launch("moe_ffn_bwd", dev, stream, block.ref, *_rows_or_none(x, dev, dtype, (C, H), "x"),
+            *_rows(gate, dev, dtype, (C, I), "gate"), *_rows(up, dev, dtype, (C, I), "up"),
+            *_rows(dh, dev, dtype, (C, I), "dh"), C, *_rows_or_none(dx, dev, dtype, (C, H), "dx"), _moe_dtype(gd),
+            *_rows_or_none(dw_gate, dev, gd, (I, H), "dw_gate"), *_rows_or_none(dw_up, dev, gd, (I, H), "dw_up"),
+            accumulate, *_scratch(ws, FfnWorkspace, dev))

@@ -13,7 +13,8 @@ ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", "routed_fp4.hip"), os.path.join(HERE, "csrc", "batched.hip"),
         os.path.join(HERE, "csrc", "latent.hip"), os.path.join(HERE, "csrc", "mxmma.hip"),
         os.path.join(HERE, "csrc", "noalloc.hip"), os.path.join(HERE, "csrc", "balance.hip"),
-        os.path.join(HERE, "csrc", "quant.hip")]
+        os.path.join(HERE, "csrc", "quant.hip"), os.path.join(HERE, "csrc", "adapter.hip"),
+        os.path.join(HERE, "csrc", "dropout.hip"), os.path.join(HERE, "csrc", "ffn.hip")]
 OUT = os.path.join(HERE, "libroutedfp4.so")
 INCLUDE = os.path.join(ROOT, "include")
 

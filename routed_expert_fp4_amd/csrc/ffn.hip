@@ -1,0 +1,716 @@
+// libroutedfp4, the gated feed-forward block with dense weights:
+//
+//   g = x Wg^T,  u = x Wu^T,  h = act(g) * u                              (forward)
+//   du = dh act(g),  dg = dh u act'(g)
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x                      (backward)
+//
+// act is SiLU, g sigmoid(g), or GELU's tanh form, g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)).
+// Sums are fp32; h is formed of them and rounded once, and dg and du are rounded
+// to the tensors' type before they meet the matrix cores again.
+//
+// Kernels:
+//   k_ffew      up to 32 tokens: bound by the stream of both weight matrices;
+//               a workgroup takes eight rows of each, its waves ranges of columns
+//   k_fgemm     more tokens, and the three products of the backward pass: one
+//               tiled matrix product, whose operands lie along the sum's axis or
+//               across it; g and u of the same rows and tokens are in the same lane
+//   k_fjoin     adds ranges of the sum's axis, where tiles alone are too few
+//   k_fact      dg and du
+//   k_fpack     tensors whose rows are not at multiples of 16 bytes, into ones
+//               that are
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+
+#include <type_traits>
+
+#include "dense.h"
+
+namespace rf4 {
+namespace {
+
+__device__ __forceinline__ float sigmoid_of(float z) { return 1.0f / (1.0f + expf(-z)); }
+constexpr float kGelu1 = 1.5957691216057308f;             // 2 sqrt(2 / pi)
+constexpr float kGelu3 = kGelu1 * 0.044715f;
+// act(g) and its slope
+__device__ __forceinline__ float act_of(int act, float g) {
+  const float z = act == MOE_ACT_SILU ? g : g * (kGelu1 + kGelu3 * g * g);
+  const float s = sigmoid_of(z);
+  return s > 0.0f ? g * s : 0.0f * s;                     // -inf, or where the sigmoid is gone: 0
+}
+__device__ __forceinline__ void act_slope(int act, float g, float& a, float& d) {
+  const bool silu = act == MOE_ACT_SILU;
+  const float z = silu ? g : g * (kGelu1 + kGelu3 * g * g);
+  const float s = sigmoid_of(z), c = sigmoid_of(-z);      // 1 - s without its cancellation
+  const float slope = silu ? 1.0f : kGelu1 + 3.0f * kGelu3 * g * g;
+  a = s > 0.0f ? g * s : 0.0f * s;
+  const float e = s * c;
+  d = s + (e > 0.0f ? g * slope * e : 0.0f * e);
+}
+
+struct FArgs {
+  int C, H, I, act;
+  const uint8_t *x, *wg, *wu;
+  int64_t x_pitch, wg_pitch, wu_pitch;                    // bytes, throughout
+  uint8_t *h, *gate, *up;
+  int64_t h_pitch, gate_pitch, up_pitch;
+  // the product's operands and sizes (k_fgemm)
+  const uint8_t *a0, *a1, *b0, *b1;
+  int64_t a_pitch, b0_pitch, b1_pitch;
+  int M, N, K;                                            // of one phase of the sum
+  int mblocks, nblocks, steps, per_split, splits;         // steps of 128 bytes over all phases
+  uint8_t *o0, *o1;
+  int64_t o0_pitch, o1_pitch;
+  int accumulate, out_f32;
+  float* part;                                            // [splits][M][N] fp32
+};
+
+// ---------------------------------------------------------------------------
+// Few tokens
+// ---------------------------------------------------------------------------
+template <int DT>
+__device__ __forceinline__ void store_elem(uint8_t* p, float v) {
+  if constexpr (DT == MOE_DT_F32) *reinterpret_cast<float*>(p) = v;
+  else *reinterpret_cast<uint16_t*>(p) = round16<DT>(v);
+}
+template <int DT>
+__device__ __forceinline__ float load_elem(const uint8_t* p) {
+  if constexpr (DT == MOE_DT_F32) return *reinterpret_cast<const float*>(p);
+  const uint16_t b = *reinterpret_cast<const uint16_t*>(p);
+  if constexpr (DT == MOE_DT_BF16) return __uint_as_float((uint32_t)b << 16);
+  return (float)__builtin_bit_cast(_Float16, b);
+}
+
+template <int DT>
+__device__ __forceinline__ void put_gated(const FArgs& a, int c, int i, float g, float u) {
+  constexpr int B = kBytes<DT>;
+  store_elem<DT>(a.h + c * a.h_pitch + (int64_t)i * B, act_of(a.act, g) * u);
+  if (a.gate) {
+    store_elem<DT>(a.gate + c * a.gate_pitch + (int64_t)i * B, g);
+    store_elem<DT>(a.up + c * a.up_pitch + (int64_t)i * B, u);
+  }
+}
+
+constexpr int kFewWG = 512, kFewWaves = kFewWG / 64;
+template <int DT, int TT>
+__global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
+  constexpr int B = kBytes<DT>;
+  __shared__ float s_red[kFewWaves][TT][64][4];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane & 15, quarter = lane >> 4;
+  const int i0 = 8 * blockIdx.x;
+  // first operand: rows 0 .. 7 of the gate, then of the up matrix (past the last: it again)
+  const int i = i0 + (row & 7) < a.I ? i0 + (row & 7) : a.I - 1;
+  const uint8_t* w = row < 8 ? a.wg + i * a.wg_pitch : a.wu + i * a.wu_pitch;
+  const uint8_t* x[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int c = 16 * t + row;
+    x[t] = a.x + (c < a.C ? c : a.C - 1) * a.x_pitch;
+  }
+  float4v acc[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) acc[t] = float4v(0.0f);
+  auto step = [&](int c, bool whole) {
+    const int k = c + 8 * quarter;
+    const Eight<DT> e = whole ? load8<DT>(w + (int64_t)k * B) : load8_some<DT>(w + (int64_t)k * B, a.H - k);
+    Eight<DT> v[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      v[t] = whole ? load8<DT>(x[t] + (int64_t)k * B) : load8_some<DT>(x[t] + (int64_t)k * B, a.H - k);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = mma8<DT>(e, v[t], acc[t]);
+  };
+  // 64 columns to a wave at a time
+  const int whole = a.H / 64 * 64;
+#pragma unroll 4
+  for (int c = 64 * wave; c < whole; c += 64 * kFewWaves) {
+    step(c, true);
+    step(c + 32, true);
+  }
+  if (whole < a.H && (whole >> 6) % kFewWaves == wave) {
+    step(whole, false);
+    if (whole + 32 < a.H) step(whole + 32, false);
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s_red[wave][t][lane][e] = acc[t][e];
+  __syncthreads();
+  // 16 tokens x 8 rows to a token tile: thread (row of eight, token); register e
+  // of lane l is weight row 4 (l / 16) + e, token l % 16
+  for (int k = tid; k < TT * 128; k += kFewWG) {
+    const int t = k >> 7, n = k & 7, c = (k >> 3) & 15;
+    const int token = 16 * t + c;
+    if (token >= a.C || i0 + n >= a.I) continue;
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kFewWaves; ++v) {
+      g += s_red[v][t][16 * (n >> 2) + c][n & 3];
+      u += s_red[v][t][16 * (2 + (n >> 2)) + c][n & 3];
+    }
+    put_gated<DT>(a, token, i0 + n, g, u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The tiled product
+// ---------------------------------------------------------------------------
+// A step takes 128 bytes along the sum's axis of an operand whose rows lie along
+// it (64 elements of 16 bits, 32 of fp32): LDS holds its rows one after the
+// other, the 16-byte unit u of row m at u ^ (m & 7).  An operand that lies across
+// the axis has that many of its rows in LDS, unit u of row k at u ^ 4 (k & 3)
+// (16 bits), and is read with the transposing LDS loads; fp32 is read element by
+// element.  Both are loaded into LDS directly, one step ahead.
+enum { kFwd, kDx, kDw };
+__device__ const uint32_t __attribute__((aligned(16))) kZeros[4] = {0, 0, 0, 0};
+
+typedef short short4v __attribute__((ext_vector_type(4)));
+template <int DT>
+__device__ __forceinline__ float16v mma32(uint4v a, uint4v b, float16v c) {
+  if constexpr (DT == MOE_DT_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+    return c;
+  } else if constexpr (DT == MOE_DT_BF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+  }
+}
+
+// 32 rows (or columns) from `m` on, quarter ks of a step: lane l holds row l % 32
+// and the eight (fp32: four) elements 2 ks + l / 32 of the step
+template <int DT, bool ALONG, int ROWS>
+__device__ __forceinline__ uint4v fragment(const uint8_t* s, int m, int ks, int lane) {
+  if constexpr (ALONG) {
+    const int row = m + (lane & 31), unit = 2 * ks + (lane >> 5);
+    return *reinterpret_cast<const uint4v*>(s + row * 128 + ((unit ^ (lane & 7)) * 16));
+  } else if constexpr (DT == MOE_DT_F32) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(s) + (8 * ks + 4 * (lane >> 5)) * ROWS + m + (lane & 31);
+    return uint4v{p[0], p[ROWS], p[2 * ROWS], p[3 * ROWS]};
+  } else {
+    // a transposing load gives lane i of 16 element i of four rows, of which lane
+    // i reads elements 4 (i % 4) .. of row i / 4
+    const int g = lane >> 4, i = lane & 15, k = 16 * ks + 8 * (g >> 1) + (i >> 2);
+    const int unit = (m >> 3) + 2 * (g & 1) + ((i >> 1) & 1);
+    const uint8_t* p = s + k * (ROWS * 2) + ((unit ^ (4 * (i >> 2))) * 16) + (i & 1) * 8;
+    const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)p);
+    const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)(p + 4 * ROWS * 2));
+    typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+    const uint2v l = __builtin_bit_cast(uint2v, lo), h = __builtin_bit_cast(uint2v, hi);
+    return uint4v{l[0], l[1], h[0], h[1]};
+  }
+}
+
+template <int DT, int MODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
+  constexpr int B = kBytes<DT>, WG = 64 * WM * WN, E = 128 / B;      // elements of a step
+  constexpr bool AL = MODE != kDw, BL = MODE == kFwd;                // rows along the sum's axis
+  constexpr int MT = BM / WM / 32, NT = 2;
+  static_assert(BN == WN * 64, "two column tiles to a wave");
+  constexpr int kA = BM * 128, kB = BN * 128, kStage = kA + kB;
+  constexpr int LA = kA / 16 / WG, LB = kB / 16 / WG;
+  extern __shared__ __align__(1024) uint8_t s_ab[];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wm = wave / WN, wn = wave % WN;
+  // workgroups b, b + 8, .. run on one XCD: consecutive tiles each, eight blocks
+  // of rows by all blocks of columns at a time, so that an XCD's tiles share both
+  const int total = a.mblocks * a.nblocks, xcd = blockIdx.x & 7, rem = total & 7;
+  const int tile = xcd * (total >> 3) + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
+  const int group = tile / (8 * a.nblocks), in = tile - group * 8 * a.nblocks;
+  const int rows = a.mblocks - 8 * group < 8 ? a.mblocks - 8 * group : 8;
+  const int mb = 8 * group + in % rows, nb = in / rows;
+  // kDw: the blocks of rows are dWg's, then dWu's
+  const int half_blocks = MODE == kDw ? a.mblocks / 2 : a.mblocks;
+  const bool second = MODE == kDw && mb >= half_blocks;
+  const int m0 = (MODE == kDw && second ? mb - half_blocks : mb) * BM;
+  const int n0 = MODE == kFwd ? nb * (BN / 2) : nb * BN;
+  const int s0 = blockIdx.y * a.per_split, s1 = s0 + a.per_split < a.steps ? s0 + a.per_split : a.steps;
+  const int phase = MODE == kDx ? a.steps / 2 : a.steps;             // steps of one phase
+
+  // this thread's units of a step
+  const uint8_t *pa[LA], *pb[LB];                                    // at step 0 of a phase
+  int64_t db[LB];                                                    // kDx: from Wg's to Wu's
+  bool ina[LA], inb[LB];
+  constexpr int UA = BM * B / 16, UB = BN * B / 16;                  // units of a row that lies across
+#pragma unroll
+  for (int i = 0; i < LA; ++i) {
+    const int u = i * WG + tid;
+    if constexpr (AL) {
+      const int r = m0 + (u >> 3), unit = (u & 7) ^ ((u >> 3) & 7);
+      pa[i] = a.a0 + (r < a.M ? r : a.M - 1) * a.a_pitch + unit * 16;
+      ina[i] = true;
+    } else {
+      const int k = u / UA, unit = (u % UA) ^ (DT == MOE_DT_F32 ? 0 : 4 * (k & 3));
+      pa[i] = (second ? a.a1 : a.a0) + k * a.a_pitch + (int64_t)m0 * B + unit * 16;
+      ina[i] = m0 + unit * (16 / B) < a.M;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < LB; ++i) {
+    const int u = i * WG + tid;
+    db[i] = 0;
+    if constexpr (BL) {
+      const int r = u >> 3, unit = (u & 7) ^ (r & 7);
+      const int n = n0 + (r < BN / 2 ? r : r - BN / 2);
+      const int nn = n < a.N ? n : a.N - 1;
+      pb[i] = (r < BN / 2 ? a.b0 + nn * a.b0_pitch : a.b1 + nn * a.b1_pitch) + unit * 16;
+      inb[i] = true;
+    } else {
+      const int k = u / UB, unit = (u % UB) ^ (DT == MOE_DT_F32 ? 0 : 4 * (k & 3));
+      const int64_t at = (int64_t)n0 * B + unit * 16;
+      pb[i] = a.b0 + k * a.b0_pitch + at;
+      if constexpr (MODE == kDx) db[i] = (a.b1 + k * a.b1_pitch + at) - pb[i];
+      inb[i] = n0 + unit * (16 / B) < a.N;
+    }
+  }
+  const int64_t da = MODE == kDx ? a.a1 - a.a0 : 0;
+  auto stage = [&](int s, uint8_t* to) {
+    const bool two = MODE == kDx && s >= phase;
+    const int k0 = (two ? s - phase : s) * E;
+    const int64_t pitch_b = two ? a.b1_pitch : a.b0_pitch;
+    auto load = [&](const uint8_t* p, bool ok, uint8_t* at) {
+      if (!ok) p = reinterpret_cast<const uint8_t*>(kZeros);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                       (__attribute__((address_space(3))) void*)at, 16, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int u = i * WG + tid;
+      const uint8_t* p = pa[i] + (two ? da : 0) + (AL ? (int64_t)k0 * B : k0 * a.a_pitch);
+      const bool ok = AL ? k0 + (((u & 7) ^ ((u >> 3) & 7)) * (16 / B)) < a.K : ina[i] && k0 + u / UA < a.K;
+      load(p, ok, to + (i * WG + wave * 64) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int u = i * WG + tid;
+      const uint8_t* p = pb[i] + (two ? db[i] : 0) + (BL ? (int64_t)k0 * B : k0 * pitch_b);
+      const bool ok = BL ? k0 + (((u & 7) ^ ((u >> 3) & 7)) * (16 / B)) < a.K : inb[i] && k0 + u / UB < a.K;
+      load(p, ok, to + kA + (i * WG + wave * 64) * 16);
+    }
+  };
+
+  float16v acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = float16v(0.0f);
+  auto column = [&](int j) { return MODE == kFwd ? 32 * wn + j * (BN / 2) : 64 * wn + 32 * j; };
+  stage(s0, s_ab);
+  int buf = 0;
+  for (int s = s0; s < s1; ++s) {
+    // this step's loads are complete in every wave, and the last step's reads
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+    const uint8_t* t = s_ab + buf * kStage;
+    uint4v fa[4][MT], fb[4][NT];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fb[k][j] = fragment<DT, BL, BN>(t + kA, column(j), k, lane);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[k][i] = fragment<DT, AL, BM>(t, wm * (BM / WM) + 32 * i, k, lane);
+    }
+    buf ^= 1;
+    if (s + 1 < s1) stage(s + 1, s_ab + buf * kStage);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mma32<DT>(fa[k][i], fb[k][j], acc[i][j]);
+  }
+
+  // register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int m = m0 + wm * (BM / WM) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+      if (m >= a.M) continue;
+      if constexpr (MODE == kFwd) {
+        const int n = n0 + 32 * wn + (lane & 31);
+        if (n < a.N) {
+          if (a.splits > 1) {
+            float* o = a.part + ((int64_t)blockIdx.y * a.M + m) * 2 * a.N + n;
+            o[0] = acc[i][0][r];
+            o[a.N] = acc[i][1][r];
+          } else {
+            put_gated<DT>(a, m, n, acc[i][0][r], acc[i][1][r]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int n = n0 + column(j) + (lane & 31);
+          if (n >= a.N) continue;
+          const float v = acc[i][j][r];
+          if (MODE == kDx && a.splits > 1) {
+            a.part[((int64_t)blockIdx.y * a.M + m) * a.N + n] = v;
+          } else if (MODE == kDw && a.out_f32) {
+            float* o = reinterpret_cast<float*>((second ? a.o1 : a.o0) + m * (second ? a.o1_pitch : a.o0_pitch)) + n;
+            *o = a.accumulate ? *o + v : v;
+          } else {
+            uint8_t* o = (second ? a.o1 : a.o0) + m * (second ? a.o1_pitch : a.o0_pitch) + (int64_t)n * B;
+            store_elem<DT>(o, a.accumulate ? load_elem<DT>(o) + v : v);
+          }
+        }
+      }
+    }
+}
+
+// The ranges of the sum's axis, added in order, then what the tile would have done.
+template <int DT, int MODE>
+__global__ __launch_bounds__(256) void k_fjoin(FArgs a) {
+  const int64_t n = (int64_t)a.M * a.N, step = MODE == kFwd ? 2 * n : n;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    const int64_t m = e / a.N;
+    const int k = (int)(e - m * a.N);
+    if constexpr (MODE == kFwd) {
+      const float* p = a.part + m * 2 * a.N + k;
+      float g = 0.0f, u = 0.0f;
+      for (int s = 0; s < a.splits; ++s) {
+        g += p[s * step];
+        u += p[s * step + a.N];
+      }
+      put_gated<DT>(a, (int)m, k, g, u);
+    } else {
+      float v = 0.0f;
+      for (int s = 0; s < a.splits; ++s) v += a.part[s * step + e];
+      uint8_t* o = a.o0 + m * a.o0_pitch + (int64_t)k * kBytes<DT>;
+      store_elem<DT>(o, a.accumulate ? load_elem<DT>(o) + v : v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dg and du, and packing
+// ---------------------------------------------------------------------------
+struct GArgs {
+  int C, I, act;
+  const uint8_t *gate, *up, *dh;
+  int64_t gate_pitch, up_pitch, dh_pitch;
+  uint8_t *dg, *du;                                       // rows of `units` eights
+  int64_t pitch;
+  int units;
+};
+// past the last column zeros: the sum over I runs on whole units
+template <int DT>
+__global__ __launch_bounds__(256) void k_fact(GArgs a) {
+  constexpr int B = kBytes<DT>;
+  const int64_t n = (int64_t)a.C * a.units;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    const int64_t c = e / a.units;
+    const int i = 8 * (int)(e - c * a.units);
+    const Eight<DT> g = load8_some<DT>(a.gate + c * a.gate_pitch + (int64_t)i * B, a.I - i);
+    const Eight<DT> u = load8_some<DT>(a.up + c * a.up_pitch + (int64_t)i * B, a.I - i);
+    const Eight<DT> d = load8_some<DT>(a.dh + c * a.dh_pitch + (int64_t)i * B, a.I - i);
+    float dg[8], du[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float act, slope;
+      act_slope(a.act, get8<DT>(g, j), act, slope);
+      const float t = get8<DT>(d, j);
+      du[j] = t * act;
+      dg[j] = t * get8<DT>(u, j) * slope;
+    }
+    store8<DT>(a.dg + c * a.pitch + (int64_t)i * B, put8<DT>(dg));
+    store8<DT>(a.du + c * a.pitch + (int64_t)i * B, put8<DT>(du));
+  }
+}
+
+struct KArgs {
+  const uint8_t* in;
+  int64_t in_pitch, rows;
+  int cols, units;
+  uint8_t* out;
+};
+template <int DT>
+__global__ __launch_bounds__(256) void k_fpack(KArgs a) {
+  constexpr int B = kBytes<DT>;
+  const int64_t n = a.rows * a.units;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    const int64_t r = e / a.units;
+    const int k = 8 * (int)(e - r * a.units);
+    store8<DT>(a.out + e * 8 * B, load8_some<DT>(a.in + r * a.in_pitch + (int64_t)k * B, a.cols - k));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+constexpr int kFewTokens = 32;
+
+moe_status ffn_status(const moe_ffn* f) {
+  if (!f) return MOE_ERR_INVALID_ARG;
+  if (!dense_dtype_ok(f->dtype) || (f->act != MOE_ACT_SILU && f->act != MOE_ACT_GELU) || f->hidden < 1 ||
+      f->hidden > MOE_MAX_QUANT_COLS || f->inter < 1 || f->inter > MOE_MAX_QUANT_COLS)
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t s = dense_size(f->dtype);
+  moe_status st = rows_status(Rows{f->w_gate, f->gate_pitch, f->hidden, f->inter, s});
+  return st != MOE_OK ? st : rows_status(Rows{f->w_up, f->up_pitch, f->hidden, f->inter, s});
+}
+
+// rows that can be loaded into LDS 16 bytes at a time, in whole units
+bool whole_units(const void* p, int64_t pitch, int64_t rows, int64_t cols, int64_t s) {
+  return (uintptr_t)p % 16 == 0 && (rows == 1 || pitch * s % 16 == 0) && cols * s % 16 == 0;
+}
+
+// How a product is tiled and split.
+struct Tiling { bool wide; int mblocks, nblocks, steps, splits, per_split; };
+Tiling tiling(int mode, int64_t M, int64_t N, int64_t K, int64_t s) {
+  Tiling t;
+  const int e = (int)(128 / s);
+  auto blocks = [&](int b) {
+    t.mblocks = (int)((M + b - 1) / b) * (mode == kDw ? 2 : 1);
+    const int n = mode == kFwd ? b / 2 : b;
+    t.nblocks = (int)((N + n - 1) / n);
+    return (int64_t)t.mblocks * t.nblocks;
+  };
+  t.wide = blocks(256) >= 192;
+  const int64_t n = t.wide ? blocks(256) : blocks(128);
+  t.steps = (int)((K + e - 1) / e) * (mode == kDx ? 2 : 1);
+  t.splits = 1;
+  t.per_split = t.steps;
+  if (!t.wide && mode != kDw && n < 256) {
+    // ranges of eight steps at least, two workgroups a CU at most
+    int64_t q = 512 / n, most = t.steps / 8;
+    q = q < most ? q : most;
+    if (q > 1) {
+      t.per_split = (int)((t.steps + q - 1) / q);
+      t.splits = (t.steps + t.per_split - 1) / t.per_split;
+    }
+  }
+  return t;
+}
+
+struct FfnWs { size_t x, wg, wu, dg, du, part, total; int64_t hp, ip; };
+FfnWs ffn_ws_for(const moe_ffn* f, int C, bool bwd) {
+  const int64_t s = dense_size(f->dtype), H = f->hidden, I = f->inter;
+  FfnWs w;
+  w.hp = (H + 7) / 8 * 8 * s;
+  w.ip = (I + 7) / 8 * 8 * s;
+  size_t o = 0;
+  // x's own alignment is not known here: room for it and for weights that need it
+  w.x = o; o = align256(o + (size_t)C * w.hp);
+  w.wg = o; o = align256(o + (whole_units(f->w_gate, f->gate_pitch, I, H, s) ? 0 : (size_t)I * w.hp));
+  w.wu = o; o = align256(o + (whole_units(f->w_up, f->up_pitch, I, H, s) ? 0 : (size_t)I * w.hp));
+  w.dg = o; o = align256(o + (bwd ? (size_t)C * w.ip : 0));
+  w.du = o; o = align256(o + (bwd ? (size_t)C * w.ip : 0));
+  w.part = o;
+  const Tiling t = bwd ? tiling(kDx, C, H, I, s) : tiling(kFwd, C, I, H, s);
+  if (t.splits > 1) o = align256(o + (size_t)t.splits * C * (bwd ? H : 2 * I) * sizeof(float));
+  w.total = o;
+  return w;
+}
+// The most that any number of tokens up to C needs: partial results come and go
+// with the ranges, which depend on tiles of 128 tokens.
+size_t ffn_workspace(const moe_ffn* f, int C) {
+  size_t most = 256;
+  for (int c = C;; c = (c - 1) / 128 * 128) {
+    const size_t a = ffn_ws_for(f, c, false).total, b = ffn_ws_for(f, c, true).total;
+    most = a > most ? a : most;
+    most = b > most ? b : most;
+    if (c <= 128) break;
+  }
+  return most;
+}
+
+template <int DT, int MODE, int BM, int BN, int WM, int WN>
+moe_status launch_gemm_t(const FArgs& a, dim3 grid, hipStream_t st) {
+  constexpr int lds = 2 * (BM + BN) * 128;
+  auto k = k_fgemm<DT, MODE, BM, BN, WM, WN>;
+  if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         lds) != hipSuccess)
+    return MOE_ERR_DEVICE;
+  hipLaunchKernelGGL(k, grid, dim3(64 * WM * WN), lds, st, a);
+  return MOE_OK;
+}
+template <int DT, int MODE>
+moe_status launch_product(FArgs a, hipStream_t st) {
+  const Tiling t = tiling(MODE, a.M, a.N, a.K, kBytes<DT>);
+  a.mblocks = t.mblocks; a.nblocks = t.nblocks;
+  a.steps = t.steps; a.splits = t.splits; a.per_split = t.per_split;
+  const dim3 grid((unsigned)(t.mblocks * t.nblocks), (unsigned)t.splits);
+  const moe_status s = t.wide ? launch_gemm_t<DT, MODE, 256, 256, 2, 4>(a, grid, st)
+                              : launch_gemm_t<DT, MODE, 128, 128, 2, 2>(a, grid, st);
+  if (s != MOE_OK) return s;
+  if constexpr (MODE != kDw) {
+    if (t.splits > 1) {
+      const int64_t n = ((int64_t)a.M * a.N + 255) / 256;
+      hipLaunchKernelGGL((k_fjoin<DT, MODE>), dim3((unsigned)(n < 65536 ? n : 65536)), dim3(256), 0, st, a);
+    }
+  }
+  return MOE_OK;
+}
+
+unsigned fill_grid(int64_t n) {
+  n = (n + 255) / 256;
+  return (unsigned)(n < 65536 ? n : 65536);
+}
+
+// x and the weights as the matrix kernel takes them: themselves, or packed.
+template <int DT>
+void operands(const moe_ffn* f, FArgs& a, const FfnWs& w, uint8_t* w8, bool weights, bool need_x, hipStream_t st) {
+  const int64_t s = kBytes<DT>;
+  auto pack = [&](const uint8_t*& p, int64_t& pitch, int64_t rows, size_t at) {
+    if (whole_units(p, pitch / s, rows, a.H, s)) return;
+    KArgs k = {p, pitch, rows, a.H, (a.H + 7) / 8, w8 + at};
+    hipLaunchKernelGGL((k_fpack<DT>), dim3(fill_grid(k.rows * k.units)), dim3(256), 0, st, k);
+    p = k.out;
+    pitch = w.hp;
+  };
+  if (need_x) pack(a.x, a.x_pitch, a.C, w.x);
+  if (weights) {
+    pack(a.wg, a.wg_pitch, a.I, w.wg);
+    pack(a.wu, a.wu_pitch, a.I, w.wu);
+  }
+}
+
+template <int DT>
+moe_status ffn_forward(const moe_ffn* f, FArgs a, const FfnWs& w, uint8_t* w8, hipStream_t st) {
+  if (a.C <= kFewTokens) {
+    const dim3 grid((unsigned)((a.I + 7) / 8));
+    if (a.C <= 16) hipLaunchKernelGGL((k_ffew<DT, 1>), grid, dim3(kFewWG), 0, st, a);
+    else hipLaunchKernelGGL((k_ffew<DT, 2>), grid, dim3(kFewWG), 0, st, a);
+    return MOE_OK;
+  }
+  operands<DT>(f, a, w, w8, true, true, st);
+  a.a0 = a.x; a.a_pitch = a.x_pitch;
+  a.b0 = a.wg; a.b0_pitch = a.wg_pitch; a.b1 = a.wu; a.b1_pitch = a.wu_pitch;
+  a.M = a.C; a.N = a.I; a.K = a.H * kBytes<DT> % 16 ? (a.H + 7) / 8 * 8 : a.H;   // packed rows end in zeros
+  a.part = reinterpret_cast<float*>(w8 + w.part);
+  return launch_product<DT, kFwd>(a, st);
+}
+
+template <int DT>
+moe_status ffn_backward(const moe_ffn* f, FArgs a, GArgs g, uint8_t* dx, int64_t dx_pitch, uint8_t* dwg,
+                        int64_t dwg_pitch, uint8_t* dwu, int64_t dwu_pitch, int out_f32, int accumulate, const FfnWs& w,
+                        uint8_t* w8, hipStream_t st) {
+  g.dg = w8 + w.dg; g.du = w8 + w.du;
+  g.pitch = w.ip;
+  g.units = (a.I + 7) / 8;
+  hipLaunchKernelGGL((k_fact<DT>), dim3(fill_grid((int64_t)a.C * g.units)), dim3(256), 0, st, g);
+  operands<DT>(f, a, w, w8, dx != nullptr, dwg != nullptr, st);
+  a.part = reinterpret_cast<float*>(w8 + w.part);
+  a.accumulate = accumulate;
+  a.a0 = g.dg; a.a1 = g.du; a.a_pitch = w.ip;
+  if (dx) {
+    FArgs p = a;
+    p.b0 = a.wg; p.b0_pitch = a.wg_pitch; p.b1 = a.wu; p.b1_pitch = a.wu_pitch;
+    p.M = a.C; p.N = a.H; p.K = a.I;
+    p.o0 = dx; p.o0_pitch = dx_pitch;
+    const moe_status s = launch_product<DT, kDx>(p, st);
+    if (s != MOE_OK) return s;
+  }
+  if (dwg) {
+    FArgs p = a;
+    p.b0 = a.x; p.b0_pitch = a.x_pitch;
+    p.M = a.I; p.N = a.H; p.K = a.C;
+    p.o0 = dwg; p.o0_pitch = dwg_pitch; p.o1 = dwu; p.o1_pitch = dwu_pitch;
+    p.out_f32 = out_f32;
+    return launch_product<DT, kDw>(p, st);
+  }
+  return MOE_OK;
+}
+
+void ffn_args(const moe_ffn* f, const void* x, int64_t x_pitch, int C, FArgs& a) {
+  const int64_t s = dense_size(f->dtype);
+  a.C = C; a.H = f->hidden; a.I = f->inter; a.act = f->act;
+  a.x = static_cast<const uint8_t*>(x); a.x_pitch = x_pitch * s;
+  a.wg = static_cast<const uint8_t*>(f->w_gate); a.wg_pitch = f->gate_pitch * s;
+  a.wu = static_cast<const uint8_t*>(f->w_up); a.wu_pitch = f->up_pitch * s;
+}
+
+}  // namespace
+}  // namespace rf4
+
+using namespace rf4;
+
+extern "C" {
+
+size_t moe_ffn_workspace_size(const moe_ffn* f, int32_t C) {
+  if (ffn_status(f) != MOE_OK || C < 1 || C > MOE_MAX_FFN_TOKENS) return 0;
+  return ffn_workspace(f, C);
+}
+
+moe_status moe_ffn_fwd(const moe_ffn* f, const void* x, int64_t x_pitch, int32_t C, void* h, int64_t h_pitch, void* gate,
+                       int64_t gate_pitch, void* up, int64_t up_pitch, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = ffn_status(f);
+  if (st != MOE_OK) return st;
+  if (C < 1 || C > MOE_MAX_FFN_TOKENS) return MOE_ERR_UNSUPPORTED;
+  const int64_t s = dense_size(f->dtype);
+  const Rows rx = {x, x_pitch, f->hidden, C, s}, rh = {h, h_pitch, f->inter, C, s};
+  const Rows rg = {gate, gate_pitch, f->inter, C, s}, ru = {up, up_pitch, f->inter, C, s};
+  const Rows w0 = {f->w_gate, f->gate_pitch, f->hidden, f->inter, s}, w1 = {f->w_up, f->up_pitch, f->hidden, f->inter, s};
+  if (!gate != !up) return MOE_ERR_INVALID_ARG;
+  if ((st = rows_status(rx)) != MOE_OK || (st = rows_status(rh)) != MOE_OK) return st;
+  if (gate && ((st = rows_status(rg)) != MOE_OK || (st = rows_status(ru)) != MOE_OK)) return st;
+  for (const Rows& o : {rh, rg, ru})
+    if (share(o, rx) || share(o, w0) || share(o, w1)) return MOE_ERR_INVALID_ARG;
+  if (share(rh, rg) || share(rh, ru) || share(rg, ru)) return MOE_ERR_INVALID_ARG;
+  const FfnWs w = ffn_ws_for(f, C, false);
+  if (!ws || (uintptr_t)ws % 256 || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
+  FArgs a = {};
+  ffn_args(f, x, x_pitch, C, a);
+  a.h = static_cast<uint8_t*>(h); a.h_pitch = h_pitch * s;
+  a.gate = static_cast<uint8_t*>(gate); a.gate_pitch = gate_pitch * s;
+  a.up = static_cast<uint8_t*>(up); a.up_pitch = up_pitch * s;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  hipStream_t q = reinterpret_cast<hipStream_t>(stream);
+  st = f->dtype == MOE_DT_F32    ? ffn_forward<MOE_DT_F32>(f, a, w, w8, q)
+       : f->dtype == MOE_DT_BF16 ? ffn_forward<MOE_DT_BF16>(f, a, w, w8, q)
+                                 : ffn_forward<MOE_DT_F16>(f, a, w, w8, q);
+  if (st != MOE_OK) return st;
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+moe_status moe_ffn_bwd(const moe_ffn* f, const void* x, int64_t x_pitch, const void* gate, int64_t gate_pitch,
+                       const void* up, int64_t up_pitch, const void* dh, int64_t dh_pitch, int32_t C, void* dx,
+                       int64_t dx_pitch, int32_t grad_dtype, void* dw_gate, int64_t dw_gate_pitch, void* dw_up,
+                       int64_t dw_up_pitch, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = ffn_status(f);
+  if (st != MOE_OK) return st;
+  if (C < 1 || C > MOE_MAX_FFN_TOKENS) return MOE_ERR_UNSUPPORTED;
+  if (!dw_gate != !dw_up || (!dx && !dw_gate)) return MOE_ERR_INVALID_ARG;
+  if (dw_gate && grad_dtype != f->dtype && grad_dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
+  const int64_t s = dense_size(f->dtype), H = f->hidden, I = f->inter;
+  const int64_t gs = dw_gate ? dense_size(grad_dtype) : s;
+  const Rows rx = {dw_gate ? x : nullptr, x_pitch, H, C, s}, rg = {gate, gate_pitch, I, C, s}, ru = {up, up_pitch, I, C, s};
+  const Rows rh = {dh, dh_pitch, I, C, s}, rd = {dx, dx_pitch, H, C, s};
+  const Rows w0 = {f->w_gate, f->gate_pitch, H, I, s}, w1 = {f->w_up, f->up_pitch, H, I, s};
+  const Rows g0 = {dw_gate, dw_gate_pitch, H, I, gs}, g1 = {dw_up, dw_up_pitch, H, I, gs};
+  for (const Rows& r : {rg, ru, rh})
+    if ((st = rows_status(r)) != MOE_OK) return st;
+  if (dx && (st = rows_status(rd)) != MOE_OK) return st;
+  if (dw_gate && ((st = rows_status(rx)) != MOE_OK || (st = rows_status(g0)) != MOE_OK || (st = rows_status(g1)) != MOE_OK))
+    return st;
+  for (const Rows& o : {rd, g0, g1})
+    for (const Rows& i : {rx, rg, ru, rh, w0, w1})
+      if (share(o, i)) return MOE_ERR_INVALID_ARG;
+  if (share(rd, g0) || share(rd, g1) || share(g0, g1)) return MOE_ERR_INVALID_ARG;
+  const FfnWs w = ffn_ws_for(f, C, true);
+  if (!ws || (uintptr_t)ws % 256 || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
+  FArgs a = {};
+  ffn_args(f, x, x_pitch, C, a);
+  GArgs g = {};
+  g.C = C; g.I = f->inter; g.act = f->act;
+  g.gate = static_cast<const uint8_t*>(gate); g.gate_pitch = gate_pitch * s;
+  g.up = static_cast<const uint8_t*>(up); g.up_pitch = up_pitch * s;
+  g.dh = static_cast<const uint8_t*>(dh); g.dh_pitch = dh_pitch * s;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  hipStream_t q = reinterpret_cast<hipStream_t>(stream);
+  auto go = [&](auto dt) {
+    return ffn_backward<decltype(dt)::value>(f, a, g, static_cast<uint8_t*>(dx), dx_pitch * s, static_cast<uint8_t*>(dw_gate),
+                                             dw_gate_pitch * gs, static_cast<uint8_t*>(dw_up), dw_up_pitch * gs,
+                                             grad_dtype == MOE_DT_F32, accumulate, w, w8, q);
+  };
+  st = f->dtype == MOE_DT_F32    ? go(std::integral_constant<int, MOE_DT_F32>())
+       : f->dtype == MOE_DT_BF16 ? go(std::integral_constant<int, MOE_DT_BF16>())
+                                 : go(std::integral_constant<int, MOE_DT_F16>());
+  if (st != MOE_OK) return st;
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+}  // extern "C"
