@@ -705,21 +705,25 @@ Split shrink_split(int tiles, int cols) {
   return p;
 }
 
+// The workspace: bounds that hold for every number of tokens up to C, so that it
+// serves fewer too.  With ranges (512 / tiles, tiles > C / 64) the partial sums are
+// those of 512 * 64 tokens at most, and there are four chunks a batch, or one to
+// 2048 tokens, besides every adapter's last.
 struct AdapterWs { size_t part, u, turned, suma, sumb, total; int64_t turn_pitch, turn_stride; };
 AdapterWs adapter_ws(const moe_adapter_bank* b, int C) {
-  const PlanLayout at = plan_layout(C, b->adapters);
   const int64_t s = dense_size(b->dtype);
-  const Split fa = shrink_split(at.max_tiles, b->cols), fb = shrink_split(at.max_tiles, b->rows);
+  const int64_t most = ((b->cols > b->rows ? b->cols : b->rows) + 511) / 512;
+  const int64_t rows = C * most < 512 * 64 ? C * most : C > 512 * 64 ? C : 512 * 64;
+  const int64_t four = C / 256 < 4 ? C / 256 : 4, chunks = (C / 2048 > four ? C / 2048 : four) + (C < b->adapters ? C : b->adapters);
   AdapterWs w;
   size_t o = 0;
-  const int splits = fa.splits > fb.splits ? fa.splits : fb.splits;
-  w.part = o; o = align256(o + (size_t)splits * C * b->rank * sizeof(float));
+  w.part = o; o = align256(o + (size_t)rows * b->rank * sizeof(float));
   w.u = o; o = align256(o + (size_t)C * b->rank * sizeof(float));
   w.turn_pitch = (b->rows * s + 15) / 16 * 16;
   w.turn_stride = w.turn_pitch * b->rank;
   w.turned = o; o = align256(o + (size_t)b->adapters * w.turn_stride);
-  w.suma = o; o = align256(o + (size_t)at.max_chunks * b->rank * b->cols * sizeof(float));
-  w.sumb = o; o = align256(o + (size_t)at.max_chunks * b->rank * b->rows * sizeof(float));
+  w.suma = o; o = align256(o + (size_t)chunks * b->rank * b->cols * sizeof(float));
+  w.sumb = o; o = align256(o + (size_t)chunks * b->rank * b->rows * sizeof(float));
   w.total = o;
   return w;
 }
@@ -787,6 +791,15 @@ void by_dtype(int dtype, F fn) {
   if (dtype == MOE_DT_F32) fn(std::integral_constant<int, MOE_DT_F32>());
   else if (dtype == MOE_DT_BF16) fn(std::integral_constant<int, MOE_DT_BF16>());
   else fn(std::integral_constant<int, MOE_DT_F16>());
+}
+
+// The bank's tensors, the plan and the seed, which no output may overlap.
+struct Reads { Rows r[5]; };
+Reads adapter_reads(const moe_adapter_bank* b, const void* plan, size_t plan_bytes, const uint64_t* rng) {
+  const int64_t s = dense_size(b->dtype), n = b->adapters - 1;
+  return Reads{{span(b->a, (n * b->a_stride + (b->rank - 1) * b->a_pitch + b->cols) * s),
+                span(b->b, (n * b->b_stride + (b->rows - 1) * b->b_pitch + b->rank) * s),
+                span(b->scales, 4 * (int64_t)b->adapters), span(plan, (int64_t)plan_bytes), span(rng, 16)}};
 }
 
 // The checks that both directions make, and the arguments that they share.
@@ -862,6 +875,9 @@ moe_status moe_adapter_fwd(const moe_adapter_bank* b, const void* plan, size_t p
   if (hidden && (st = rows_status(rh)) != MOE_OK) return st;
   if (share(rx, ry) || (share(rb, ry) && !same(rb, ry)) || share(rh, ry) || share(rh, rx) || share(rh, rb))
     return MOE_ERR_INVALID_ARG;
+  const Rows outs[] = {ry, rh, span(ws, (int64_t)ws_bytes)};
+  const Rows tensors[] = {rx, ry, rb, rh};
+  if (any_share(outs, adapter_reads(b, plan, plan_bytes, p > 0 ? rng : nullptr).r) || any_share({outs[2]}, tensors)) return MOE_ERR_INVALID_ARG;
   Call c = {};
   if ((st = adapter_call(b, plan, plan_bytes, C, p, rng, ws, ws_bytes, c)) != MOE_OK) return st;
   hipStream_t q = reinterpret_cast<hipStream_t>(stream);
@@ -903,11 +919,12 @@ moe_status moe_adapter_bwd(const moe_adapter_bank* b, const void* plan, size_t p
   if (da && (st = rows_status(rx)) != MOE_OK) return st;
   if (db && (st = rows_status(rh)) != MOE_OK) return st;
   if ((uintptr_t)da % 4 || (uintptr_t)db % 4) return MOE_ERR_INVALID_ARG;
-  const Rows outs[3] = {rg, ga, gb};
-  const Rows ins[3] = {rd, da ? rx : Rows{}, db ? rh : Rows{}};
-  for (const Rows& o : outs)
-    for (const Rows& i : ins)
-      if (share(o, i)) return MOE_ERR_INVALID_ARG;
+  const Rows outs[] = {rg, ga, gb, span(ws, (int64_t)ws_bytes)};
+  const Rows ins[] = {rd, da ? rx : Rows{}, db ? rh : Rows{}};
+  const Rows grads[] = {rg, ga, gb, dx ? rb : Rows{}};
+  if (any_share(outs, ins) || any_share({outs[3]}, grads) ||
+      any_share(outs, adapter_reads(b, plan, plan_bytes, p > 0 ? rng : nullptr).r))
+    return MOE_ERR_INVALID_ARG;
   if (share(rg, ga) || share(rg, gb) || share(ga, gb)) return MOE_ERR_INVALID_ARG;
   if (dx && base && ((share(rb, rg) && !same(rb, rg)) || share(rb, ga) || share(rb, gb))) return MOE_ERR_INVALID_ARG;
   Call c = {};

@@ -197,6 +197,15 @@ inline bool share(const Rows& a, const Rows& b) {
   if (a.n == b.n) return rows_overlap(a.p, a.cols * a.size, a.pitch * a.size, b.p, b.cols * b.size, b.pitch * b.size, a.n);
   return overlap(a.p, ((a.n - 1) * a.pitch + a.cols) * a.size, b.p, ((b.n - 1) * b.pitch + b.cols) * b.size);
 }
+inline Rows span(const void* p, int64_t bytes) { return Rows{p, bytes, bytes, 1, 1}; }
+// whether something that is written shares a byte with something else
+template <size_t A, size_t B>
+inline bool any_share(const Rows (&outs)[A], const Rows (&others)[B]) {
+  for (const Rows& o : outs)
+    for (const Rows& i : others)
+      if (share(o, i)) return true;
+  return false;
+}
 // the same rows of one matrix
 inline bool same(const Rows& a, const Rows& b) { return a.p == b.p && (a.n == 1 || a.pitch == b.pitch); }
 

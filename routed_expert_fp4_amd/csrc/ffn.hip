@@ -28,22 +28,26 @@
 namespace rf4 {
 namespace {
 
-__device__ __forceinline__ float sigmoid_of(float z) { return 1.0f / (1.0f + expf(-z)); }
+// sigmoid(z) and sigmoid(-z), both to fp32's precision down to its smallest
+__device__ __forceinline__ void sigmoids(float z, float& s, float& c) {
+  const float e = expf(-fabsf(z)), r = 1.0f / (1.0f + e);
+  s = z < 0.0f ? e * r : r;
+  c = z < 0.0f ? r : e * r;
+}
 constexpr float kGelu1 = 1.5957691216057308f;             // 2 sqrt(2 / pi)
 constexpr float kGelu3 = kGelu1 * 0.044715f;
-// act(g) and its slope
+// act(g) and its slope; where the sigmoid is gone they are 0, however large g
 __device__ __forceinline__ float act_of(int act, float g) {
-  const float z = act == MOE_ACT_SILU ? g : g * (kGelu1 + kGelu3 * g * g);
-  const float s = sigmoid_of(z);
-  return s > 0.0f ? g * s : 0.0f * s;                     // -inf, or where the sigmoid is gone: 0
+  float s, c;
+  sigmoids(act == MOE_ACT_SILU ? g : g * (kGelu1 + kGelu3 * g * g), s, c);
+  return s > 0.0f ? g * s : 0.0f * s;
 }
 __device__ __forceinline__ void act_slope(int act, float g, float& a, float& d) {
   const bool silu = act == MOE_ACT_SILU;
-  const float z = silu ? g : g * (kGelu1 + kGelu3 * g * g);
-  const float s = sigmoid_of(z), c = sigmoid_of(-z);      // 1 - s without its cancellation
-  const float slope = silu ? 1.0f : kGelu1 + 3.0f * kGelu3 * g * g;
+  float s, c;
+  sigmoids(silu ? g : g * (kGelu1 + kGelu3 * g * g), s, c);
+  const float slope = silu ? 1.0f : kGelu1 + 3.0f * kGelu3 * g * g, e = s * c;
   a = s > 0.0f ? g * s : 0.0f * s;
-  const float e = s * c;
   d = s + (e > 0.0f ? g * slope * e : 0.0f * e);
 }
 
@@ -647,8 +651,8 @@ moe_status moe_ffn_fwd(const moe_ffn* f, const void* x, int64_t x_pitch, int32_t
   if (!gate != !up) return MOE_ERR_INVALID_ARG;
   if ((st = rows_status(rx)) != MOE_OK || (st = rows_status(rh)) != MOE_OK) return st;
   if (gate && ((st = rows_status(rg)) != MOE_OK || (st = rows_status(ru)) != MOE_OK)) return st;
-  for (const Rows& o : {rh, rg, ru})
-    if (share(o, rx) || share(o, w0) || share(o, w1)) return MOE_ERR_INVALID_ARG;
+  const Rows outs[] = {rh, rg, ru, span(ws, (int64_t)ws_bytes)}, ins[] = {rx, w0, w1};
+  if (any_share(outs, ins) || any_share({outs[3]}, {rh, rg, ru})) return MOE_ERR_INVALID_ARG;
   if (share(rh, rg) || share(rh, ru) || share(rg, ru)) return MOE_ERR_INVALID_ARG;
   const FfnWs w = ffn_ws_for(f, C, false);
   if (!ws || (uintptr_t)ws % 256 || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
@@ -686,9 +690,8 @@ moe_status moe_ffn_bwd(const moe_ffn* f, const void* x, int64_t x_pitch, const v
   if (dx && (st = rows_status(rd)) != MOE_OK) return st;
   if (dw_gate && ((st = rows_status(rx)) != MOE_OK || (st = rows_status(g0)) != MOE_OK || (st = rows_status(g1)) != MOE_OK))
     return st;
-  for (const Rows& o : {rd, g0, g1})
-    for (const Rows& i : {rx, rg, ru, rh, w0, w1})
-      if (share(o, i)) return MOE_ERR_INVALID_ARG;
+  const Rows outs[] = {rd, g0, g1, span(ws, (int64_t)ws_bytes)}, ins[] = {rx, rg, ru, rh, w0, w1};
+  if (any_share(outs, ins) || any_share({outs[3]}, {rd, g0, g1})) return MOE_ERR_INVALID_ARG;
   if (share(rd, g0) || share(rd, g1) || share(g0, g1)) return MOE_ERR_INVALID_ARG;
   const FfnWs w = ffn_ws_for(f, C, true);
   if (!ws || (uintptr_t)ws % 256 || ws_bytes < w.total) return MOE_ERR_WORKSPACE;
