@@ -34,25 +34,30 @@ __device__ __forceinline__ void sigmoids(float z, float& s, float& c) {
   s = z < 0.0f ? e * r : r;
   c = z < 0.0f ? r : e * r;
 }
-constexpr float kGelu1 = 1.5957691216057308f;             // 2 sqrt(2 / pi)
-constexpr float kGelu3 = kGelu1 * 0.044715f;
+// The argument of the sigmoid is g (k1 + k3 g^2): SiLU (1, 0), GELU's tanh form 2
+// sqrt(2 / pi) (1, 0.044715).
+struct Act { float k1, k3; };
+inline Act act_constants(int act) {
+  return act == MOE_ACT_SILU ? Act{1.0f, 0.0f} : Act{1.5957691216057308f, (float)(1.5957691216057308 * 0.044715)};
+}
 // act(g) and its slope; where the sigmoid is gone they are 0, however large g
-__device__ __forceinline__ float act_of(int act, float g) {
+__device__ __forceinline__ float act_of(const Act& k, float g) {
   float s, c;
-  sigmoids(act == MOE_ACT_SILU ? g : g * (kGelu1 + kGelu3 * g * g), s, c);
+  sigmoids(g * (k.k1 + k.k3 * g * g), s, c);
   return s > 0.0f ? g * s : 0.0f * s;
 }
-__device__ __forceinline__ void act_slope(int act, float g, float& a, float& d) {
-  const bool silu = act == MOE_ACT_SILU;
+__device__ __forceinline__ void act_slope(const Act& k, float g, float& a, float& d) {
+  const float q = k.k3 * g * g;
   float s, c;
-  sigmoids(silu ? g : g * (kGelu1 + kGelu3 * g * g), s, c);
-  const float slope = silu ? 1.0f : kGelu1 + 3.0f * kGelu3 * g * g, e = s * c;
+  sigmoids(g * (k.k1 + q), s, c);
+  const float slope = k.k1 + 3.0f * q, e = s * c;
   a = s > 0.0f ? g * s : 0.0f * s;
   d = s + (e > 0.0f ? g * slope * e : 0.0f * e);
 }
 
 struct FArgs {
-  int C, H, I, act;
+  int C, H, I;
+  Act act;
   const uint8_t *x, *wg, *wu;
   int64_t x_pitch, wg_pitch, wu_pitch;                    // bytes, throughout
   uint8_t *h, *gate, *up;
@@ -165,6 +170,26 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
 // (16 bits), and is read with the transposing LDS loads; fp32 is read element by
 // element.  Both are loaded into LDS directly, one step ahead.
 enum { kFwd, kDx, kDw };
+
+// 16 bytes a lane into LDS, at `at` + 16 lane, by inline assembly: behind the
+// compiler's own form it lets every transposing LDS read wait for all of them.  They
+// have no register to write, and are waited for before the barrier that opens them.
+// m0, which holds the LDS address, has no other use on this device.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
+}
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+  return reinterpret_cast<const uint8_t*>((uintptr_t)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, const uint8_t* at) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(uniform(base)), "s"(lds_address(at)));
+}
+__device__ __forceinline__ void load_lds(const uint8_t* p, const uint8_t* at) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(lds_address(at)));
+}
 __device__ const uint32_t __attribute__((aligned(16))) kZeros[4] = {0, 0, 0, 0};
 
 typedef short short4v __attribute__((ext_vector_type(4)));
@@ -232,65 +257,64 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
   const int s0 = blockIdx.y * a.per_split, s1 = s0 + a.per_split < a.steps ? s0 + a.per_split : a.steps;
   const int phase = MODE == kDx ? a.steps / 2 : a.steps;             // steps of one phase
 
-  // this thread's units of a step
-  const uint8_t *pa[LA], *pb[LB];                                    // at step 0 of a phase
-  int64_t db[LB];                                                    // kDx: from Wg's to Wu's
-  bool ina[LA], inb[LB];
+  // This thread's units of a step as offsets from the step's (scalar) bases; rows
+  // and columns past the last are the last again, whose sums are not used.
   constexpr int UA = BM * B / 16, UB = BN * B / 16;                  // units of a row that lies across
+  uint32_t oa[LA], ob[LB];
+  auto unit_along = [&](int u) { return (u & 7) ^ ((u >> 3) & 7); };
+  auto unit_across = [&](int u, int n) { return (u % n) ^ (DT == MOE_DT_F32 ? 0 : 4 * ((u / n) & 3)); };
 #pragma unroll
   for (int i = 0; i < LA; ++i) {
     const int u = i * WG + tid;
     if constexpr (AL) {
-      const int r = m0 + (u >> 3), unit = (u & 7) ^ ((u >> 3) & 7);
-      pa[i] = a.a0 + (r < a.M ? r : a.M - 1) * a.a_pitch + unit * 16;
-      ina[i] = true;
+      const int r = u >> 3, most = a.M - 1 - m0;
+      oa[i] = (uint32_t)((r < most ? r : most) * (uint32_t)a.a_pitch + unit_along(u) * 16);
     } else {
-      const int k = u / UA, unit = (u % UA) ^ (DT == MOE_DT_F32 ? 0 : 4 * (k & 3));
-      pa[i] = (second ? a.a1 : a.a0) + k * a.a_pitch + (int64_t)m0 * B + unit * 16;
-      ina[i] = m0 + unit * (16 / B) < a.M;
+      const int most = (a.M * B + 15) / 16 - 1 - m0 * B / 16, n = unit_across(u, UA);
+      oa[i] = (uint32_t)(u / UA) * (uint32_t)a.a_pitch + (n < most ? n : most) * 16;
     }
   }
 #pragma unroll
   for (int i = 0; i < LB; ++i) {
     const int u = i * WG + tid;
-    db[i] = 0;
     if constexpr (BL) {
-      const int r = u >> 3, unit = (u & 7) ^ (r & 7);
-      const int n = n0 + (r < BN / 2 ? r : r - BN / 2);
-      const int nn = n < a.N ? n : a.N - 1;
-      pb[i] = (r < BN / 2 ? a.b0 + nn * a.b0_pitch : a.b1 + nn * a.b1_pitch) + unit * 16;
-      inb[i] = true;
+      const int r = (u >> 3) & (BN / 2 - 1), most = a.N - 1 - n0;
+      ob[i] = (uint32_t)(r < most ? r : most) * (uint32_t)(i < LB / 2 ? a.b0_pitch : a.b1_pitch) + unit_along(u) * 16;
     } else {
-      const int k = u / UB, unit = (u % UB) ^ (DT == MOE_DT_F32 ? 0 : 4 * (k & 3));
-      const int64_t at = (int64_t)n0 * B + unit * 16;
-      pb[i] = a.b0 + k * a.b0_pitch + at;
-      if constexpr (MODE == kDx) db[i] = (a.b1 + k * a.b1_pitch + at) - pb[i];
-      inb[i] = n0 + unit * (16 / B) < a.N;
+      const int most = (a.N * B + 15) / 16 - 1 - n0 * B / 16, n = unit_across(u, UB);
+      ob[i] = (uint32_t)(u / UB) * (uint32_t)a.b0_pitch + (n < most ? n : most) * 16;
     }
   }
-  const int64_t da = MODE == kDx ? a.a1 - a.a0 : 0;
+  const uint8_t* a0 = (second ? a.a1 : a.a0) + (AL ? m0 * a.a_pitch : (int64_t)m0 * B);
+  const uint8_t* b0 = a.b0 + (BL ? n0 * a.b0_pitch : (int64_t)n0 * B);
+  const uint8_t* b1 = MODE == kFwd ? a.b1 + n0 * a.b1_pitch : a.b1 + (int64_t)n0 * B;
   auto stage = [&](int s, uint8_t* to) {
     const bool two = MODE == kDx && s >= phase;
     const int k0 = (two ? s - phase : s) * E;
-    const int64_t pitch_b = two ? a.b1_pitch : a.b0_pitch;
-    auto load = [&](const uint8_t* p, bool ok, uint8_t* at) {
-      if (!ok) p = reinterpret_cast<const uint8_t*>(kZeros);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
-                                       (__attribute__((address_space(3))) void*)at, 16, 0, 0);
-    };
+    const uint8_t* pa = AL ? a0 + (two ? a.a1 - a.a0 : 0) + (int64_t)k0 * B : a0 + k0 * a.a_pitch;
+    const uint8_t* pb = BL ? b0 + (int64_t)k0 * B : (two ? b1 : b0) + k0 * a.b0_pitch;
+    const uint8_t* pu = b1 + (int64_t)k0 * B;
+    const bool whole = k0 + E <= a.K;                                // else: zeros past the sum's end
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      const int u = i * WG + tid;
-      const uint8_t* p = pa[i] + (two ? da : 0) + (AL ? (int64_t)k0 * B : k0 * a.a_pitch);
-      const bool ok = AL ? k0 + (((u & 7) ^ ((u >> 3) & 7)) * (16 / B)) < a.K : ina[i] && k0 + u / UA < a.K;
-      load(p, ok, to + (i * WG + wave * 64) * 16);
-    }
+      for (int i = 0; i < LA; ++i) load_lds(pa, oa[i], to + (i * WG + wave * 64) * 16);
 #pragma unroll
-    for (int i = 0; i < LB; ++i) {
-      const int u = i * WG + tid;
-      const uint8_t* p = pb[i] + (two ? db[i] : 0) + (BL ? (int64_t)k0 * B : k0 * pitch_b);
-      const bool ok = BL ? k0 + (((u & 7) ^ ((u >> 3) & 7)) * (16 / B)) < a.K : inb[i] && k0 + u / UB < a.K;
-      load(p, ok, to + kA + (i * WG + wave * 64) * 16);
+      for (int i = 0; i < LB; ++i) load_lds(BL && i >= LB / 2 ? pu : pb, ob[i], to + kA + (i * WG + wave * 64) * 16);
+    } else {
+      auto load = [&](const uint8_t* base, uint32_t off, bool ok, uint8_t* at) {
+        load_lds(ok ? base + off : reinterpret_cast<const uint8_t*>(kZeros), at);
+      };
+#pragma unroll
+      for (int i = 0; i < LA; ++i) {
+        const int u = i * WG + tid;
+        load(pa, oa[i], k0 + (AL ? unit_along(u) * (16 / B) : u / UA) < a.K, to + (i * WG + wave * 64) * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < LB; ++i) {
+        const int u = i * WG + tid;
+        load(BL && i >= LB / 2 ? pu : pb, ob[i], k0 + (BL ? unit_along(u) * (16 / B) : u / UB) < a.K,
+             to + kA + (i * WG + wave * 64) * 16);
+      }
     }
   };
 
@@ -300,30 +324,55 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = float16v(0.0f);
   auto column = [&](int j) { return MODE == kFwd ? 32 * wn + j * (BN / 2) : 64 * wn + 32 * j; };
-  stage(s0, s_ab);
-  int buf = 0;
-  for (int s = s0; s < s1; ++s) {
-    // this step's loads are complete in every wave, and the last step's reads
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+  uint4v fa[2][MT], fb[2][NT];
+  auto read = [&](const uint8_t* t, int k) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fb[k & 1][j] = fragment<DT, BL, BN>(t + kA, column(j), k, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fa[k & 1][i] = fragment<DT, AL, BM>(t, wm * (BM / WM) + 32 * i, k, lane);
+  };
+  auto product = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = mma32<DT>(fa[k & 1][i], fb[k & 1][j], acc[i][j]);
+  };
+  // this wave's loads into LDS and reads from it are complete, and so every wave's
+  auto meet = [&] {
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);                    // lgkmcnt(0) too, in the compiler's own count
     __builtin_amdgcn_s_barrier();
     asm volatile("" : : : "memory");
+  };
+  // A step is four quarters.  A quarter's operands are read during the one before;
+  // the move to the next step comes before the last quarter's products, so that
+  // they cover it: by then this step is read, and its buffer is free for the step
+  // after the next.
+  stage(s0, s_ab);
+  meet();
+  read(s_ab, 0);
+  if (s0 + 1 < s1) stage(s0 + 1, s_ab + kStage);
+  // nothing is on its way when the loop begins, scalar loads among it: they would
+  // make every wait in it one for all LDS reads
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_sched_barrier(0);
+  int buf = 0;
+  for (int s = s0; s < s1; ++s) {
     const uint8_t* t = s_ab + buf * kStage;
-    uint4v fa[4][MT], fb[4][NT];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) fb[k][j] = fragment<DT, BL, BN>(t + kA, column(j), k, lane);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fa[k][i] = fragment<DT, AL, BM>(t, wm * (BM / WM) + 32 * i, k, lane);
+    for (int k = 0; k < 3; ++k) {
+      read(t, k + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      product(k);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    meet();
+    read(s_ab + (buf ^ 1) * kStage, 0);                    // behind the last step: read, and not used
+    if (s + 2 < s1) stage(s + 2, s_ab + buf * kStage);
+    __builtin_amdgcn_sched_barrier(0);
+    product(3);
+    __builtin_amdgcn_sched_barrier(0);
     buf ^= 1;
-    if (s + 1 < s1) stage(s + 1, s_ab + buf * kStage);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mma32<DT>(fa[k][i], fb[k][j], acc[i][j]);
   }
 
   // register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
@@ -392,7 +441,8 @@ __global__ __launch_bounds__(256) void k_fjoin(FArgs a) {
 // dg and du, and packing
 // ---------------------------------------------------------------------------
 struct GArgs {
-  int C, I, act;
+  int C, I;
+  Act act;
   const uint8_t *gate, *up, *dh;
   int64_t gate_pitch, up_pitch, dh_pitch;
   uint8_t *dg, *du;                                       // rows of `units` eights
@@ -456,9 +506,10 @@ moe_status ffn_status(const moe_ffn* f) {
   return st != MOE_OK ? st : rows_status(Rows{f->w_up, f->up_pitch, f->hidden, f->inter, s});
 }
 
-// rows that can be loaded into LDS 16 bytes at a time, in whole units
+// rows that can be loaded into LDS 16 bytes at a time, in whole units, 256 of them
+// by 32-bit offsets
 bool whole_units(const void* p, int64_t pitch, int64_t rows, int64_t cols, int64_t s) {
-  return (uintptr_t)p % 16 == 0 && (rows == 1 || pitch * s % 16 == 0) && cols * s % 16 == 0;
+  return (uintptr_t)p % 16 == 0 && (rows == 1 || (pitch * s % 16 == 0 && pitch * s <= (1 << 23))) && cols * s % 16 == 0;
 }
 
 // How a product is tiled and split.
@@ -621,7 +672,7 @@ moe_status ffn_backward(const moe_ffn* f, FArgs a, GArgs g, uint8_t* dx, int64_t
 
 void ffn_args(const moe_ffn* f, const void* x, int64_t x_pitch, int C, FArgs& a) {
   const int64_t s = dense_size(f->dtype);
-  a.C = C; a.H = f->hidden; a.I = f->inter; a.act = f->act;
+  a.C = C; a.H = f->hidden; a.I = f->inter; a.act = act_constants(f->act);
   a.x = static_cast<const uint8_t*>(x); a.x_pitch = x_pitch * s;
   a.wg = static_cast<const uint8_t*>(f->w_gate); a.wg_pitch = f->gate_pitch * s;
   a.wu = static_cast<const uint8_t*>(f->w_up); a.wu_pitch = f->up_pitch * s;
@@ -698,7 +749,7 @@ moe_status moe_ffn_bwd(const moe_ffn* f, const void* x, int64_t x_pitch, const v
   FArgs a = {};
   ffn_args(f, x, x_pitch, C, a);
   GArgs g = {};
-  g.C = C; g.I = f->inter; g.act = f->act;
+  g.C = C; g.I = f->inter; g.act = act_constants(f->act);
   g.gate = static_cast<const uint8_t*>(gate); g.gate_pitch = gate_pitch * s;
   g.up = static_cast<const uint8_t*>(up); g.up_pitch = up_pitch * s;
   g.dh = static_cast<const uint8_t*>(dh); g.dh_pitch = dh_pitch * s;
