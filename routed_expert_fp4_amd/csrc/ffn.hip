@@ -165,7 +165,8 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
 // ---------------------------------------------------------------------------
 // A step takes 128 bytes along the sum's axis of an operand whose rows lie along
 // it (64 elements of 16 bits, 32 of fp32): LDS holds its rows one after the
-// other, the 16-byte unit u of row m at u ^ (m & 7).  An operand that lies across
+// other, the 16-byte unit u of row m at u ^ (m / 2 & 7) (16 rows that are read
+// together fill the 256 bytes of the banks).  An operand that lies across
 // the axis has that many of its rows in LDS, unit u of row k at u ^ 4 (k & 3)
 // (16 bits), and is read with the transposing LDS loads; fp32 is read element by
 // element.  Both are loaded into LDS directly, one step ahead.
@@ -213,7 +214,7 @@ template <int DT, bool ALONG, int ROWS>
 __device__ __forceinline__ uint4v fragment(const uint8_t* s, int m, int ks, int lane) {
   if constexpr (ALONG) {
     const int row = m + (lane & 31), unit = 2 * ks + (lane >> 5);
-    return *reinterpret_cast<const uint4v*>(s + row * 128 + ((unit ^ (lane & 7)) * 16));
+    return *reinterpret_cast<const uint4v*>(s + row * 128 + ((unit ^ ((lane >> 1) & 7)) * 16));
   } else if constexpr (DT == MOE_DT_F32) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(s) + (8 * ks + 4 * (lane >> 5)) * ROWS + m + (lane & 31);
     return uint4v{p[0], p[ROWS], p[2 * ROWS], p[3 * ROWS]};
@@ -232,11 +233,10 @@ __device__ __forceinline__ uint4v fragment(const uint8_t* s, int m, int ks, int 
 }
 
 template <int DT, int MODE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
   constexpr int B = kBytes<DT>, WG = 64 * WM * WN, E = 128 / B;      // elements of a step
   constexpr bool AL = MODE != kDw, BL = MODE == kFwd;                // rows along the sum's axis
-  constexpr int MT = BM / WM / 32, NT = 2;
-  static_assert(BN == WN * 64, "two column tiles to a wave");
+  constexpr int MT = BM / WM / 32, NT = BN / WN / 32, NH = NT / 2;   // row and column tiles of a wave
   constexpr int kA = BM * 128, kB = BN * 128, kStage = kA + kB;
   constexpr int LA = kA / 16 / WG, LB = kB / 16 / WG;
   extern __shared__ __align__(1024) uint8_t s_ab[];
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
   // and columns past the last are the last again, whose sums are not used.
   constexpr int UA = BM * B / 16, UB = BN * B / 16;                  // units of a row that lies across
   uint32_t oa[LA], ob[LB];
-  auto unit_along = [&](int u) { return (u & 7) ^ ((u >> 3) & 7); };
+  auto unit_along = [&](int u) { return (u & 7) ^ ((u >> 4) & 7); };
   auto unit_across = [&](int u, int n) { return (u % n) ^ (DT == MOE_DT_F32 ? 0 : 4 * ((u / n) & 3)); };
 #pragma unroll
   for (int i = 0; i < LA; ++i) {
@@ -288,31 +288,38 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
   const uint8_t* a0 = (second ? a.a1 : a.a0) + (AL ? m0 * a.a_pitch : (int64_t)m0 * B);
   const uint8_t* b0 = a.b0 + (BL ? n0 * a.b0_pitch : (int64_t)n0 * B);
   const uint8_t* b1 = MODE == kFwd ? a.b1 + n0 * a.b1_pitch : a.b1 + (int64_t)n0 * B;
-  auto stage = [&](int s, uint8_t* to) {
+  // where a step's operands lie
+  struct From { const uint8_t *pa, *pb, *pu; int k0; };
+  auto from = [&](int s) {
     const bool two = MODE == kDx && s >= phase;
     const int k0 = (two ? s - phase : s) * E;
-    const uint8_t* pa = AL ? a0 + (two ? a.a1 - a.a0 : 0) + (int64_t)k0 * B : a0 + k0 * a.a_pitch;
-    const uint8_t* pb = BL ? b0 + (int64_t)k0 * B : (two ? b1 : b0) + k0 * a.b0_pitch;
-    const uint8_t* pu = b1 + (int64_t)k0 * B;
-    const bool whole = k0 + E <= a.K;                                // else: zeros past the sum's end
-    if (whole) {
+    return From{AL ? a0 + (two ? a.a1 - a.a0 : 0) + (int64_t)k0 * B : a0 + k0 * a.a_pitch,
+                BL ? b0 + (int64_t)k0 * B : (two ? b1 : b0) + k0 * a.b0_pitch, b1 + (int64_t)k0 * B, k0};
+  };
+  auto stage_one = [&](const From& f, const uint8_t* to, int i) {
+    if (i < LA) load_lds(f.pa, oa[i], to + (i * WG + wave * 64) * 16);
+    else load_lds(BL && i - LA >= LB / 2 ? f.pu : f.pb, ob[i - LA], to + kA + ((i - LA) * WG + wave * 64) * 16);
+  };
+  auto stage = [&](int s, const uint8_t* to) {
+    const From f = from(s);
+    const int k0 = f.k0;
+    if (k0 + E <= a.K) {
 #pragma unroll
-      for (int i = 0; i < LA; ++i) load_lds(pa, oa[i], to + (i * WG + wave * 64) * 16);
-#pragma unroll
-      for (int i = 0; i < LB; ++i) load_lds(BL && i >= LB / 2 ? pu : pb, ob[i], to + kA + (i * WG + wave * 64) * 16);
+      for (int i = 0; i < LA + LB; ++i) stage_one(f, to, i);
     } else {
-      auto load = [&](const uint8_t* base, uint32_t off, bool ok, uint8_t* at) {
+      // zeros past the sum's end
+      auto load = [&](const uint8_t* base, uint32_t off, bool ok, const uint8_t* at) {
         load_lds(ok ? base + off : reinterpret_cast<const uint8_t*>(kZeros), at);
       };
 #pragma unroll
       for (int i = 0; i < LA; ++i) {
         const int u = i * WG + tid;
-        load(pa, oa[i], k0 + (AL ? unit_along(u) * (16 / B) : u / UA) < a.K, to + (i * WG + wave * 64) * 16);
+        load(f.pa, oa[i], k0 + (AL ? unit_along(u) * (16 / B) : u / UA) < a.K, to + (i * WG + wave * 64) * 16);
       }
 #pragma unroll
       for (int i = 0; i < LB; ++i) {
         const int u = i * WG + tid;
-        load(BL && i >= LB / 2 ? pu : pb, ob[i], k0 + (BL ? unit_along(u) * (16 / B) : u / UB) < a.K,
+        load(BL && i >= LB / 2 ? f.pu : f.pb, ob[i], k0 + (BL ? unit_along(u) * (16 / B) : u / UB) < a.K,
              to + kA + (i * WG + wave * 64) * 16);
       }
     }
@@ -323,7 +330,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = float16v(0.0f);
-  auto column = [&](int j) { return MODE == kFwd ? 32 * wn + j * (BN / 2) : 64 * wn + 32 * j; };
+  // the column tiles of a wave: forward, NH of the gate's and the same of up's
+  auto column = [&](int j) {
+    return MODE == kFwd ? 32 * (NH * wn + j % NH) + (j / NH) * (BN / 2) : 32 * (NT * wn + j);
+  };
   uint4v fa[2][MT], fb[2][NT];
   auto read = [&](const uint8_t* t, int k) {
 #pragma unroll
@@ -331,11 +341,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) fa[k & 1][i] = fragment<DT, AL, BM>(t, wm * (BM / WM) + 32 * i, k, lane);
   };
-  auto product = [&](int k) {
+  // a quarter's products, and loads n0 .. n1 - 1 of a step to come between them: a
+  // matrix instruction leaves the time for one
+  From f = from(s0 + 1);
+  bool more = false;
+  auto product = [&](int k, int n0, int n1, const uint8_t* to) {
+    int n = n0;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mma32<DT>(fa[k & 1][i], fb[k & 1][j], acc[i][j]);
+      for (int j = 0; j < NT; ++j) {
+        acc[i][j] = mma32<DT>(fa[k & 1][i], fb[k & 1][j], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+        const int upto = n0 + (n1 - n0) * (i * NT + j + 1) / (MT * NT);
+#pragma unroll
+        for (; n < upto; ++n)
+          if (more) stage_one(f, to, n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   };
   // this wave's loads into LDS and reads from it are complete, and so every wave's
   auto meet = [&] {
@@ -347,7 +370,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
   // A step is four quarters.  A quarter's operands are read during the one before;
   // the move to the next step comes before the last quarter's products, so that
   // they cover it: by then this step is read, and its buffer is free for the step
-  // after the next.
+  // after the next, whose loads go out between those products (spread over three
+  // quarters they came too late: 4096 tokens x 7168 x 4096, dx 473 us against 430).
   stage(s0, s_ab);
   meet();
   read(s_ab, 0);
@@ -358,20 +382,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
   __builtin_amdgcn_sched_barrier(0);
   int buf = 0;
   for (int s = s0; s < s1; ++s) {
-    const uint8_t* t = s_ab + buf * kStage;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      read(t, k + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      product(k);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    const uint8_t *t = s_ab + buf * kStage, *next = s_ab + (buf ^ 1) * kStage;
+    read(t, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    product(0, 0, 0, t);
+    read(t, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    product(1, 0, 0, t);
+    read(t, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    product(2, 0, 0, t);
     meet();
-    read(s_ab + (buf ^ 1) * kStage, 0);                    // behind the last step: read, and not used
-    if (s + 2 < s1) stage(s + 2, s_ab + buf * kStage);
+    read(next, 0);                                         // behind the last step: read, and not used
     __builtin_amdgcn_sched_barrier(0);
-    product(3);
-    __builtin_amdgcn_sched_barrier(0);
+    f = from(s + 2);
+    more = s + 2 < s1 && f.k0 + E <= a.K;
+    if (!more && s + 2 < s1) stage(s + 2, t);
+    product(3, 0, LA + LB, t);
     buf ^= 1;
   }
 
@@ -383,14 +410,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fgemm(FArgs a) {
       const int m = m0 + wm * (BM / WM) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
       if (m >= a.M) continue;
       if constexpr (MODE == kFwd) {
-        const int n = n0 + 32 * wn + (lane & 31);
-        if (n < a.N) {
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+          const int n = n0 + column(j) + (lane & 31);
+          if (n >= a.N) continue;
           if (a.splits > 1) {
             float* o = a.part + ((int64_t)blockIdx.y * a.M + m) * 2 * a.N + n;
-            o[0] = acc[i][0][r];
-            o[a.N] = acc[i][1][r];
+            o[0] = acc[i][j][r];
+            o[a.N] = acc[i][j + NH][r];
           } else {
-            put_gated<DT>(a, m, n, acc[i][0][r], acc[i][1][r]);
+            put_gated<DT>(a, m, n, acc[i][j][r], acc[i][j + NH][r]);
           }
         }
       } else {
