@@ -23,7 +23,7 @@
 //   k_ashrink   t or u: a tile's tokens by a range of columns; partial sums
 //   k_aexpand   y or dx: a tile's tokens by a range of columns; adds the partial
 //               sums up first and keeps them (t for the caller, u for the next)
-//   k_aouter    dA and dB of a chunk's tokens, 128 columns to a workgroup
+//   k_aouter    dA and dB of a chunk's tokens, 128 columns (fp32: 64) to a workgroup
 //   k_areduce   adds the chunks up
 //   k_aturn     B by rank for u's product
 #include <hip/hip_bf16.h>
@@ -225,20 +225,27 @@ __device__ __forceinline__ void turn8(const uint4v (&in)[8], uint4v (&out)[8]) {
 }
 
 struct Tile { int who, first, count; };
+// Entry i of a list (i < its room in the plan, whatever the plan says); false where
+// the plan has no such entry or is of another batch: then nothing is done.
 __device__ __forceinline__ bool plan_entry(const int32_t* plan, int C, int n, int slot, int64_t list, int i, Tile& t) {
-  // a plan of another batch: nothing is done
-  if (plan[0] != kPlanMagic || plan[1] != C || plan[2] != n || i >= plan[slot]) return false;
-  const int4 v = *reinterpret_cast<const int4*>(plan + list + 4 * (int64_t)i);
+  const int4 h = *reinterpret_cast<const int4*>(plan), v = *reinterpret_cast<const int4*>(plan + list + 4 * (int64_t)i);
+  const int most = slot == 3 ? h.w : plan[4];
   t = Tile{__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y), __builtin_amdgcn_readfirstlane(v.z)};
-  return true;
+  return h.x == kPlanMagic && h.y == C && h.z == n && i < most;
 }
+
+// Tiles of 16 columns that a wave takes in k_aexpand and k_aouter: a lane has that
+// many consecutive ones, 16 bytes.
+template <int DT>
+constexpr int kTiles = DT == MOE_DT_F32 ? 4 : 8;
+
+__device__ const uint32_t __attribute__((aligned(16))) kZeroRow[8] = {};
 
 struct AArgs {
   const int32_t* plan;
   PlanLayout at;
   int C, n, r;
-  // shrink: in [C][cols] by w [n][r][cols]; expand: out [C][cols] from w [n][cols][r] or (BWD) [n][r][cols];
-  // outer: in [C][cols] by small [C][r]
+  // shrink: in [C][cols] by w [n][r][cols]; expand: out [C][cols] from w [n][cols][r] or (BWD) [n][r][cols]
   int cols;
   const uint8_t* in;
   int64_t in_pitch;                     // pitches and strides in bytes
@@ -249,39 +256,41 @@ struct AArgs {
   uint8_t* out;
   int64_t out_pitch;
   const float* scales;
-  float* part;                          // shrink, expand: [splits][C][r] in the plan's order
+  float* part;                          // [splits][C][r] in the plan's order
   int splits, per_split;                // column ranges, columns in each (multiple of 256)
   float* keep;                          // expand: the finished sums [C][r] by token, or NULL
-  const float* small;                   // outer: [C][r] by token
-  float* sums;                          // outer: [chunks][r][cols]
   Dropout drop;
 };
 
 // ---------------------------------------------------------------------------
 // t = x A^T over a range of columns
 // ---------------------------------------------------------------------------
+// A workgroup has a tile's tokens, 64 ranks at most and a range of columns, of which
+// its waves take 128 bytes of every row in turn; a wave loads the next columns
+// before it multiplies the last.
 template <int DT, int NT, int TT, bool DROP>
 __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
-  constexpr int B = kBytes<DT>, T = 16 * TT;
+  constexpr int B = kBytes<DT>, T = 16 * TT, S = 2 / (B / 2), U = 32 * S;   // steps and columns of a wave's turn
   __shared__ float s_red[2][T][NT * 16];
   Tile t;
   if (!plan_entry(a.plan, a.C, a.n, 3, a.at.tiles, blockIdx.x, t) || t.who < 0) return;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane & 15, quarter = lane >> 4;
+  const int r0 = 64 * blockIdx.z, ranks = a.r - r0 < 64 ? a.r - r0 : 64;
   Counter ctr = {};
   if constexpr (DROP) ctr = counter_of(a.drop.rng);
   const uint8_t *xr[TT], *ar[NT];
   int token[TT];
+  // rows past the last repeat it: their sums are not used
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const int k = 16 * i + row;
     token[i] = a.plan[a.at.perm + t.first + (k < t.count ? k : t.count - 1)];
-    xr[i] = a.in + token[i] * a.in_pitch;
+    xr[i] = a.in + token[i] * a.in_pitch + 8 * quarter * B;
   }
-  // rows past the last repeat it: their sums are not used
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int k = 16 * j + row;
-    ar[j] = a.w + t.who * a.w_stride + (k < a.r ? k : a.r - 1) * a.w_pitch;
+    ar[j] = a.w + t.who * a.w_stride + (r0 + (k < ranks ? k : ranks - 1)) * a.w_pitch + 8 * quarter * B;
   }
   float4v acc[TT][NT];
 #pragma unroll
@@ -289,30 +298,45 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = float4v(0.0f);
   const int c0 = blockIdx.y * a.per_split, c1 = c0 + a.per_split < a.cols ? c0 + a.per_split : a.cols;
-  auto step = [&](int c, bool whole) {
-    Eight<DT> x[TT], w[NT];
-    const int k = c + 8 * quarter;
+  struct Turn { Eight<DT> x[S][TT], w[S][NT]; };
+  auto load = [&](int c, Turn& u) {
 #pragma unroll
-    for (int i = 0; i < TT; ++i) x[i] = whole ? load8<DT>(xr[i] + k * B) : load8_some<DT>(xr[i] + k * B, a.cols - k);
+    for (int q = 0; q < S; ++q) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) w[j] = whole ? load8<DT>(ar[j] + k * B) : load8_some<DT>(ar[j] + k * B, a.cols - k);
+      for (int i = 0; i < TT; ++i) u.x[q][i] = load8<DT>(xr[i] + (int64_t)(c + 32 * q) * B);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) u.w[q][j] = load8<DT>(ar[j] + (int64_t)(c + 32 * q) * B);
+    }
+  };
+  auto multiply = [&](int c, Turn& u, int q) {
     if constexpr (DROP) {
 #pragma unroll
-      for (int i = 0; i < TT; ++i) x[i] = drop8<DT>(x[i], a.drop, ctr, k, (uint32_t)token[i]);
+      for (int i = 0; i < TT; ++i) u.x[q][i] = drop8<DT>(u.x[q][i], a.drop, ctr, c + 32 * q + 8 * quarter, (uint32_t)token[i]);
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mma8<DT>(x[i], w[j], acc[i][j]);
+      for (int j = 0; j < NT; ++j) acc[i][j] = mma8<DT>(u.x[q][i], u.w[q][j], acc[i][j]);
   };
-  // 64 columns to a wave: whole lines of 16-bit rows
-  for (int c = c0 + 64 * wave; c < c1; c += 256) {
-    if (c + 64 <= a.cols) {
-      step(c, true);
-      step(c + 32, true);
-    } else {
-      step(c, false);
-      if (c + 32 < a.cols) step(c + 32, false);
+  const int whole = c1 - (c1 - c0) % U;      // whole turns end here
+  int c = c0 + U * wave;
+  Turn u, v;
+  if (c < whole) load(c, u);
+  for (; c < whole; c += 4 * U) {
+    if (c + 4 * U < whole) load(c + 4 * U, v);
+#pragma unroll
+    for (int q = 0; q < S; ++q) multiply(c, u, q);
+    u = v;
+  }
+  if (whole < c1 && (whole - c0) / U % 4 == wave) {
+    // a row's last columns, zeros behind them
+    for (int q = 0; q < S && whole + 32 * q < c1; ++q) {
+      const int k = whole + 32 * q, n = c1 - k - 8 * quarter;
+#pragma unroll
+      for (int i = 0; i < TT; ++i) u.x[0][i] = load8_some<DT>(xr[i] + (int64_t)k * B, n);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) u.w[0][j] = load8_some<DT>(ar[j] + (int64_t)k * B, n);
+      multiply(k, u, 0);
     }
   }
   // the four waves' sums, in a fixed order
@@ -340,7 +364,7 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
   __syncthreads();
   if (wave == 0) {
     add(0);
-    float* o = a.part + ((int64_t)blockIdx.y * a.C + t.first) * a.r;
+    float* o = a.part + ((int64_t)blockIdx.y * a.C + t.first) * a.r + r0;
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
@@ -349,7 +373,7 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
         if (k >= t.count) continue;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          if (16 * j + row < a.r) o[(int64_t)k * a.r + 16 * j + row] = acc[i][j][e];
+          if (16 * j + row < ranks) o[(int64_t)k * a.r + 16 * j + row] = acc[i][j][e];
       }
   }
 }
@@ -357,249 +381,402 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
 // ---------------------------------------------------------------------------
 // y = base + s B t, dx = base + drop'(A^T u)
 // ---------------------------------------------------------------------------
-// A wave's lane l holds, of 128 columns, eight consecutive ones 8 (l % 16) ..:
-// as tile i of eight those 8 (l % 16) + i, so that B's and A's rows are read,
-// and y's written, 16 bytes (of 16-bit types) at a time.
-template <int DT, int TT, bool BWD, bool DROP>
+// A wave's lane l holds, of 128 (fp32: 64) columns, eight (four) consecutive ones from
+// 8 (l % 16) on: as tile i those 8 (l % 16) + i, so that B's and A's rows are read,
+// and y's written, 16 bytes at a time.  The columns' rows of B (or columns of A)
+// stay in registers for all of the tile's tokens, 16 at a time.
+// For fp16, t and u are two fp16 terms under a power of two per token that puts the
+// token's largest below 2^15: 22 bits, or 2^-39 of the largest; for bf16 three bf16
+// pieces, exact.
+template <int DT, int KT, bool BWD, bool DROP>
 __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
-  constexpr int B = kBytes<DT>, T = 16 * TT, P = DT == MOE_DT_F32 ? 1 : 3;
-  // the sums as pieces, [piece][rank / 8][token][8]
+  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, P = DT == MOE_DT_F32 ? 1 : DT == MOE_DT_F16 ? 2 : 3;
+  // the sums as operands, [piece][rank / 8][token][8], and the tokens
   extern __shared__ __align__(16) uint8_t s_t[];
+  __shared__ int s_token[64];
+  __shared__ float s_inv[64];
   Tile t;
   if (!plan_entry(a.plan, a.C, a.n, 3, a.at.tiles, blockIdx.x, t)) return;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane & 15, quarter = lane >> 4;
-  const int kt = (a.r + 31) / 32, r32 = 32 * kt;
+  const int subs = (t.count + 15) / 16, T = 16 * subs;
   const bool idle = t.who < 0;
   const float s = idle ? 0.0f : a.scales ? a.scales[t.who] : 1.0f;
-  for (int e = tid; e < T * r32; e += kAWG) {
-    const int k = e / r32, j = e - k * r32;
-    float v = 0.0f;
-    if (!idle && k < t.count && j < a.r) {
-      const float* p = a.part + (int64_t)(t.first + k) * a.r + j;
-      const int64_t step = (int64_t)a.C * a.r;
-      int q = 0;
-      for (; q + 8 <= a.splits; q += 8) {
-        float w[8];
+  const uint8_t* w = a.w + (idle ? 0 : t.who) * a.w_stride;
+  Eight<DT> f[KT][NTL];                 // tile i of rank 32 k + 8 quarter .. + 7: column c + i
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kZeroRow);     // ranks past the last
+  auto operands = [&](int c0) {
+    const int c = c0 + NTL * row;
+    if constexpr (!BWD) {
+      const bool eights = a.r % 8 == 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = p[(q + i) * step];
+      for (int k = 0; k < KT; ++k) {
+        const int j0 = 32 * k + 8 * quarter;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += w[i];
+        for (int i = 0; i < NTL; ++i) {
+          const int n = c + i < a.cols ? c + i : a.cols - 1;
+          const uint8_t* p = w + n * a.w_pitch;
+          if (eights) f[k][i] = load8<DT>(j0 < a.r ? p + j0 * B : zeros);
+          else f[k][i] = load8_some<DT>(p + j0 * B, a.r - j0);
+        }
       }
-      for (; q < a.splits; ++q) v += p[q * step];
-    }
-    // forward: t, then times s_a; backward: u
-    v *= BWD ? s : a.drop.scale;
-    if (a.keep && blockIdx.y == 0 && k < t.count && j < a.r) a.keep[(int64_t)a.plan[a.at.perm + t.first + k] * a.r + j] = v;
-    if (!BWD) v *= s;
-    const int at = ((j >> 3) * T + k) * 8 + (j & 7);
-    if constexpr (DT == MOE_DT_F32) {
-      reinterpret_cast<float*>(s_t)[at] = v;
     } else {
-      uint32_t p0, p1, p2;
-      pieces3(v, p0, p1, p2);
-      uint16_t* o = reinterpret_cast<uint16_t*>(s_t);
-      o[at] = p0 >> 16;
-      o[at + T * r32] = p1 >> 16;
-      o[at + 2 * T * r32] = p2 >> 16;
+      const bool whole = c0 + W <= a.cols;
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const int j0 = 32 * k + 8 * quarter;
+        uint4v g[8];                    // rank j0 + i, columns c ..
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = j0 + i < a.r ? j0 + i : a.r - 1;
+          const uint8_t* p = w + j * a.w_pitch + (int64_t)c * B;
+          if (whole) {
+            g[i] = load16(j0 + i < a.r ? p : zeros);
+          } else if (j0 + i >= a.r) {
+            g[i] = uint4v(0u);
+          } else if constexpr (DT == MOE_DT_F32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[i][e] = c + e < a.cols ? reinterpret_cast<const uint32_t*>(p)[e] : 0u;
+          } else {
+            g[i] = load8_some<DT>(p, a.cols - c).v[0];
+          }
+        }
+        if constexpr (DT == MOE_DT_F32) {
+#pragma unroll
+          for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[k][i].v[e >> 2][e & 3] = g[e][i];
+        } else {
+          uint4v o[8];
+          turn8(g, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[k][i].v[0] = o[i];
+        }
+      }
+    }
+  };
+  int c0 = W * (blockIdx.y * 4 + wave);
+  const int step = 4 * W * gridDim.y;
+  if (!idle && c0 < a.cols) operands(c0);
+  // t (or u) of the tile: 16 lanes to a token, two ranks a lane and 32
+  if (tid < T) s_token[tid] = a.plan[a.at.perm + t.first + (tid < t.count ? tid : t.count - 1)];
+  for (int k = tid >> 4; k < T; k += 16) {
+    float v[KT][2];
+    const bool live = !idle && k < t.count;
+    const int64_t range = (int64_t)a.C * a.r;
+#pragma unroll
+    for (int q = 0; q < KT; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = 32 * q + 2 * row + e;
+        v[q][e] = 0.0f;
+        if (!live || j >= a.r) continue;
+        const float* p = a.part + (int64_t)(t.first + k) * a.r + j;
+        int x = 0;
+        for (; x + 4 <= a.splits; x += 4) {
+          const float p0 = p[x * range], p1 = p[(x + 1) * range], p2 = p[(x + 2) * range], p3 = p[(x + 3) * range];
+          v[q][e] += p0;
+          v[q][e] += p1;
+          v[q][e] += p2;
+          v[q][e] += p3;
+        }
+        for (; x < a.splits; ++x) v[q][e] += p[x * range];
+        // forward: t, then times s_a; backward: u
+        v[q][e] *= BWD ? s : a.drop.scale;
+      }
+    if (a.keep && blockIdx.y == 0 && k < t.count) {
+      float* o = a.keep + (int64_t)a.plan[a.at.perm + t.first + k] * a.r;
+#pragma unroll
+      for (int q = 0; q < KT; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (32 * q + 2 * row + e < a.r) o[32 * q + 2 * row + e] = v[q][e];
+    }
+    float m = 1.0f;
+    if constexpr (DT == MOE_DT_F16) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int q = 0; q < KT; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!BWD) v[q][e] *= s;
+          const uint32_t b = __float_as_uint(v[q][e]) & 0x7FFFFFFFu;
+          most = b > most ? b : most;
+        }
+#pragma unroll
+      for (int d = 8; d >= 1; d >>= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)most, d, 16);
+        most = o > most ? o : most;
+      }
+      // the power of two that takes it below 2^15, within fp32's normal range
+      int e = 14 - ((int)(most >> 23) - 127);
+      if (most >= 0x7F800000u) e = 0;
+      e = e > 126 ? 126 : e;
+      m = __uint_as_float((uint32_t)(127 + e) << 23);
+      if (row == 0) s_inv[k] = __uint_as_float((uint32_t)(127 - e) << 23);
+    } else if constexpr (!BWD) {
+#pragma unroll
+      for (int q = 0; q < KT; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) v[q][e] *= s;
+    }
+#pragma unroll
+    for (int q = 0; q < KT; ++q) {
+      const int at = (((32 * q + 2 * row) >> 3) * T + k) * 8 + ((2 * row) & 7), piece = 32 * KT * T;
+      if constexpr (DT == MOE_DT_F32) {
+        *reinterpret_cast<float2*>(s_t + at * 4) = make_float2(v[q][0], v[q][1]);
+      } else {
+        uint32_t p[2][3] = {};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (DT == MOE_DT_F16) {
+            // not finite: its own first term, and the finite ones beside it in range
+            float z = v[q][e] * m;
+            const bool fine = fabsf(z) < INFINITY;
+            if (fine) z = fminf(fmaxf(z, -65504.0f), 65504.0f);
+            const _Float16 h = (_Float16)z;
+            p[e][0] = (uint32_t)__builtin_bit_cast(uint16_t, h) << 16;
+            p[e][1] = fine ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)(z - (float)h)) << 16 : 0u;
+          } else {
+            pieces3(v[q][e], p[e][0], p[e][1], p[e][2]);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < P; ++x) *reinterpret_cast<uint32_t*>(s_t + (x * piece + at) * 2) = high_pair(p[0][x], p[1][x]);
+      }
     }
   }
   __syncthreads();
   Counter ctr = {};
   if constexpr (DROP) ctr = counter_of(a.drop.rng);
-  const uint8_t* w = a.w + (idle ? 0 : t.who) * a.w_stride;
-  for (int c0 = 128 * (blockIdx.y * 4 + wave); c0 < a.cols; c0 += 512 * gridDim.y) {
-    float4v acc[TT][8];
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = float4v(0.0f);
-    const int c = c0 + 8 * row;
-    if (!idle) {
-      for (int k = 0; k < kt; ++k) {
-        const int j0 = 32 * k + 8 * quarter;
-        Eight<DT> f[8];                 // tile i: column c + i, rank j0 .. j0 + 7
-        if constexpr (!BWD) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int n = c + i < a.cols ? c + i : a.cols - 1;
-            f[i] = load8_some<DT>(w + n * a.w_pitch + j0 * B, a.r - j0);
-          }
-        } else {
-          Eight<DT> g[8];               // rank j0 + i, columns c .. c + 7
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            g[i] = j0 + i < a.r ? load8_some<DT>(w + (j0 + i) * a.w_pitch + c * B, a.cols - c) : zero8<DT>();
-          if constexpr (DT == MOE_DT_F32) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[i].v[e >> 2][e & 3] = g[e].v[i >> 2][i & 3];
-          } else {
-            uint4v gi[8], fo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) gi[i] = g[i].v[0];
-            turn8(gi, fo);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i].v[0] = fo[i];
-          }
-        }
-        if constexpr (DT == MOE_DT_F32) {
-#pragma unroll
-          for (int i = 0; i < TT; ++i) {
-            Eight<DT> u = *reinterpret_cast<const Eight<DT>*>(s_t + (((4 * k + quarter) * T + 16 * i + row) * 8) * 4);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = mma8<DT>(u, f[j], acc[i][j]);
-          }
-        } else {
-          uint4v u[TT][3];
-#pragma unroll
-          for (int i = 0; i < TT; ++i)
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-              u[i][p] = *reinterpret_cast<const uint4v*>(s_t + (p * T * r32 + ((4 * k + quarter) * T + 16 * i + row) * 8) * 2);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4v b[kPieces<DT>];
-            pieces<DT>(f[j].v[0], b);
-#pragma unroll
-            for (int i = 0; i < TT; ++i) acc[i][j] = mma_pieces<DT>(u[i], b, acc[i][j]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
+  for (; c0 < a.cols; c0 += step) {
+    const int c = c0 + NTL * row, left = a.cols - c;
+    const bool whole = c0 + W <= a.cols;
+    // base's rows of 16 tokens, loaded while those before are multiplied
+    uint4v old[4], next[4];
+    auto base_rows = [&](int sub, uint4v (&b)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int k = 16 * i + 4 * quarter + e;
-        if (k >= t.count || c >= a.cols) continue;
-        const int token = a.plan[a.at.perm + t.first + k];
-        float v[8];
+        const uint8_t* p = a.base + s_token[16 * sub + 4 * quarter + e] * a.base_pitch + (int64_t)c * B;
+        if (whole) {
+          b[e] = load16(p);
+        } else if constexpr (DT == MOE_DT_F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = acc[i][j][e];
-        if constexpr (BWD && DROP) drop8f(v, a.drop, ctr, c, (uint32_t)token);
-        if (a.base) {
-          const Eight<DT> b = load8_some<DT>(a.base + token * a.base_pitch + (int64_t)c * B, a.cols - c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = idle ? get8<DT>(b, j) : v[j] + get8<DT>(b, j);
+          for (int i = 0; i < 4; ++i) b[e][i] = i < left ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+        } else {
+          b[e] = load8_some<DT>(p, left).v[0];
         }
-        store8_some<DT>(a.out + token * a.out_pitch + (int64_t)c * B, put8<DT>(v), a.cols - c);
       }
+    };
+    if (a.base) base_rows(0, old);
+    for (int sub = 0; sub < subs; ++sub) {
+      if (a.base && sub + 1 < subs) base_rows(sub + 1, next);
+      float4v acc[NTL];
+#pragma unroll
+      for (int i = 0; i < NTL; ++i) acc[i] = float4v(0.0f);
+      if (!idle) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          const int at = ((4 * k + quarter) * T + 16 * sub + row) * 8;
+          if constexpr (DT == MOE_DT_F32) {
+            const Eight<DT> u = *reinterpret_cast<const Eight<DT>*>(s_t + at * 4);
+#pragma unroll
+            for (int i = 0; i < NTL; ++i) acc[i] = mma8<DT>(u, f[k][i], acc[i]);
+          } else {
+            uint4v u[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) u[p] = *reinterpret_cast<const uint4v*>(s_t + (p * 32 * KT * T + at) * 2);
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+              for (int i = 0; i < NTL; ++i) acc[i] = DT == MOE_DT_F16 ? mma_f16(u[p], f[k][i].v[0], acc[i]) : mma_bf16(u[p], f[k][i].v[0], acc[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 16 * sub + 4 * quarter + e, token = s_token[k];
+        const float inv = DT == MOE_DT_F16 ? s_inv[k] : 1.0f;
+        float v[NTL];
+#pragma unroll
+        for (int i = 0; i < NTL; ++i) v[i] = DT == MOE_DT_F16 ? acc[i][e] * inv : acc[i][e];
+        if constexpr (BWD && DROP) drop_some<NTL>(v, a.drop, ctr, c, (uint32_t)token);
+        if (a.base) {
+          const Eight<DT> b = first_of<DT>(old[e]);
+#pragma unroll
+          for (int i = 0; i < NTL; ++i) v[i] = idle ? get8<DT>(b, i) : v[i] + get8<DT>(b, i);
+        }
+        if (k < t.count) {
+          uint8_t* o = a.out + token * a.out_pitch + (int64_t)c * B;
+          const uint4v q = pack16<DT>(v);
+          if (whole) store16(o, q);
+          else store16_some<DT>(o, q, left);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[e] = next[e];
+    }
+    if (!idle && c0 + step < a.cols) operands(c0 + step);
   }
 }
 
 // ---------------------------------------------------------------------------
 // sums[j][col] = sum over a chunk's tokens of small[token][j] in[token][col]
 // ---------------------------------------------------------------------------
-template <int DT, int NT, bool DROP>
-__global__ __launch_bounds__(kAWG) void k_aouter(AArgs a) {
-  constexpr int B = kBytes<DT>;
-  __shared__ float s_red[2][NT * 16][132];
+// dA (x by u) and dB (dy by t) in one launch.  A workgroup has 128 (fp32: 64) columns
+// of a chunk; of its eight waves RH share the ranks, 16 NT each, and the others the
+// tokens, 32 at a time, whose rows are transposed in registers.
+struct Outer {
+  const uint8_t* in;                    // [C][cols]
+  int64_t in_pitch;
+  const float* small;                   // [C][r] by token
+  float* sums;                          // [chunks][r][cols]
+  int cols, blocks;                     // of columns
+};
+struct OArgs {
+  const int32_t* plan;
+  PlanLayout at;
+  int C, n, r;
+  Outer da, db;                         // blocks 0: not asked for
+  Dropout drop;                         // of da's input
+};
+
+constexpr int kOWG = 512, kOWaves = kOWG / 64;
+template <int DT, int NT, int RH, bool DROP>
+__global__ __launch_bounds__(kOWG) void k_aouter(OArgs a) {
+  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, TG = kOWaves / RH, R = 16 * NT;
+  extern __shared__ __align__(16) uint8_t s_o[];
+  int* s_token = reinterpret_cast<int*>(s_o);                       // [2048], then the sums
+  float* s_red = reinterpret_cast<float*>(s_o);                     // [TG / 2][RH][R][W + 4]
   Tile t;
   if (!plan_entry(a.plan, a.C, a.n, 4, a.at.chunks, blockIdx.y, t)) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane & 15, quarter = lane >> 4;
-  const int c = 128 * blockIdx.x + 8 * row, r0 = 64 * blockIdx.z;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int row = lane & 15, quarter = lane >> 4;
+  const bool second = (int)blockIdx.x >= a.da.blocks;
+  const Outer& o = second ? a.db : a.da;
+  const int c0 = W * (blockIdx.x - (second ? a.da.blocks : 0)), c = c0 + NTL * row, left = o.cols - c;
+  const bool whole = c0 + W <= o.cols, drops = DROP && !second;
+  const int rh = wave % RH, tg = wave / RH, r0 = R * rh;
   Counter ctr = {};
   if constexpr (DROP) ctr = counter_of(a.drop.rng);
-  float4v acc[NT][8];
+  // the tokens, the last again behind it up to whole steps
+  const int steps = (t.count + 31) / 32;
+  for (int i = tid; i < 32 * steps; i += kOWG) s_token[i] = a.plan[a.at.perm + t.first + (i < t.count ? i : t.count - 1)];
+  __syncthreads();
+  float4v acc[NT][NTL];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = float4v(0.0f);
-  const int32_t* perm = a.plan + a.at.perm + t.first;
-  for (int k0 = 32 * wave; k0 < t.count; k0 += 128) {
-    int token[8];
-    bool in[8];
+    for (int j = 0; j < NTL; ++j) acc[i][j] = float4v(0.0f);
+  int rank[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) rank[j] = r0 + 16 * j + row < a.r ? r0 + 16 * j + row : a.r - 1;
+  struct Turn { uint4v g[8]; float sm[NT][8]; int token[8]; };
+  auto load = [&](int s, Turn& u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u.token[i] = s_token[32 * s + 8 * quarter + i];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int k = k0 + 8 * quarter + i;
-      in[i] = k < t.count;
-      token[i] = perm[in[i] ? k : 0];
-    }
-    Eight<DT> g[8];                     // tokens k0 + 8 quarter + i, columns c .. c + 7
+      const uint8_t* p = o.in + u.token[i] * o.in_pitch + (int64_t)c * B;
+      if (whole) {
+        u.g[i] = load16(p);
+      } else if constexpr (DT == MOE_DT_F32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      g[i] = in[i] ? load8_some<DT>(a.in + token[i] * a.in_pitch + (int64_t)c * B, a.cols - c) : zero8<DT>();
-    float sm[NT][8];
+        for (int e = 0; e < 4; ++e) u.g[i][e] = e < left ? reinterpret_cast<const uint32_t*>(p)[e] : 0u;
+      } else {
+        u.g[i] = load8_some<DT>(p, left).v[0];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = r0 + 16 * j + row;
-        sm[j][i] = in[i] && k < a.r ? a.small[(int64_t)token[i] * a.r + k] : 0.0f;
-      }
-    if constexpr (DROP) {
+      for (int i = 0; i < 8; ++i) u.sm[j][i] = o.small[(int64_t)u.token[i] * a.r + rank[j]];
+  };
+  Turn u, v;
+  if (tg < steps) load(tg, u);
+  for (int s = tg; s < steps; s += TG) {
+    if (s + TG < steps) load(s + TG, v);
+    if (32 * s + 32 > t.count) {        // tokens behind the last add nothing
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = drop8<DT>(g[i], a.drop, ctr, c, (uint32_t)token[i]);
+      for (int i = 0; i < 8; ++i)
+        if (32 * s + 8 * quarter + i >= t.count) {
+          u.g[i] = uint4v(0u);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) u.sm[j][i] = 0.0f;
+        }
+    }
+    if (drops) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u.g[i] = drop16<DT>(u.g[i], a.drop, ctr, c, (uint32_t)u.token[i]);
     }
     if constexpr (DT == MOE_DT_F32) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < NTL; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(sm[j][e], get8<DT>(g[e], i), acc[j][i], 0, 0, 0);
+            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(u.sm[j][e], __uint_as_float(u.g[e][i]), acc[j][i], 0, 0, 0);
     } else {
-      uint4v gi[8], f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) gi[i] = g[i].v[0];
-      turn8(gi, f);
-      uint4v u[NT][3];
+      uint4v f[8], m[NT][3];
+      turn8(u.g, f);
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t p[2][3];
-          pieces3(sm[j][2 * i], p[0][0], p[0][1], p[0][2]);
-          pieces3(sm[j][2 * i + 1], p[1][0], p[1][1], p[1][2]);
+          pieces3(u.sm[j][2 * i], p[0][0], p[0][1], p[0][2]);
+          pieces3(u.sm[j][2 * i + 1], p[1][0], p[1][1], p[1][2]);
 #pragma unroll
-          for (int q = 0; q < 3; ++q) u[j][q][i] = high_pair(p[0][q], p[1][q]);
+          for (int q = 0; q < 3; ++q) m[j][q][i] = high_pair(p[0][q], p[1][q]);
         }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         uint4v b[kPieces<DT>];
         pieces<DT>(f[i], b);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][i] = mma_pieces<DT>(u[j], b, acc[j][i]);
+        for (int j = 0; j < NT; ++j) acc[j][i] = mma_pieces<DT>(m[j], b, acc[j][i]);
       }
     }
+    u = v;
   }
-  auto put = [&](int s) {
+  // the sums of the waves that share the tokens, in a fixed order
+  float* mine = s_red + rh * R * (W + 4);
+  constexpr int slot = RH * R * (W + 4);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int h = TG / 2; h >= 1; h /= 2) {
+    __syncthreads();
+    if (tg >= h && tg < 2 * h) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s_red[s][16 * j + 4 * quarter + e][8 * row + i] = acc[j][i][e];
-  };
-  auto add = [&](int s) {
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+          for (int i = 0; i < NTL; ++i) mine[(tg - h) * slot + (16 * j + 4 * quarter + e) * (W + 4) + NTL * row + i] = acc[j][i][e];
+    }
+    __syncthreads();
+    if (tg < h) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[j][i][e] += s_red[s][16 * j + 4 * quarter + e][8 * row + i];
-  };
-  if (wave >= 2) put(wave - 2);
-  __syncthreads();
-  if (wave < 2) add(wave);
-  __syncthreads();
-  if (wave == 1) put(0);
-  __syncthreads();
-  if (wave == 0) {
-    add(0);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int i = 0; i < NTL; ++i) acc[j][i][e] += mine[tg * slot + (16 * j + 4 * quarter + e) * (W + 4) + NTL * row + i];
+    }
+  }
+  if (tg == 0) {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int k = r0 + 16 * j + 4 * quarter + e;
-        if (k >= a.r || c >= a.cols) continue;
-        float* o = a.sums + ((int64_t)blockIdx.y * a.r + k) * a.cols + c;
-        float v[8];
+        if (k >= a.r) continue;
+        float* p = o.sums + ((int64_t)blockIdx.y * a.r + k) * o.cols + c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = acc[j][i][e];
-        store8_some<MOE_DT_F32>(o, put8<MOE_DT_F32>(v), a.cols - c);
+        for (int h = 0; h < NTL; h += 4) {
+          const float q[4] = {acc[j][h][e], acc[j][h + 1][e], acc[j][h + 2][e], acc[j][h + 3][e]};
+          if (whole) store16(p + h, pack16<MOE_DT_F32>(q));
+          else store16_some<MOE_DT_F32>(p + h, pack16<MOE_DT_F32>(q), left - h);
+        }
       }
   }
 }
@@ -607,34 +784,52 @@ __global__ __launch_bounds__(kAWG) void k_aouter(AArgs a) {
 struct RArgs {
   const int32_t* plan;
   PlanLayout at;
-  int C, n, r, cols;
-  const float* sums;                    // [chunks][r][cols]
-  float* out;                           // [n][r][cols], or [n][cols][r] (turned)
-  const float* scales;                  // a factor by adapter, or NULL
-  float factor;
-  int accumulate;
+  int C, n, r, accumulate;
+  int ca, cb;                           // columns of dA, of dB; 0: not asked for
+  int64_t xa;                           // workgroups of dA's
+  const float *sa, *sb;                 // [chunks][r][columns]
+  float *da, *db;                       // [n][r][ca], [n][cb][r]
+  const float* scales;                  // dB's factor by adapter, or NULL
+  float factor;                         // dA's
 };
 
-// Adds an adapter's chunks in order; an adapter without tokens has zeros.
-template <bool TURN>
+// Adds an adapter's chunks in order; an adapter without tokens has zeros.  dB is
+// transposed on the way: a thread has a column's four ranks.
 __global__ __launch_bounds__(256) void k_areduce(RArgs a) {
   const int32_t* plan = a.plan;
   if (plan[0] != kPlanMagic || plan[1] != a.C || plan[2] != a.n) return;
-  for (int who = blockIdx.y; who < a.n; who += gridDim.y) {
-    const int q0 = plan[a.at.first + who], q1 = plan[a.at.first + who + 1];
-    if (a.accumulate && q0 == q1) continue;
-    const float f = a.scales ? a.scales[who] * a.factor : a.factor;
-    const int64_t n = (int64_t)a.r * a.cols;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
-      // e runs over the sums' order, or (TURN) over the output's
-      const int64_t at = TURN ? (e % a.r) * a.cols + e / a.r : e;
-      float v = 0.0f;
-      for (int q = q0; q < q1; ++q) v += a.sums[(int64_t)q * n + at];
-      float* o = a.out + (int64_t)who * n + e;
-      v *= f;
-      *o = a.accumulate ? *o + v : v;
+  const bool second = blockIdx.x >= a.xa;
+  const int64_t x = (int64_t)(second ? blockIdx.x - a.xa : blockIdx.x) * 256 + threadIdx.x;
+  const int who = blockIdx.y;
+  const int q0 = plan[a.at.first + who], q1 = plan[a.at.first + who + 1];
+  if (a.accumulate && q0 == q1) return;
+  const int cols = second ? a.cb : a.ca;
+  const int64_t n = (int64_t)a.r * cols;
+  const float f = second ? (a.scales ? a.scales[who] : 1.0f) : a.factor;
+  // four elements: of a row of dA's sums, or (dB) of four rows, at one column
+  const int64_t at = second ? (x / cols) * 4 * cols + x % cols : 4 * x, step = second ? cols : 1;
+  if (second ? x / cols * 4 >= a.r : at >= n) return;
+  const int most = second ? a.r - (int)(x / cols) * 4 : n - at < 4 ? (int)(n - at) : 4;
+  float v[4] = {};
+  const float* s = (second ? a.sb : a.sa) + at;
+  for (int q = q0; q < q1; ++q) {
+    if (!second && most >= 4) {
+      const uint4v w = load16(s + q * n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < most) v[i] += s[q * n + i * step];
     }
   }
+  float* o = second ? a.db + who * n + x % cols * a.r + x / cols * 4 : a.da + who * n + at;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] *= f;
+    if (a.accumulate && i < most) v[i] += o[i];
+  }
+  store16_some<MOE_DT_F32>(o, pack16<MOE_DT_F32>(v), most);
 }
 
 struct TArgs {
@@ -730,11 +925,10 @@ AdapterWs adapter_ws(const moe_adapter_bank* b, int C) {
 
 template <int DT, int TT, bool DROP>
 void launch_shrink_t(const AArgs& a, int tiles, hipStream_t st) {
-  const dim3 grid((unsigned)tiles, (unsigned)a.splits);
+  const dim3 grid((unsigned)tiles, (unsigned)a.splits, (unsigned)((a.r + 63) / 64));
   if (a.r <= 16) hipLaunchKernelGGL((k_ashrink<DT, 1, TT, DROP>), grid, dim3(kAWG), 0, st, a);
   else if (a.r <= 32) hipLaunchKernelGGL((k_ashrink<DT, 2, TT, DROP>), grid, dim3(kAWG), 0, st, a);
-  else if (a.r <= 64) hipLaunchKernelGGL((k_ashrink<DT, 4, TT, DROP>), grid, dim3(kAWG), 0, st, a);
-  else hipLaunchKernelGGL((k_ashrink<DT, 8, TT, DROP>), grid, dim3(kAWG), 0, st, a);
+  else hipLaunchKernelGGL((k_ashrink<DT, 4, TT, DROP>), grid, dim3(kAWG), 0, st, a);
 }
 template <int DT>
 void launch_shrink(const AArgs& a, int tiles, bool drop, hipStream_t st) {
@@ -747,42 +941,36 @@ void launch_shrink(const AArgs& a, int tiles, bool drop, hipStream_t st) {
   }
 }
 
-template <int DT, bool BWD>
-void launch_expand(const AArgs& a, int tiles, bool drop, hipStream_t st) {
-  // blocks of 128 columns, one or more to a wave, about two workgroups a CU
-  const int blocks = a.cols > 0 ? (a.cols + 511) / 512 : 1;
-  int y = 512 / tiles;
+template <int DT, bool BWD, bool DROP>
+void launch_expand(const AArgs& a, int tiles, hipStream_t st) {
+  // a wave's columns once, or again where that makes more than four workgroups a CU
+  const int per = 64 * kTiles<DT>, blocks = a.cols > 0 ? (a.cols + per - 1) / per : 1;
+  int y = 1024 / tiles;
   y = y < 1 ? 1 : y > blocks ? blocks : y;
   const dim3 grid((unsigned)tiles, (unsigned)y);
-  const int T = plan_tile(a.C), r32 = (a.r + 31) / 32 * 32;
-  const size_t lds = (size_t)T * r32 * (DT == MOE_DT_F32 ? 4 : 6);
-  if (T == 16) {
-    if (drop) hipLaunchKernelGGL((k_aexpand<DT, 1, BWD, true>), grid, dim3(kAWG), lds, st, a);
-    else hipLaunchKernelGGL((k_aexpand<DT, 1, BWD, false>), grid, dim3(kAWG), lds, st, a);
-  } else {
-    if (drop) hipLaunchKernelGGL((k_aexpand<DT, 4, BWD, true>), grid, dim3(kAWG), lds, st, a);
-    else hipLaunchKernelGGL((k_aexpand<DT, 4, BWD, false>), grid, dim3(kAWG), lds, st, a);
-  }
+  const int kt = a.r <= 32 ? 1 : a.r <= 64 ? 2 : 4;
+  const size_t lds = (size_t)plan_tile(a.C) * 32 * kt * (DT == MOE_DT_F32 ? 4 : DT == MOE_DT_F16 ? 4 : 6);
+  if (kt == 1) hipLaunchKernelGGL((k_aexpand<DT, 1, BWD, DROP>), grid, dim3(kAWG), lds, st, a);
+  else if (kt == 2) hipLaunchKernelGGL((k_aexpand<DT, 2, BWD, DROP>), grid, dim3(kAWG), lds, st, a);
+  else hipLaunchKernelGGL((k_aexpand<DT, 4, BWD, DROP>), grid, dim3(kAWG), lds, st, a);
 }
 
+template <int DT, int NT, int RH, bool DROP>
+moe_status launch_outer_t(const OArgs& a, int chunks, hipStream_t st) {
+  constexpr int W = 16 * kTiles<DT>, sums = kOWaves / 2 * 16 * NT * (W + 4) * 4, lds = sums > 8192 ? sums : 8192;
+  auto k = k_aouter<DT, NT, RH, DROP>;
+  if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         lds) != hipSuccess)
+    return MOE_ERR_DEVICE;
+  hipLaunchKernelGGL(k, dim3((unsigned)(a.da.blocks + a.db.blocks), (unsigned)chunks), dim3(kOWG), lds, st, a);
+  return MOE_OK;
+}
 template <int DT, bool DROP>
-void launch_outer_t(const AArgs& a, int chunks, hipStream_t st) {
-  const dim3 grid((unsigned)((a.cols + 127) / 128), (unsigned)chunks, (unsigned)((a.r + 63) / 64));
-  if (a.r <= 16) hipLaunchKernelGGL((k_aouter<DT, 1, DROP>), grid, dim3(kAWG), 0, st, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((k_aouter<DT, 2, DROP>), grid, dim3(kAWG), 0, st, a);
-  else hipLaunchKernelGGL((k_aouter<DT, 4, DROP>), grid, dim3(kAWG), 0, st, a);
-}
-template <int DT>
-void launch_outer(const AArgs& a, int chunks, bool drop, hipStream_t st) {
-  if (drop) launch_outer_t<DT, true>(a, chunks, st);
-  else launch_outer_t<DT, false>(a, chunks, st);
-}
-
-template <bool TURN>
-void launch_reduce(const RArgs& a, hipStream_t st) {
-  const int64_t n = (int64_t)a.r * a.cols;
-  const unsigned x = (unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
-  hipLaunchKernelGGL((k_areduce<TURN>), dim3(x, (unsigned)a.n), dim3(256), 0, st, a);
+moe_status launch_outer(const OArgs& a, int chunks, hipStream_t st) {
+  if (a.r <= 16) return launch_outer_t<DT, 1, 1, DROP>(a, chunks, st);
+  if (a.r <= 32) return launch_outer_t<DT, 2, 1, DROP>(a, chunks, st);
+  if (a.r <= 64) return launch_outer_t<DT, 2, 2, DROP>(a, chunks, st);
+  return launch_outer_t<DT, 2, 4, DROP>(a, chunks, st);
 }
 
 // fn(dtype constant)
@@ -895,7 +1083,7 @@ moe_status moe_adapter_fwd(const moe_adapter_bank* b, const void* plan, size_t p
     a.base = static_cast<const uint8_t*>(base); a.base_pitch = base_pitch * s;
     a.out = static_cast<uint8_t*>(y); a.out_pitch = y_pitch * s;
     a.keep = hidden;
-    launch_expand<DT, false>(a, c.at.max_tiles, false, q);
+    launch_expand<DT, false, false>(a, c.at.max_tiles, q);
   });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
@@ -955,41 +1143,34 @@ moe_status moe_adapter_bwd(const moe_adapter_bank* b, const void* plan, size_t p
       a.out = static_cast<uint8_t*>(dx); a.out_pitch = dx_pitch * s;
       a.keep = u;
       if (!dx) a.cols = 0;              // u alone
-      launch_expand<DT, true>(a, c.at.max_tiles, drop, q);
+      if (drop) launch_expand<DT, true, true>(a, c.at.max_tiles, q);
+      else launch_expand<DT, true, false>(a, c.at.max_tiles, q);
     }
-    if (da) {
-      a.cols = b->cols;
-      a.in = static_cast<const uint8_t*>(x); a.in_pitch = x_pitch * s;
-      a.small = u;
-      a.sums = reinterpret_cast<float*>(c.w8 + c.ws.suma);
-      launch_outer<DT>(a, c.at.max_chunks, drop, q);
-    }
-    if (db) {
-      a.cols = b->rows;
-      a.in = static_cast<const uint8_t*>(dy); a.in_pitch = dy_pitch * s;
-      a.small = hidden;
-      a.sums = reinterpret_cast<float*>(c.w8 + c.ws.sumb);
-      launch_outer<DT>(a, c.at.max_chunks, false, q);
+    if (da || db) {
+      OArgs o = {};
+      o.plan = a.plan; o.at = c.at;
+      o.C = C; o.n = b->adapters; o.r = b->rank;
+      o.drop = a.drop;
+      constexpr int W = 16 * kTiles<DT>;
+      if (da) o.da = Outer{static_cast<const uint8_t*>(x), x_pitch * s, u, reinterpret_cast<float*>(c.w8 + c.ws.suma), b->cols, (b->cols + W - 1) / W};
+      if (db) o.db = Outer{static_cast<const uint8_t*>(dy), dy_pitch * s, hidden, reinterpret_cast<float*>(c.w8 + c.ws.sumb), b->rows, (b->rows + W - 1) / W};
+      st = drop && da ? launch_outer<DT, true>(o, c.at.max_chunks, q) : launch_outer<DT, false>(o, c.at.max_chunks, q);
     }
   });
-  RArgs r2 = {};
-  r2.plan = c.a.plan; r2.at = c.at;
-  r2.C = C; r2.n = b->adapters; r2.r = b->rank;
-  r2.accumulate = accumulate;
-  if (da) {
-    r2.cols = b->cols;
-    r2.sums = reinterpret_cast<const float*>(c.w8 + c.ws.suma);
-    r2.out = da;
-    r2.factor = c.a.drop.scale;
-    launch_reduce<false>(r2, q);
-  }
-  if (db) {
-    r2.cols = b->rows;
-    r2.sums = reinterpret_cast<const float*>(c.w8 + c.ws.sumb);
-    r2.out = db;
-    r2.factor = 1.0f;
+  if (st != MOE_OK) return st;
+  if (da || db) {
+    RArgs r2 = {};
+    r2.plan = c.a.plan; r2.at = c.at;
+    r2.C = C; r2.n = b->adapters; r2.r = b->rank;
+    r2.accumulate = accumulate;
+    r2.ca = da ? b->cols : 0; r2.cb = db ? b->rows : 0;
+    r2.sa = reinterpret_cast<const float*>(c.w8 + c.ws.suma); r2.sb = reinterpret_cast<const float*>(c.w8 + c.ws.sumb);
+    r2.da = da; r2.db = db;
     r2.scales = b->scales;
-    launch_reduce<true>(r2, q);
+    r2.factor = c.a.drop.scale;
+    r2.xa = ((r * r2.ca + 3) / 4 + 255) / 256;
+    const int64_t xb = ((r + 3) / 4 * r2.cb + 255) / 256;
+    hipLaunchKernelGGL(k_areduce, dim3((unsigned)(r2.xa + xb), (unsigned)b->adapters), dim3(256), 0, q, r2);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }

@@ -91,6 +91,38 @@ __device__ __forceinline__ void store8_some(void* p, const Eight<DT>& e, int n) 
   }
 }
 
+// 16 bytes' worth of them: eight of 16 bits, four of fp32
+template <int DT>
+__device__ __forceinline__ Eight<DT> first_of(uint4v v) {
+  Eight<DT> e = {};
+  e.v[0] = v;
+  return e;
+}
+template <int DT, int N>
+__device__ __forceinline__ uint4v pack16(const float (&f)[N]) {
+  static_assert(N * kBytes<DT> == 16, "16 bytes");
+  uint4v v;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (DT == MOE_DT_F32) v[i] = __float_as_uint(f[i]);
+    else if (i & 1) v[i >> 1] |= (uint32_t)round16<DT>(f[i]) << 16;
+    else v[i >> 1] = round16<DT>(f[i]);
+  }
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ void store16_some(void* p, uint4v v, int n) {
+  constexpr int N = 16 / kBytes<DT>;
+  if (n >= N) { store16(p, v); return; }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i < n) {
+      if constexpr (DT == MOE_DT_F32) static_cast<uint32_t*>(p)[i] = v[i];
+      else static_cast<uint16_t*>(p)[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
 __device__ __forceinline__ float4v mma_f16(uint4v a, uint4v b, float4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
@@ -166,12 +198,39 @@ __device__ __forceinline__ Eight<DT> drop8(Eight<DT> e, const Dropout& d, const 
   }
   return e;
 }
+// The same of 16 bytes from column `col` on: of fp32, half of a block of eight.
+template <int DT>
+__device__ __forceinline__ uint4v drop16(uint4v v, const Dropout& d, const Counter& c, int col, uint32_t row) {
+  if constexpr (DT != MOE_DT_F32) {
+    return drop8<DT>(first_of<DT>(v), d, c, col, row).v[0];
+  } else {
+    const uint4v w = philox(c, (uint32_t)col >> 3, row);
+    const bool up = col & 4;
+    const uint32_t w0 = up ? w[2] : w[0], w1 = up ? w[3] : w[1];
+    return uint4v{(w0 & 0xFFFFu) >= d.drop ? v[0] : 0u, (w0 >> 16) >= d.drop ? v[1] : 0u,
+                  (w1 & 0xFFFFu) >= d.drop ? v[2] : 0u, (w1 >> 16) >= d.drop ? v[3] : 0u};
+  }
+}
 __device__ __forceinline__ void drop8f(float (&f)[8], const Dropout& d, const Counter& c, int col, uint32_t row) {
   const uint4v w = philox(c, (uint32_t)col >> 3, row);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t h = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu;
     f[i] = h >= d.drop ? f[i] * d.scale : 0.0f;
+  }
+}
+// N = 8, or 4: half of a block
+template <int N>
+__device__ __forceinline__ void drop_some(float (&f)[N], const Dropout& d, const Counter& c, int col, uint32_t row) {
+  if constexpr (N == 8) {
+    drop8f(f, d, c, col, row);
+  } else {
+    uint4v v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(f[i] * d.scale);
+    v = drop16<MOE_DT_F32>(v, d, c, col, row);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
   }
 }
 
