@@ -194,10 +194,9 @@ __device__ __forceinline__ void pieces(uint4v v, uint4v (&p)[kPieces<DT>]) {
       const float f0 = (float)__builtin_bit_cast(_Float16, (uint16_t)v[i]);
       const float f1 = (float)__builtin_bit_cast(_Float16, (uint16_t)(v[i] >> 16));
       const uint32_t a0 = __float_as_uint(f0) & 0xFFFF0000u, a1 = __float_as_uint(f1) & 0xFFFF0000u;
-      // the rest of an infinity or NaN is left out (a NaN of 11 bits keeps one in its first 8: it is quiet)
       const uint32_t b0 = __float_as_uint(f0 - __uint_as_float(a0)), b1 = __float_as_uint(f1 - __uint_as_float(a1));
       p[0][i] = high_pair(a0, a1);
-      p[1][i] = high_pair((a0 & 0x7F800000u) == 0x7F800000u ? 0u : b0, (a1 & 0x7F800000u) == 0x7F800000u ? 0u : b1);
+      p[1][i] = high_pair(b0, b1);       // of an infinity: NaN
     }
   } else {
     p[0] = v;
@@ -459,29 +458,62 @@ __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
   if (!idle && c0 < a.cols) operands(c0);
   // t (or u) of the tile: 16 lanes to a token, two ranks a lane and 32
   if (tid < T) s_token[tid] = a.plan[a.at.perm + t.first + (tid < t.count ? tid : t.count - 1)];
-  for (int k = tid >> 4; k < T; k += 16) {
-    float v[KT][2];
-    const bool live = !idle && k < t.count;
+  float sum[4][KT][2];                  // of tokens tid / 16 + 16 i
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < KT; ++q) sum[i][q][0] = sum[i][q][1] = 0.0f;
+  if (!idle) {
+    // two ranges' loads, of all tokens, on their way together
     const int64_t range = (int64_t)a.C * a.r;
+    auto add = [&](const float* p, float (&w)[4][KT][2]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= subs) break;
+        const int k = (tid >> 4) + 16 * i;
+#pragma unroll
+        for (int q = 0; q < KT; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = 32 * q + 2 * row + e;
+            w[i][q][e] = p[(int64_t)(k < t.count ? k : t.count - 1) * a.r + (j < a.r ? j : a.r - 1)];
+          }
+      }
+    };
+    auto into = [&](const float (&w)[4][KT][2]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < KT; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sum[i][q][e] += w[i][q][e];
+    };
+    const float* p = a.part + (int64_t)t.first * a.r;
+    int x = 0;
+    float w0[4][KT][2] = {}, w1[4][KT][2] = {};
+    for (; x + 2 <= a.splits; x += 2) {
+      add(p + x * range, w0);
+      add(p + (x + 1) * range, w1);
+      into(w0);
+      into(w1);
+    }
+    if (x < a.splits) {
+      add(p + x * range, w0);
+      into(w0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= subs) break;
+    const int k = (tid >> 4) + 16 * i;
+    float v[KT][2];
 #pragma unroll
     for (int q = 0; q < KT; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = 32 * q + 2 * row + e;
-        v[q][e] = 0.0f;
-        if (!live || j >= a.r) continue;
-        const float* p = a.part + (int64_t)(t.first + k) * a.r + j;
-        int x = 0;
-        for (; x + 4 <= a.splits; x += 4) {
-          const float p0 = p[x * range], p1 = p[(x + 1) * range], p2 = p[(x + 2) * range], p3 = p[(x + 3) * range];
-          v[q][e] += p0;
-          v[q][e] += p1;
-          v[q][e] += p2;
-          v[q][e] += p3;
-        }
-        for (; x < a.splits; ++x) v[q][e] += p[x * range];
         // forward: t, then times s_a; backward: u
-        v[q][e] *= BWD ? s : a.drop.scale;
+        const bool live = k < t.count && 32 * q + 2 * row + e < a.r;
+        v[q][e] = live ? sum[i][q][e] * (BWD ? s : a.drop.scale) : 0.0f;
       }
     if (a.keep && blockIdx.y == 0 && k < t.count) {
       float* o = a.keep + (int64_t)a.plan[a.at.perm + t.first + k] * a.r;
@@ -623,8 +655,9 @@ __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
 // sums[j][col] = sum over a chunk's tokens of small[token][j] in[token][col]
 // ---------------------------------------------------------------------------
 // dA (x by u) and dB (dy by t) in one launch.  A workgroup has 128 (fp32: 64) columns
-// of a chunk; of its eight waves RH share the ranks, 16 NT each, and the others the
-// tokens, 32 at a time, whose rows are transposed in registers.
+// of a chunk; of its waves RH share the ranks, 16 NT each, and the others the tokens,
+// 32 at a time, whose rows are transposed in registers.  Up to 32 ranks eight waves,
+// two to a SIMD; above, where the sums fill half the registers, four.
 struct Outer {
   const uint8_t* in;                    // [C][cols]
   int64_t in_pitch;
@@ -640,10 +673,9 @@ struct OArgs {
   Dropout drop;                         // of da's input
 };
 
-constexpr int kOWG = 512, kOWaves = kOWG / 64;
-template <int DT, int NT, int RH, bool DROP>
-__global__ __launch_bounds__(kOWG) void k_aouter(OArgs a) {
-  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, TG = kOWaves / RH, R = 16 * NT;
+template <int DT, int NT, int RH, int WAVES, bool DROP>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
+  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, TG = WAVES / RH, R = 16 * NT;
   extern __shared__ __align__(16) uint8_t s_o[];
   int* s_token = reinterpret_cast<int*>(s_o);                       // [2048], then the sums
   float* s_red = reinterpret_cast<float*>(s_o);                     // [TG / 2][RH][R][W + 4]
@@ -660,7 +692,7 @@ __global__ __launch_bounds__(kOWG) void k_aouter(OArgs a) {
   if constexpr (DROP) ctr = counter_of(a.drop.rng);
   // the tokens, the last again behind it up to whole steps
   const int steps = (t.count + 31) / 32;
-  for (int i = tid; i < 32 * steps; i += kOWG) s_token[i] = a.plan[a.at.perm + t.first + (i < t.count ? i : t.count - 1)];
+  for (int i = tid; i < 32 * steps; i += 64 * WAVES) s_token[i] = a.plan[a.at.perm + t.first + (i < t.count ? i : t.count - 1)];
   __syncthreads();
   float4v acc[NT][NTL];
 #pragma unroll
@@ -812,16 +844,25 @@ __global__ __launch_bounds__(256) void k_areduce(RArgs a) {
   const int most = second ? a.r - (int)(x / cols) * 4 : n - at < 4 ? (int)(n - at) : 4;
   float v[4] = {};
   const float* s = (second ? a.sb : a.sa) + at;
-  for (int q = q0; q < q1; ++q) {
-    if (!second && most >= 4) {
-      const uint4v w = load16(s + q * n);
+  // four chunks on their way together
+  for (int q = q0; q < q1; q += 4) {
+    float w[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(w[i]);
-    } else {
+    for (int k = 0; k < 4; ++k) {
+      const float* p = s + (q + k < q1 ? q + k : q0) * n;
+      if (!second && most >= 4) {
+        const uint4v x4 = load16(p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < most) v[i] += s[q * n + i * step];
+        for (int i = 0; i < 4; ++i) w[k][i] = __uint_as_float(x4[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[k][i] = p[i < most ? i * step : 0];
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += q + k < q1 ? w[k][i] : 0.0f;
   }
   float* o = second ? a.db + who * n + x % cols * a.r + x / cols * 4 : a.da + who * n + at;
 #pragma unroll
@@ -842,27 +883,29 @@ struct TArgs {
   int64_t out_stride, pitch;
 };
 
-// B [rows][r] of the adapters that have tokens to [r][rows]: 64 rows to a workgroup.
-template <int B>
+// B [rows][r] of the adapters that have tokens to [r][rows]: 64 rows by eight ranks
+// to a wave at a time.
+template <int DT>
 __global__ __launch_bounds__(256) void k_aturn(TArgs a) {
+  constexpr int B = kBytes<DT>;
   typedef typename std::conditional<B == 4, uint32_t, uint16_t>::type E;
-  __shared__ E s[64][MOE_MAX_RANK + 2];
   const int32_t* plan = a.plan;
   if (plan[0] != kPlanMagic || plan[1] != a.C || plan[2] != a.n) return;
-  for (int who = blockIdx.y; who < a.n; who += gridDim.y) {
-    if (plan[a.at.first + who] == plan[a.at.first + who + 1]) continue;
-    const int n0 = 64 * blockIdx.x;
-    for (int e = threadIdx.x; e < 64 * a.r; e += 256) {
-      const int k = e / a.r, j = e - k * a.r;
-      if (n0 + k < a.rows)
-        s[k][j] = reinterpret_cast<const E*>(a.b + who * a.b_stride + (n0 + k) * a.b_pitch)[j];
+  const int who = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (plan[a.at.first + who] == plan[a.at.first + who + 1]) return;
+  const int n = 64 * blockIdx.x + lane;
+  if (n >= a.rows) return;
+  const uint8_t* b = a.b + who * a.b_stride + n * a.b_pitch;
+  E* o = reinterpret_cast<E*>(a.out + who * a.out_stride) + n;
+  for (int j = 8 * wave; j < a.r; j += 32) {
+    const Eight<DT> v = load8_some<DT>(b + j * B, a.r - j);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (j + i >= a.r) break;
+      E* p = reinterpret_cast<E*>(reinterpret_cast<uint8_t*>(o) + (j + i) * a.pitch);
+      if constexpr (B == 4) *p = v.v[i >> 2][i & 3];
+      else *p = (uint16_t)(v.v[0][i >> 1] >> (16 * (i & 1)));
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < 64 * a.r; e += 256) {
-      const int j = e >> 6, k = e & 63;
-      if (n0 + k < a.rows) reinterpret_cast<E*>(a.out + who * a.out_stride + j * a.pitch)[n0 + k] = s[k][j];
-    }
-    __syncthreads();
   }
 }
 
@@ -955,22 +998,22 @@ void launch_expand(const AArgs& a, int tiles, hipStream_t st) {
   else hipLaunchKernelGGL((k_aexpand<DT, 4, BWD, DROP>), grid, dim3(kAWG), lds, st, a);
 }
 
-template <int DT, int NT, int RH, bool DROP>
+template <int DT, int NT, int RH, int WAVES, bool DROP>
 moe_status launch_outer_t(const OArgs& a, int chunks, hipStream_t st) {
-  constexpr int W = 16 * kTiles<DT>, sums = kOWaves / 2 * 16 * NT * (W + 4) * 4, lds = sums > 8192 ? sums : 8192;
-  auto k = k_aouter<DT, NT, RH, DROP>;
+  constexpr int W = 16 * kTiles<DT>, sums = WAVES / 2 * 16 * NT * (W + 4) * 4, lds = sums > 8192 ? sums : 8192;
+  auto k = k_aouter<DT, NT, RH, WAVES, DROP>;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          lds) != hipSuccess)
     return MOE_ERR_DEVICE;
-  hipLaunchKernelGGL(k, dim3((unsigned)(a.da.blocks + a.db.blocks), (unsigned)chunks), dim3(kOWG), lds, st, a);
+  hipLaunchKernelGGL(k, dim3((unsigned)(a.da.blocks + a.db.blocks), (unsigned)chunks), dim3(64 * WAVES), lds, st, a);
   return MOE_OK;
 }
 template <int DT, bool DROP>
 moe_status launch_outer(const OArgs& a, int chunks, hipStream_t st) {
-  if (a.r <= 16) return launch_outer_t<DT, 1, 1, DROP>(a, chunks, st);
-  if (a.r <= 32) return launch_outer_t<DT, 2, 1, DROP>(a, chunks, st);
-  if (a.r <= 64) return launch_outer_t<DT, 2, 2, DROP>(a, chunks, st);
-  return launch_outer_t<DT, 2, 4, DROP>(a, chunks, st);
+  if (a.r <= 16) return launch_outer_t<DT, 1, 1, 8, DROP>(a, chunks, st);
+  if (a.r <= 32) return launch_outer_t<DT, 2, 1, 8, DROP>(a, chunks, st);
+  if (a.r <= 64) return launch_outer_t<DT, 4, 1, 4, DROP>(a, chunks, st);
+  return launch_outer_t<DT, 4, 2, 4, DROP>(a, chunks, st);
 }
 
 // fn(dtype constant)
@@ -1129,7 +1172,7 @@ moe_status moe_adapter_bwd(const moe_adapter_bank* b, const void* plan, size_t p
       t.C = C; t.n = b->adapters; t.r = b->rank; t.rows = b->rows;
       t.b = static_cast<const uint8_t*>(b->b); t.b_stride = b->b_stride * s; t.b_pitch = b->b_pitch * s;
       t.out = c.w8 + c.ws.turned; t.out_stride = c.ws.turn_stride; t.pitch = c.ws.turn_pitch;
-      hipLaunchKernelGGL((k_aturn<kBytes<DT>>), dim3((unsigned)((b->rows + 63) / 64), (unsigned)b->adapters), dim3(256), 0,
+      hipLaunchKernelGGL((k_aturn<DT>), dim3((unsigned)((b->rows + 63) / 64), (unsigned)b->adapters), dim3(256), 0,
                          q, t);
       const Split f = shrink_split(c.at.max_tiles, b->rows);
       a.splits = f.splits; a.per_split = f.per;

@@ -168,14 +168,16 @@ __device__ __forceinline__ Counter counter_of(const uint64_t* rng) {
   c.o1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(o >> 32));
   return c;
 }
+// one instruction, which the compiler does not find
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
 __device__ __forceinline__ uint4v philox(const Counter& c, uint32_t block, uint32_t row) {
   uint32_t w0 = c.o0, w1 = c.o1, w2 = block, w3 = row, k0 = c.k0, k1 = c.k1;
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t p = (uint64_t)w0 * 0xD2511F53u, q = (uint64_t)w2 * 0xCD9E8D57u;
-    w0 = (uint32_t)(q >> 32) ^ w1 ^ k0;
+    w0 = xor3((uint32_t)(q >> 32), w1, k0);
     w1 = (uint32_t)q;
-    w2 = (uint32_t)(p >> 32) ^ w3 ^ k1;
+    w2 = xor3((uint32_t)(p >> 32), w3, k1);
     w3 = (uint32_t)p;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
