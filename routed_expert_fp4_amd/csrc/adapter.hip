@@ -46,10 +46,10 @@ constexpr int kPlanMagic = 0x41504C4E;
 // A batch of more tokens has tiles of 64: a tile's columns of A and B are read
 // once for all of its tokens.
 inline int plan_tile(int C) { return C > 1024 ? 64 : 16; }
-// Tokens to a chunk: four chunks in a batch, 256 .. 2048 tokens each.
+// Tokens to a chunk: eight chunks in a batch, 256 .. 2048 tokens each.
 inline int plan_chunk(int C) {
   int q = 256;
-  while (q < 2048 && q * 4 < C) q *= 2;
+  while (q < 2048 && q * 8 < C) q *= 2;
   return q;
 }
 struct PlanLayout { int64_t perm, tiles, chunks, first, total; int max_tiles, max_chunks; };   // in int32
@@ -258,6 +258,7 @@ struct AArgs {
   float* part;                          // [splits][C][r] in the plan's order
   int splits, per_split;                // column ranges, columns in each (multiple of 256)
   float* keep;                          // expand: the finished sums [C][r] by token, or NULL
+  int column_parts;                     // expand: workgroups to a tile
   Dropout drop;
 };
 
@@ -387,15 +388,63 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
 // For fp16, t and u are two fp16 terms under a power of two per token that puts the
 // token's largest below 2^15: 22 bits, or 2^-39 of the largest; for bf16 three bf16
 // pieces, exact.
+//
+// sum += the partial sums of a tile's tokens tid / 16 + 16 i, ranks 32 q + 2 (tid % 16)
+// and the next, over all ranges in order, U of them at a time.
+template <int SUBS, int KT, int U>
+__device__ __forceinline__ void add_ranges(const AArgs& a, const Tile& t, float (&sum)[4][KT][2], int tid) {
+  const int row = tid & 15;
+  const int64_t range = (int64_t)a.C * a.r;
+  const float* p = a.part + (int64_t)t.first * a.r;
+  uint32_t at[SUBS][KT][2];
+#pragma unroll
+  for (int i = 0; i < SUBS; ++i) {
+    const int k = (tid >> 4) + 16 * i;
+#pragma unroll
+    for (int q = 0; q < KT; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = 32 * q + 2 * row + e;
+        at[i][q][e] = (uint32_t)((k < t.count ? k : t.count - 1) * a.r + (j < a.r ? j : a.r - 1));
+      }
+  }
+  for (int x = 0; x < a.splits; x += U) {
+    float w[U][SUBS][KT][2];
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      const float* f = p + (x + y < a.splits ? x + y : x) * range;
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+        for (int q = 0; q < KT; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) w[y][i][q][e] = f[at[i][q][e]];
+    }
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      if (x + y >= a.splits) break;
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+        for (int q = 0; q < KT; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sum[i][q][e] += w[y][i][q][e];
+    }
+  }
+}
+
 template <int DT, int KT, bool BWD, bool DROP>
-__global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
+__global__ __launch_bounds__(kAWG, KT <= 2 ? 2 : 1) void k_aexpand(AArgs a) {
   constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, P = DT == MOE_DT_F32 ? 1 : DT == MOE_DT_F16 ? 2 : 3;
   // the sums as operands, [piece][rank / 8][token][8], and the tokens
   extern __shared__ __align__(16) uint8_t s_t[];
   __shared__ int s_token[64];
   __shared__ float s_inv[64];
+  // workgroups b, b + 8, .. run on one XCD: those of one tile, which read the same
+  // partial sums, follow each other on one
+  const int run = blockIdx.x >> 3, part = run % a.column_parts, tile = run / a.column_parts * 8 + (blockIdx.x & 7);
   Tile t;
-  if (!plan_entry(a.plan, a.C, a.n, 3, a.at.tiles, blockIdx.x, t)) return;
+  if (tile >= a.at.max_tiles || !plan_entry(a.plan, a.C, a.n, 3, a.at.tiles, tile, t)) return;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, row = lane & 15, quarter = lane >> 4;
   const int subs = (t.count + 15) / 16, T = 16 * subs;
   const bool idle = t.who < 0;
@@ -403,58 +452,84 @@ __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
   const uint8_t* w = a.w + (idle ? 0 : t.who) * a.w_stride;
   Eight<DT> f[KT][NTL];                 // tile i of rank 32 k + 8 quarter .. + 7: column c + i
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(kZeroRow);     // ranks past the last
+  // (One branch for all of a set of loads, here and below: a branch at each would keep
+  // them from being on their way together.)
   auto operands = [&](int c0) {
     const int c = c0 + NTL * row;
     if constexpr (!BWD) {
-      const bool eights = a.r % 8 == 0;
+      auto column = [&](int i) { return w + (c + i < a.cols ? c + i : a.cols - 1) * a.w_pitch; };
+      if (a.r % 8 == 0) {
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const int j0 = 32 * k + 8 * quarter;
+        for (int k = 0; k < KT; ++k) {
+          const int j0 = 32 * k + 8 * quarter;
 #pragma unroll
-        for (int i = 0; i < NTL; ++i) {
-          const int n = c + i < a.cols ? c + i : a.cols - 1;
-          const uint8_t* p = w + n * a.w_pitch;
-          if (eights) f[k][i] = load8<DT>(j0 < a.r ? p + j0 * B : zeros);
-          else f[k][i] = load8_some<DT>(p + j0 * B, a.r - j0);
+          for (int i = 0; i < NTL; ++i) f[k][i] = load8<DT>(j0 < a.r ? column(i) + j0 * B : zeros);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          const int j0 = 32 * k + 8 * quarter;
+#pragma unroll
+          for (int i = 0; i < NTL; ++i) f[k][i] = load8_some<DT>(column(i) + j0 * B, a.r - j0);
         }
       }
     } else {
-      const bool whole = c0 + W <= a.cols;
+      uint4v g[KT][8];                  // rank 32 k + 8 quarter + i, columns c ..
+      auto rank = [&](int j) { return w + j * a.w_pitch + (int64_t)c * B; };
+      if (c0 + W <= a.cols) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = 32 * k + 8 * quarter + i;
+            g[k][i] = load16(j < a.r ? rank(j) : zeros);
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = 32 * k + 8 * quarter + i;
+            g[k][i] = load16_some<DT>(rank(j), j < a.r ? a.cols - c : 0);
+          }
+      }
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
-        const int j0 = 32 * k + 8 * quarter;
-        uint4v g[8];                    // rank j0 + i, columns c ..
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = j0 + i < a.r ? j0 + i : a.r - 1;
-          const uint8_t* p = w + j * a.w_pitch + (int64_t)c * B;
-          if (whole) {
-            g[i] = load16(j0 + i < a.r ? p : zeros);
-          } else if (j0 + i >= a.r) {
-            g[i] = uint4v(0u);
-          } else if constexpr (DT == MOE_DT_F32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) g[i][e] = c + e < a.cols ? reinterpret_cast<const uint32_t*>(p)[e] : 0u;
-          } else {
-            g[i] = load8_some<DT>(p, a.cols - c).v[0];
-          }
-        }
         if constexpr (DT == MOE_DT_F32) {
 #pragma unroll
           for (int i = 0; i < NTL; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[k][i].v[e >> 2][e & 3] = g[e][i];
+            for (int e = 0; e < 8; ++e) f[k][i].v[e >> 2][e & 3] = g[k][e][i];
         } else {
           uint4v o[8];
-          turn8(g, o);
+          turn8(g[k], o);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[k][i].v[0] = o[i];
         }
       }
     }
   };
-  int c0 = W * (blockIdx.y * 4 + wave);
-  const int step = 4 * W * gridDim.y;
+  int c0 = W * (part * 4 + wave);
+  const int step = 4 * W * a.column_parts;
+  // base's rows of 16 tokens, loaded while those before are multiplied; the first
+  // before anything else
+  uint4v old[4], next[4];
+  auto base_rows = [&](const int (&token)[4], int c0) {
+    const int c = c0 + NTL * row;
+    if (c0 + W <= a.cols) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) next[e] = load16(a.base + token[e] * a.base_pitch + (int64_t)c * B);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) next[e] = load16_some<DT>(a.base + token[e] * a.base_pitch + (int64_t)c * B, a.cols - c);
+    }
+  };
+  if (a.base && c0 < a.cols) {
+    int token[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) token[e] = a.plan[a.at.perm + t.first + (4 * quarter + e < t.count ? 4 * quarter + e : t.count - 1)];
+    base_rows(token, c0);
+  }
   if (!idle && c0 < a.cols) operands(c0);
   // t (or u) of the tile: 16 lanes to a token, two ranks a lane and 32
   if (tid < T) s_token[tid] = a.plan[a.at.perm + t.first + (tid < t.count ? tid : t.count - 1)];
@@ -464,43 +539,9 @@ __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
 #pragma unroll
     for (int q = 0; q < KT; ++q) sum[i][q][0] = sum[i][q][1] = 0.0f;
   if (!idle) {
-    // two ranges' loads, of all tokens, on their way together
-    const int64_t range = (int64_t)a.C * a.r;
-    auto add = [&](const float* p, float (&w)[4][KT][2]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= subs) break;
-        const int k = (tid >> 4) + 16 * i;
-#pragma unroll
-        for (int q = 0; q < KT; ++q)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = 32 * q + 2 * row + e;
-            w[i][q][e] = p[(int64_t)(k < t.count ? k : t.count - 1) * a.r + (j < a.r ? j : a.r - 1)];
-          }
-      }
-    };
-    auto into = [&](const float (&w)[4][KT][2]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < KT; ++q)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) sum[i][q][e] += w[i][q][e];
-    };
-    const float* p = a.part + (int64_t)t.first * a.r;
-    int x = 0;
-    float w0[4][KT][2] = {}, w1[4][KT][2] = {};
-    for (; x + 2 <= a.splits; x += 2) {
-      add(p + x * range, w0);
-      add(p + (x + 1) * range, w1);
-      into(w0);
-      into(w1);
-    }
-    if (x < a.splits) {
-      add(p + x * range, w0);
-      into(w0);
-    }
+    // as many ranges' loads on their way together as 64 registers hold
+    if (subs == 1) add_ranges<1, KT, 16 / KT>(a, t, sum, tid);
+    else add_ranges<4, KT, 8 / KT>(a, t, sum, tid);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -515,7 +556,7 @@ __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
         const bool live = k < t.count && 32 * q + 2 * row + e < a.r;
         v[q][e] = live ? sum[i][q][e] * (BWD ? s : a.drop.scale) : 0.0f;
       }
-    if (a.keep && blockIdx.y == 0 && k < t.count) {
+    if (a.keep && part == 0 && k < t.count) {
       float* o = a.keep + (int64_t)a.plan[a.at.perm + t.first + k] * a.r;
 #pragma unroll
       for (int q = 0; q < KT; ++q)
@@ -583,25 +624,17 @@ __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
   for (; c0 < a.cols; c0 += step) {
     const int c = c0 + NTL * row, left = a.cols - c;
     const bool whole = c0 + W <= a.cols;
-    // base's rows of 16 tokens, loaded while those before are multiplied
-    uint4v old[4], next[4];
-    auto base_rows = [&](int sub, uint4v (&b)[4]) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint8_t* p = a.base + s_token[16 * sub + 4 * quarter + e] * a.base_pitch + (int64_t)c * B;
-        if (whole) {
-          b[e] = load16(p);
-        } else if constexpr (DT == MOE_DT_F32) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) b[e][i] = i < left ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
-        } else {
-          b[e] = load8_some<DT>(p, left).v[0];
-        }
-      }
-    };
-    if (a.base) base_rows(0, old);
     for (int sub = 0; sub < subs; ++sub) {
-      if (a.base && sub + 1 < subs) base_rows(sub + 1, next);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[e] = next[e];
+      // the next 16 tokens', or the next columns' first
+      const bool last = sub + 1 == subs;
+      if (a.base && (!last || c0 + step < a.cols)) {
+        int token[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) token[e] = s_token[(last ? 0 : 16 * (sub + 1)) + 4 * quarter + e];
+        base_rows(token, last ? c0 + step : c0);
+      }
       float4v acc[NTL];
 #pragma unroll
       for (int i = 0; i < NTL; ++i) acc[i] = float4v(0.0f);
@@ -644,8 +677,6 @@ __global__ __launch_bounds__(kAWG) void k_aexpand(AArgs a) {
           else store16_some<DT>(o, q, left);
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) old[e] = next[e];
     }
     if (!idle && c0 + step < a.cols) operands(c0 + step);
   }
@@ -706,17 +737,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
   auto load = [&](int s, Turn& u) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) u.token[i] = s_token[32 * s + 8 * quarter + i];
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint8_t* p = o.in + u.token[i] * o.in_pitch + (int64_t)c * B;
-      if (whole) {
-        u.g[i] = load16(p);
-      } else if constexpr (DT == MOE_DT_F32) {
+      for (int i = 0; i < 8; ++i) u.g[i] = load16(o.in + u.token[i] * o.in_pitch + (int64_t)c * B);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u.g[i][e] = e < left ? reinterpret_cast<const uint32_t*>(p)[e] : 0u;
-      } else {
-        u.g[i] = load8_some<DT>(p, left).v[0];
-      }
+      for (int i = 0; i < 8; ++i) u.g[i] = load16_some<DT>(o.in + u.token[i] * o.in_pitch + (int64_t)c * B, left);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -945,14 +971,14 @@ Split shrink_split(int tiles, int cols) {
 
 // The workspace: bounds that hold for every number of tokens up to C, so that it
 // serves fewer too.  With ranges (512 / tiles, tiles > C / 64) the partial sums are
-// those of 512 * 64 tokens at most, and there are four chunks a batch, or one to
+// those of 512 * 64 tokens at most, and there are eight chunks a batch, or one to
 // 2048 tokens, besides every adapter's last.
 struct AdapterWs { size_t part, u, turned, suma, sumb, total; int64_t turn_pitch, turn_stride; };
 AdapterWs adapter_ws(const moe_adapter_bank* b, int C) {
   const int64_t s = dense_size(b->dtype);
   const int64_t most = ((b->cols > b->rows ? b->cols : b->rows) + 511) / 512;
   const int64_t rows = C * most < 512 * 64 ? C * most : C > 512 * 64 ? C : 512 * 64;
-  const int64_t four = C / 256 < 4 ? C / 256 : 4, chunks = (C / 2048 > four ? C / 2048 : four) + (C < b->adapters ? C : b->adapters);
+  const int64_t few = C / 256 < 8 ? C / 256 : 8, chunks = (C / 2048 > few ? C / 2048 : few) + (C < b->adapters ? C : b->adapters);
   AdapterWs w;
   size_t o = 0;
   w.part = o; o = align256(o + (size_t)rows * b->rank * sizeof(float));
@@ -985,12 +1011,13 @@ void launch_shrink(const AArgs& a, int tiles, bool drop, hipStream_t st) {
 }
 
 template <int DT, bool BWD, bool DROP>
-void launch_expand(const AArgs& a, int tiles, hipStream_t st) {
+void launch_expand(AArgs a, int tiles, hipStream_t st) {
   // a wave's columns once, or again where that makes more than four workgroups a CU
   const int per = 64 * kTiles<DT>, blocks = a.cols > 0 ? (a.cols + per - 1) / per : 1;
   int y = 1024 / tiles;
   y = y < 1 ? 1 : y > blocks ? blocks : y;
-  const dim3 grid((unsigned)tiles, (unsigned)y);
+  a.column_parts = y;
+  const dim3 grid((unsigned)((tiles + 7) / 8 * 8 * y));
   const int kt = a.r <= 32 ? 1 : a.r <= 64 ? 2 : 4;
   const size_t lds = (size_t)plan_tile(a.C) * 32 * kt * (DT == MOE_DT_F32 ? 4 : DT == MOE_DT_F16 ? 4 : 6);
   if (kt == 1) hipLaunchKernelGGL((k_aexpand<DT, 1, BWD, DROP>), grid, dim3(kAWG), lds, st, a);

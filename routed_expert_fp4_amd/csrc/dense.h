@@ -110,6 +110,16 @@ __device__ __forceinline__ uint4v pack16(const float (&f)[N]) {
   }
   return v;
 }
+// the first n of 16 bytes' elements, zeros for the others
+template <int DT>
+__device__ __forceinline__ uint4v load16_some(const void* p, int n) {
+  if constexpr (DT != MOE_DT_F32) return load8_some<DT>(p, n).v[0];
+  uint4v v = uint4v(0u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) v[i] = static_cast<const uint32_t*>(p)[i];
+  return v;
+}
 template <int DT>
 __device__ __forceinline__ void store16_some(void* p, uint4v v, int n) {
   constexpr int N = 16 / kBytes<DT>;
