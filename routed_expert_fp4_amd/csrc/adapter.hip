@@ -23,6 +23,7 @@
 //   k_ashrink   t or u: a tile's tokens by a range of columns; partial sums
 //   k_aexpand   y or dx: a tile's tokens by a range of columns; adds the partial
 //               sums up first and keeps them (t for the caller, u for the next)
+//   k_apieces   t and u laid out as operands
 //   k_aouter    dA and dB of a chunk's tokens, 128 columns (fp32: 64) to a workgroup
 //   k_areduce   adds the chunks up
 //   k_aturn     B by rank for u's product
@@ -168,18 +169,12 @@ __global__ __launch_bounds__(kPlanWG) void k_aplan(PArgs a) {
 // Pieces of operands
 // ---------------------------------------------------------------------------
 // v as three bf16 that sum to it exactly, each the truncation of what is left.
-// An infinity or NaN is its own first piece and has no others.
+// (What is left of an infinity or NaN is NaN.)
 __device__ __forceinline__ void pieces3(float v, uint32_t& a, uint32_t& b, uint32_t& c) {
   a = __float_as_uint(v) & 0xFFFF0000u;
   const float r = v - __uint_as_float(a);
   b = __float_as_uint(r) & 0xFFFF0000u;
-  const float s = r - __uint_as_float(b);
-  c = __float_as_uint(s);
-  if ((a & 0x7F800000u) == 0x7F800000u) {
-    if (v != v) a = 0x7FC00000u;           // a NaN whose truncation would be an infinity
-    b = 0;
-    c = 0;
-  }
+  c = __float_as_uint(r - __uint_as_float(b));
 }
 __device__ __forceinline__ uint32_t high_pair(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
 
@@ -689,10 +684,14 @@ __global__ __launch_bounds__(kAWG, KT <= 2 ? 2 : 1) void k_aexpand(AArgs a) {
 // of a chunk; of its waves RH share the ranks, 16 NT each, and the others the tokens,
 // 32 at a time, whose rows are transposed in registers.  Up to 32 ranks eight waves,
 // two to a SIMD; above, where the sums fill half the registers, four.
+// u and t are needed by every workgroup of a chunk: k_apieces lays them out once as
+// the first operand, [32 tokens][16 ranks][piece][lane], three bf16 pieces, or the
+// two halves of eight fp32.
 struct Outer {
   const uint8_t* in;                    // [C][cols]
   int64_t in_pitch;
   const float* small;                   // [C][r] by token
+  uint8_t* pieces;                      // small laid out
   float* sums;                          // [chunks][r][cols]
   int cols, blocks;                     // of columns
 };
@@ -703,10 +702,57 @@ struct OArgs {
   Outer da, db;                         // blocks 0: not asked for
   Dropout drop;                         // of da's input
 };
+template <int DT>
+constexpr int kParts = DT == MOE_DT_F32 ? 2 : 3;
+// The 32 tokens from step s of chunk q on have a place of their own: chunks start
+// anywhere, and each may end in a partial step: C / 32 + chunks + 1 places in all.
+__device__ __forceinline__ int64_t step_place(const Tile& t, int q, int s) { return t.first / 32 + q + s; }
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_apieces(OArgs a) {
+  const Outer& o = blockIdx.z == 0 && a.da.blocks ? a.da : a.db;
+  Tile t;
+  if (!plan_entry(a.plan, a.C, a.n, 4, a.at.chunks, blockIdx.y, t)) return;
+  const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4, s = blockIdx.x, tiles = (a.r + 15) / 16;
+  if (32 * s >= t.count) return;
+  int token[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = 32 * s + 8 * quarter + i;
+    token[i] = a.plan[a.at.perm + t.first + (k < t.count ? k : t.count - 1)];
+  }
+  for (int j = threadIdx.x >> 6; j < tiles; j += 4) {
+    const int rank = 16 * j + row;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = o.small[(int64_t)token[i] * a.r + (rank < a.r ? rank : a.r - 1)];
+    // tokens behind the last, and ranks, are zeros
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (32 * s + 8 * quarter + i >= t.count || rank >= a.r) v[i] = 0.0f;
+    uint4v* out = reinterpret_cast<uint4v*>(o.pieces) + ((step_place(t, blockIdx.y, s) * tiles + j) * kParts<DT>) * 64 + lane;
+    if constexpr (DT == MOE_DT_F32) {
+      out[0] = uint4v{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      out[64] = uint4v{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    } else {
+      uint4v m[3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t p[2][3];
+        pieces3(v[2 * i], p[0][0], p[0][1], p[0][2]);
+        pieces3(v[2 * i + 1], p[1][0], p[1][1], p[1][2]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) m[q][i] = high_pair(p[0][q], p[1][q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) out[64 * q] = m[q];
+    }
+  }
+}
 
 template <int DT, int NT, int RH, int WAVES, bool DROP>
 __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
-  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, TG = WAVES / RH, R = 16 * NT;
+  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, TG = WAVES / RH, R = 16 * NT, P = kParts<DT>;
   extern __shared__ __align__(16) uint8_t s_o[];
   int* s_token = reinterpret_cast<int*>(s_o);                       // [2048], then the sums
   float* s_red = reinterpret_cast<float*>(s_o);                     // [TG / 2][RH][R][W + 4]
@@ -718,7 +764,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
   const Outer& o = second ? a.db : a.da;
   const int c0 = W * (blockIdx.x - (second ? a.da.blocks : 0)), c = c0 + NTL * row, left = o.cols - c;
   const bool whole = c0 + W <= o.cols, drops = DROP && !second;
-  const int rh = wave % RH, tg = wave / RH, r0 = R * rh;
+  const int rh = wave % RH, tg = wave / RH, r0 = R * rh, tiles = (a.r + 15) / 16;
   Counter ctr = {};
   if constexpr (DROP) ctr = counter_of(a.drop.rng);
   // the tokens, the last again behind it up to whole steps
@@ -730,41 +776,36 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < NTL; ++j) acc[i][j] = float4v(0.0f);
-  int rank[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) rank[j] = r0 + 16 * j + row < a.r ? r0 + 16 * j + row : a.r - 1;
-  struct Turn { uint4v g[8]; float sm[NT][8]; int token[8]; };
+  const uint4v* small = reinterpret_cast<const uint4v*>(o.pieces) + step_place(t, blockIdx.y, 0) * tiles * P * 64;
+  struct Turn { uint4v g[8], m[NT][P]; };
   auto load = [&](int s, Turn& u) {
+    const uint8_t* p[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u.token[i] = s_token[32 * s + 8 * quarter + i];
+    for (int i = 0; i < 8; ++i) p[i] = o.in + s_token[32 * s + 8 * quarter + i] * o.in_pitch + (int64_t)c * B;
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.g[i] = load16(o.in + u.token[i] * o.in_pitch + (int64_t)c * B);
+      for (int i = 0; i < 8; ++i) u.g[i] = load16(p[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.g[i] = load16_some<DT>(o.in + u.token[i] * o.in_pitch + (int64_t)c * B, left);
+      for (int i = 0; i < 8; ++i) u.g[i] = load16_some<DT>(p[i], left);
     }
+    // (tiles past the last: the last again, whose sums are not used)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      const int k = r0 / 16 + j < tiles ? r0 / 16 + j : tiles - 1;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.sm[j][i] = o.small[(int64_t)u.token[i] * a.r + rank[j]];
+      for (int q = 0; q < P; ++q) u.m[j][q] = small[((int64_t)s * tiles + k) * (P * 64) + 64 * q + lane];
+    }
   };
-  Turn u, v;
-  if (tg < steps) load(tg, u);
-  for (int s = tg; s < steps; s += TG) {
-    if (s + TG < steps) load(s + TG, v);
+  auto multiply = [&](int s, Turn& u) {
     if (32 * s + 32 > t.count) {        // tokens behind the last add nothing
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (32 * s + 8 * quarter + i >= t.count) {
-          u.g[i] = uint4v(0u);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) u.sm[j][i] = 0.0f;
-        }
+        if (32 * s + 8 * quarter + i >= t.count) u.g[i] = uint4v(0u);
     }
     if (drops) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.g[i] = drop16<DT>(u.g[i], a.drop, ctr, c, (uint32_t)u.token[i]);
+      for (int i = 0; i < 8; ++i) u.g[i] = drop16<DT>(u.g[i], a.drop, ctr, c, (uint32_t)s_token[32 * s + 8 * quarter + i]);
     }
     if constexpr (DT == MOE_DT_F32) {
 #pragma unroll
@@ -773,29 +814,33 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
         for (int i = 0; i < NTL; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(u.sm[j][e], __uint_as_float(u.g[e][i]), acc[j][i], 0, 0, 0);
+            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(u.m[j][e >> 2][e & 3]), __uint_as_float(u.g[e][i]),
+                                                             acc[j][i], 0, 0, 0);
     } else {
-      uint4v f[8], m[NT][3];
+      uint4v f[8];
       turn8(u.g, f);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t p[2][3];
-          pieces3(u.sm[j][2 * i], p[0][0], p[0][1], p[0][2]);
-          pieces3(u.sm[j][2 * i + 1], p[1][0], p[1][1], p[1][2]);
-#pragma unroll
-          for (int q = 0; q < 3; ++q) m[j][q][i] = high_pair(p[0][q], p[1][q]);
-        }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         uint4v b[kPieces<DT>];
         pieces<DT>(f[i], b);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][i] = mma_pieces<DT>(m[j], b, acc[j][i]);
+        for (int j = 0; j < NT; ++j) acc[j][i] = mma_pieces<DT>(u.m[j], b, acc[j][i]);
       }
     }
-    u = v;
+  };
+  // (two sets by turns: a copy would wait for what is on its way)
+  Turn even, odd;
+  if (tg < steps) load(tg, even);
+  for (int s = tg; s < steps; s += 2 * TG) {
+    if (s + TG < steps) load(s + TG, odd);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(s, even);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + TG >= steps) break;
+    if (s + 2 * TG < steps) load(s + 2 * TG, even);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(s + TG, odd);
+    __builtin_amdgcn_sched_barrier(0);
   }
   // the sums of the waves that share the tokens, in a fixed order
   float* mine = s_red + rh * R * (W + 4);
@@ -973,7 +1018,7 @@ Split shrink_split(int tiles, int cols) {
 // serves fewer too.  With ranges (512 / tiles, tiles > C / 64) the partial sums are
 // those of 512 * 64 tokens at most, and there are eight chunks a batch, or one to
 // 2048 tokens, besides every adapter's last.
-struct AdapterWs { size_t part, u, turned, suma, sumb, total; int64_t turn_pitch, turn_stride; };
+struct AdapterWs { size_t part, u, turned, suma, sumb, pieces, piece_bytes, total; int64_t turn_pitch, turn_stride; };
 AdapterWs adapter_ws(const moe_adapter_bank* b, int C) {
   const int64_t s = dense_size(b->dtype);
   const int64_t most = ((b->cols > b->rows ? b->cols : b->rows) + 511) / 512;
@@ -988,6 +1033,8 @@ AdapterWs adapter_ws(const moe_adapter_bank* b, int C) {
   w.turned = o; o = align256(o + (size_t)b->adapters * w.turn_stride);
   w.suma = o; o = align256(o + (size_t)chunks * b->rank * b->cols * sizeof(float));
   w.sumb = o; o = align256(o + (size_t)chunks * b->rank * b->rows * sizeof(float));
+  w.piece_bytes = align256((size_t)(C / 32 + chunks + 1) * ((b->rank + 15) / 16) * (s == 4 ? 2 : 3) * 1024);
+  w.pieces = o; o += 2 * w.piece_bytes;
   w.total = o;
   return w;
 }
@@ -1222,8 +1269,10 @@ moe_status moe_adapter_bwd(const moe_adapter_bank* b, const void* plan, size_t p
       o.C = C; o.n = b->adapters; o.r = b->rank;
       o.drop = a.drop;
       constexpr int W = 16 * kTiles<DT>;
-      if (da) o.da = Outer{static_cast<const uint8_t*>(x), x_pitch * s, u, reinterpret_cast<float*>(c.w8 + c.ws.suma), b->cols, (b->cols + W - 1) / W};
-      if (db) o.db = Outer{static_cast<const uint8_t*>(dy), dy_pitch * s, hidden, reinterpret_cast<float*>(c.w8 + c.ws.sumb), b->rows, (b->rows + W - 1) / W};
+      if (da) o.da = Outer{static_cast<const uint8_t*>(x), x_pitch * s, u, c.w8 + c.ws.pieces, reinterpret_cast<float*>(c.w8 + c.ws.suma), b->cols, (b->cols + W - 1) / W};
+      if (db) o.db = Outer{static_cast<const uint8_t*>(dy), dy_pitch * s, hidden, c.w8 + c.ws.pieces + c.ws.piece_bytes, reinterpret_cast<float*>(c.w8 + c.ws.sumb), b->rows, (b->rows + W - 1) / W};
+      const unsigned steps = (unsigned)(plan_chunk(C) / 32);
+      hipLaunchKernelGGL((k_apieces<DT>), dim3(steps, (unsigned)c.at.max_chunks, da && db ? 2 : 1), dim3(256), 0, q, o);
       st = drop && da ? launch_outer<DT, true>(o, c.at.max_chunks, q) : launch_outer<DT, false>(o, c.at.max_chunks, q);
     }
   });
