@@ -167,9 +167,8 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
 // it (64 elements of 16 bits, 32 of fp32): LDS holds its rows one after the
 // other, the 16-byte unit u of row m at u ^ (m / 2 & 7) (16 rows that are read
 // together fill the 256 bytes of the banks).  An operand that lies across
-// the axis has that many of its rows in LDS, unit u of row k at u ^ 4 (k & 3)
-// (16 bits), and is read with the transposing LDS loads; fp32 is read element by
-// element.  Both are loaded into LDS directly, one step ahead.
+// the axis has that many of its rows in LDS, units exchanged too, and is read with
+// the transposing LDS loads; fp32 is read element by element.  Both are loaded into LDS directly, one step ahead.
 enum { kFwd, kDx, kDw };
 
 // 16 bytes a lane into LDS, at `at` + 16 lane, by inline assembly: behind the
@@ -208,6 +207,14 @@ __device__ __forceinline__ float16v mma32(uint4v a, uint4v b, float16v c) {
   }
 }
 
+// The exchange of units in row k (mod 4) of an operand that lies across, `units` to a
+// row: the 64 bytes that a transposing load takes of each of four rows fill the 256
+// bytes of the banks.
+template <int DT>
+__device__ __forceinline__ int across_swap(int k, int units) {
+  return DT == MOE_DT_F32 ? 0 : units >= 16 ? 4 * (k & 3) : 4 * (k >> 1 & 1);
+}
+
 // 32 rows (or columns) from `m` on, quarter ks of a step: lane l holds row l % 32
 // and the eight (fp32: four) elements 2 ks + l / 32 of the step
 template <int DT, bool ALONG, int ROWS>
@@ -223,7 +230,7 @@ __device__ __forceinline__ uint4v fragment(const uint8_t* s, int m, int ks, int 
     // i reads elements 4 (i % 4) .. of row i / 4
     const int g = lane >> 4, i = lane & 15, k = 16 * ks + 8 * (g >> 1) + (i >> 2);
     const int unit = (m >> 3) + 2 * (g & 1) + ((i >> 1) & 1);
-    const uint8_t* p = s + k * (ROWS * 2) + ((unit ^ (4 * (i >> 2))) * 16) + (i & 1) * 8;
+    const uint8_t* p = s + k * (ROWS * 2) + ((unit ^ across_swap<DT>(i >> 2, ROWS / 8)) * 16) + (i & 1) * 8;
     const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)p);
     const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)(p + 4 * ROWS * 2));
     typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
@@ -262,7 +269,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
   constexpr int UA = BM * B / 16, UB = BN * B / 16;                  // units of a row that lies across
   uint32_t oa[LA], ob[LB];
   auto unit_along = [&](int u) { return (u & 7) ^ ((u >> 4) & 7); };
-  auto unit_across = [&](int u, int n) { return (u % n) ^ (DT == MOE_DT_F32 ? 0 : 4 * ((u / n) & 3)); };
+  auto unit_across = [&](int u, int n) { return (u % n) ^ across_swap<DT>(u / n, n); };
 #pragma unroll
   for (int i = 0; i < LA; ++i) {
     const int u = i * WG + tid;
@@ -403,11 +410,48 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
   }
 
   // register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+  auto row_of = [&](int i, int r) { return wm * (BM / WM) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); };
+  if constexpr (B == 2) {
+    if (a.splits == 1 && !a.accumulate && !a.out_f32) {
+      // The results through LDS, so that rows are stored 16 bytes a lane: as they lie
+      // in registers a store holds 64 bytes of two rows.  Forward: h, then g and u.
+      constexpr int WN0 = MODE == kFwd ? BN / 2 : BN, kPitch = WN0 * 2 + 16;   // bytes of a row; 16 more spread the banks
+      static_assert(BM * kPitch <= 2 * kStage + BM * 16, "the results fit the LDS");
+      auto through = [&](uint8_t* out, int64_t pitch, auto value) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+#pragma unroll
+            for (int j = 0; j < (MODE == kFwd ? NH : NT); ++j)
+              *reinterpret_cast<uint16_t*>(s_ab + row_of(i, r) * kPitch + (column(j) + (lane & 31)) * 2) = round16<DT>(value(i, j, r));
+        __syncthreads();
+        constexpr int per = WN0 / 8;                         // lanes to a row
+        for (int k = tid; k < BM * per; k += WG) {
+          const int m = k / per, n = k % per * 8;
+          if (m0 + m >= a.M) break;
+          store16_some<DT>(out + (m0 + m) * pitch + (int64_t)(n0 + n) * 2,
+                           *reinterpret_cast<const uint4v*>(s_ab + m * kPitch + n * 2), a.N - n0 - n);
+        }
+      };
+      if constexpr (MODE == kFwd) {
+        through(a.h, a.h_pitch, [&](int i, int j, int r) { return act_of(a.act, acc[i][j][r]) * acc[i][j + NH][r]; });
+        if (a.gate) {
+          through(a.gate, a.gate_pitch, [&](int i, int j, int r) { return acc[i][j][r]; });
+          through(a.up, a.up_pitch, [&](int i, int j, int r) { return acc[i][j + NH][r]; });
+        }
+      } else {
+        through(second ? a.o1 : a.o0, second ? a.o1_pitch : a.o0_pitch, [&](int i, int j, int r) { return acc[i][j][r]; });
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int m = m0 + wm * (BM / WM) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+      const int m = m0 + row_of(i, r);
       if (m >= a.M) continue;
       if constexpr (MODE == kFwd) {
 #pragma unroll
@@ -503,20 +547,25 @@ __global__ __launch_bounds__(256) void k_fact(GArgs a) {
   }
 }
 
-struct KArgs {
+struct Pack {
   const uint8_t* in;
   int64_t in_pitch, rows;
-  int cols, units;
   uint8_t* out;
 };
+struct KArgs {
+  Pack t[3];
+  int cols, units;
+};
+// rows of `cols` elements into rows of `units` eights, zeros behind them
 template <int DT>
 __global__ __launch_bounds__(256) void k_fpack(KArgs a) {
   constexpr int B = kBytes<DT>;
-  const int64_t n = a.rows * a.units;
+  const Pack& p = a.t[blockIdx.y];
+  const int64_t n = p.rows * a.units;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
     const int64_t r = e / a.units;
     const int k = 8 * (int)(e - r * a.units);
-    store8<DT>(a.out + e * 8 * B, load8_some<DT>(a.in + r * a.in_pitch + (int64_t)k * B, a.cols - k));
+    store8<DT>(p.out + e * 8 * B, load8_some<DT>(p.in + r * p.in_pitch + (int64_t)k * B, a.cols - k));
   }
 }
 
@@ -542,24 +591,28 @@ bool whole_units(const void* p, int64_t pitch, int64_t rows, int64_t cols, int64
 }
 
 // How a product is tiled and split.
-struct Tiling { bool wide; int mblocks, nblocks, steps, splits, per_split; };
+struct Tiling { int bm, bn, mblocks, nblocks, steps, splits, per_split; };
 Tiling tiling(int mode, int64_t M, int64_t N, int64_t K, int64_t s) {
   Tiling t;
   const int e = (int)(128 / s);
-  auto blocks = [&](int b) {
-    t.mblocks = (int)((M + b - 1) / b) * (mode == kDw ? 2 : 1);
-    const int n = mode == kFwd ? b / 2 : b;
+  auto blocks = [&](int bm, int bn) {
+    t.bm = bm; t.bn = bn;
+    t.mblocks = (int)((M + bm - 1) / bm) * (mode == kDw ? 2 : 1);
+    const int n = mode == kFwd ? bn / 2 : bn;
     t.nblocks = (int)((N + n - 1) / n);
     return (int64_t)t.mblocks * t.nblocks;
   };
-  t.wide = blocks(256) >= 192;
-  const int64_t n = t.wide ? blocks(256) : blocks(128);
+  // 256 x 256 where its tiles, one a CU, come near the number of CUs; 64 x 128 for up
+  // to 64 rows, for few tiles, and where the sum's axis is not split
+  int64_t n = blocks(256, 256);
+  if (n < 192) n = blocks(128, 128);
+  if (t.bm == 128 && (M <= 64 || n < 64 || (mode == kDw && n < 256))) n = blocks(64, 128);
   t.steps = (int)((K + e - 1) / e) * (mode == kDx ? 2 : 1);
   t.splits = 1;
   t.per_split = t.steps;
-  if (!t.wide && mode != kDw && n < 256) {
-    // ranges of eight steps at least, two workgroups a CU at most
-    int64_t q = 512 / n, most = t.steps / 8;
+  if (t.bm < 256 && mode != kDw) {
+    // ranges of four steps at least, as many workgroups as the CUs hold
+    int64_t q = (t.bm == 64 ? 768 : 512) / n, most = t.steps / 4;
     q = q < most ? q : most;
     if (q > 1) {
       t.per_split = (int)((t.steps + q - 1) / q);
@@ -589,21 +642,21 @@ FfnWs ffn_ws_for(const moe_ffn* f, int C, bool bwd) {
   return w;
 }
 // The most that any number of tokens up to C needs: partial results come and go
-// with the ranges, which depend on tiles of 128 tokens.
+// with the ranges, which depend on tiles of 64 tokens.
 size_t ffn_workspace(const moe_ffn* f, int C) {
   size_t most = 256;
-  for (int c = C;; c = (c - 1) / 128 * 128) {
+  for (int c = C;; c = (c - 1) / 64 * 64) {
     const size_t a = ffn_ws_for(f, c, false).total, b = ffn_ws_for(f, c, true).total;
     most = a > most ? a : most;
     most = b > most ? b : most;
-    if (c <= 128) break;
+    if (c <= 64) break;
   }
   return most;
 }
 
 template <int DT, int MODE, int BM, int BN, int WM, int WN>
 moe_status launch_gemm_t(const FArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int lds = 2 * (BM + BN) * 128;
+  constexpr int lds = 2 * (BM + BN) * 128 + BM * 16;         // two stages, or the results
   auto k = k_fgemm<DT, MODE, BM, BN, WM, WN>;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          lds) != hipSuccess)
@@ -617,8 +670,9 @@ moe_status launch_product(FArgs a, hipStream_t st) {
   a.mblocks = t.mblocks; a.nblocks = t.nblocks;
   a.steps = t.steps; a.splits = t.splits; a.per_split = t.per_split;
   const dim3 grid((unsigned)(t.mblocks * t.nblocks), (unsigned)t.splits);
-  const moe_status s = t.wide ? launch_gemm_t<DT, MODE, 256, 256, 2, 4>(a, grid, st)
-                              : launch_gemm_t<DT, MODE, 128, 128, 2, 2>(a, grid, st);
+  const moe_status s = t.bm == 256   ? launch_gemm_t<DT, MODE, 256, 256, 2, 4>(a, grid, st)
+                       : t.bm == 128 ? launch_gemm_t<DT, MODE, 128, 128, 2, 2>(a, grid, st)
+                                     : launch_gemm_t<DT, MODE, 64, 128, 2, 2>(a, grid, st);
   if (s != MOE_OK) return s;
   if constexpr (MODE != kDw) {
     if (t.splits > 1) {
@@ -638,11 +692,16 @@ unsigned fill_grid(int64_t n) {
 template <int DT>
 void operands(const moe_ffn* f, FArgs& a, const FfnWs& w, uint8_t* w8, bool weights, bool need_x, hipStream_t st) {
   const int64_t s = kBytes<DT>;
+  KArgs k = {};
+  int n = 0;
+  int64_t most = 0;
+  k.cols = a.H;
+  k.units = (a.H + 7) / 8;
   auto pack = [&](const uint8_t*& p, int64_t& pitch, int64_t rows, size_t at) {
     if (whole_units(p, pitch / s, rows, a.H, s)) return;
-    KArgs k = {p, pitch, rows, a.H, (a.H + 7) / 8, w8 + at};
-    hipLaunchKernelGGL((k_fpack<DT>), dim3(fill_grid(k.rows * k.units)), dim3(256), 0, st, k);
-    p = k.out;
+    k.t[n++] = Pack{p, pitch, rows, w8 + at};
+    most = rows > most ? rows : most;
+    p = w8 + at;
     pitch = w.hp;
   };
   if (need_x) pack(a.x, a.x_pitch, a.C, w.x);
@@ -650,6 +709,7 @@ void operands(const moe_ffn* f, FArgs& a, const FfnWs& w, uint8_t* w8, bool weig
     pack(a.wg, a.wg_pitch, a.I, w.wg);
     pack(a.wu, a.wu_pitch, a.I, w.wu);
   }
+  if (n) hipLaunchKernelGGL((k_fpack<DT>), dim3(fill_grid(most * k.units), (unsigned)n), dim3(256), 0, st, k);
 }
 
 template <int DT>
