@@ -118,26 +118,45 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
   float4v acc[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) acc[t] = float4v(0.0f);
-  auto step = [&](int c, bool whole) {
-    const int k = c + 8 * quarter;
-    const Eight<DT> e = whole ? load8<DT>(w + (int64_t)k * B) : load8_some<DT>(w + (int64_t)k * B, a.H - k);
-    Eight<DT> v[TT];
+  // 128 columns to a wave at a time, the next on their way while these are multiplied
+  // (by turns in two sets of registers: a copy would wait for them)
+  constexpr int S = 4, U = 32 * S;
+  struct Turn { Eight<DT> w[S], x[S][TT]; };
+  auto load = [&](int c, Turn& u) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-      v[t] = whole ? load8<DT>(x[t] + (int64_t)k * B) : load8_some<DT>(x[t] + (int64_t)k * B, a.H - k);
+    for (int q = 0; q < S; ++q) u.w[q] = load8<DT>(w + (int64_t)(c + 32 * q + 8 * quarter) * B);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = mma8<DT>(e, v[t], acc[t]);
+    for (int q = 0; q < S; ++q)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) u.x[q][t] = load8<DT>(x[t] + (int64_t)(c + 32 * q + 8 * quarter) * B);
   };
-  // 64 columns to a wave at a time
-  const int whole = a.H / 64 * 64;
-#pragma unroll 4
-  for (int c = 64 * wave; c < whole; c += 64 * kFewWaves) {
-    step(c, true);
-    step(c + 32, true);
+  auto multiply = [&](const Turn& u) {
+#pragma unroll
+    for (int q = 0; q < S; ++q)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[t] = mma8<DT>(u.w[q], u.x[q][t], acc[t]);
+  };
+  constexpr int kStep = U * kFewWaves;
+  const int whole = a.H / U * U;
+  Turn even, odd;
+  int c = U * wave;
+  if (c < whole) load(c, even);
+  for (; c < whole; c += 2 * kStep) {
+    if (c + kStep < whole) load(c + kStep, odd);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(even);
+    if (c + kStep >= whole) break;
+    if (c + 2 * kStep < whole) load(c + 2 * kStep, even);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(odd);
   }
-  if (whole < a.H && (whole >> 6) % kFewWaves == wave) {
-    step(whole, false);
-    if (whole + 32 < a.H) step(whole + 32, false);
+  if (whole < a.H && whole / U % kFewWaves == wave) {
+    // a row's last columns, zeros behind them
+    for (int k = whole + 8 * quarter, q = 0; q < S && whole + 32 * q < a.H; ++q, k += 32) {
+      const Eight<DT> e = load8_some<DT>(w + (int64_t)k * B, a.H - k);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[t] = mma8<DT>(e, load8_some<DT>(x[t] + (int64_t)k * B, a.H - k), acc[t]);
+    }
   }
 #pragma unroll
   for (int t = 0; t < TT; ++t)
@@ -166,9 +185,10 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
 // A step takes 128 bytes along the sum's axis of an operand whose rows lie along
 // it (64 elements of 16 bits, 32 of fp32): LDS holds its rows one after the
 // other, the 16-byte unit u of row m at u ^ (m / 2 & 7) (16 rows that are read
-// together fill the 256 bytes of the banks).  An operand that lies across
-// the axis has that many of its rows in LDS, units exchanged too, and is read with
-// the transposing LDS loads; fp32 is read element by element.  Both are loaded into LDS directly, one step ahead.
+// together fill the 256 bytes of the banks).  An operand that lies across the axis
+// has that many of its rows in LDS, units exchanged too, and is read with the
+// transposing LDS loads; fp32 is read element by element.  Both are loaded into LDS
+// directly, one step ahead.
 enum { kFwd, kDx, kDw };
 
 // 16 bytes a lane into LDS, at `at` + 16 lane, by inline assembly: behind the
