@@ -471,9 +471,15 @@ def _launch(fn, dev, stream, *args):
         raise MoeError(fn, status)
 
 
+_dtypes = {}      # torch types to moe_dtype, filled on first use
+
+
 def _moe_dtype(dtype):
-    import torch
-    d = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}.get(dtype)
+    d = _dtypes.get(dtype)
+    if d is None and not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16})
+        d = _dtypes.get(dtype)
     if d is None:
         raise ValueError(f"type must be float32, bfloat16 or float16, got {dtype}")
     return d
@@ -610,10 +616,10 @@ def _rows_or_none(t, dev, dtype, shape, name):
     return (None, 0) if t is None else _rows(t, dev, dtype, shape, name)
 
 
-def _rng(rng, dev, name="rng"):
+def _rng(rng, dev):
     """Seed and offset: a device tensor of two int64 (None: no dropout)."""
     import torch
-    return None if rng is None else _dense(rng, dev, torch.int64, (2,), name)
+    return None if rng is None else _dense(rng, dev, torch.int64, (2,), "rng")
 
 
 def moe_dropout(x, p, rng, y, base=None, stream=None):
@@ -622,9 +628,10 @@ def moe_dropout(x, p, rng, y, base=None, stream=None):
     pass.  Rows dense, any pitch; y may be x or base."""
     if x.dim() != 2:
         raise ValueError(f"x must be a matrix, got shape {tuple(x.shape)}")
-    dev, dtype, (C, K) = x.get_device(), x.dtype, x.shape
-    _launch("moe_dropout", dev, stream, _moe_dtype(dtype), *_rows(x, dev, dtype, (C, K), "x"), C, K,
-            *_rows_or_none(base, dev, dtype, (C, K), "base"), *_rows(y, dev, dtype, (C, K), "y"), p,
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    C, K = shape
+    _launch("moe_dropout", dev, stream, _moe_dtype(dtype), *_rows(x, dev, dtype, shape, "x"), C, K,
+            *_rows_or_none(base, dev, dtype, shape, "base"), *_rows(y, dev, dtype, shape, "y"), p,
             _rng(rng, dev))
 
 
