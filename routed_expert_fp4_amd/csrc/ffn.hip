@@ -301,15 +301,22 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
       oa[i] = (uint32_t)(u / UA) * (uint32_t)a.a_pitch + (n < most ? n : most) * 16;
     }
   }
+  // (dx: those of the phase's matrix, whose rows may be another pitch apart)
+  bool two_now = MODE == kDx && s0 >= phase;
+  auto offsets_b = [&] {
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int u = i * WG + tid, most = (a.N * B + 15) / 16 - 1 - n0 * B / 16, n = unit_across(u, UB);
+      ob[i] = (uint32_t)(u / UB) * (uint32_t)(two_now ? a.b1_pitch : a.b0_pitch) + (n < most ? n : most) * 16;
+    }
+  };
+  if constexpr (!BL) offsets_b();
 #pragma unroll
   for (int i = 0; i < LB; ++i) {
     const int u = i * WG + tid;
     if constexpr (BL) {
       const int r = (u >> 3) & (BN / 2 - 1), most = a.N - 1 - n0;
       ob[i] = (uint32_t)(r < most ? r : most) * (uint32_t)(i < LB / 2 ? a.b0_pitch : a.b1_pitch) + unit_along(u) * 16;
-    } else {
-      const int most = (a.N * B + 15) / 16 - 1 - n0 * B / 16, n = unit_across(u, UB);
-      ob[i] = (uint32_t)(u / UB) * (uint32_t)a.b0_pitch + (n < most ? n : most) * 16;
     }
   }
   const uint8_t* a0 = (second ? a.a1 : a.a0) + (AL ? m0 * a.a_pitch : (int64_t)m0 * B);
@@ -320,8 +327,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
   auto from = [&](int s) {
     const bool two = MODE == kDx && s >= phase;
     const int k0 = (two ? s - phase : s) * E;
+    if constexpr (MODE == kDx) {
+      if (two != two_now) {
+        two_now = two;
+        offsets_b();
+      }
+    }
     return From{AL ? a0 + (two ? a.a1 - a.a0 : 0) + (int64_t)k0 * B : a0 + k0 * a.a_pitch,
-                BL ? b0 + (int64_t)k0 * B : (two ? b1 : b0) + k0 * a.b0_pitch, b1 + (int64_t)k0 * B, k0};
+                BL ? b0 + (int64_t)k0 * B : two ? b1 + k0 * a.b1_pitch : b0 + k0 * a.b0_pitch, b1 + (int64_t)k0 * B, k0};
   };
   auto stage_one = [&](const From& f, const uint8_t* to, int i) {
     if (i < LA) load_lds(f.pa, oa[i], to + (i * WG + wave * 64) * 16);
@@ -370,7 +383,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
   };
   // a quarter's products, and loads n0 .. n1 - 1 of a step to come between them: a
   // matrix instruction leaves the time for one
-  From f = from(s0 + 1);
+  From f = {};
   bool more = false;
   auto product = [&](int k, int n0, int n1, const uint8_t* to) {
     int n = n0;

@@ -142,6 +142,23 @@ def test_slices_of_wider_tensors(C, xt, pad, off):
     c.check_backward("slices")
 
 
+def test_matrices_of_different_pitches():
+    """w_gate and w_up as views of wider tensors of different widths, and the gradients
+    too."""
+    import routed_expert_fp4_amd as rf
+    for C, H, I, xt in ((5, 256, 96, "bf16"), (90, 256, 200, "f16"), (300, 512, 320, "f32"), (300, 24600, 40, "bf16")):
+        c = Case(C, H, I, xt)
+        for wide, name in ((64, "wu"), (40, "dwu"), (24, "x"), (88, "dx"), (16, "up")):
+            setattr(c, name, device(host(getattr(c, name)), c.t, wide))
+        c.block = rf.FfnBlock(c.wg, c.wu)
+        c.forward()
+        torch.cuda.synchronize()
+        c.check_forward((C, H, I, xt))
+        c.backward()
+        torch.cuda.synchronize()
+        c.check_backward((C, H, I, xt))
+
+
 def test_every_shape_of_call():
     import routed_expert_fp4_amd as rf
     for C, H, I in ((20, 256, 96), (300, 300, 400)):
