@@ -261,11 +261,12 @@ struct AArgs {
 // t = x A^T over a range of columns
 // ---------------------------------------------------------------------------
 // A workgroup has a tile's tokens, 64 ranks at most and a range of columns, of which
-// its waves take 128 bytes of every row in turn; a wave loads the next columns
-// before it multiplies the last.
+// its waves take 32 in turn; a wave loads the next columns before it multiplies the
+// last.  (64 at a time, whole lines of 16-bit rows, took more registers than two waves
+// a SIMD have: 8192 fp16 tokens x 3584, rank 64, with dropout 36 us against 28.)
 template <int DT, int NT, int TT, bool DROP>
 __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
-  constexpr int B = kBytes<DT>, T = 16 * TT, S = 2 / (B / 2), U = 32 * S;   // steps and columns of a wave's turn
+  constexpr int B = kBytes<DT>, T = 16 * TT, S = 1, U = 32 * S;   // steps and columns of a wave's turn
   __shared__ float s_red[2][T][NT * 16];
   Tile t;
   if (!plan_entry(a.plan, a.C, a.n, 3, a.at.tiles, blockIdx.x, t) || t.who < 0) return;
