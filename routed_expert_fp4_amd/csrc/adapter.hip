@@ -682,9 +682,10 @@ __global__ __launch_bounds__(kAWG, KT <= 2 ? 2 : 1) void k_aexpand(AArgs a) {
 // sums[j][col] = sum over a chunk's tokens of small[token][j] in[token][col]
 // ---------------------------------------------------------------------------
 // dA (x by u) and dB (dy by t) in one launch.  A workgroup has 128 (fp32: 64) columns
-// of a chunk; of its waves RH share the ranks, 16 NT each, and the others the tokens,
-// 32 at a time, whose rows are transposed in registers.  Up to 32 ranks eight waves,
-// two to a SIMD; above, where the sums fill half the registers, four.
+// of a chunk; of its eight waves RH share the ranks, 16 NT each (32 at most: two waves
+// to a SIMD), and the others the tokens, 32 at a time, whose rows are transposed in
+// registers.  (Four waves with 64 ranks each, which read and drop x once and not
+// twice: 8192 fp16 tokens, rank 64, 122 us against 109.)
 // u and t are needed by every workgroup of a chunk: k_apieces lays them out once as
 // the first operand, [32 tokens][16 ranks][piece][lane], three bf16 pieces, or the
 // two halves of eight fp32.
@@ -751,9 +752,10 @@ __global__ __launch_bounds__(256) void k_apieces(OArgs a) {
   }
 }
 
-template <int DT, int NT, int RH, int WAVES, bool DROP>
-__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
-  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, TG = WAVES / RH, R = 16 * NT, P = kParts<DT>;
+constexpr int kOWaves = 8;
+template <int DT, int NT, int RH, bool DROP>
+__global__ __launch_bounds__(64 * kOWaves, 2) void k_aouter(OArgs a) {
+  constexpr int B = kBytes<DT>, NTL = kTiles<DT>, W = 16 * NTL, TG = kOWaves / RH, R = 16 * NT, P = kParts<DT>;
   extern __shared__ __align__(16) uint8_t s_o[];
   int* s_token = reinterpret_cast<int*>(s_o);                       // [2048], then the sums
   float* s_red = reinterpret_cast<float*>(s_o);                     // [TG / 2][RH][R][W + 4]
@@ -770,7 +772,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
   if constexpr (DROP) ctr = counter_of(a.drop.rng);
   // the tokens, the last again behind it up to whole steps
   const int steps = (t.count + 31) / 32;
-  for (int i = tid; i < 32 * steps; i += 64 * WAVES) s_token[i] = a.plan[a.at.perm + t.first + (i < t.count ? i : t.count - 1)];
+  for (int i = tid; i < 32 * steps; i += 64 * kOWaves) s_token[i] = a.plan[a.at.perm + t.first + (i < t.count ? i : t.count - 1)];
   __syncthreads();
   float4v acc[NT][NTL];
 #pragma unroll
@@ -778,7 +780,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
 #pragma unroll
     for (int j = 0; j < NTL; ++j) acc[i][j] = float4v(0.0f);
   const uint4v* small = reinterpret_cast<const uint4v*>(o.pieces) + step_place(t, blockIdx.y, 0) * tiles * P * 64;
-  struct Turn { uint4v g[8], m[NT][P]; };
+  struct Turn { uint4v g[8]; };
+  uint4v m[NT][P];
   auto load = [&](int s, Turn& u) {
     const uint8_t* p[8];
 #pragma unroll
@@ -790,12 +793,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) u.g[i] = load16_some<DT>(p[i], left);
     }
+  };
+  // (loaded as they are needed: a step ahead they take the registers of a second wave)
+  auto small_of = [&](int s) {
     // (tiles past the last: the last again, whose sums are not used)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int k = r0 / 16 + j < tiles ? r0 / 16 + j : tiles - 1;
 #pragma unroll
-      for (int q = 0; q < P; ++q) u.m[j][q] = small[((int64_t)s * tiles + k) * (P * 64) + 64 * q + lane];
+      for (int q = 0; q < P; ++q) m[j][q] = small[((int64_t)s * tiles + k) * (P * 64) + 64 * q + lane];
     }
   };
   auto multiply = [&](int s, Turn& u) {
@@ -815,7 +821,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
         for (int i = 0; i < NTL; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(u.m[j][e >> 2][e & 3]), __uint_as_float(u.g[e][i]),
+            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(m[j][e >> 2][e & 3]), __uint_as_float(u.g[e][i]),
                                                              acc[j][i], 0, 0, 0);
     } else {
       uint4v f[8];
@@ -825,7 +831,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
         uint4v b[kPieces<DT>];
         pieces<DT>(f[i], b);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][i] = mma_pieces<DT>(u.m[j], b, acc[j][i]);
+        for (int j = 0; j < NT; ++j) acc[j][i] = mma_pieces<DT>(m[j], b, acc[j][i]);
       }
     }
   };
@@ -833,11 +839,13 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void k_aouter(OArgs a) {
   Turn even, odd;
   if (tg < steps) load(tg, even);
   for (int s = tg; s < steps; s += 2 * TG) {
+    small_of(s);
     if (s + TG < steps) load(s + TG, odd);
     __builtin_amdgcn_sched_barrier(0);
     multiply(s, even);
     __builtin_amdgcn_sched_barrier(0);
     if (s + TG >= steps) break;
+    small_of(s + TG);
     if (s + 2 * TG < steps) load(s + 2 * TG, even);
     __builtin_amdgcn_sched_barrier(0);
     multiply(s + TG, odd);
@@ -1073,22 +1081,22 @@ void launch_expand(AArgs a, int tiles, hipStream_t st) {
   else hipLaunchKernelGGL((k_aexpand<DT, 4, BWD, DROP>), grid, dim3(kAWG), lds, st, a);
 }
 
-template <int DT, int NT, int RH, int WAVES, bool DROP>
+template <int DT, int NT, int RH, bool DROP>
 moe_status launch_outer_t(const OArgs& a, int chunks, hipStream_t st) {
-  constexpr int W = 16 * kTiles<DT>, sums = WAVES / 2 * 16 * NT * (W + 4) * 4, lds = sums > 8192 ? sums : 8192;
-  auto k = k_aouter<DT, NT, RH, WAVES, DROP>;
+  constexpr int W = 16 * kTiles<DT>, sums = kOWaves / 2 * 16 * NT * (W + 4) * 4, lds = sums > 8192 ? sums : 8192;
+  auto k = k_aouter<DT, NT, RH, DROP>;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          lds) != hipSuccess)
     return MOE_ERR_DEVICE;
-  hipLaunchKernelGGL(k, dim3((unsigned)(a.da.blocks + a.db.blocks), (unsigned)chunks), dim3(64 * WAVES), lds, st, a);
+  hipLaunchKernelGGL(k, dim3((unsigned)(a.da.blocks + a.db.blocks), (unsigned)chunks), dim3(64 * kOWaves), lds, st, a);
   return MOE_OK;
 }
 template <int DT, bool DROP>
 moe_status launch_outer(const OArgs& a, int chunks, hipStream_t st) {
-  if (a.r <= 16) return launch_outer_t<DT, 1, 1, 8, DROP>(a, chunks, st);
-  if (a.r <= 32) return launch_outer_t<DT, 2, 1, 8, DROP>(a, chunks, st);
-  if (a.r <= 64) return launch_outer_t<DT, 4, 1, 4, DROP>(a, chunks, st);
-  return launch_outer_t<DT, 4, 2, 4, DROP>(a, chunks, st);
+  if (a.r <= 16) return launch_outer_t<DT, 1, 1, DROP>(a, chunks, st);
+  if (a.r <= 32) return launch_outer_t<DT, 2, 1, DROP>(a, chunks, st);
+  if (a.r <= 64) return launch_outer_t<DT, 2, 2, DROP>(a, chunks, st);
+  return launch_outer_t<DT, 2, 4, DROP>(a, chunks, st);
 }
 
 // fn(dtype constant)
