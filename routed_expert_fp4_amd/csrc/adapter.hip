@@ -461,6 +461,15 @@ __global__ __launch_bounds__(kAWG, KT <= 2 ? 2 : 1) void k_aexpand(AArgs a) {
 #pragma unroll
           for (int i = 0; i < NTL; ++i) f[k][i] = load8<DT>(j0 < a.r ? column(i) + j0 * B : zeros);
         }
+      } else if (c0 + W + 7 <= a.cols) {
+        // what a load takes behind a row's end, seven elements at most, lies in the matrix:
+        // seven rows of one element at least follow these columns'
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          const int j0 = 32 * k + 8 * quarter;
+#pragma unroll
+          for (int i = 0; i < NTL; ++i) f[k][i] = load8_first<DT>(j0 < a.r ? column(i) + j0 * B : zeros, a.r - j0);
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < KT; ++k) {

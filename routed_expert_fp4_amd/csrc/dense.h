@@ -33,17 +33,35 @@ __device__ __forceinline__ Eight<DT> load8(const void* p) {
   if constexpr (DT == MOE_DT_F32) e.v[1] = load16(static_cast<const uint8_t*>(p) + 16);
   return e;
 }
-// the first `n` of them (n may be 0 or less, or more than 8), zeros for the others
+// the first `n` of them (n may be 0 or less, or more than 8), zeros for the others:
+// one by one from the last, in a loop that stays one (unrolled at every use, it was
+// most of the kernels' code)
 template <int DT>
 __device__ __forceinline__ Eight<DT> load8_some(const void* p, int n) {
   if (n >= 8) return load8<DT>(p);
   Eight<DT> e = {};
+#pragma unroll 1
+  for (int i = n - 1; i >= 0; --i) {
+    if constexpr (DT == MOE_DT_F32) {
+#pragma unroll
+      for (int k = 7; k > 0; --k) e.v[k >> 2][k & 3] = e.v[(k - 1) >> 2][(k - 1) & 3];
+      e.v[0][0] = static_cast<const uint32_t*>(p)[i];
+    } else {
+#pragma unroll
+      for (int k = 3; k > 0; --k) e.v[0][k] = (e.v[0][k] << 16) | (e.v[0][k - 1] >> 16);
+      e.v[0][0] = (e.v[0][0] << 16) | static_cast<const uint16_t*>(p)[i];
+    }
+  }
+  return e;
+}
+// The same by one load, for n >= 0 and where eight elements may be read.
+template <int DT>
+__device__ __forceinline__ Eight<DT> load8_first(const void* p, int n) {
+  Eight<DT> e = load8<DT>(p);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (i < n) {
-      if constexpr (DT == MOE_DT_F32) e.v[i >> 2][i & 3] = static_cast<const uint32_t*>(p)[i];
-      else e.v[0][i >> 1] |= (uint32_t)static_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-    }
+    if constexpr (DT == MOE_DT_F32) e.v[i >> 2][i & 3] = i < n ? e.v[i >> 2][i & 3] : 0u;
+    else if (!(i & 1)) e.v[0][i >> 1] &= (i < n ? 0xFFFFu : 0u) | (i + 1 < n ? 0xFFFF0000u : 0u);
   }
   return e;
 }
@@ -115,20 +133,27 @@ template <int DT>
 __device__ __forceinline__ uint4v load16_some(const void* p, int n) {
   if constexpr (DT != MOE_DT_F32) return load8_some<DT>(p, n).v[0];
   uint4v v = uint4v(0u);
+#pragma unroll 1
+  for (int i = (n < 4 ? n : 4) - 1; i >= 0; --i) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) v[i] = static_cast<const uint32_t*>(p)[i];
+    for (int k = 3; k > 0; --k) v[k] = v[k - 1];
+    v[0] = static_cast<const uint32_t*>(p)[i];
+  }
   return v;
 }
 template <int DT>
 __device__ __forceinline__ void store16_some(void* p, uint4v v, int n) {
-  constexpr int N = 16 / kBytes<DT>;
-  if (n >= N) { store16(p, v); return; }
+  if (n >= 16 / kBytes<DT>) { store16(p, v); return; }
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    if constexpr (DT == MOE_DT_F32) {
+      static_cast<uint32_t*>(p)[i] = v[0];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i < n) {
-      if constexpr (DT == MOE_DT_F32) static_cast<uint32_t*>(p)[i] = v[i];
-      else static_cast<uint16_t*>(p)[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+      for (int k = 0; k < 3; ++k) v[k] = v[k + 1];
+    } else {
+      static_cast<uint16_t*>(p)[i] = (uint16_t)v[0];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = (v[k] >> 16) | (k < 3 ? v[k + 1] << 16 : 0u);
     }
   }
 }
