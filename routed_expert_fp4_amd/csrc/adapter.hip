@@ -327,11 +327,11 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
   if (whole < c1 && (whole - c0) / U % 4 == wave) {
     // a row's last columns, zeros behind them
     for (int q = 0; q < S && whole + 32 * q < c1; ++q) {
-      const int k = whole + 32 * q, n = c1 - k - 8 * quarter;
+      const int k = whole + 32 * q;
 #pragma unroll
-      for (int i = 0; i < TT; ++i) u.x[0][i] = load8_some<DT>(xr[i] + (int64_t)k * B, n);
+      for (int i = 0; i < TT; ++i) u.x[0][i] = load8_of<DT>(xr[i] - 8 * quarter * B, k + 8 * quarter, c1);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) u.w[0][j] = load8_some<DT>(ar[j] + (int64_t)k * B, n);
+      for (int j = 0; j < NT; ++j) u.w[0][j] = load8_of<DT>(ar[j] - 8 * quarter * B, k + 8 * quarter, c1);
       multiply(k, u, 0);
     }
   }
@@ -461,6 +461,11 @@ __global__ __launch_bounds__(kAWG, KT <= 2 ? 2 : 1) void k_aexpand(AArgs a) {
 #pragma unroll
           for (int i = 0; i < NTL; ++i) f[k][i] = load8<DT>(j0 < a.r ? column(i) + j0 * B : zeros);
         }
+      } else if (a.r > 8) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int i = 0; i < NTL; ++i) f[k][i] = load8_of<DT>(column(i), 32 * k + 8 * quarter, a.r);
       } else if (c0 + W + 7 <= a.cols) {
         // what a load takes behind a row's end, seven elements at most, lies in the matrix:
         // seven rows of one element at least follow these columns'
@@ -495,7 +500,7 @@ __global__ __launch_bounds__(kAWG, KT <= 2 ? 2 : 1) void k_aexpand(AArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int j = 32 * k + 8 * quarter + i;
-            g[k][i] = load16_some<DT>(rank(j), j < a.r ? a.cols - c : 0);
+            g[k][i] = load16_of<DT>(w + (j < a.r ? j : a.r - 1) * a.w_pitch, j < a.r ? c : a.cols, a.cols);
           }
       }
 #pragma unroll
@@ -526,7 +531,7 @@ __global__ __launch_bounds__(kAWG, KT <= 2 ? 2 : 1) void k_aexpand(AArgs a) {
       for (int e = 0; e < 4; ++e) next[e] = load16(a.base + token[e] * a.base_pitch + (int64_t)c * B);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) next[e] = load16_some<DT>(a.base + token[e] * a.base_pitch + (int64_t)c * B, a.cols - c);
+      for (int e = 0; e < 4; ++e) next[e] = load16_of<DT>(a.base + token[e] * a.base_pitch, c, a.cols);
     }
   };
   if (a.base && c0 < a.cols) {
@@ -800,7 +805,7 @@ __global__ __launch_bounds__(64 * kOWaves, 2) void k_aouter(OArgs a) {
       for (int i = 0; i < 8; ++i) u.g[i] = load16(p[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.g[i] = load16_some<DT>(p[i], left);
+      for (int i = 0; i < 8; ++i) u.g[i] = load16_of<DT>(p[i] - (int64_t)c * B, c, o.cols);
     }
   };
   // (loaded as they are needed: a step ahead they take the registers of a second wave)
@@ -987,7 +992,7 @@ __global__ __launch_bounds__(256) void k_aturn(TArgs a) {
   const uint8_t* b = a.b + who * a.b_stride + n * a.b_pitch;
   E* o = reinterpret_cast<E*>(a.out + who * a.out_stride) + n;
   for (int j = 8 * wave; j < a.r; j += 32) {
-    const Eight<DT> v = load8_some<DT>(b + j * B, a.r - j);
+    const Eight<DT> v = load8_of<DT>(b, j, a.r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (j + i >= a.r) break;

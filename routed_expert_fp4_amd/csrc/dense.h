@@ -128,18 +128,47 @@ __device__ __forceinline__ uint4v pack16(const float (&f)[N]) {
   }
   return v;
 }
-// the first n of 16 bytes' elements, zeros for the others
+// Elements k .. k + 7 of a row of `cols`, zeros behind its end: the load ends with
+// the row, and what came too early is shifted out.  No element outside the row is
+// read, and lanes at a row's end load like the others.
 template <int DT>
-__device__ __forceinline__ uint4v load16_some(const void* p, int n) {
-  if constexpr (DT != MOE_DT_F32) return load8_some<DT>(p, n).v[0];
-  uint4v v = uint4v(0u);
-#pragma unroll 1
-  for (int i = (n < 4 ? n : 4) - 1; i >= 0; --i) {
+__device__ __forceinline__ Eight<DT> load8_of(const uint8_t* row, int k, int cols) {
+  if (cols < 8) return load8_some<DT>(row + (int64_t)k * kBytes<DT>, cols - k);
+  const int over = k + 8 - cols, s = over < 0 ? 0 : over > 8 ? 8 : over;   // elements to shift out
+  Eight<DT> e = load8<DT>(row + (int64_t)(k + 8 < cols ? k : cols - 8) * kBytes<DT>);
+  constexpr int N = DT == MOE_DT_F32 ? 8 : 4;                              // words
+  uint32_t w[N];
 #pragma unroll
-    for (int k = 3; k > 0; --k) v[k] = v[k - 1];
-    v[0] = static_cast<const uint32_t*>(p)[i];
+  for (int i = 0; i < N; ++i) w[i] = e.v[i >> 2][i & 3];
+#pragma unroll
+  for (int b = N / 2; b >= 1; b /= 2) {                                    // by b words
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = s & (DT == MOE_DT_F32 ? b : 2 * b) ? (i + b < N ? w[i + b] : 0u) : w[i];
   }
-  return v;
+  if constexpr (DT != MOE_DT_F32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = s & 1 ? (w[i] >> 16) | (i + 1 < N ? w[i + 1] << 16 : 0u) : w[i];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) e.v[i >> 2][i & 3] = s >= 8 ? 0u : w[i];
+  return e;
+}
+// load8_of of 16 bytes: eight elements of 16 bits, four of fp32.
+template <int DT>
+__device__ __forceinline__ uint4v load16_of(const uint8_t* row, int k, int cols) {
+  if constexpr (DT != MOE_DT_F32) return load8_of<DT>(row, k, cols).v[0];
+  uint4v w = uint4v(0u);
+  if (cols < 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k + i < cols) w[i] = reinterpret_cast<const uint32_t*>(row)[k + i];
+    return w;
+  }
+  const int over = k + 4 - cols, s = over < 0 ? 0 : over > 4 ? 4 : over;
+  w = load16(row + (int64_t)(k + 4 < cols ? k : cols - 4) * 4);
+  if (s & 2) w = uint4v{w[2], w[3], 0u, 0u};
+  if (s & 1) w = uint4v{w[1], w[2], w[3], 0u};
+  return s >= 4 ? uint4v(0u) : w;
 }
 template <int DT>
 __device__ __forceinline__ void store16_some(void* p, uint4v v, int n) {

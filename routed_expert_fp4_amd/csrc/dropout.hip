@@ -32,9 +32,15 @@ __global__ __launch_bounds__(256) void k_dropout(DArgs a) {
     const int64_t c = i / a.blocks;
     const int k = 8 * (int)(i - c * a.blocks);
     float v[8];
-    const Eight<DT> x = load8_some<DT>(a.x + c * a.x_pitch + (int64_t)k * B, a.K - k);
-    Eight<DT> b = {};
-    if constexpr (BASE) b = load8_some<DT>(a.base + c * a.base_pitch + (int64_t)k * B, a.K - k);
+    const uint8_t *px = a.x + c * a.x_pitch, *pb = a.base + c * a.base_pitch;
+    Eight<DT> x, b = {};
+    if (a.K % 8 == 0) {                 // one branch for both, which are then on their way together
+      x = load8<DT>(px + (int64_t)k * B);
+      if constexpr (BASE) b = load8<DT>(pb + (int64_t)k * B);
+    } else {
+      x = load8_of<DT>(px, k, a.K);
+      if constexpr (BASE) b = load8_of<DT>(pb, k, a.K);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = get8<DT>(x, j);
     if constexpr (DROP) drop8f(v, a.drop, ctr, k, (uint32_t)c);

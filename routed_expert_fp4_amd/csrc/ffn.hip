@@ -153,9 +153,9 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
   if (whole < a.H && whole / U % kFewWaves == wave) {
     // a row's last columns, zeros behind them
     for (int k = whole + 8 * quarter, q = 0; q < S && whole + 32 * q < a.H; ++q, k += 32) {
-      const Eight<DT> e = load8_some<DT>(w + (int64_t)k * B, a.H - k);
+      const Eight<DT> e = load8_of<DT>(w, k, a.H);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) acc[t] = mma8<DT>(e, load8_some<DT>(x[t] + (int64_t)k * B, a.H - k), acc[t]);
+      for (int t = 0; t < TT; ++t) acc[t] = mma8<DT>(e, load8_of<DT>(x[t], k, a.H), acc[t]);
     }
   }
 #pragma unroll
@@ -563,9 +563,17 @@ __global__ __launch_bounds__(256) void k_fact(GArgs a) {
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
     const int64_t c = e / a.units;
     const int i = 8 * (int)(e - c * a.units);
-    const Eight<DT> g = load8_some<DT>(a.gate + c * a.gate_pitch + (int64_t)i * B, a.I - i);
-    const Eight<DT> u = load8_some<DT>(a.up + c * a.up_pitch + (int64_t)i * B, a.I - i);
-    const Eight<DT> d = load8_some<DT>(a.dh + c * a.dh_pitch + (int64_t)i * B, a.I - i);
+    const uint8_t *pg = a.gate + c * a.gate_pitch, *pu = a.up + c * a.up_pitch, *pd = a.dh + c * a.dh_pitch;
+    Eight<DT> g, u, d;
+    if (a.I % 8 == 0) {                 // one branch for the three, which are then on their way together
+      g = load8<DT>(pg + (int64_t)i * B);
+      u = load8<DT>(pu + (int64_t)i * B);
+      d = load8<DT>(pd + (int64_t)i * B);
+    } else {
+      g = load8_of<DT>(pg, i, a.I);
+      u = load8_of<DT>(pu, i, a.I);
+      d = load8_of<DT>(pd, i, a.I);
+    }
     float dg[8], du[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -598,7 +606,7 @@ __global__ __launch_bounds__(256) void k_fpack(KArgs a) {
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
     const int64_t r = e / a.units;
     const int k = 8 * (int)(e - r * a.units);
-    store8<DT>(p.out + e * 8 * B, load8_some<DT>(p.in + r * p.in_pitch + (int64_t)k * B, a.cols - k));
+    store8<DT>(p.out + e * 8 * B, load8_of<DT>(p.in + r * p.in_pitch, k, a.cols));
   }
 }
 
