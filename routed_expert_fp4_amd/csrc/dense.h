@@ -65,8 +65,6 @@ __device__ __forceinline__ Eight<DT> load8_first(const void* p, int n) {
   }
   return e;
 }
-template <int DT>
-__device__ __forceinline__ Eight<DT> zero8() { return Eight<DT>{}; }
 
 template <int DT>
 __device__ __forceinline__ float get8(const Eight<DT>& e, int i) {

@@ -99,6 +99,9 @@ __device__ __forceinline__ void put_gated(const FArgs& a, int c, int i, float g,
   }
 }
 
+// Bound by the weights' stream: one bf16 token x 7168 x 1536 9.8 us for 44 MB (4.5 TB/s,
+// the launch included), 16 tokens x 7168 x 4096 27.2 for 117 (4.3).  Eight rows of each
+// matrix are a 16-row operand; sixteen of each would leave half the workgroups.
 constexpr int kFewWG = 512, kFewWaves = kFewWG / 64;
 template <int DT, int TT>
 __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
@@ -189,6 +192,10 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
 // has that many of its rows in LDS, units exchanged too, and is read with the
 // transposing LDS loads; fp32 is read element by element.  Both are loaded into LDS
 // directly, one step ahead.
+// First launches in bf16 x 7168 x 4096: 2048 tokens 200 us (1.2 PFLOP/s), matrix cores
+// busy for 60% of the cycles; 4096 tokens' dx 449 and weights' gradients 448 (1.07), 53%.
+// A copy of the forward case as it was at 203 us took 173 without loads into LDS, 170
+// without LDS reads and 140 without both: each costs about as much beside the other.
 enum { kFwd, kDx, kDw };
 
 // 16 bytes a lane into LDS, at `at` + 16 lane, by inline assembly: behind the
@@ -555,7 +562,8 @@ struct GArgs {
   int64_t pitch;
   int units;
 };
-// past the last column zeros: the sum over I runs on whole units
+// past the last column zeros: the sum over I runs on whole units.  Bound by memory: 4096 x
+// 4096 in bf16 31.6 us for 168 MB (5.3 TB/s).
 template <int DT>
 __global__ __launch_bounds__(256) void k_fact(GArgs a) {
   constexpr int B = kBytes<DT>;
