@@ -532,7 +532,10 @@ moe_status moe_ffn_fwd(const moe_ffn *f, const void *x, int64_t x_pitch, int32_t
                        int64_t up_pitch, void *ws, size_t ws_bytes, void *stream);
 
 /* Its gradients for dh [C][dh_pitch], from gate and up as the forward pass wrote them:
- *   du = dh act(g), dg = dh u act'(g)    formed in fp32, rounded to the type
+ *   du = dh act(g), dg = dh u act'(g)    formed in fp32, then held as two terms of the
+ *                                        type (fp32: one): to 2^-17 of a value in bf16; in
+ *                                        fp16 to 2^-23, or to 2^-39 of the call's largest
+ *                                        finite one, and of any size
  *   dx = dg w_gate + du w_up             [C][dx_pitch], of the type
  *   dw_gate = dg^T x, dw_up = du^T x     [inter][..pitch], of grad_dtype: the type, or
  *                                        MOE_DT_F32

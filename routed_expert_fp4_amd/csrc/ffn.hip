@@ -5,8 +5,9 @@
 //   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x                      (backward)
 //
 // act is SiLU, g sigmoid(g), or GELU's tanh form, g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3)).
-// Sums are fp32; h is formed of them and rounded once, and dg and du are rounded
-// to the tensors' type before they meet the matrix cores again.
+// Sums are fp32; h is formed of them and rounded once.  dg and du of 16-bit tensors
+// meet the matrix cores again in two terms of that type, so that a gradient carries
+// the rounding of its result and no other that counts.
 //
 // Kernels:
 //   k_ffew      up to 32 tokens: bound by the stream of both weight matrices;
@@ -15,7 +16,8 @@
 //               tiled matrix product, whose operands lie along the sum's axis or
 //               across it; g and u of the same rows and tokens are in the same lane
 //   k_fjoin     adds ranges of the sum's axis, where tiles alone are too few
-//   k_fact      dg and du
+//   k_fact      dg and du as operands; in fp16 under a power of two, for which
+//               k_fmost finds their largest
 //   k_fpack     tensors whose rows are not at multiples of 16 bytes, into ones
 //               that are
 #include <hip/hip_bf16.h>
@@ -71,6 +73,7 @@ struct FArgs {
   int64_t o0_pitch, o1_pitch;
   int accumulate, out_f32;
   float* part;                                            // [splits][M][N] fp32
+  const float* unscale;                                   // fp16 gradients: undoes dg's and du's power of two
 };
 
 // ---------------------------------------------------------------------------
@@ -192,11 +195,23 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
 // has that many of its rows in LDS, units exchanged too, and is read with the
 // transposing LDS loads; fp32 is read element by element.  Both are loaded into LDS
 // directly, one step ahead.
+// dg and du in 16 bits are two terms (hi, then lo) by turns of 32 elements of a row: a
+// step is 128 bytes of 32 positions, quarters hi and lo of one 16, then of the other, and
+// the second operand's fragments, half as many, serve both.
 // First launches in bf16 x 7168 x 4096: 2048 tokens 200 us (1.2 PFLOP/s), matrix cores
-// busy for 60% of the cycles; 4096 tokens' dx 449 and weights' gradients 448 (1.07), 53%.
+// busy for 60% of the cycles; 4096 tokens' dx 772 and weights' gradients 777, 1.25 PFLOP/s
+// of both terms (in one term, rounded to the type, 449 and 448).
 // A copy of the forward case as it was at 203 us took 173 without loads into LDS, 170
 // without LDS reads and 140 without both: each costs about as much beside the other.
 enum { kFwd, kDx, kDw };
+template <int DT, int MODE>
+constexpr int kTerms = DT != MOE_DT_F32 && MODE != kFwd ? 2 : 1;
+// two stages, or the results
+template <int DT, int MODE, int BM, int BN>
+constexpr int kGemmLds = [] {
+  constexpr int stages = 2 * (BM * 128 + BN * 128 / kTerms<DT, MODE>), results = BM * ((MODE == kFwd ? BN / 2 : BN) * 2 + 16);
+  return DT == MOE_DT_F32 || stages > results ? stages : results;
+}();
 
 // 16 bytes a lane into LDS, at `at` + 16 lane, by inline assembly: behind the
 // compiler's own form it lets every transposing LDS read wait for all of them.  They
@@ -268,10 +283,11 @@ __device__ __forceinline__ uint4v fragment(const uint8_t* s, int m, int ks, int 
 
 template <int DT, int MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
-  constexpr int B = kBytes<DT>, WG = 64 * WM * WN, E = 128 / B;      // elements of a step
+  constexpr int TERMS = kTerms<DT, MODE>;
+  constexpr int B = kBytes<DT>, WG = 64 * WM * WN, E = 128 / B / TERMS;   // positions of a step
   constexpr bool AL = MODE != kDw, BL = MODE == kFwd;                // rows along the sum's axis
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32, NH = NT / 2;   // row and column tiles of a wave
-  constexpr int kA = BM * 128, kB = BN * 128, kStage = kA + kB;
+  constexpr int kA = BM * 128, kB = BN * 128 / TERMS, kStage = kA + kB;
   constexpr int LA = kA / 16 / WG, LB = kB / 16 / WG;
   extern __shared__ __align__(1024) uint8_t s_ab[];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -305,7 +321,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
       oa[i] = (uint32_t)((r < most ? r : most) * (uint32_t)a.a_pitch + unit_along(u) * 16);
     } else {
       const int most = (a.M * B + 15) / 16 - 1 - m0 * B / 16, n = unit_across(u, UA);
-      oa[i] = (uint32_t)(u / UA) * (uint32_t)a.a_pitch + (n < most ? n : most) * 16;
+      const int w = n < most ? n : most, r = u / UA;
+      oa[i] = (uint32_t)(r % E) * (uint32_t)a.a_pitch + (TERMS == 2 ? (w >> 2) * 128 + r / E * 64 + (w & 3) * 16 : w * 16);
     }
   }
   // (dx: those of the phase's matrix, whose rows may be another pitch apart)
@@ -326,7 +343,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
       ob[i] = (uint32_t)(r < most ? r : most) * (uint32_t)(i < LB / 2 ? a.b0_pitch : a.b1_pitch) + unit_along(u) * 16;
     }
   }
-  const uint8_t* a0 = (second ? a.a1 : a.a0) + (AL ? m0 * a.a_pitch : (int64_t)m0 * B);
+  const uint8_t* a0 = (second ? a.a1 : a.a0) + (AL ? m0 * a.a_pitch : (int64_t)m0 * (B * TERMS));
   const uint8_t* b0 = a.b0 + (BL ? n0 * a.b0_pitch : (int64_t)n0 * B);
   const uint8_t* b1 = MODE == kFwd ? a.b1 + n0 * a.b1_pitch : a.b1 + (int64_t)n0 * B;
   // where a step's operands lie
@@ -340,7 +357,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
         offsets_b();
       }
     }
-    return From{AL ? a0 + (two ? a.a1 - a.a0 : 0) + (int64_t)k0 * B : a0 + k0 * a.a_pitch,
+    return From{AL ? a0 + (two ? a.a1 - a.a0 : 0) + (int64_t)k0 * (B * TERMS) : a0 + k0 * a.a_pitch,
                 BL ? b0 + (int64_t)k0 * B : two ? b1 + k0 * a.b1_pitch : b0 + k0 * a.b0_pitch, b1 + (int64_t)k0 * B, k0};
   };
   auto stage_one = [&](const From& f, const uint8_t* to, int i) {
@@ -354,14 +371,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
 #pragma unroll
       for (int i = 0; i < LA + LB; ++i) stage_one(f, to, i);
     } else {
-      // zeros past the sum's end
+      // zeros past the sum's end (rows of two terms hold them themselves)
       auto load = [&](const uint8_t* base, uint32_t off, bool ok, const uint8_t* at) {
         load_lds(ok ? base + off : reinterpret_cast<const uint8_t*>(kZeros), at);
       };
 #pragma unroll
       for (int i = 0; i < LA; ++i) {
         const int u = i * WG + tid;
-        load(f.pa, oa[i], k0 + (AL ? unit_along(u) * (16 / B) : u / UA) < a.K, to + (i * WG + wave * 64) * 16);
+        load(f.pa, oa[i], k0 + (!AL ? u / UA % E : TERMS == 2 ? 0 : unit_along(u) * (16 / B)) < a.K, to + (i * WG + wave * 64) * 16);
       }
 #pragma unroll
       for (int i = 0; i < LB; ++i) {
@@ -382,11 +399,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
     return MODE == kFwd ? 32 * (NH * wn + j % NH) + (j / NH) * (BN / 2) : 32 * (NT * wn + j);
   };
   uint4v fa[2][MT], fb[2][NT];
+  auto second_of = [](int k) { return TERMS == 2 ? k >> 1 : k; };    // quarter k's of the second operand
   auto read = [&](const uint8_t* t, int k) {
+    if (TERMS == 1 || !(k & 1)) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) fb[k & 1][j] = fragment<DT, BL, BN>(t + kA, column(j), k, lane);
+      for (int j = 0; j < NT; ++j) fb[second_of(k) & 1][j] = fragment<DT, BL, BN>(t + kA, column(j), second_of(k), lane);
+    }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) fa[k & 1][i] = fragment<DT, AL, BM>(t, wm * (BM / WM) + 32 * i, k, lane);
+    for (int i = 0; i < MT; ++i)
+      fa[k & 1][i] = fragment<DT, AL, BM>(t, wm * (BM / WM) + 32 * i, TERMS == 2 ? 2 * (k & 1) + (k >> 1) : k, lane);
   };
   // a quarter's products, and loads n0 .. n1 - 1 of a step to come between them: a
   // matrix instruction leaves the time for one
@@ -398,7 +419,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        acc[i][j] = mma32<DT>(fa[k & 1][i], fb[k & 1][j], acc[i][j]);
+        acc[i][j] = mma32<DT>(fa[k & 1][i], fb[second_of(k) & 1][j], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
         const int upto = n0 + (n1 - n0) * (i * NT + j + 1) / (MT * NT);
 #pragma unroll
@@ -418,7 +439,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
   // the move to the next step comes before the last quarter's products, so that
   // they cover it: by then this step is read, and its buffer is free for the step
   // after the next, whose loads go out between those products (spread over three
-  // quarters they came too late: 4096 tokens x 7168 x 4096, dx 473 us against 430).
+  // quarters they came too late: 4096 tokens x 7168 x 4096, dx of one term 473 us against 430).
   stage(s0, s_ab);
   meet();
   read(s_ab, 0);
@@ -449,6 +470,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
     buf ^= 1;
   }
 
+  if constexpr (DT == MOE_DT_F16 && TERMS == 2) {
+    const float un = *a.unscale;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] *= un;
+  }
   // register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
   auto row_of = [&](int i, int r) { return wm * (BM / WM) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); };
   if constexpr (B == 2) {
@@ -456,7 +484,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_fgemm(FArgs a) {
       // The results through LDS, so that rows are stored 16 bytes a lane: as they lie
       // in registers a store holds 64 bytes of two rows.  Forward: h, then g and u.
       constexpr int WN0 = MODE == kFwd ? BN / 2 : BN, kPitch = WN0 * 2 + 16;   // bytes of a row; 16 more spread the banks
-      static_assert(BM * kPitch <= 2 * kStage + BM * 16, "the results fit the LDS");
+      static_assert(BM * kPitch <= kGemmLds<DT, MODE, BM, BN> && 2 * kStage <= kGemmLds<DT, MODE, BM, BN>, "the results fit the LDS");
       auto through = [&](uint8_t* out, int64_t pitch, auto value) {
         __syncthreads();
 #pragma unroll
@@ -553,46 +581,118 @@ __global__ __launch_bounds__(256) void k_fjoin(FArgs a) {
 // ---------------------------------------------------------------------------
 // dg and du, and packing
 // ---------------------------------------------------------------------------
+constexpr int kMostParts = 256;
 struct GArgs {
   int C, I;
   Act act;
   const uint8_t *gate, *up, *dh;
   int64_t gate_pitch, up_pitch, dh_pitch;
-  uint8_t *dg, *du;                                       // rows of `units` eights
+  uint8_t *dg, *du;                                       // rows of `units` eights, in 16 bits of two terms
   int64_t pitch;
   int units;
+  float* most;                                            // fp16: [kMostParts], then what undoes the scale
+  int parts;
 };
-// past the last column zeros: the sum over I runs on whole units.  Bound by memory: 4096 x
-// 4096 in bf16 31.6 us for 168 MB (5.3 TB/s).
+// Columns i .. i + 7 of a token's dg and du, zeros past the last.
+template <int DT>
+__device__ __forceinline__ void gate_grads(const GArgs& a, int64_t c, int i, float (&dg)[8], float (&du)[8]) {
+  constexpr int B = kBytes<DT>;
+  const uint8_t *pg = a.gate + c * a.gate_pitch, *pu = a.up + c * a.up_pitch, *pd = a.dh + c * a.dh_pitch;
+  Eight<DT> g, u, d;
+  if (a.units * 8 == a.I) {             // one branch for the three, which are then on their way together
+    g = load8<DT>(pg + (int64_t)i * B);
+    u = load8<DT>(pu + (int64_t)i * B);
+    d = load8<DT>(pd + (int64_t)i * B);
+  } else {
+    g = load8_of<DT>(pg, i, a.I);
+    u = load8_of<DT>(pu, i, a.I);
+    d = load8_of<DT>(pd, i, a.I);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float act, slope;
+    act_slope(a.act, get8<DT>(g, j), act, slope);
+    const float t = get8<DT>(d, j);
+    du[j] = t * act;
+    dg[j] = t * get8<DT>(u, j) * slope;
+  }
+}
+
+// The largest finite magnitude of dg and du (fp16), a part of them to a workgroup.
+__device__ __forceinline__ uint32_t most_of(uint32_t v, uint32_t* s) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, d, 64);
+    v = o > v ? o : v;
+  }
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) v = s[w] > v ? s[w] : v;
+  return v;
+}
+__global__ __launch_bounds__(256) void k_fmost(GArgs a) {
+  __shared__ uint32_t s_most[4];
+  const int64_t n = (int64_t)a.C * a.units;
+  uint32_t most = 0;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    const int64_t c = e / a.units;
+    float dg[8], du[8];
+    gate_grads<MOE_DT_F16>(a, c, 8 * (int)(e - c * a.units), dg, du);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t x = __float_as_uint(dg[j]) & 0x7FFFFFFFu, y = __float_as_uint(du[j]) & 0x7FFFFFFFu;
+      if (x < 0x7F800000u) most = x > most ? x : most;
+      if (y < 0x7F800000u) most = y > most ? y : most;
+    }
+  }
+  most = most_of(most, s_most);
+  if (threadIdx.x == 0) a.most[blockIdx.x] = __uint_as_float(most);
+}
+
+// dg and du as operands; past the last column zeros, the sum over I runs on whole steps.
+// Bound by memory: 4096 x 4096 in bf16 40.8 us for 235 MB (5.8 TB/s).  In 16 bits a value is two terms, itself rounded and what is
+// left rounded: 2^-17 of it is lost in bf16.  In fp16 both are under the power of two
+// that puts the call's largest finite value below 2^15 (2^-23 of a value is lost, or
+// 2^-39 of the largest), so that neither an infinity nor a zero comes of its range.
 template <int DT>
 __global__ __launch_bounds__(256) void k_fact(GArgs a) {
   constexpr int B = kBytes<DT>;
+  __shared__ uint32_t s_most[4];
+  float m = 1.0f;
+  if constexpr (DT == MOE_DT_F16) {
+    const uint32_t most = most_of((int)threadIdx.x < a.parts ? __float_as_uint(a.most[threadIdx.x]) : 0u, s_most);
+    int e = most ? 14 - ((int)(most >> 23) - 127) : 0;
+    e = e > 126 ? 126 : e;
+    m = __uint_as_float((uint32_t)(127 + e) << 23);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.most[kMostParts] = __uint_as_float((uint32_t)(127 - e) << 23);
+  }
   const int64_t n = (int64_t)a.C * a.units;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
     const int64_t c = e / a.units;
     const int i = 8 * (int)(e - c * a.units);
-    const uint8_t *pg = a.gate + c * a.gate_pitch, *pu = a.up + c * a.up_pitch, *pd = a.dh + c * a.dh_pitch;
-    Eight<DT> g, u, d;
-    if (a.I % 8 == 0) {                 // one branch for the three, which are then on their way together
-      g = load8<DT>(pg + (int64_t)i * B);
-      u = load8<DT>(pu + (int64_t)i * B);
-      d = load8<DT>(pd + (int64_t)i * B);
-    } else {
-      g = load8_of<DT>(pg, i, a.I);
-      u = load8_of<DT>(pu, i, a.I);
-      d = load8_of<DT>(pd, i, a.I);
-    }
     float dg[8], du[8];
+    gate_grads<DT>(a, c, i, dg, du);
+    auto put = [&](uint8_t* row, float (&v)[8]) {
+      if constexpr (DT == MOE_DT_F32) {
+        store8<DT>(row + (int64_t)i * B, put8<DT>(v));
+      } else {
+        uint8_t* p = row + (i >> 5) * 128 + (i & 31) * 2;
+        float lo[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float act, slope;
-      act_slope(a.act, get8<DT>(g, j), act, slope);
-      const float t = get8<DT>(d, j);
-      du[j] = t * act;
-      dg[j] = t * get8<DT>(u, j) * slope;
-    }
-    store8<DT>(a.dg + c * a.pitch + (int64_t)i * B, put8<DT>(dg));
-    store8<DT>(a.du + c * a.pitch + (int64_t)i * B, put8<DT>(du));
+        for (int j = 0; j < 8; ++j) v[j] *= m;
+        const Eight<DT> hi = put8<DT>(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float h = get8<DT>(hi, j);
+          lo[j] = fabsf(h) < INFINITY ? v[j] - h : 0.0f;   // not finite: its own first term
+        }
+        store8<DT>(p, hi);
+        store8<DT>(p + 64, put8<DT>(lo));
+      }
+    };
+    put(a.dg + c * a.pitch, dg);
+    put(a.du + c * a.pitch, du);
   }
 }
 
@@ -643,7 +743,7 @@ bool whole_units(const void* p, int64_t pitch, int64_t rows, int64_t cols, int64
 struct Tiling { int bm, bn, mblocks, nblocks, steps, splits, per_split; };
 Tiling tiling(int mode, int64_t M, int64_t N, int64_t K, int64_t s) {
   Tiling t;
-  const int e = (int)(128 / s);
+  const int e = (int)(s == 2 && mode != kFwd ? 32 : 128 / s);       // positions of a step
   auto blocks = [&](int bm, int bn) {
     t.bm = bm; t.bn = bn;
     t.mblocks = (int)((M + bm - 1) / bm) * (mode == kDw ? 2 : 1);
@@ -671,12 +771,12 @@ Tiling tiling(int mode, int64_t M, int64_t N, int64_t K, int64_t s) {
   return t;
 }
 
-struct FfnWs { size_t x, wg, wu, dg, du, part, total; int64_t hp, ip; };
+struct FfnWs { size_t x, wg, wu, dg, du, most, part, total; int64_t hp, ip; };
 FfnWs ffn_ws_for(const moe_ffn* f, int C, bool bwd) {
   const int64_t s = dense_size(f->dtype), H = f->hidden, I = f->inter;
   FfnWs w;
   w.hp = (H + 7) / 8 * 8 * s;
-  w.ip = (I + 7) / 8 * 8 * s;
+  w.ip = s == 2 ? (I + 31) / 32 * 128 : (I + 7) / 8 * 8 * s;
   size_t o = 0;
   // x's own alignment is not known here: room for it and for weights that need it
   w.x = o; o = align256(o + (size_t)C * w.hp);
@@ -684,6 +784,7 @@ FfnWs ffn_ws_for(const moe_ffn* f, int C, bool bwd) {
   w.wu = o; o = align256(o + (whole_units(f->w_up, f->up_pitch, I, H, s) ? 0 : (size_t)I * w.hp));
   w.dg = o; o = align256(o + (bwd ? (size_t)C * w.ip : 0));
   w.du = o; o = align256(o + (bwd ? (size_t)C * w.ip : 0));
+  w.most = o; o = align256(o + (bwd && f->dtype == MOE_DT_F16 ? (kMostParts + 1) * sizeof(float) : 0));
   w.part = o;
   const Tiling t = bwd ? tiling(kDx, C, H, I, s) : tiling(kFwd, C, I, H, s);
   if (t.splits > 1) o = align256(o + (size_t)t.splits * C * (bwd ? H : 2 * I) * sizeof(float));
@@ -705,7 +806,7 @@ size_t ffn_workspace(const moe_ffn* f, int C) {
 
 template <int DT, int MODE, int BM, int BN, int WM, int WN>
 moe_status launch_gemm_t(const FArgs& a, dim3 grid, hipStream_t st) {
-  constexpr int lds = 2 * (BM + BN) * 128 + BM * 16;         // two stages, or the results
+  constexpr int lds = kGemmLds<DT, MODE, BM, BN>;
   auto k = k_fgemm<DT, MODE, BM, BN, WM, WN>;
   if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                          lds) != hipSuccess)
@@ -783,7 +884,14 @@ moe_status ffn_backward(const moe_ffn* f, FArgs a, GArgs g, uint8_t* dx, int64_t
                         uint8_t* w8, hipStream_t st) {
   g.dg = w8 + w.dg; g.du = w8 + w.du;
   g.pitch = w.ip;
-  g.units = (a.I + 7) / 8;
+  g.units = DT == MOE_DT_F32 ? (a.I + 7) / 8 : (a.I + 31) / 32 * 4;
+  if constexpr (DT == MOE_DT_F16) {
+    g.most = reinterpret_cast<float*>(w8 + w.most);
+    const unsigned most = fill_grid((int64_t)a.C * g.units);
+    g.parts = most < kMostParts ? (int)most : kMostParts;
+    hipLaunchKernelGGL(k_fmost, dim3((unsigned)g.parts), dim3(256), 0, st, g);
+    a.unscale = g.most + kMostParts;
+  }
   hipLaunchKernelGGL((k_fact<DT>), dim3(fill_grid((int64_t)a.C * g.units)), dim3(256), 0, st, g);
   operands<DT>(f, a, w, w8, dx != nullptr, dwg != nullptr, st);
   a.part = reinterpret_cast<float*>(w8 + w.part);
