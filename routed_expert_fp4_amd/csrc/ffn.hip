@@ -42,14 +42,16 @@ struct Act { float k1, k3; };
 inline Act act_constants(int act) {
   return act == MOE_ACT_SILU ? Act{1.0f, 0.0f} : Act{1.5957691216057308f, (float)(1.5957691216057308 * 0.044715)};
 }
+// k3 g^2, and 0 for SiLU whatever g is: 0 times an infinity is NaN
+__device__ __forceinline__ float cubic(const Act& k, float g) { return k.k3 != 0.0f ? k.k3 * g * g : 0.0f; }
 // act(g) and its slope; where the sigmoid is gone they are 0, however large g
 __device__ __forceinline__ float act_of(const Act& k, float g) {
   float s, c;
-  sigmoids(g * (k.k1 + k.k3 * g * g), s, c);
+  sigmoids(g * (k.k1 + cubic(k, g)), s, c);
   return s > 0.0f ? g * s : 0.0f * s;
 }
 __device__ __forceinline__ void act_slope(const Act& k, float g, float& a, float& d) {
-  const float q = k.k3 * g * g;
+  const float q = cubic(k, g);
   float s, c;
   sigmoids(g * (k.k1 + q), s, c);
   const float slope = k.k1 + 3.0f * q, e = s * c;
