@@ -471,6 +471,13 @@ moe_status moe_adapter_plan(const int32_t *token_adapter, int32_t C, int32_t ada
  * no initialisation, nothing is kept in it between calls, one call at a time. */
 size_t moe_adapter_workspace_size(const moe_adapter_bank *bank, int32_t C);
 
+/* What serving needs: the forward pass alone keeps partial sums of t, a few rows of
+ * `rank` fp32 for each token, however many adapters there are.  moe_adapter_fwd is told of
+ * such a workspace by MOE_WS_FORWARD added to its ws_bytes (without it, it asks for a
+ * workspace of both directions); moe_adapter_bwd refuses one. */
+#define MOE_WS_FORWARD ((size_t)1 << 62)
+size_t moe_adapter_fwd_workspace_size(const moe_adapter_bank *bank, int32_t C);
+
 /* y [C][y_pitch] from x [C][x_pitch] and base [C][base_pitch] (NULL: zeros; y may be
  * base itself, other overlaps of an output are refused), 1 <= C <=
  * MOE_MAX_BATCH_TOKENS.  hidden: NULL, or [C][rank] fp32 that receives t (zeros for a
@@ -523,6 +530,9 @@ typedef struct {
 /* Workspace of both directions for up to C tokens (0 outside the supported range): no
  * initialisation, nothing is kept in it between calls, one call at a time. */
 size_t moe_ffn_workspace_size(const moe_ffn *f, int32_t C);
+
+/* What moe_ffn_fwd alone needs of it. */
+size_t moe_ffn_fwd_workspace_size(const moe_ffn *f, int32_t C);
 
 /* h [C][h_pitch] from x [C][x_pitch], 1 <= C <= MOE_MAX_FFN_TOKENS.  gate, up
  * [C][..pitch]: NULL both, or they receive g and u, rounded to the type, for the

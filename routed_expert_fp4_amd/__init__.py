@@ -31,8 +31,8 @@ EXPORTS = ("moe_version", "moe_status_string", "moe_bank_layout", "moe_workspace
            "moe_quant_linear", "moe_expert_counts", "moe_balance_workspace_size",
            "moe_balance_fwd", "moe_balance_bwd", "moe_route_bwd", "moe_dropout",
            "moe_adapter_plan_size", "moe_adapter_plan", "moe_adapter_workspace_size",
-           "moe_adapter_fwd", "moe_adapter_bwd", "moe_ffn_workspace_size", "moe_ffn_fwd",
-           "moe_ffn_bwd")
+           "moe_adapter_fwd_workspace_size", "moe_adapter_fwd", "moe_adapter_bwd", "moe_ffn_workspace_size",
+           "moe_ffn_fwd_workspace_size", "moe_ffn_fwd", "moe_ffn_bwd")
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 1, 2, 3
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 1, 2
 MOE_MAX_QUANT_ROWS, MOE_MAX_QUANT_COLS = 1 << 22, 1 << 17
@@ -40,6 +40,7 @@ MOE_MAX_BATCH_TOKENS, MOE_MAX_SEQUENCES = 1 << 20, 65535
 MOE_MAX_ADAPTERS, MOE_MAX_RANK = 1024, 128
 MOE_ACT_SILU, MOE_ACT_GELU = 1, 2
 MOE_MAX_FFN_TOKENS = 1 << 17
+MOE_WS_FORWARD = 1 << 62
 ACTIVATIONS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU}
 SCORES = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 
@@ -124,10 +125,12 @@ def lib() -> ctypes.CDLL:
             "moe_adapter_plan_size": ([i32, i32], sz),
             "moe_adapter_plan": ([P, i32, i32, P, sz, P], i32),
             "moe_adapter_workspace_size": ([P, i32], sz),
+            "moe_adapter_fwd_workspace_size": ([P, i32], sz),
             "moe_adapter_fwd": ([P, P, sz, P, i64, i32, P, i64, P, i64, P, f64, P, P, sz, P], i32),
             "moe_adapter_bwd": ([P, P, sz, P, i64, P, P, i64, i32, P, i64, P, i64, P, P, i32, f64, P, P, sz, P],
                                 i32),
             "moe_ffn_workspace_size": ([P, i32], sz),
+            "moe_ffn_fwd_workspace_size": ([P, i32], sz),
             "moe_ffn_fwd": ([P, P, i64, i32, P, i64, P, i64, P, i64, P, sz, P], i32),
             "moe_ffn_bwd": ([P, P, i64, P, i64, P, i64, P, i64, i32, P, i64, i32, P, i64, P, i64, i32, P, sz, P],
                             i32),
@@ -686,15 +689,18 @@ def moe_adapter_plan(token_adapter, C, n, plan: AdapterPlan, stream=None):
 
 
 class AdapterWorkspace:
-    """Device memory of the adapters' calls for up to C tokens; nothing is kept in
+    """Device memory of the adapters' calls for up to C tokens, of both directions or
+    (backward=False) of the forward pass alone, which takes far less; nothing is kept in
     it between calls."""
 
-    def __init__(self, bank: AdapterBank, C: int):
+    def __init__(self, bank: AdapterBank, C: int, backward: bool = True):
         import torch
-        self.nbytes, self.device = lib().moe_adapter_workspace_size(bank.ref, C), bank.device
-        if self.nbytes == 0:
-            raise MoeError("moe_adapter_workspace_size", MOE_ERR_UNSUPPORTED)
-        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=f"cuda:{bank.device}")
+        fn = "moe_adapter_workspace_size" if backward else "moe_adapter_fwd_workspace_size"
+        size, self.device = getattr(lib(), fn)(bank.ref, C), bank.device
+        if size == 0:
+            raise MoeError(fn, MOE_ERR_UNSUPPORTED)
+        self.tensor = torch.empty(size, dtype=torch.uint8, device=f"cuda:{bank.device}")
+        self.nbytes = size if backward else size | MOE_WS_FORWARD      # as the calls take it
 
 
 def _adapter_plan(plan, bank, C):
@@ -755,14 +761,15 @@ class FfnBlock:
 
 
 class FfnWorkspace:
-    """Device memory of a gated block's calls for up to C tokens; nothing is kept in
-    it between calls."""
+    """Device memory of a gated block's calls for up to C tokens, of both directions or
+    (backward=False) of the forward pass alone; nothing is kept in it between calls."""
 
-    def __init__(self, block: FfnBlock, C: int):
+    def __init__(self, block: FfnBlock, C: int, backward: bool = True):
         import torch
-        self.nbytes, self.device = lib().moe_ffn_workspace_size(block.ref, C), block.device
+        fn = "moe_ffn_workspace_size" if backward else "moe_ffn_fwd_workspace_size"
+        self.nbytes, self.device = getattr(lib(), fn)(block.ref, C), block.device
         if self.nbytes == 0:
-            raise MoeError("moe_ffn_workspace_size", MOE_ERR_UNSUPPORTED)
+            raise MoeError(fn, MOE_ERR_UNSUPPORTED)
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=f"cuda:{block.device}")
 
 

@@ -1046,18 +1046,20 @@ Split shrink_split(int tiles, int cols) {
 }
 
 // The workspace: bounds that hold for every number of tokens up to C, so that it
-// serves fewer too.  With ranges (512 / tiles, tiles > C / 64) the partial sums are
-// those of 512 * 64 tokens at most, and there are eight chunks a batch, or one to
-// 2048 tokens, besides every adapter's last.
+// serves fewer too.  With ranges (512 / tiles, tiles > C / 64) the partial sums, the
+// first part and all that the forward pass uses, are those of 512 * 64 tokens at most,
+// and there are eight chunks a batch, or one to 2048 tokens, besides every adapter's last.
+size_t partial_sums(int C, int64_t cols, int rank) {
+  const int64_t most = (cols + 511) / 512, rows = C * most < 512 * 64 ? C * most : C > 512 * 64 ? C : 512 * 64;
+  return align256((size_t)rows * rank * sizeof(float));
+}
 struct AdapterWs { size_t part, u, turned, suma, sumb, pieces, piece_bytes, total; int64_t turn_pitch, turn_stride; };
 AdapterWs adapter_ws(const moe_adapter_bank* b, int C) {
   const int64_t s = dense_size(b->dtype);
-  const int64_t most = ((b->cols > b->rows ? b->cols : b->rows) + 511) / 512;
-  const int64_t rows = C * most < 512 * 64 ? C * most : C > 512 * 64 ? C : 512 * 64;
   const int64_t few = C / 256 < 8 ? C / 256 : 8, chunks = (C / 2048 > few ? C / 2048 : few) + (C < b->adapters ? C : b->adapters);
   AdapterWs w;
   size_t o = 0;
-  w.part = o; o = align256(o + (size_t)rows * b->rank * sizeof(float));
+  w.part = o; o += partial_sums(C, b->cols > b->rows ? b->cols : b->rows, b->rank);
   w.u = o; o = align256(o + (size_t)C * b->rank * sizeof(float));
   w.turn_pitch = (b->rows * s + 15) / 16 * 16;
   w.turn_stride = w.turn_pitch * b->rank;
@@ -1138,7 +1140,8 @@ Reads adapter_reads(const moe_adapter_bank* b, const void* plan, size_t plan_byt
                 span(b->scales, 4 * (int64_t)b->adapters), span(plan, (int64_t)plan_bytes), span(rng, 16)}};
 }
 
-// The checks that both directions make, and the arguments that they share.
+// The checks that both directions make, and the arguments that they share; `need`: the
+// workspace's bytes.
 struct Call {
   AArgs a;
   PlanLayout at;
@@ -1147,13 +1150,13 @@ struct Call {
   int64_t s;
 };
 moe_status adapter_call(const moe_adapter_bank* b, const void* plan, size_t plan_bytes, int32_t C, double p,
-                        const uint64_t* rng, void* ws, size_t ws_bytes, Call& c) {
+                        const uint64_t* rng, void* ws, size_t ws_bytes, size_t need, Call& c) {
   moe_status st = dropout_of(p, rng, c.a.drop);
   if (st != MOE_OK) return st;
   c.at = plan_layout(C, b->adapters);
   if (!plan || (uintptr_t)plan % 256 || plan_bytes < (size_t)c.at.total * sizeof(int32_t)) return MOE_ERR_WORKSPACE;
   c.ws = adapter_ws(b, C);
-  if (!ws || (uintptr_t)ws % 256 || ws_bytes < c.ws.total) return MOE_ERR_WORKSPACE;
+  if (!ws || (uintptr_t)ws % 256 || ws_bytes < need) return MOE_ERR_WORKSPACE;
   c.s = dense_size(b->dtype);
   c.w8 = static_cast<uint8_t*>(ws);
   c.a.plan = static_cast<const int32_t*>(plan);
@@ -1197,6 +1200,11 @@ size_t moe_adapter_workspace_size(const moe_adapter_bank* b, int32_t C) {
   return adapter_ws(b, C).total;
 }
 
+size_t moe_adapter_fwd_workspace_size(const moe_adapter_bank* b, int32_t C) {
+  if (adapter_status(b) != MOE_OK || C < 1 || C > MOE_MAX_BATCH_TOKENS) return 0;
+  return partial_sums(C, b->cols, b->rank);
+}
+
 moe_status moe_adapter_fwd(const moe_adapter_bank* b, const void* plan, size_t plan_bytes, const void* x,
                            int64_t x_pitch, int32_t C, const void* base, int64_t base_pitch, void* y, int64_t y_pitch,
                            float* hidden, double p, const uint64_t* rng, void* ws, size_t ws_bytes, void* stream) {
@@ -1211,11 +1219,14 @@ moe_status moe_adapter_fwd(const moe_adapter_bank* b, const void* plan, size_t p
   if (hidden && (st = rows_status(rh)) != MOE_OK) return st;
   if (share(rx, ry) || (share(rb, ry) && !same(rb, ry)) || share(rh, ry) || share(rh, rx) || share(rh, rb))
     return MOE_ERR_INVALID_ARG;
+  const bool forward = ws_bytes & MOE_WS_FORWARD;
+  ws_bytes &= ~MOE_WS_FORWARD;
   const Rows outs[] = {ry, rh, span(ws, (int64_t)ws_bytes)};
   const Rows tensors[] = {rx, ry, rb, rh};
   if (any_share(outs, adapter_reads(b, plan, plan_bytes, p > 0 ? rng : nullptr).r) || any_share({outs[2]}, tensors)) return MOE_ERR_INVALID_ARG;
   Call c = {};
-  if ((st = adapter_call(b, plan, plan_bytes, C, p, rng, ws, ws_bytes, c)) != MOE_OK) return st;
+  const size_t need = forward ? partial_sums(C, b->cols, b->rank) : adapter_ws(b, C).total;
+  if ((st = adapter_call(b, plan, plan_bytes, C, p, rng, ws, ws_bytes, need, c)) != MOE_OK) return st;
   hipStream_t q = reinterpret_cast<hipStream_t>(stream);
   by_dtype(b->dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
@@ -1255,6 +1266,7 @@ moe_status moe_adapter_bwd(const moe_adapter_bank* b, const void* plan, size_t p
   if (da && (st = rows_status(rx)) != MOE_OK) return st;
   if (db && (st = rows_status(rh)) != MOE_OK) return st;
   if ((uintptr_t)da % 4 || (uintptr_t)db % 4) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes & MOE_WS_FORWARD) return MOE_ERR_WORKSPACE;
   const Rows outs[] = {rg, ga, gb, span(ws, (int64_t)ws_bytes)};
   const Rows ins[] = {rd, da ? rx : Rows{}, db ? rh : Rows{}};
   const Rows grads[] = {rg, ga, gb, dx ? rb : Rows{}};
@@ -1264,7 +1276,7 @@ moe_status moe_adapter_bwd(const moe_adapter_bank* b, const void* plan, size_t p
   if (share(rg, ga) || share(rg, gb) || share(ga, gb)) return MOE_ERR_INVALID_ARG;
   if (dx && base && ((share(rb, rg) && !same(rb, rg)) || share(rb, ga) || share(rb, gb))) return MOE_ERR_INVALID_ARG;
   Call c = {};
-  if ((st = adapter_call(b, plan, plan_bytes, C, p, rng, ws, ws_bytes, c)) != MOE_OK) return st;
+  if ((st = adapter_call(b, plan, plan_bytes, C, p, rng, ws, ws_bytes, adapter_ws(b, C).total, c)) != MOE_OK) return st;
   hipStream_t q = reinterpret_cast<hipStream_t>(stream);
   const bool drop = c.a.drop.drop != 0;
   float* u = reinterpret_cast<float*>(c.w8 + c.ws.u);

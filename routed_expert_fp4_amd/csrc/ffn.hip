@@ -776,10 +776,14 @@ Tiling tiling(int mode, int64_t M, int64_t N, int64_t K, int64_t s) {
 struct FfnWs { size_t x, wg, wu, dg, du, most, part, total; int64_t hp, ip; };
 FfnWs ffn_ws_for(const moe_ffn* f, int C, bool bwd) {
   const int64_t s = dense_size(f->dtype), H = f->hidden, I = f->inter;
-  FfnWs w;
+  FfnWs w = {};
   w.hp = (H + 7) / 8 * 8 * s;
   w.ip = s == 2 ? (I + 31) / 32 * 128 : (I + 7) / 8 * 8 * s;
   size_t o = 0;
+  if (!bwd && C <= kFewTokens) {
+    w.total = 0;                        // k_ffew takes everything as it is
+    return w;
+  }
   // x's own alignment is not known here: room for it and for weights that need it
   w.x = o; o = align256(o + (size_t)C * w.hp);
   w.wg = o; o = align256(o + (whole_units(f->w_gate, f->gate_pitch, I, H, s) ? 0 : (size_t)I * w.hp));
@@ -795,10 +799,10 @@ FfnWs ffn_ws_for(const moe_ffn* f, int C, bool bwd) {
 }
 // The most that any number of tokens up to C needs: partial results come and go
 // with the ranges, which depend on tiles of 64 tokens.
-size_t ffn_workspace(const moe_ffn* f, int C) {
+size_t ffn_workspace(const moe_ffn* f, int C, bool bwd) {
   size_t most = 256;
   for (int c = C;; c = (c - 1) / 64 * 64) {
-    const size_t a = ffn_ws_for(f, c, false).total, b = ffn_ws_for(f, c, true).total;
+    const size_t a = ffn_ws_for(f, c, false).total, b = bwd ? ffn_ws_for(f, c, true).total : 0;
     most = a > most ? a : most;
     most = b > most ? b : most;
     if (c <= 64) break;
@@ -935,7 +939,12 @@ extern "C" {
 
 size_t moe_ffn_workspace_size(const moe_ffn* f, int32_t C) {
   if (ffn_status(f) != MOE_OK || C < 1 || C > MOE_MAX_FFN_TOKENS) return 0;
-  return ffn_workspace(f, C);
+  return ffn_workspace(f, C, true);
+}
+
+size_t moe_ffn_fwd_workspace_size(const moe_ffn* f, int32_t C) {
+  if (ffn_status(f) != MOE_OK || C < 1 || C > MOE_MAX_FFN_TOKENS) return 0;
+  return ffn_workspace(f, C, false);
 }
 
 moe_status moe_ffn_fwd(const moe_ffn* f, const void* x, int64_t x_pitch, int32_t C, void* h, int64_t h_pitch, void* gate,
