@@ -181,6 +181,10 @@ def run(state):
     op, C = case["op"], case["C"]
     if own:
         import routed_expert_fp4_amd as rf
+        if op in ("adapter", "tune"):
+            # the batch's order by adapter, made of its tokens in every pass (a program's
+            # further projections of the step take the same one)
+            state["plan"].update(state["who"])
         if op == "adapter":
             rf.moe_adapter_fwd(state["bank"], state["plan"], state["x"], C, state["y"], state["ws"],
                                base=state["base"])
