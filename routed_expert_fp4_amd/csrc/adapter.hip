@@ -969,7 +969,7 @@ __global__ __launch_bounds__(256) void k_areduce(RArgs a) {
   float* o = second ? a.db + who * n + x % cols * a.r + x / cols * 4 : a.da + who * n + at;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] *= f;
+    v[i] = q0 == q1 ? 0.0f : v[i] * f;   // no tokens: zeros, whatever an unused adapter's scale is
     if (a.accumulate && i < most) v[i] += o[i];
   }
   store16_some<MOE_DT_F32>(o, pack16<MOE_DT_F32>(v), most);
