@@ -433,7 +433,9 @@ moe_status moe_dropout(int32_t dtype, const void *x, int64_t x_pitch, int32_t C,
  *   t_c = A_a d(x_c),   y_c = base_c + scales[a] B_a t_c
  * with d dropout of x in training (kept as moe_dropout keeps element (c, k) of x)
  * and the identity else.  A token without adapter has y_c = base_c.  t and every
- * sum are fp32, y is rounded once.  A sum that an infinity or NaN enters is not finite
+ * sum are fp32, y is rounded once.  (fp16: t, and u below, enter y and dx to 2^-23 of a
+ * value, or to 2^-39 of the token's largest where that is more; the products of da and
+ * db are within 2^-22.)  A sum that an infinity or NaN enters is not finite
  * (which of the two it is, is not defined: operands enter in several pieces).
  * Requirements (checked): 1 .. MOE_MAX_ADAPTERS adapters of one rank 1 ..
  * MOE_MAX_RANK (fill up smaller ones with zero rows of A), cols and rows up to

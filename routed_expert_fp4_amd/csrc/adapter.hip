@@ -8,11 +8,15 @@
 //
 // A rank is small (1 .. 128), so every product is bound by reading x, dy and the
 // adapters and by writing y and dx as long as the matrix cores are fed; t and u
-// stay in fp32.  Where t or u is an operand it enters as three bf16 pieces that
-// sum to it exactly (24 bits), where a 16-bit tensor meets them it is one bf16
-// (bf16) or two (fp16: 11 bits as 8 + 3), so every product is exact and only the
-// fp32 sums round.  The first product (x by A, dy by B) takes both sides as
-// stored, fp16 on the fp16 matrix cores.  fp32 tensors use the fp32 ones.
+// stay in fp32.  The first product (x by A, dy by B) takes both sides as stored,
+// fp16 on the fp16 matrix cores; fp32 tensors use the fp32 ones throughout: exact
+// products, fp32 sums.  Beside 16-bit tensors t and u are operands in pieces:
+//   bf16   three bf16 that sum to them exactly (24 bits): exact products again
+//   fp16   y and dx: two fp16 terms under a power of two per token, that lose 2^-23
+//          of a value, or 2^-39 of the token's largest (a rank whose t is that far
+//          below the others' loses its bits, which a large B shows in y);
+//          dA and dB: the three bf16, by the two that an fp16 element is (11 bits as
+//          8 + 3), without the product of the lowest two, below 2^-22 of the whole
 //
 // Tokens are taken in the order of a plan: sorted by adapter, in tiles of one
 // adapter's tokens (16, or 64 in large batches), and for the gradients of A and
@@ -199,8 +203,9 @@ __device__ __forceinline__ void pieces(uint4v v, uint4v (&p)[kPieces<DT>]) {
   }
 }
 
-// c += (the sum of small's pieces) * (the sum of big's): the products of the
-// two lowest, below 2^-24 of the whole, are left out
+// c += (the sum of small's pieces) * (the sum of big's).  Of fp16's six products that of
+// the two lowest pieces is left out: they are truncations, below 2^-15 of a value and at
+// most 7 2^-10 of an fp16 element, so 2^-22.2 of their product at most, of its sign.
 template <int DT>
 __device__ __forceinline__ float4v mma_pieces(const uint4v (&s)[3], const uint4v (&b)[kPieces<DT>], float4v c) {
 #pragma unroll
@@ -387,8 +392,9 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
 // Bound by latency, then by base and y: 4096 bf16 tokens x 3584, rank 64, 25.7 us for 58
 // MB, all workgroups at once; 8192 fp16 x 7168 70 us for 235 MB, 3.3 TB/s.
 // For fp16, t and u are two fp16 terms under a power of two per token that puts the
-// token's largest below 2^15: 22 bits, or 2^-39 of the largest; for bf16 three bf16
-// pieces, exact.
+// token's largest at 2^14 or more and below 2^15: the first leaves half a step of 11 bits,
+// the second half a step of that, 2^-23 of a value, or half of fp16's smallest, 2^-39 of
+// the largest; for bf16 three bf16 pieces, exact.
 //
 // sum += the partial sums of a tile's tokens tid / 16 + 16 i, ranks 32 q + 2 (tid % 16)
 // and the next, over all ranges in order, U of them at a time.
