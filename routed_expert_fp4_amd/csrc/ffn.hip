@@ -217,8 +217,8 @@ constexpr int kGemmLds = [] {
 
 // 16 bytes a lane into LDS, at `at` + 16 lane, by inline assembly: behind the
 // compiler's own form it lets every transposing LDS read wait for all of them.  They
-// have no register to write, and are waited for before the barrier that opens them.
-// m0, which holds the LDS address, has no other use on this device.
+// have no register to write but m0, which holds the LDS address, and are waited for
+// before the barrier that opens them.
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
 }
@@ -229,10 +229,10 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>((uintptr_t)(((uint64_t)hi << 32) | lo));
 }
 __device__ __forceinline__ void load_lds(const uint8_t* base, uint32_t off, const uint8_t* at) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(uniform(base)), "s"(lds_address(at)));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(uniform(base)), "s"(lds_address(at)) : "m0", "memory");
 }
 __device__ __forceinline__ void load_lds(const uint8_t* p, const uint8_t* at) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(lds_address(at)));
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(p), "s"(lds_address(at)) : "m0", "memory");
 }
 __device__ const uint32_t __attribute__((aligned(16))) kZeros[4] = {0, 0, 0, 0};
 
