@@ -167,3 +167,39 @@ def test_a_gradient_that_is_not_finite_stays_alone():
                     assert not torch.isfinite(got[at].float()).any(), (xt, bad, C, k)
                     keep = np.arange(w.shape[0]) != at
                     check(got[torch.from_numpy(keep).cuda()], w[keep], t[keep], 0, f"{xt} {bad} {C} {k}", rel=False)
+
+
+@pytest.mark.parametrize("xt", ["bf16", "f16", "f32"])
+def test_sums_that_are_added_to(xt):
+    for grad in (None, torch.float32):
+        c = Case(140, 200, 96, xt, grad=grad)
+        c.dx.fill_(1), c.dwg.fill_(2), c.dwu.fill_(3)
+        c.backward(accumulate=True)
+        want = c.wanted()[0]
+        for k, was in (("dx", 1), ("dwg", 2), ("dwu", 3)):
+            w = was + want[k][0]
+            check(getattr(c, k), w, want[k][1] + 2 * ref.U * np.abs(w), 0, f"{xt} {grad} {k}", rel=False)
+
+
+def test_each_replay_of_a_captured_call_takes_its_own_power_of_two():
+    """Gradients of other sizes on every replay, eager calls on another workspace
+    between them."""
+    for C in (6, 300):
+        c, other = Case(C, 200, 96, "f16", grad=torch.float32), Case(C, 200, 96, "f16", dh=100.0)
+        c.backward()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            import routed_expert_fp4_amd as rf
+            rf.moe_ffn_bwd(c.block, c.x, c.gate, c.up, c.dh, C, c.dx, c.dwg, c.dwu, c.ws)
+        dh = c.dh.clone()
+        for size in (1.0, 2.0 ** -10, 2.0 ** 12, 1.0, 0.0):
+            c.dh.copy_(dh * size)
+            for v in (c.dx, c.dwg, c.dwu):
+                v.fill_(9)
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [v.clone() for v in (c.dx, c.dwg, c.dwu)]
+            c.check((C, size))
+            other.backward()
+            c.backward()
+            assert all(torch.equal(a, b) for a, b in zip(got, (c.dx, c.dwg, c.dwu)))
