@@ -78,8 +78,10 @@ struct PArgs {
   PlanLayout at;
 };
 
-// (64 tokens of 24 adapters 6.3 us, 8192 of 4 21: a batch's once, for all projections.)
-// One workgroup: eight waves take an eighth of the tokens each, count them by
+// One workgroup, since tokens keep their order without any exchange between workgroups:
+// 64 tokens of 24 adapters 5.6 us, 8192 of 4 16; a batch's once, for all projections.  Its
+// time is the last loop's, over the adapters among 64 tokens: 8192 of 48 56 us.
+// Eight waves take an eighth of the tokens each, count them by
 // adapter (adapter n: none), and after a scan over (adapter, wave) place them in
 // order, so that tokens of one adapter stay in the batch's order.
 __global__ __launch_bounds__(kPlanWG) void k_aplan(PArgs a) {
@@ -271,7 +273,8 @@ struct AArgs {
 // last.  Bound by x and, once a tile, A: 4096 bf16 tokens x 7168 of 8 adapters of rank 64
 // 23.8 us, 118 MB together.  (64 at a time, whole lines of 16-bit rows, took more
 // registers than two waves a SIMD have: 8192 fp16 tokens x 3584, rank 64, with dropout
-// 36 us against 28.)
+// 36 us against 28.  fp32 with dropout, tiles of 64 tokens and more than 32 ranks takes
+// more than half of a SIMD's registers, one wave.)
 template <int DT, int NT, int TT, bool DROP>
 __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
   constexpr int B = kBytes<DT>, T = 16 * TT, S = 1, U = 32 * S;   // steps and columns of a wave's turn
@@ -391,6 +394,9 @@ __global__ __launch_bounds__(kAWG) void k_ashrink(AArgs a) {
 // stay in registers for all of the tile's tokens, 16 at a time.
 // Bound by latency, then by base and y: 4096 bf16 tokens x 3584, rank 64, 25.7 us for 58
 // MB, all workgroups at once; 8192 fp16 x 7168 70 us for 235 MB, 3.3 TB/s.
+// Registers: ranks above 64 take more than half of a SIMD's, one wave; dx of ranks 33 to 64
+// with dropout in 16 bits keeps two waves and puts 28 bytes a lane into scratch (8192 x
+// 3584: 47 us).
 // For fp16, t and u are two fp16 terms under a power of two per token that puts the
 // token's largest at 2^14 or more and below 2^15: the first leaves half a step of 11 bits,
 // the second half a step of that, 2^-23 of a value, or half of fp16's smallest, 2^-39 of

@@ -201,10 +201,8 @@ __global__ __launch_bounds__(kFewWG) void k_ffew(FArgs a) {
 // step is 128 bytes of 32 positions, quarters hi and lo of one 16, then of the other, and
 // the second operand's fragments, half as many, serve both.
 // First launches in bf16 x 7168 x 4096: 2048 tokens 200 us (1.2 PFLOP/s), matrix cores
-// busy for 60% of the cycles; 4096 tokens' dx 772 and weights' gradients 777, 1.25 PFLOP/s
-// of both terms (in one term, rounded to the type, 449 and 448).
-// A copy of the forward case as it was at 203 us took 173 without loads into LDS, 170
-// without LDS reads and 140 without both: each costs about as much beside the other.
+// busy for 60% of the cycles; 4096 tokens' dx 760 and weights' gradients 763, 1.26 PFLOP/s
+// of both terms, 57% and 59% (in one term, rounded to the type, 449 and 448).
 enum { kFwd, kDx, kDw };
 template <int DT, int MODE>
 constexpr int kTerms = DT != MOE_DT_F32 && MODE != kFwd ? 2 : 1;
@@ -654,10 +652,11 @@ __global__ __launch_bounds__(256) void k_fmost(GArgs a) {
 }
 
 // dg and du as operands; past the last column zeros, the sum over I runs on whole steps.
-// Bound by memory: 4096 x 4096 in bf16 40.8 us for 235 MB (5.8 TB/s).  In 16 bits a value is two terms, itself rounded and what is
-// left rounded: 2^-17 of it is lost in bf16.  In fp16 both are under the power of two
-// that puts the call's largest finite value below 2^15 (2^-23 of a value is lost, or
-// 2^-39 of the largest), so that neither an infinity nor a zero comes of its range.
+// In 16 bits a value is two terms, itself rounded and what is left rounded: 2^-17 of it
+// is lost in bf16.  In fp16 both are under the power of two that puts the call's largest
+// finite value at 2^14 or more and below 2^15 (2^-23 of a value is lost, or 2^-39 of the
+// largest), so that neither an infinity nor a zero comes of its range.  Bound by memory:
+// 4096 x 4096 in bf16 40.8 us for 235 MB (5.8 TB/s).
 template <int DT>
 __global__ __launch_bounds__(256) void k_fact(GArgs a) {
   constexpr int B = kBytes<DT>;
