@@ -696,11 +696,16 @@ class AdapterWorkspace:
     def __init__(self, bank: AdapterBank, C: int, backward: bool = True):
         import torch
         fn = "moe_adapter_workspace_size" if backward else "moe_adapter_fwd_workspace_size"
-        size, self.device = getattr(lib(), fn)(bank.ref, C), bank.device
-        if size == 0:
+        self.nbytes, self.device = getattr(lib(), fn)(bank.ref, C), bank.device
+        if self.nbytes == 0:
             raise MoeError(fn, MOE_ERR_UNSUPPORTED)
-        self.tensor = torch.empty(size, dtype=torch.uint8, device=f"cuda:{bank.device}")
-        self.nbytes = size if backward else size | MOE_WS_FORWARD      # as the calls take it
+        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=f"cuda:{bank.device}")
+        self.of = 0 if backward else MOE_WS_FORWARD
+
+
+def _adapter_scratch(ws, dev):
+    ptr, nbytes = _scratch(ws, AdapterWorkspace, dev)
+    return ptr, nbytes | ws.of
 
 
 def _adapter_plan(plan, bank, C):
@@ -721,7 +726,7 @@ def moe_adapter_fwd(bank: AdapterBank, plan: AdapterPlan, x, C, y, ws: AdapterWo
     _launch("moe_adapter_fwd", dev, stream, bank.ref, *_adapter_plan(plan, bank, C), xp, xs, C,
             *_rows_or_none(base, dev, dtype, (C, bank.N), "base"), *_rows(y, dev, dtype, (C, bank.N), "y"),
             _maybe(hidden, dev, torch.float32, (C, bank.r), "hidden"), p, _rng(rng, dev),
-            *_scratch(ws, AdapterWorkspace, dev))
+            *_adapter_scratch(ws, dev))
 
 
 def moe_adapter_bwd(bank: AdapterBank, plan: AdapterPlan, x, hidden, dy, C, dx, dA, dB, ws: AdapterWorkspace,
@@ -737,7 +742,7 @@ def moe_adapter_bwd(bank: AdapterBank, plan: AdapterPlan, x, hidden, dy, C, dx, 
             _maybe(hidden, dev, f32, (C, bank.r), "hidden"), dp, ds, C,
             *_rows_or_none(base, dev, dtype, (C, bank.K), "base"), *_rows_or_none(dx, dev, dtype, (C, bank.K), "dx"),
             _maybe(dA, dev, f32, (bank.n, bank.r, bank.K), "dA"), _maybe(dB, dev, f32, (bank.n, bank.N, bank.r), "dB"),
-            accumulate, p, _rng(rng, dev), *_scratch(ws, AdapterWorkspace, dev))
+            accumulate, p, _rng(rng, dev), *_adapter_scratch(ws, dev))
 
 
 # ---------------------------------------------------------------------------

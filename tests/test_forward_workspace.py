@@ -89,6 +89,7 @@ def test_adapters_in_it(C, K, N, n, r, xt):
     y, hidden = c.y.clone(), c.hidden.clone()
     ws = rf.AdapterWorkspace(c.bank, C, backward=False)
     size = ws.tensor.numel()
+    assert ws.nbytes == size < rf.AdapterWorkspace(c.bank, C).nbytes
     wide = torch.full((size + 4096,), 171, dtype=torch.uint8, device="cuda")
     ws.tensor = wide[:size]
     c.ws = ws
